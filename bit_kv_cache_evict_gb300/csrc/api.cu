@@ -57,7 +57,9 @@ static int bf16_items(const oscar_shape* s) { return (s->sink + s->recent + 63) 
 // log2(quant_group / 32) and the (page, KV head) block size: K and V codes
 // (2 x 2048 B) + K and V (s, z) pairs (2 x 64 tokens x d/g x 4 B)
 static int gshift_of(const oscar_shape* s) { return s->quant_group == 32 ? 0 : (s->quant_group == 64 ? 1 : 2); }
-static int block_bytes_of(const oscar_shape* s) { return 4096 + 512 * (kD / s->quant_group); }
+static int block_bytes_of(const oscar_shape* s, int bits = 2) {
+    return bits == 4 ? 2 * half_bytes4(gshift_of(s)) : 4096 + 512 * (kD / s->quant_group);
+}
 
 // Pages at the end of each (sequence, KV head) that go to short items
 // queued after all the long ones, so that the last waves of the persistent
@@ -120,6 +122,11 @@ extern "C" {
 size_t oscar_block_bytes(const oscar_shape* shape) {
     if (check_shape(shape) != OSCAR_OK) return 0;
     return (size_t)block_bytes_of(shape);
+}
+
+size_t oscar_block_bytes_int4(const oscar_shape* shape) {
+    if (check_shape(shape) != OSCAR_OK) return 0;
+    return (size_t)block_bytes_of(shape, 4);
 }
 
 const char* oscar_status_string(oscar_status st) {
@@ -210,7 +217,8 @@ static oscar_status evict_impl(const oscar_shape* shape, int32_t n_tok, const vo
                                const int32_t* src_row, const int32_t* dst_seq, const int32_t* dst_pos,
                                const void* new_kv, const float* U, const float* clip, const float* codebook,
                                uint8_t* pool, uint8_t* boost, const int32_t* page_table, int32_t batch,
-                               int32_t max_pages, int32_t num_pages, int32_t* dev_status, void* stream) {
+                               int32_t max_pages, int32_t num_pages, int32_t* dev_status, void* stream,
+                               int bits = 2) {
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (n_tok < 0 || src_rows < 0 || batch < 0 || max_pages <= 0 || num_pages < 0) return OSCAR_ERR_INVALID_ARG;
@@ -241,7 +249,8 @@ static oscar_status evict_impl(const oscar_shape* shape, int32_t n_tok, const vo
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.gshift = gshift_of(shape);
-    p.block_bytes = block_bytes_of(shape);
+    p.block_bytes = block_bytes_of(shape, bits);
+    p.bits4 = bits == 4;
     const cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
 }
@@ -278,11 +287,23 @@ oscar_status oscar_evict_quantize_codebook(const oscar_shape* shape, int32_t n_t
                       nullptr, page_table, batch, max_pages, num_pages, dev_status, stream);
 }
 
+oscar_status oscar_evict_quantize_int4(const oscar_shape* shape, int32_t n_tok, const void* src_kv,
+                                       int32_t src_rows, const int32_t* src_row, const int32_t* dst_seq,
+                                       const int32_t* dst_pos, const void* new_kv, const float* U,
+                                       const float* clip, uint8_t* pool, const int32_t* page_table,
+                                       int32_t batch, int32_t max_pages, int32_t num_pages,
+                                       int32_t* dev_status, void* stream) {
+    if (max_pages > INT32_MAX / kPage) return OSCAR_ERR_INVALID_ARG;  // positions are int32
+    return evict_impl(shape, n_tok, src_kv, src_rows, src_row, dst_seq, dst_pos, new_kv, U, clip, nullptr, pool,
+                      nullptr, page_table, batch, max_pages, num_pages, dev_status, stream, 4);
+}
+
 static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const void* q, const void* bf16_kv,
                                 const int32_t* bf16_len, const uint8_t* pool, const int32_t* page_table,
                                 int32_t max_pages, int32_t num_pages, const int32_t* hist_len, const float* U,
                                 const float* codebook, const uint8_t* boost, float sm_scale, float* out,
-                                void* workspace, size_t* ws_bytes, int32_t* dev_status, void* stream) {
+                                void* workspace, size_t* ws_bytes, int32_t* dev_status, void* stream,
+                                int bits = 2, int out_type = OSCAR_OUT_F32) {
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (batch < 0 || max_pages <= 0 || num_pages < 0 || !ws_bytes) return OSCAR_ERR_INVALID_ARG;
@@ -297,8 +318,8 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     if (batch == 0) return OSCAR_OK;
     if (!q || !bf16_kv || !bf16_len || !hist_len || !U || !out || !page_table) return OSCAR_ERR_INVALID_ARG;
     if (num_pages > 0 && !pool) return OSCAR_ERR_INVALID_ARG;
-    if (!aligned(q, 8) || !aligned(bf16_kv, 16) || !aligned(U, 16) || !aligned(pool, 16) || !aligned(out, 16) ||
-        !aligned(workspace, 16) || !aligned(dev_status, 4))
+    if (!aligned(q, 8) || !aligned(bf16_kv, 16) || !aligned(U, 16) || !aligned(pool, 16) ||
+        !aligned(out, out_type == OSCAR_OUT_BF16 ? 8 : 16) || !aligned(workspace, 16) || !aligned(dev_status, 4))
         return OSCAR_ERR_INVALID_ARG;
     if (!(sm_scale == sm_scale)) return OSCAR_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -338,7 +359,9 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.gshift = gshift_of(shape);
-    p.block_bytes = block_bytes_of(shape);
+    p.block_bytes = block_bytes_of(shape, bits);
+    p.bits4 = bits == 4;
+    p.out_bf16 = out_type == OSCAR_OUT_BF16;
     p.pps = w.pps;
     p.tail_pg = w.tail_pg;
     p.part_stride = w.part_stride;
@@ -383,6 +406,120 @@ oscar_status oscar_decode_attn_codebook(const oscar_shape* shape, int32_t batch,
     if (workspace && (!codebook || !aligned(codebook, 4))) return OSCAR_ERR_INVALID_ARG;
     return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
                        codebook, nullptr, sm_scale, out, workspace, ws_bytes, dev_status, stream);
+}
+
+oscar_status oscar_decode_attn_int4(const oscar_shape* shape, int32_t batch, const void* q, const void* bf16_kv,
+                                    const int32_t* bf16_len, const uint8_t* pool, const int32_t* page_table,
+                                    int32_t max_pages, int32_t num_pages, const int32_t* hist_len, const float* U,
+                                    float sm_scale, void* out, int32_t out_type, void* workspace, size_t* ws_bytes,
+                                    int32_t* dev_status, void* stream) {
+    const oscar_status sst = check_shape(shape);
+    if (sst != OSCAR_OK) return sst;
+    if (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) return OSCAR_ERR_INVALID_ARG;
+    if (max_pages > INT32_MAX / kPage) return OSCAR_ERR_INVALID_ARG;  // positions are int32
+    return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
+                       nullptr, nullptr, sm_scale, static_cast<float*>(out), workspace, ws_bytes, dev_status, stream,
+                       4, out_type);
+}
+
+oscar_status oscar_history_read(const oscar_shape* shape, int32_t bits, int32_t n_tok, const int32_t* seq,
+                                const int32_t* pos, const uint8_t* pool, const int32_t* page_table, int32_t batch,
+                                int32_t max_pages, int32_t num_pages, void* out, int32_t out_type,
+                                int32_t* dev_status, void* stream) {
+    const oscar_status sst = check_shape(shape);
+    if (sst != OSCAR_OK) return sst;
+    if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
+    if (n_tok < 0 || batch < 0 || max_pages <= 0 || max_pages > INT32_MAX / kPage || num_pages < 0 ||
+        (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) || shape->num_kv_heads > 65535)
+        return OSCAR_ERR_INVALID_ARG;
+    if (n_tok == 0) return OSCAR_OK;
+    if (!seq || !pos || !page_table || !out || (num_pages > 0 && !pool)) return OSCAR_ERR_INVALID_ARG;
+    if (!aligned(seq, 4) || !aligned(pos, 4) || !aligned(page_table, 4) || !aligned(pool, 16) || !aligned(out, 16) ||
+        !aligned(dev_status, 4))
+        return OSCAR_ERR_INVALID_ARG;
+    HistoryReadParams p{};
+    p.seq = seq;
+    p.pos = pos;
+    p.pool = pool;
+    p.page_table = page_table;
+    p.out = out;
+    p.status = dev_status;
+    p.n_tok = n_tok;
+    p.hk = shape->num_kv_heads;
+    p.batch = batch;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.gshift = gshift_of(shape);
+    p.block_bytes = block_bytes_of(shape, bits);
+    p.bits4 = bits == 4;
+    p.out_bf16 = out_type == OSCAR_OUT_BF16;
+    const cudaError_t e = launch_history_read(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
+}
+
+oscar_status oscar_history_gather(const oscar_shape* shape, int32_t bits, int32_t batch, uint8_t* pool,
+                                  uint8_t* boost, const int32_t* src_table, int32_t src_max_pages,
+                                  const int32_t* dst_table, int32_t dst_max_pages, const int32_t* keep,
+                                  int32_t keep_stride, const int32_t* n_keep, int32_t num_pages,
+                                  int32_t* dev_status, void* stream) {
+    const oscar_status sst = check_shape(shape);
+    if (sst != OSCAR_OK) return sst;
+    if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
+    if (batch < 0 || src_max_pages <= 0 || dst_max_pages <= 0 || keep_stride < 0 || num_pages < 0 ||
+        src_max_pages > INT32_MAX / kPage || dst_max_pages > INT32_MAX / kPage || (boost && bits != 2))
+        return OSCAR_ERR_INVALID_ARG;
+    if ((double)batch * dst_max_pages * shape->num_kv_heads > (double)INT32_MAX) return OSCAR_ERR_INVALID_ARG;
+    if (batch == 0 || keep_stride == 0) return OSCAR_OK;
+    if (!src_table || !dst_table || !keep || !n_keep || (num_pages > 0 && !pool)) return OSCAR_ERR_INVALID_ARG;
+    if (!aligned(pool, 16) || !aligned(boost, 16) || !aligned(src_table, 4) || !aligned(dst_table, 4) ||
+        !aligned(keep, 4) || !aligned(n_keep, 4) || !aligned(dev_status, 4))
+        return OSCAR_ERR_INVALID_ARG;
+    HistoryGatherParams p{};
+    p.pool = pool;
+    p.boost = boost;
+    p.src_table = src_table;
+    p.dst_table = dst_table;
+    p.keep = keep;
+    p.n_keep = n_keep;
+    p.status = dev_status;
+    p.batch = batch;
+    p.hk = shape->num_kv_heads;
+    p.src_max_pages = src_max_pages;
+    p.dst_max_pages = dst_max_pages;
+    p.keep_stride = keep_stride;
+    p.num_pages = num_pages;
+    p.gshift = gshift_of(shape);
+    p.block_bytes = block_bytes_of(shape, bits);
+    p.bits4 = bits == 4;
+    const cudaError_t e = launch_history_gather(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
+}
+
+oscar_status oscar_pages_copy_device(size_t page_bytes, int32_t n_copies, const int32_t* src, const int32_t* dst,
+                                     uint8_t* const* pools, int32_t n_pools, int32_t num_pages, int32_t* dev_status,
+                                     void* stream) {
+    if (page_bytes == 0 || page_bytes % 16 != 0 || n_copies < 0 || n_pools < 0 || n_pools > OSCAR_MAX_COPY_POOLS ||
+        num_pages < 0)
+        return OSCAR_ERR_INVALID_ARG;
+    const int64_t pieces = pages_copy_pieces(page_bytes);
+    if ((double)pieces * n_copies * n_pools > (double)INT32_MAX) return OSCAR_ERR_INVALID_ARG;
+    if (n_copies == 0 || n_pools == 0) return OSCAR_OK;
+    if (!src || !dst || !pools || !aligned(src, 4) || !aligned(dst, 4) || !aligned(dev_status, 4))
+        return OSCAR_ERR_INVALID_ARG;
+    PagesCopyParams p{};
+    for (int32_t i = 0; i < n_pools; ++i) {
+        if (!pools[i] || !aligned(pools[i], 16)) return OSCAR_ERR_INVALID_ARG;
+        p.pool[i] = pools[i];
+    }
+    p.src = src;
+    p.dst = dst;
+    p.status = dev_status;
+    p.page_bytes = page_bytes;
+    p.n = n_copies;
+    p.pieces = (int)pieces;
+    p.num_pages = num_pages;
+    const cudaError_t e = launch_pages_copy(p, n_pools, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
 }
 
 oscar_status oscar_calibrate_rotation(const oscar_shape* shape, int32_t n_q, const void* q, int32_t n_t,

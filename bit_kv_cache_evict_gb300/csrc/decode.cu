@@ -32,6 +32,7 @@
 // q' 2^e and W are split into fp16 hi + lo (22 bits); codes are exact and
 // carry no offset.
 #include "oscar_common.cuh"
+#include "splitk.cuh"
 
 namespace oscar {
 
@@ -241,9 +242,11 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p) {
         // fragments: lane -> (ks, tq), k-step ks = (group g = ks/2, half h = ks%2)
         // covers in-group indices 8tq + 4h + {0,2} (b0) and + {1,3} (b1), the
         // four codes of bytes 4(2tq+h)..4(2tq+h)+3 of group g's slot; column
-        // 2hh = hi, 2hh+1 = lo
-        const int base = 32 * (ks >> 1) + 8 * tq + 4 * (ks & 1);
-        const float v[4] = {qs[base] * up, qs[base + 2] * up, qs[base + 1] * up, qs[base + 3] * up};
+        // 2hh = hi, 2hh+1 = lo.  (4-bit codes: in-group indices 8tq + 2h +
+        // {0,4} and + {1,5}, the nibbles 2h, 2h+1 of both halves of word tq.)
+        const int second = p.bits4 ? 4 : 2;
+        const int base = 32 * (ks >> 1) + 8 * tq + (p.bits4 ? 2 : 4) * (ks & 1);
+        const float v[4] = {qs[base] * up, qs[base + second] * up, qs[base + 1] * up, qs[base + second + 1] * up};
         uint32_t h01, h23, l01, l23;
         split_f16(v, h01, h23, l01, l23);
         if (p.NT == 2) {
@@ -278,15 +281,8 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p) {
 // the consumers find it in shared memory at the item's first page.  Every
 // wait is bounded; on a timeout the block reports OSCAR_STATUS_TIMEOUT, lets
 // its copies land and exits.
-constexpr int kConsumerWarps = 4;
 constexpr int kStages = 2 * kConsumerWarps;
-// Poll budget of every bounded mbarrier wait: a try_wait suspends about 4 us
-// when the phase is not complete (measured on GB300), so 2^18 polls give up
-// after about a second, far beyond any legitimate wait (a page copy, or the
-// other consumer warps finishing an item).
-constexpr int kWaitPolls = 1 << 18;
 constexpr int kInt2Threads = (kConsumerWarps + 1) * 32;
-constexpr int kFlagFirst = 1, kFlagLast = 2, kFlagPad = 4;
 
 struct StageInfo {
     int item, b, kv, valid_flags;  // valid tokens in bits 0-7, flags above
@@ -342,16 +338,6 @@ struct Int2Smem {
     static_assert(kQb % 16 == 0 && kQbBytes % 16 == 0, "bulk-copy destinations 16-byte aligned");
 };
 
-__device__ __forceinline__ int find_seq(const int32_t* item_start, int B, int item) {
-    int lo = 0, hi = B;  // largest b with item_start[b] <= item
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(item_start + mid) <= item) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // A-operand registers of one K k-step (slot g, word half h) from the
 // token-row words of rows gID and gID + 8 (w*) and their >> 8 copies (w*8).
 template <int G>
@@ -373,20 +359,6 @@ __device__ __forceinline__ void v_operands(uint32_t r0, uint32_t r1, uint32_t r0
     a2 = code_pair_hi<G>(r0, r0s);
     a3 = code_pair_hi<G>(r1, r1s);
 }
-
-// Position of token t (0..63) in the warp's probability and V-scale rows.
-// The P.V products take the page's tokens in 16 groups of four: k-step m of
-// lane quad tq covers group q = 4 tq + m (tokens 4q .. 4q+3, whose V codes
-// are bytes 4q .. 4q+3 of every code plane, so one 16-byte load per plane
-// serves all four k-steps).  Group q sits in 16-byte chunk 4 tq + (m ^ tq)
-// of a row, which keeps the lanes of one shared-memory wavefront on
-// distinct banks; inside a chunk the order is pv_slot (tokens 4q, 4q+2 |
-// 4q+1, 4q+3 as the two B-operand pairs).
-__device__ __forceinline__ int pv_pos(int t) {
-    const int q = t >> 2, tq = q >> 2, m = q & 3;
-    return 4 * (4 * tq + (m ^ tq)) + pv_slot(t & 3);
-}
-constexpr int kPvRow = 72;  // floats per probability / V-scale row (64 + 8: conflict-free stores)
 
 // The page's scales into the warp's scratch: for each token row and each
 // 32-position block b (quantisation group b >> GS), fp32 s scaled by the
@@ -754,17 +726,6 @@ __device__ __forceinline__ void attend_page(const uint8_t* blk, int valid, uint8
             }
         }
     }
-}
-
-// Split two fp32 values into f16x2 registers of their high parts (the
-// values with the low 13 bits cleared, see split_pair_f16) and of the
-// rounded remainders.
-__device__ __forceinline__ void split_both(float2 w, uint32_t& hi, uint32_t& lo) {
-    const float2 h = make_float2(__uint_as_float(__float_as_uint(w.x) & 0xffffe000u),
-                                 __uint_as_float(__float_as_uint(w.y) & 0xffffe000u));
-    hi = pack_f16x2_rn(h.x, h.y);
-    const float2 r = sub2(w, h);
-    lo = pack_f16x2_rn(r.x, r.y);
 }
 
 // attend_page for eight query heads per KV head: the MMA columns are the
@@ -1796,10 +1757,22 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
         __syncthreads();  // shares read before the rows' w overwrite them
     }
     const bool lead = active && sub == 0;
+    float wup = 1.f;  // 4-bit history: w is split as w * 2^e, e from its largest entry, so that small rows keep 22 bits too
     if (sub == 0) {  // the row's w (zero for rows past the batch)
         const float inv = (L > 0.f) ? 1.f / L : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = active ? y[k] * inv : 0.f;
+        if (p.bits4) {
+            float mx = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
+            // |w| <= sqrt(d) max|y|: below 2^4 times the power of two above mx
+            const int e = min(100, max(-100, 10 - ((int)((__float_as_uint(mx) >> 23) & 0xffu) - 127)));
+            wup = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] *= wup;
+            wup = __uint_as_float((uint32_t)(127 - e) << 23);  // and back after the un-rotation
+        }
         {
             const float t0 = y[0] + y[1], t1 = y[0] - y[1], t2 = y[2] + y[3], t3 = y[2] - y[3];
             y[0] = t0 + t2;
@@ -1881,11 +1854,22 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
         }
     }
     const float Mx = fmaxf(L > 0.f ? M : -INFINITY, lb > 0.f ? mb : -INFINITY);
-    const float wi = (L > 0.f) ? ex2(M - Mx) * L : 0.f;
+    const float wl = (L > 0.f) ? ex2(M - Mx) * L : 0.f;
+    const float wi = wl * wup;
     const float wb = (lb > 0.f) ? ex2(mb - Mx) : 0.f;
-    const float den = wi + wb * lb;
+    const float den = wl + wb * lb;
     const float inv = (den > 0.f) ? 1.f / den : 0.f;
-    float* o = p.out + ((size_t)b * p.hq + kv * p.G + hh) * kD;
+    const size_t at = ((size_t)b * p.hq + kv * p.G + hh) * kD;
+    if (p.out_bf16) {  // a model's next product reads bf16: rounded once, here
+        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int a2 = lane + 32 * c;
+            o[a2] = __float2bfloat16_rn((wi * yrow[a2] + wb * ob[c]) * inv);
+        }
+        return;
+    }
+    float* o = p.out + at;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int a2 = lane + 32 * c;
@@ -1907,21 +1891,6 @@ static Int2Attr& attr_for_device(int dev) {
     return attrs[dev & 63];
 }
 
-// Dynamic shared memory of a kernel, and the largest L1 / shared carveout:
-// an SM changes its split only when idle, so every kernel of the chain asks
-// for the same split and a programmatically launched kernel can start on SMs
-// where its predecessor still runs.  (Not for the eight-head Lloyd-Max INT2
-// kernel: its register spills go through L1, which the largest split leaves
-// at 28 KB; it took 9 % longer with it.)
-template <typename... Args>
-static cudaError_t set_smem(void (*kernel)(Args...), int bytes, bool max_carveout = true) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && max_carveout)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                 (int)cudaSharedmemCarveoutMaxShared);
-    return e;
-}
-
 template <int NT, bool LM = false, bool BOOST = false>
 static cudaError_t launch_int2(const DecodeParams& p, cudaStream_t st, int sms, bool& attr_set) {
     using SM = Int2Smem<NT, int2_stages<NT, LM, BOOST>()>;
@@ -1940,24 +1909,6 @@ static cudaError_t launch_int2(const DecodeParams& p, cudaStream_t st, int sms, 
     if (blocks < 1) blocks = 1;
     cudaError_t e = launch_pdl(int2_kernel<NT, LM, BOOST>, dim3(blocks), dim3(kInt2Threads), smem, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-// Launch with a programmatic dependency on the previous kernel in the stream
-// (the kernel itself decides where it waits, see pdl_wait).
-template <typename... Args>
-static cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              const DecodeParams& p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t ev_int2_start,
@@ -1995,7 +1946,9 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
     dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
     if ((e = launch_pdl(prep_kernel, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
     if (ev_int2_start && (e = cudaEventRecord(ev_int2_start, st)) != cudaSuccess) return e;
-    if (p.codebook)  // Lloyd-Max levels
+    if (p.bits4)
+        e = launch_int4(p, st, dev, at.sms);
+    else if (p.codebook)  // Lloyd-Max levels
         e = (p.NT == 1) ? launch_int2<1, true>(p, st, at.sms, at.setl) : launch_int2<2, true>(p, st, at.sms, at.setl2);
     else if (p.boost)  // K channel boost
         e = (p.NT == 1) ? launch_int2<1, false, true>(p, st, at.sms, at.setk)

@@ -1,0 +1,701 @@
+// int4.cu -- split-K decode attention over the 4-bit history (blocks of
+// oscar_evict_quantize_int4), between prep_kernel and bf16_kernel of the
+// decode chain (decode.cu), which are those of the 2-bit history: rotated
+// query fragments and plan before, un-rotation and log-sum-exp merge after.
+//
+// The mathematics.  A stored value is s c + z (c in 0..15, one fp16 pair per
+// token and quantisation group).  With the codes centred, c' = c - 8 and
+// z' = z + 8 s, and b the 32-position blocks of a vector:
+//   logit_t = sum_b s_tb D_tb + z'_tb Q_b,  D_tb = sum_{j in b} c'_tj q'_j,
+//                                           Q_b = sum_{j in b} q'_j;
+//   o'_j    = sum_t W_tb(j) c'_tj + sum_t p_t z'_tb,  W_tb = p_t s_tb.
+// D and the W products are tensor-core products (mma.sync m16n8k16, fp16 in,
+// fp32 sums) with the codes as the A operand, exact in fp16; q' (times 2^e,
+// from prep) and W (times 2^w) enter as fp16 high and low parts, 22 bits.
+// The sums stay centred, so that a flat softmax over a long history does not
+// subtract two sums that are far larger than their difference (uncentred
+// codes give sums of 7.5 s against values of 4.6 s).
+//
+// Operands.  A 16-bit pattern 0x6400 | c is the fp16 1024 + c and
+// 0x6400 | 16 c is 1024 + 16 c: one AND-OR on the code word in place and one
+// fp16 add (-1032) or fused multiply-add (/ 16, -72) give c - 8 exactly; a
+// shift by 8 serves the other two nibbles of each half: nine instructions
+// for a word of eight codes, five of them on the integer pipe.
+//
+// 2^w: W is scaled by a power of two per warp and item, from the largest V
+// scale seen so far, so that its fp16 parts keep 22 bits whatever the
+// values' size; a page with a larger scale rescales the sums.
+//
+// What bounds it: 160 bytes and 4 d G flops per (token, KV head) make it a
+// stream of the pages, so K and V halves travel separately (each consumer
+// warp owns a ring of halves and gives one back as soon as it has read it).
+#include "splitk.cuh"
+
+namespace oscar {
+
+namespace {
+
+constexpr int kThreads4 = (kConsumerWarps + 1) * 32;
+constexpr int kHalfMax = kCodes4 + kPage * 16;  // bytes of a half at g = 32
+
+struct PageInfo {  // one per page of a consumer warp; 16 bytes
+    int item, b, kv, valid_flags;
+};
+
+template <int NT>
+struct Int4Smem {
+    static constexpr int G4 = NT * 4;
+    // halves per consumer warp: three (one being read, two in flight) for up
+    // to four heads; for eight heads the larger scratch of three blocks per
+    // SM leaves two
+    static constexpr int NSW = NT == 1 ? 3 : 2;
+    // per-warp scratch.  Logit phase: K s [64] float4 | K z' [64] float4.
+    // Value phase: V s 2^w [4][kPvRow] (token order pv_pos) | V z' [64]
+    // float4, then P [G4][kPvRow] over the z'.  Item end: the warp's state
+    // [G4][kD + 2].
+    static constexpr int kWVs = 0, kWVz = 4 * kPvRow * 4, kWP = kWVz;
+    static constexpr int kWarp1 = 2 * kPage * 16, kWarp2 = kWP + G4 * kPvRow * 4, kWarp3 = G4 * (kD + 2) * 4;
+    static constexpr int kWarpBytes0 = kWarp1 > kWarp2 ? kWarp1 : kWarp2;
+    static constexpr int kWarpBytes = kWarpBytes0 > kWarp3 ? kWarpBytes0 : kWarp3;
+    static constexpr int kStage = 0;
+    static constexpr int kInfo = kStage + kConsumerWarps * NSW * kHalfMax;  // [4][2] PageInfo
+    static constexpr int kWarp = kInfo + kConsumerWarps * 2 * 16;
+    // two item buffers: q' fragments [NT][8][32] uint2, group sums [G4] float4, 2^-e
+    static constexpr int kQbSum = NT * 8 * 32 * 8, kQbKinv = kQbSum + G4 * 16, kQbBytes = kQbKinv + 16;
+    static constexpr int kQb = kWarp + kConsumerWarps * kWarpBytes;
+    // full / empty per half, qfull[2], qempty[2], merge
+    static constexpr int kBars = kQb + 2 * kQbBytes;
+    static constexpr int kBytes = kBars + (2 * kConsumerWarps * NSW + 5) * 8;
+    static_assert(kWarp % 16 == 0 && kWarpBytes % 16 == 0 && kQb % 16 == 0 && kQbBytes % 16 == 0 && kBars % 8 == 0,
+                  "16-byte vectors and bulk copies");
+    static_assert(3 * (kBytes + 1024) <= 228 * 1024, "three blocks per SM");
+};
+
+// Ring position: half `slot` of NSW, in its `phase`-th use.
+template <int NSW>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++slot == NSW) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    return r;
+}
+
+// Eight codes of a word as four f16x2 operand registers of c - 8: nibble n
+// of the low and of the high half.
+__device__ __forceinline__ void unpack4(uint32_t x, uint32_t (&r)[4]) {
+    const uint32_t y = x >> 8;
+    const uint32_t n0 = and_or(x, 0x000f000fu, 0x64006400u), n1 = and_or(x, 0x00f000f0u, 0x64006400u);
+    const uint32_t n2 = and_or(y, 0x000f000fu, 0x64006400u), n3 = and_or(y, 0x00f000f0u, 0x64006400u);
+    // 0xE408 = -1032, 0x2C00 = 1/16, 0xD480 = -72
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[0]) : "r"(n0), "r"(0xE408E408u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(n1), "r"(0x2C002C00u), "r"(0xD480D480u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r[2]) : "r"(n2), "r"(0xE408E408u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(n3), "r"(0x2C002C00u), "r"(0xD480D480u));
+}
+
+// The (s, z) words of token t of a half, one per 32-position block.
+template <int GS>
+__device__ __forceinline__ void load_pairs(const uint8_t* half, int t, uint32_t (&w)[4]) {
+    const uint8_t* at = half + kCodes4 + t * (16 >> GS);
+    if constexpr (GS == 0) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (GS == 1) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        w[0] = w[1] = v.x; w[2] = w[3] = v.y;
+    } else {
+        w[0] = w[1] = w[2] = w[3] = *reinterpret_cast<const uint32_t*>(at);
+    }
+}
+__device__ __forceinline__ void load_pairs(const uint8_t* half, int t, int gshift, uint32_t (&w)[4]) {
+    switch (gshift) {  // warp-uniform
+        case 0: load_pairs<0>(half, t, w); break;
+        case 1: load_pairs<1>(half, t, w); break;
+        default: load_pairs<2>(half, t, w); break;
+    }
+}
+
+__device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// State of one consumer warp inside an item.
+template <int NT>
+struct WarpState {
+    float m_run[NT], l_run[NT], zacc[NT][4];  // per head of the lane: max, sum, sum p z' per block (lane partials)
+    // [M tile][row gID: columns 2tq, 2tq+1; row gID+8]; up to four heads: columns = (hi, lo) of head tq; eight: heads 2tq, 2tq+1
+    float acc[8][4];
+    int wexp;                                  // 2^wexp scales W; kNoScale before the first page
+};
+constexpr int kNoScale = 64;
+
+// K half of a page: logits (base 2) of the lane's tokens 16m + gID and
+// 16m + gID + 8.  Up to four heads: lg[m][0], lg[m][1] = the two tokens of
+// head tq; eight heads: (token a, heads 2tq, 2tq+1), (token b, the same).
+template <int NT, bool FULL>
+__device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint8_t* wbuf, const uint2* qf,
+                                            const float4 (&qsv)[NT], float kq, int gshift, float (&lg)[4][2 * NT]) {
+    const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
+    float4* ksS = reinterpret_cast<float4*>(wbuf);
+    float4* kzS = ksS + kPage;
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        const int t = lane + 32 * it;
+        float4 sv = make_float4(0.f, 0.f, 0.f, 0.f), zv = sv;
+        if (FULL || t < valid) {
+            uint32_t w[4];
+            load_pairs(half, t, gshift, w);
+            const float s[4] = {half_lo(w[0]), half_lo(w[1]), half_lo(w[2]), half_lo(w[3])};
+            sv = make_float4(s[0] * kq, s[1] * kq, s[2] * kq, s[3] * kq);
+            zv = make_float4(fmaf(8.f, s[0], half_hi(w[0])), fmaf(8.f, s[1], half_hi(w[1])),
+                             fmaf(8.f, s[2], half_hi(w[2])), fmaf(8.f, s[3], half_hi(w[3])));
+        }
+        ksS[t] = sv;
+        kzS[t] = zv;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2 * NT; ++e) lg[m][e] = -INFINITY;
+        if (!FULL && 16 * m >= valid) continue;
+        const int ta = 16 * m + gID;
+        const uint4 xa = *reinterpret_cast<const uint4*>(half + ta * (kD / 2) + 16 * tq);
+        const uint4 xb = *reinterpret_cast<const uint4*>(half + (ta + 8) * (kD / 2) + 16 * tq);
+        const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
+        float acc[4][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+            uint32_t ra[4], rb[4];
+            unpack4(wa[b], ra);
+            unpack4(wb[b], rb);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {  // eight heads: the high, then the low parts
+                    const uint2 q = qf[(nt * 8 + 2 * b + h) * 32 + lane];
+                    mma_f16_16816(acc[b], ra[2 * h], rb[2 * h], ra[2 * h + 1], rb[2 * h + 1], q.x, q.y);
+                }
+        }
+        const float4 sA = ksS[ta], sB = ksS[ta + 8], zA = kzS[ta], zB = kzS[ta + 8];
+        const float sa[4] = {sA.x, sA.y, sA.z, sA.w}, za[4] = {zA.x, zA.y, zA.z, zA.w};
+        const float sb[4] = {sB.x, sB.y, sB.z, sB.w}, zb[4] = {zB.x, zB.y, zB.z, zB.w};
+        const bool va = FULL || ta < valid, vb = FULL || ta + 8 < valid;
+        if constexpr (NT == 1) {
+            const float qg[4] = {qsv[0].x, qsv[0].y, qsv[0].z, qsv[0].w};
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                x = fmaf(sa[b], acc[b][0] + acc[b][1], fmaf(za[b], qg[b], x));
+                y = fmaf(sb[b], acc[b][2] + acc[b][3], fmaf(zb[b], qg[b], y));
+            }
+            lg[m][0] = va ? x : -INFINITY;
+            lg[m][1] = vb ? y : -INFINITY;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float qg[4] = {qsv[j].x, qsv[j].y, qsv[j].z, qsv[j].w};
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    x = fmaf(sa[b], acc[b][j], fmaf(za[b], qg[b], x));
+                    y = fmaf(sb[b], acc[b][2 + j], fmaf(zb[b], qg[b], y));
+                }
+                lg[m][j] = va ? x : -INFINITY;
+                lg[m][2 + j] = vb ? y : -INFINITY;
+            }
+        }
+    }
+}
+
+// Online softmax of a page's logits: lg becomes p, l_run advances, alpha is
+// the factor that the older sums take.  Returns whether any lane's is not 1.
+template <int NT>
+__device__ __forceinline__ bool page_softmax(float (&lg)[4][2 * NT], WarpState<NT>& st, float (&alpha)[NT]) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {  // j: token pair entries (NT == 1: 0 and 1; NT == 2: j and 2 + j)
+        const int e1 = NT == 1 ? 1 : 2 + j;
+        float mx = fmaxf(lg[0][j], lg[0][e1]);
+#pragma unroll
+        for (int m = 1; m < 4; ++m) mx = fmaxf(mx, fmaxf(lg[m][j], lg[m][e1]));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+        const float m_new = fmaxf(st.m_run[j], mx);
+        alpha[j] = 1.f;
+        if (__any_sync(kFull, m_new > st.m_run[j])) {
+            any = true;
+            alpha[j] = (m_new > st.m_run[j]) ? ex2(st.m_run[j] - m_new) : 1.f;
+            st.l_run[j] *= alpha[j];
+            st.m_run[j] = m_new;
+        }
+        const float sub = (m_new == -INFINITY) ? 0.f : m_new;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            lg[m][j] = ex2(lg[m][j] - sub);
+            lg[m][e1] = ex2(lg[m][e1] - sub);
+            st.l_run[j] += lg[m][j] + lg[m][e1];
+        }
+    }
+    return any;
+}
+
+// V half of a page: the scales, the rescaling of the sums, sum p z', and the
+// products W . (c - 8).
+template <int NT, bool FULL>
+__device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint8_t* wbuf, const float (&p)[4][2 * NT],
+                                            const float (&alpha)[NT], bool any, int gshift, const SplitSel& take_lo,
+                                            WarpState<NT>& st) {
+    using SM = Int4Smem<NT>;
+    const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
+    float* vsS = reinterpret_cast<float*>(wbuf + SM::kWVs);
+    float4* vzS = reinterpret_cast<float4*>(wbuf + SM::kWVz);
+    float* pS = reinterpret_cast<float*>(wbuf + SM::kWP);
+    // -- pairs; the largest scale of the page picks 2^w: s 2^w < 2^14
+    uint32_t w[2][4];
+    uint32_t smax = 0;
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        const int t = lane + 32 * it;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) w[it][b] = 0u;
+        if (FULL || t < valid) load_pairs(half, t, gshift, w[it]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) smax = max(smax, w[it][b] & 0x7fffu);
+    }
+    smax = __reduce_max_sync(kFull, smax);
+    const int wexp = 13 - (max((int)(smax >> 10), 1) - 15);
+    if (any || wexp < st.wexp) {  // warp-uniform
+        float down = 1.f;
+        if (wexp < st.wexp) {
+            down = st.wexp == kNoScale ? 0.f : pow2_bits(wexp - st.wexp);  // (no sums before the first page)
+            st.wexp = wexp;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) st.zacc[j][b] *= alpha[j];
+        // column 2tq + e: up to four heads, both columns belong to head tq; eight: heads 2tq, 2tq + 1
+        const float f0 = alpha[0] * down, f1 = alpha[NT - 1] * down;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            st.acc[mt][0] *= f0;
+            st.acc[mt][1] *= f1;
+            st.acc[mt][2] *= f0;
+            st.acc[mt][3] *= f1;
+        }
+    }
+    const float up = pow2_bits(st.wexp);
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        const int t = lane + 32 * it, ps = pv_pos(t);
+        float s[4], z[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            s[b] = half_lo(w[it][b]);
+            z[b] = fmaf(8.f, s[b], half_hi(w[it][b]));
+            vsS[b * kPvRow + ps] = s[b] * up;
+        }
+        vzS[t] = make_float4(z[0], z[1], z[2], z[3]);
+    }
+    __syncwarp();
+    // -- sum p z'
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if (!FULL && 16 * m >= valid) continue;
+        const int ta = 16 * m + gID;
+        const float4 zA = vzS[ta], zB = vzS[ta + 8];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float pa = p[m][j], pb = p[m][NT == 1 ? 1 : 2 + j];
+            st.zacc[j][0] = fmaf(pa, zA.x, fmaf(pb, zB.x, st.zacc[j][0]));
+            st.zacc[j][1] = fmaf(pa, zA.y, fmaf(pb, zB.y, st.zacc[j][1]));
+            st.zacc[j][2] = fmaf(pa, zA.z, fmaf(pb, zB.z, st.zacc[j][2]));
+            st.zacc[j][3] = fmaf(pa, zA.w, fmaf(pb, zB.w, st.zacc[j][3]));
+        }
+    }
+    __syncwarp();  // z' read: P takes its place
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float* row = pS + (NT == 1 ? tq : 2 * tq + j) * kPvRow;
+            row[pv_pos(16 * m + gID)] = p[m][j];
+            row[pv_pos(16 * m + gID + 8)] = p[m][NT == 1 ? 1 : 2 + j];
+        }
+    __syncwarp();
+    // -- products: M tile mt = planes 8 mt + gID (rows gID: position
+    //    16 mt + 2 gID, rows gID + 8: the next one), k-step m = token group
+    //    4 tq + m; two blocks (four M tiles) at a time
+    const uint8_t* vb = half + gID * kPage + 16 * tq;
+#pragma unroll
+    for (int hb = 0; hb < 2; ++hb) {
+        uint4 v4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v4[k] = *reinterpret_cast<const uint4*>(vb + (4 * hb + k) * 8 * kPage);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int chunk = 4 * (4 * tq + (m ^ tq));
+            const float4 pp = *reinterpret_cast<const float4*>(pS + (NT == 1 ? gID >> 1 : gID) * kPvRow + chunk);
+#pragma unroll
+            for (int bb = 0; bb < 2; ++bb) {
+                const float4 sg = *reinterpret_cast<const float4*>(vsS + (2 * hb + bb) * kPvRow + chunk);
+                const float2 p0 = make_float2(pp.x, pp.y), p1 = make_float2(pp.z, pp.w);
+                const float2 s0 = make_float2(sg.x, sg.y), s1 = make_float2(sg.z, sg.w);
+                uint32_t b0, b1, l0 = 0, l1 = 0;
+                if constexpr (NT == 1) {
+                    b0 = split_w_pair_f16(p0, s0, take_lo);
+                    b1 = split_w_pair_f16(p1, s1, take_lo);
+                } else {
+                    split_both(mul2(p0, s0), b0, l0);
+                    split_both(mul2(p1, s1), b1, l1);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 v = v4[2 * bb + k];
+                    uint32_t r[4];
+                    unpack4(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w, r);
+                    float(&acc)[4] = st.acc[4 * hb + 2 * bb + k];
+                    mma_f16_16816(acc, r[0], r[1], r[2], r[3], b0, b1);
+                    if constexpr (NT == 2) mma_f16_16816(acc, r[0], r[1], r[2], r[3], l0, l1);
+                }
+            }
+        }
+    }
+}
+
+// Persistent blocks: the producer warp takes split-K items from the work
+// counter and streams their pages, page i of an item to consumer warp i % 4,
+// as two halves (K, then V) into the warp's ring; in each round of four
+// pages the four K halves go first.  Every wait is bounded: on a timeout the
+// block reports OSCAR_STATUS_TIMEOUT, lets its copies land and exits.
+template <int NT>
+__global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    using SM = Int4Smem<NT>;
+    constexpr int NSW = SM::NSW;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);  // [warp][NSW]
+    uint64_t* empty = full + kConsumerWarps * NSW;
+    uint64_t* qfull = empty + kConsumerWarps * NSW;
+    uint64_t* qempty = qfull + 2;
+    uint64_t* merge_bar = qempty + 2;
+    PageInfo* info = reinterpret_cast<PageInfo*>(smem + SM::kInfo);  // [warp][2]
+    const uint32_t half_bytes = (uint32_t)half_bytes4(p.gshift);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kConsumerWarps * NSW; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&qfull[s], 1);
+            mbar_init(&qempty[s], kConsumerWarps);
+        }
+        mbar_init(merge_bar, kConsumerWarps);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();     // q' fragments, plan and counter come from prep_kernel
+    pdl_trigger();  // the BF16 segment kernel may take SMs as this grid retires
+
+    if (warp == kConsumerWarps) {
+        // ------------------------------ producer ------------------------------
+        const int total_long = __ldg(p.item_start + p.B);
+        const int total = total_long + __ldg(p.item_start2 + p.B);
+        Ring<NSW> ring;       // the same for the four warps: every round gives each two halves
+        uint32_t halves = 0;  // halves issued to each warp
+        uint32_t round = 0, pitem = 0;
+        bool ok = true;
+        // wait until the ring's slot is free in the four warps (lane w polls
+        // warp w's barrier, so that one wait covers the round)
+        auto wait_free = [&]() -> bool {
+            if (halves < (uint32_t)NSW) return true;
+            const bool w = lane >= kConsumerWarps ||
+                           mbar_wait_bounded(&empty[lane * NSW + ring.slot], ring.phase ^ 1u, kWaitPolls);
+            return __all_sync(kFull, w);
+        };
+        for (;;) {
+            int item = 0;
+            if (lane == 0) item = atomicAdd(p.counter, 1);
+            item = __shfl_sync(kFull, item, 0);
+            if (item >= total) {  // an end marker for each consumer warp
+                ok = wait_free();
+                if (ok && lane < kConsumerWarps) {
+                    info[lane * 2 + (round & 1u)].item = -1;
+                    mbar_arrive(&full[lane * NSW + ring.slot]);
+                }
+                break;
+            }
+            const bool is_long = item < total_long;
+            const int32_t* starts = is_long ? p.item_start : p.item_start2;
+            const int rel = is_long ? item : item - total_long;
+            const int b = find_seq(starts, p.B, rel);
+            const int s0 = __ldg(starts + b);
+            const int splits = (__ldg(starts + b + 1) - s0) / p.hk;
+            const int kv = (rel - s0) / splits;
+            const int split = (rel - s0) % splits;
+            const int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+            const int seq_pages = (hist + kPage - 1) / kPage;
+            const SeqSplits sp = seq_splits(seq_pages, p.pps, p.tail_pg);
+            const int pg0 = is_long ? split * p.pps : sp.long_pages + split * kShortItemPages;
+            const int npg = is_long ? min(p.pps, sp.long_pages - pg0) : min(kShortItemPages, seq_pages - pg0);
+            const int rounds = (npg + kConsumerWarps - 1) / kConsumerWarps;
+            {   // the item's q' data into its buffer, once item k - 2 has left it
+                const uint32_t qs = pitem & 1u;
+                if (pitem >= 2) {
+                    const bool w = mbar_wait_bounded(&qempty[qs], ((pitem >> 1) - 1) & 1u, kWaitPolls);
+                    if (!__all_sync(kFull, w)) {
+                        ok = false;
+                        break;
+                    }
+                }
+                if (lane == 0) {
+                    const size_t bk = (size_t)b * p.hk + kv;
+                    uint8_t* qb = smem + SM::kQb + qs * SM::kQbBytes;
+                    mbar_arrive_expect_tx(&qfull[qs], SM::kQbBytes);
+                    bulk_g2s(qb, p.qfrag + bk * NT * 8 * 32 * 2, NT * 8 * 32 * 8, &qfull[qs]);
+                    bulk_g2s(qb + SM::kQbSum, p.qsum + bk * SM::G4 * 4, SM::G4 * 16, &qfull[qs]);
+                    bulk_g2s(qb + SM::kQbKinv, p.qkinv + bk * 4, 16, &qfull[qs]);
+                }
+                __syncwarp();
+                ++pitem;
+            }
+            int pid = -1;
+            for (int r = 0; r < rounds && ok; ++r, ++round) {
+                if ((r & 7) == 0) {  // page ids of the next eight rounds, one per lane
+                    const int pl = 4 * r + lane;
+                    pid = pl < npg ? __ldg(p.page_table + (size_t)b * p.max_pages + pg0 + pl) : -1;
+                }
+                // lane w < 4 serves warp w: page 4 r + w of the item
+                const int pl = 4 * r + (lane & 3);
+                const int page = __shfl_sync(kFull, pid, (4 * r + (lane & 3)) & 31);
+                bool pad = pl >= npg;
+                if (!pad && (page < 0 || page >= p.num_pages)) {
+                    if (lane < kConsumerWarps) report(p.status, OSCAR_STATUS_BAD_PAGE);
+                    pad = true;
+                }
+                const uint8_t* src = p.pool + ((size_t)(pad ? 0 : page) * p.hk + kv) * p.block_bytes;
+                if (!(ok = wait_free())) break;
+                if (lane < kConsumerWarps) {
+                    const int flags = (r == 0 ? kFlagFirst : 0) | (r == rounds - 1 ? kFlagLast : 0) | (pad ? kFlagPad : 0);
+                    PageInfo& pi = info[lane * 2 + (round & 1u)];
+                    pi.item = item;
+                    pi.b = b;
+                    pi.kv = kv;
+                    pi.valid_flags = (pad ? 0 : min(kPage, hist - (pg0 + pl) * kPage)) | (flags << 8);
+                    uint64_t* bar = &full[lane * NSW + ring.slot];
+                    if (pad) {
+                        mbar_arrive(bar);
+                    } else {
+                        mbar_arrive_expect_tx(bar, half_bytes);
+                        bulk_g2s(smem + SM::kStage + (lane * NSW + ring.slot) * kHalfMax, src, half_bytes, bar);
+                    }
+                }
+                __syncwarp();
+                ring.step();
+                ++halves;
+                if (!(ok = wait_free())) break;
+                if (lane < kConsumerWarps) {
+                    uint64_t* bar = &full[lane * NSW + ring.slot];
+                    if (pad) {
+                        mbar_arrive(bar);
+                    } else {
+                        mbar_arrive_expect_tx(bar, half_bytes);
+                        bulk_g2s(smem + SM::kStage + (lane * NSW + ring.slot) * kHalfMax, src + half_bytes, half_bytes, bar);
+                    }
+                }
+                __syncwarp();
+                ring.step();
+                ++halves;
+            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            if (lane == 0) report(p.status, OSCAR_STATUS_TIMEOUT);
+            // let issued copies land before the block can exit: the last use of every slot
+            for (int s = 0; s < NSW; ++s) {
+                if ((uint32_t)s >= halves) break;
+                // slots at or past the ring position were last used a turn earlier
+                const uint32_t ph = s < ring.slot ? ring.phase : ring.phase ^ 1u;
+                if (lane < kConsumerWarps) (void)mbar_wait_bounded(&full[lane * NSW + s], ph, kWaitPolls);
+                __syncwarp();
+            }
+            for (uint32_t k = pitem > 2 ? pitem - 2 : 0; k < pitem; ++k)
+                (void)mbar_wait_bounded(&qfull[k & 1u], (k >> 1) & 1u, kWaitPolls);
+        }
+        return;
+    }
+
+    // ------------------------------- consumers ---------------------------------
+    const int gID = lane >> 2, tq = lane & 3;
+    uint8_t* wbuf = smem + SM::kWarp + warp * SM::kWarpBytes;
+    const uint8_t* stages = smem + SM::kStage + warp * NSW * kHalfMax;
+    full += warp * NSW;
+    empty += warp * NSW;
+    const SplitSel take_lo = split_sel(gID & 1);
+
+    uint32_t merge_phase = 0;
+    auto consumer_sync = [&]() -> bool {  // bounded rendezvous of the four consumer warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merge_bar);
+        const bool w = mbar_wait_bounded(merge_bar, merge_phase & 1u, kWaitPolls);
+        ++merge_phase;
+        return __all_sync(kFull, w);
+    };
+    auto give_up = [&]() {
+        if (lane == 0) report(p.status, OSCAR_STATUS_TIMEOUT);
+    };
+
+    WarpState<NT> st;
+    float4 qsv[NT];
+    float kq = 1.f;
+    uint32_t citem = 0, cur_qs = 0;
+    const uint2* qf = nullptr;
+    Ring<NSW> ring;
+
+    for (uint32_t j = 0;; ++j) {
+        if (!__all_sync(kFull, mbar_wait_bounded(&full[ring.slot], ring.phase, kWaitPolls))) return give_up();
+        const int4 sraw = *reinterpret_cast<const int4*>(&info[warp * 2 + (j & 1u)]);
+        const int item = sraw.x, flags = sraw.w >> 8, valid = sraw.w & 0xff;
+        if (item < 0) break;
+        if (flags & kFlagFirst) {
+            cur_qs = citem & 1u;
+            if (!__all_sync(kFull, mbar_wait_bounded(&qfull[cur_qs], (citem >> 1) & 1u, kWaitPolls))) return give_up();
+            ++citem;
+            const uint8_t* qb = smem + SM::kQb + cur_qs * SM::kQbBytes;
+            qf = reinterpret_cast<const uint2*>(qb);
+            kq = *reinterpret_cast<const float*>(qb + SM::kQbKinv);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                qsv[n] = reinterpret_cast<const float4*>(qb + SM::kQbSum)[NT == 1 ? tq : 2 * tq + n];
+                st.m_run[n] = -INFINITY;
+                st.l_run[n] = 0.f;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) st.zacc[n][b] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.acc[mt][e] = 0.f;
+            st.wexp = kNoScale;
+        }
+        float lg[4][2 * NT], alpha[NT];
+        bool any = false;
+        const bool on = !(flags & kFlagPad);
+        if (on) {
+            const uint8_t* half = stages + ring.slot * kHalfMax;
+            if (valid == kPage) page_logits<NT, true>(half, valid, wbuf, qf, qsv, kq, p.gshift, lg);
+            else page_logits<NT, false>(half, valid, wbuf, qf, qsv, kq, p.gshift, lg);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[ring.slot]);
+        ring.step();
+        if (on) any = page_softmax<NT>(lg, st, alpha);
+        if (!__all_sync(kFull, mbar_wait_bounded(&full[ring.slot], ring.phase, kWaitPolls))) return give_up();
+        if (on) {
+            const uint8_t* half = stages + ring.slot * kHalfMax;
+            if (valid == kPage) page_values<NT, true>(half, valid, wbuf, lg, alpha, any, p.gshift, take_lo, st);
+            else page_values<NT, false>(half, valid, wbuf, lg, alpha, any, p.gshift, take_lo, st);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[ring.slot]);
+        ring.step();
+
+        if (!(flags & kFlagLast)) continue;
+        if (lane == 0) mbar_arrive(&qempty[cur_qs]);  // done with the item's q' data
+        // this warp's partial state -> its scratch
+        float* mw = reinterpret_cast<float*>(wbuf);
+        const float down = st.wexp == kNoScale ? 0.f : pow2_bits(-st.wexp);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float l = st.l_run[n];
+            l += __shfl_xor_sync(kFull, l, 4);
+            l += __shfl_xor_sync(kFull, l, 8);
+            l += __shfl_xor_sync(kFull, l, 16);
+            float z[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                z[b] = st.zacc[n][b];
+                z[b] += __shfl_xor_sync(kFull, z[b], 4);
+                z[b] += __shfl_xor_sync(kFull, z[b], 8);
+                z[b] += __shfl_xor_sync(kFull, z[b], 16);
+            }
+            float* o = mw + (size_t)(NT == 1 ? tq : 2 * tq + n) * (kD + 2);
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+                const float a = NT == 1 ? st.acc[mt][0] + st.acc[mt][1] : st.acc[mt][n];
+                const float c = NT == 1 ? st.acc[mt][2] + st.acc[mt][3] : st.acc[mt][2 + n];
+                *reinterpret_cast<float2*>(o + 16 * mt + 2 * gID) =
+                    make_float2(fmaf(a, down, z[mt >> 1]), fmaf(c, down, z[mt >> 1]));
+            }
+            if (gID == 0) {
+                o[kD] = st.m_run[n];
+                o[kD + 1] = l;
+            }
+        }
+        if (!consumer_sync()) return give_up();
+        // merge the four warps: thread -> stored position, all heads
+        float* part = p.part + (size_t)item * p.part_stride;
+        const int d = threadIdx.x;  // 0..127
+        for (int hl = 0; hl < p.G; ++hl) {
+            float M = -INFINITY;
+#pragma unroll
+            for (int ww = 0; ww < kConsumerWarps; ++ww)
+                M = fmaxf(M, reinterpret_cast<const float*>(smem + SM::kWarp + ww * SM::kWarpBytes)[hl * (kD + 2) + kD]);
+            float acc = 0.f, L = 0.f;
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int ww = 0; ww < kConsumerWarps; ++ww) {
+                    const float* src =
+                        reinterpret_cast<const float*>(smem + SM::kWarp + ww * SM::kWarpBytes) + hl * (kD + 2);
+                    const float sc = ex2(src[kD] - M);
+                    acc = fmaf(sc, src[d], acc);
+                    L = fmaf(sc, src[kD + 1], L);
+                }
+            }
+            part[(size_t)hl * kD + d] = acc;
+            if (d == 0) {
+                part[(size_t)p.G * kD + hl] = M;
+                part[(size_t)p.G * kD + p.G + hl] = L;
+            }
+        }
+        if (!consumer_sync()) return give_up();
+    }
+}
+
+template <int NT>
+cudaError_t launch(const DecodeParams& p, cudaStream_t st, int sms, bool& attr_set) {
+    if (!attr_set) {
+        const cudaError_t e = set_smem(int4_kernel<NT>, Int4Smem<NT>::kBytes);
+        if (e != cudaSuccess) return e;
+        attr_set = true;
+    }
+    const int64_t max_items =
+        (int64_t)p.B * p.hk * ((p.max_pages + p.pps - 1) / p.pps + p.tail_pg / kShortItemPages);
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)3 * sms, max_items));
+    const cudaError_t e =
+        launch_pdl(int4_kernel<NT>, dim3(blocks), dim3(kThreads4), Int4Smem<NT>::kBytes, st, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev, int sms) {
+    static bool attr_set[64][2];
+    bool(&at)[2] = attr_set[dev & 63];
+    return p.NT == 1 ? launch<1>(p, st, sms, at[0]) : launch<2>(p, st, sms, at[1]);
+}
+
+}  // namespace oscar

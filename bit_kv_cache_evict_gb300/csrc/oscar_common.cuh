@@ -339,8 +339,19 @@ struct EvictParams {
     int32_t* status;
     int n_tok, hk, src_rows, batch, max_pages, num_pages;
     int gshift;       // log2(quant_group / 32): 0, 1, 2
-    int block_bytes;  // bytes per (page, KV head) block: 4096 + 512 * (4 >> gshift)
+    int block_bytes;  // bytes per (page, KV head) block: 4096 + 512 * (4 >> gshift); 4-bit blocks 2 * half_bytes4
+    int bits4;        // 1: 4-bit blocks
 };
+
+// A 4-bit (page, KV head) block is two halves of the same size, K then V,
+// each 4096 bytes of codes and the (s, z) pairs behind them, so that a half
+// is one bulk copy:
+//   K codes, token-major: byte 64 t + 16 a + 4 k + i holds stored positions
+//     32 k + 8 a + 2 i (low nibble) and the next one: word k of a token's
+//     16-byte chunk a is group k's share of lane quad member a;
+//   V codes, byte-plane-major: byte 64 j + t, positions 2 j and 2 j + 1.
+constexpr int kCodes4 = kPage * kD / 2;  // code bytes of a half
+__host__ __device__ __forceinline__ int half_bytes4(int gshift) { return kCodes4 + kPage * 4 * (4 >> gshift); }
 
 // Scale/zero pairs per token vector (4, 2 or 1) and the V scale/zero offset
 // inside a block (the K pairs start at kKScale).
@@ -376,6 +387,8 @@ struct DecodeParams {
     float qscale;  // sm_scale * log2(e)
     const float* codebook;  // [hk][2] Lloyd-Max inner level a, or null (uniform levels)
     const uint8_t* boost;   // K boost records [num_pages][hk][kBoostBlock], or null (no boost)
+    int bits4;     // 1: 4-bit history blocks (int4.cu), 0: 2-bit blocks
+    int out_bf16;  // 1: out is bf16
 };
 
 // Split-K geometry of one sequence with npg history pages: the last
@@ -428,6 +441,41 @@ struct FitParams {
     int n_t, hk, gshift;
 };
 cudaError_t launch_calibrate_codebook(const FitParams& p, cudaStream_t st);
+
+// stored tokens as rows, kept tokens into fresh pages, page copies (history.cu)
+struct HistoryReadParams {
+    const int32_t* seq;        // [n_tok]
+    const int32_t* pos;        // [n_tok]
+    const uint8_t* pool;
+    const int32_t* page_table;
+    void* out;                 // [n_tok][hk][2][kD] fp32 or bf16
+    int32_t* status;
+    int n_tok, hk, batch, max_pages, num_pages, gshift, block_bytes, bits4, out_bf16;
+};
+cudaError_t launch_history_read(const HistoryReadParams& p, cudaStream_t st);
+
+struct HistoryGatherParams {
+    uint8_t* pool;
+    uint8_t* boost;            // K boost records, or null
+    const int32_t* src_table;  // [batch][src_max_pages]
+    const int32_t* dst_table;  // [batch][dst_max_pages]
+    const int32_t* keep;       // [batch][keep_stride] source positions
+    const int32_t* n_keep;     // [batch]
+    int32_t* status;
+    int batch, hk, src_max_pages, dst_max_pages, keep_stride, num_pages, gshift, block_bytes, bits4;
+};
+cudaError_t launch_history_gather(const HistoryGatherParams& p, cudaStream_t st);
+
+struct PagesCopyParams {
+    const int32_t* src;        // [n]
+    const int32_t* dst;        // [n]
+    int32_t* status;
+    size_t page_bytes;
+    int n, pieces, num_pages;
+    uint8_t* pool[OSCAR_MAX_COPY_POOLS];
+};
+int64_t pages_copy_pieces(size_t page_bytes);  // thread blocks per (pair, pool)
+cudaError_t launch_pages_copy(const PagesCopyParams& p, int n_pools, cudaStream_t st);
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t st, cudaEvent_t ev_int2_start,

@@ -113,6 +113,19 @@ def lib() -> ctypes.CDLL:
         L.oscar_decode_attn_boost.argtypes = [S, ctypes.c_int32, _P, _P, _P, _P, _P, _P, ctypes.c_int32,
                                               ctypes.c_int32, _P, _P, ctypes.c_float, _P, _P,
                                               ctypes.POINTER(ctypes.c_size_t), _P, _P]
+        L.oscar_block_bytes_int4.restype = ctypes.c_size_t
+        L.oscar_block_bytes_int4.argtypes = [S]
+        L.oscar_evict_quantize_int4.restype = ctypes.c_int
+        L.oscar_evict_quantize_int4.argtypes = L.oscar_evict_quantize.argtypes
+        L.oscar_decode_attn_int4.restype = ctypes.c_int
+        L.oscar_decode_attn_int4.argtypes = [S, I32, _P, _P, _P, _P, _P, I32, I32, _P, _P, ctypes.c_float, _P, I32, _P,
+                                             ctypes.POINTER(ctypes.c_size_t), _P, _P]
+        L.oscar_history_read.restype = ctypes.c_int
+        L.oscar_history_read.argtypes = [S, I32, I32, _P, _P, _P, _P, I32, I32, I32, _P, I32, _P, _P]
+        L.oscar_history_gather.restype = ctypes.c_int
+        L.oscar_history_gather.argtypes = [S, I32, I32, _P, _P, _P, I32, _P, I32, _P, I32, _P, I32, _P, _P]
+        L.oscar_pages_copy_device.restype = ctypes.c_int
+        L.oscar_pages_copy_device.argtypes = [ctypes.c_size_t, I32, _P, _P, _P, I32, I32, _P, _P]
         L.oscar_calibrate_codebook.restype = ctypes.c_int
         L.oscar_calibrate_codebook.argtypes = [S, ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.POINTER(ctypes.c_size_t),
                                                _P]
@@ -518,3 +531,146 @@ def oscar_calibrate_codebook(shape: oscar_shape, kv, U, clip, codebook, workspac
         _dptr(clip, "clip", torch.float32), _dptr(codebook, "codebook", torch.float32),
         _dptr(workspace, "workspace", torch.uint8), ctypes.byref(ws), _stream_ptr(stream))
     _check("oscar_calibrate_codebook", st)
+
+
+OSCAR_OUT_F32, OSCAR_OUT_BF16 = 0, 1
+MAX_COPY_POOLS = 128
+
+
+def _out_type(out, what: str = "out") -> int:
+    """OSCAR_OUT_* of an output tensor."""
+    import torch
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{what}: expected float32 or bfloat16, got {out.dtype}")
+    return OSCAR_OUT_BF16 if out.dtype == torch.bfloat16 else OSCAR_OUT_F32
+
+
+def _room(t, need: int, what: str) -> None:
+    """A tensor that the device reads or writes up to element `need`."""
+    if t is not None and t.numel() < need:
+        raise ValueError(f"{what}: {t.numel()} elements, {need} are needed")
+
+
+def block_bytes_int4(shape: oscar_shape) -> int:
+    """Bytes of a (page, KV head) block of a 4-bit pool, 0 if unsupported."""
+    return int(lib().oscar_block_bytes_int4(ctypes.byref(shape)))
+
+
+def oscar_evict_quantize_int4(shape: oscar_shape, src_kv, dst_seq, dst_pos, U, clip, pool, page_table, batch: int,
+                              max_pages: int, num_pages: int, src_row=None, new_kv=None, dev_status=None,
+                              stream=None) -> None:
+    """oscar_evict_quantize into a 4-bit pool (num_pages * Hk blocks of
+    block_bytes_int4(shape) bytes); see include/oscar.h."""
+    import torch
+    n_tok = int(dst_seq.numel())
+    row = shape.num_kv_heads * 2 * shape.head_dim
+    _room(dst_pos, n_tok, "dst_pos")
+    _room(src_row, n_tok, "src_row")
+    _room(new_kv, n_tok * row, "new_kv")
+    _room(src_kv, int(src_kv.shape[0]) * row, "src_kv")
+    _room(page_table, batch * max_pages, "page_table")
+    _room(pool, num_pages * shape.num_kv_heads * block_bytes_int4(shape), "pool")
+    st = lib().oscar_evict_quantize_int4(
+        ctypes.byref(shape), n_tok, _dptr(src_kv, "src_kv", torch.bfloat16), int(src_kv.shape[0]),
+        _dptr(src_row, "src_row", torch.int32), _dptr(dst_seq, "dst_seq", torch.int32),
+        _dptr(dst_pos, "dst_pos", torch.int32), _dptr(new_kv, "new_kv", torch.bfloat16),
+        _dptr(U, "U", torch.float32), _dptr(clip, "clip", torch.float32), _dptr(pool, "pool", torch.uint8),
+        _dptr(page_table, "page_table", torch.int32), batch, max_pages, num_pages,
+        _dptr(dev_status, "dev_status", torch.int32), _stream_ptr(stream))
+    _check("oscar_evict_quantize_int4", st)
+
+
+def oscar_decode_workspace_bytes_int4(shape: oscar_shape, batch: int, max_pages: int) -> int:
+    ws = ctypes.c_size_t(0)
+    st = lib().oscar_decode_attn_int4(ctypes.byref(shape), batch, None, None, None, None, None, max_pages, 0, None,
+                                      None, ctypes.c_float(1.0), None, OSCAR_OUT_F32, None, ctypes.byref(ws), None,
+                                      None)
+    _check("oscar_decode_attn_int4", st)
+    return int(ws.value)
+
+
+def oscar_decode_attn_int4(shape: oscar_shape, q, bf16_kv, bf16_len, pool, page_table, max_pages: int,
+                           num_pages: int, hist_len, U, sm_scale: float, out, workspace, dev_status=None,
+                           stream=None) -> None:
+    """oscar_decode_attn over a 4-bit pool; out may be float32 or bfloat16 (see
+    include/oscar.h).  ``workspace``: CUDA uint8 tensor of at least
+    oscar_decode_workspace_bytes_int4(shape, batch, max_pages) bytes."""
+    import torch
+    B = int(q.shape[0])
+    _room(q, B * shape.num_q_heads * shape.head_dim, "q")
+    _room(bf16_kv, B * (shape.sink + shape.recent) * shape.num_kv_heads * 2 * shape.head_dim, "bf16_kv")
+    _room(bf16_len, B, "bf16_len")
+    _room(hist_len, B, "hist_len")
+    _room(page_table, B * max_pages, "page_table")
+    _room(pool, num_pages * shape.num_kv_heads * block_bytes_int4(shape), "pool")
+    _room(out, B * shape.num_q_heads * shape.head_dim, "out")
+    ws = ctypes.c_size_t(int(workspace.numel()))
+    st = lib().oscar_decode_attn_int4(
+        ctypes.byref(shape), B, _dptr(q, "q", torch.bfloat16), _dptr(bf16_kv, "bf16_kv", torch.bfloat16),
+        _dptr(bf16_len, "bf16_len", torch.int32), _dptr(pool, "pool", torch.uint8),
+        _dptr(page_table, "page_table", torch.int32), max_pages, num_pages, _dptr(hist_len, "hist_len", torch.int32),
+        _dptr(U, "U", torch.float32), ctypes.c_float(sm_scale), _dptr(out, "out"), _out_type(out),
+        _dptr(workspace, "workspace", torch.uint8), ctypes.byref(ws), _dptr(dev_status, "dev_status", torch.int32),
+        _stream_ptr(stream))
+    _check("oscar_decode_attn_int4", st)
+
+
+def _pool_block(shape: oscar_shape, bits: int) -> int:
+    return block_bytes_int4(shape) if bits == 4 else block_bytes(shape)
+
+
+def oscar_history_read(shape: oscar_shape, bits: int, seq, pos, pool, page_table, batch: int, max_pages: int,
+                       num_pages: int, out, dev_status=None, stream=None) -> None:
+    """Stored tokens (seq, pos: int32 [n]) as rows out [n][Hk][2][d] (float32 or
+    bfloat16) in the rotated domain; bits: 2 or 4, the pool's codes; see
+    include/oscar.h."""
+    import torch
+    n = int(seq.numel())
+    _room(pos, n, "pos")
+    _room(page_table, batch * max_pages, "page_table")
+    _room(pool, num_pages * shape.num_kv_heads * _pool_block(shape, bits), "pool")
+    _room(out, n * shape.num_kv_heads * 2 * shape.head_dim, "out")
+    st = lib().oscar_history_read(
+        ctypes.byref(shape), bits, n, _dptr(seq, "seq", torch.int32), _dptr(pos, "pos", torch.int32),
+        _dptr(pool, "pool", torch.uint8), _dptr(page_table, "page_table", torch.int32), batch, max_pages, num_pages,
+        _dptr(out, "out"), _out_type(out), _dptr(dev_status, "dev_status", torch.int32), _stream_ptr(stream))
+    _check("oscar_history_read", st)
+
+
+def oscar_history_gather(shape: oscar_shape, bits: int, pool, src_table, dst_table, keep, n_keep, num_pages: int,
+                         boost=None, dev_status=None, stream=None) -> None:
+    """The kept tokens (keep: int32 [B][stride] source positions, the first
+    n_keep[b] of row b) of each history moved to positions 0, 1, ... of its
+    row of dst_table (int32 [B][pages], fresh pages); see include/oscar.h."""
+    import torch
+    B = int(src_table.shape[0])
+    if dst_table.shape[0] != B or keep.shape[0] != B:
+        raise ValueError("src_table, dst_table and keep: one row per sequence")
+    _room(n_keep, B, "n_keep")
+    _room(pool, num_pages * shape.num_kv_heads * _pool_block(shape, bits), "pool")
+    _room(boost, num_pages * shape.num_kv_heads * BOOST_BLOCK_BYTES, "boost")
+    st = lib().oscar_history_gather(
+        ctypes.byref(shape), bits, B, _dptr(pool, "pool", torch.uint8), _dptr(boost, "boost", torch.uint8),
+        _dptr(src_table, "src_table", torch.int32), int(src_table.shape[1]), _dptr(dst_table, "dst_table", torch.int32),
+        int(dst_table.shape[1]), _dptr(keep, "keep", torch.int32), int(keep.shape[1]),
+        _dptr(n_keep, "n_keep", torch.int32), num_pages, _dptr(dev_status, "dev_status", torch.int32),
+        _stream_ptr(stream))
+    _check("oscar_history_gather", st)
+
+
+def oscar_pages_copy_device(page_bytes: int, src, dst, pools, num_pages: int, dev_status=None, stream=None) -> None:
+    """Page src[i] copied to page dst[i] (int32 CUDA tensors) in every pool of
+    the list (uint8 CUDA tensors of num_pages pages of page_bytes each) by
+    one launch; see include/oscar.h."""
+    import torch
+    n = int(src.numel())
+    _room(dst, n, "dst")
+    ptrs = (ctypes.c_void_p * max(len(pools), 1))()
+    for i, t in enumerate(pools):
+        _room(t, num_pages * page_bytes, f"pools[{i}]")
+        ptrs[i] = _dptr(t, f"pools[{i}]", torch.uint8)
+    st = lib().oscar_pages_copy_device(
+        page_bytes, n, _dptr(src, "src", torch.int32), _dptr(dst, "dst", torch.int32),
+        ctypes.cast(ptrs, _P), len(pools), num_pages, _dptr(dev_status, "dev_status", torch.int32),
+        _stream_ptr(stream))
+    _check("oscar_pages_copy_device", st)

@@ -52,6 +52,12 @@
  *   oscar_radix_*                          radix prefix cache over pages
  *   oscar_evict_quantize_boost,
  *   oscar_decode_attn_boost                K channel precision boost
+ *   oscar_block_bytes_int4,
+ *   oscar_evict_quantize_int4,
+ *   oscar_decode_attn_int4                 the history held in 4 bits
+ *   oscar_history_read                     stored tokens back as rows
+ *   oscar_history_gather                   kept tokens into fresh pages
+ *   oscar_pages_copy_device                pages copied in every layer's pool
  *   oscar_calibrate_codebook               offline fit of the Lloyd-Max levels
  *   oscar_calibrate_rotation               offline U_K, U_V
  *   oscar_calibrate_clip                   offline clip ratios
@@ -439,6 +445,126 @@ oscar_status oscar_decode_attn_boost(const oscar_shape* shape, int32_t batch, co
                                      const int32_t* page_table, int32_t max_pages, int32_t num_pages,
                                      const int32_t* hist_len, const float* U, float sm_scale, float* out,
                                      void* workspace, size_t* ws_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * A history held in 4 bits (the pages describe 2 bits; this is the same
+ * method with 16 levels for a layer or model that 2 bits hurt).  Reading:
+ * rotation, clipping, groups, pages and windows as for 2 bits; a group's
+ * scale is s = fp16((max - min) / 15), its zero z = fp16(min) (of the
+ * clipped values), a code is clamp(rne((y - z) / s), 0, 15) from the stored
+ * s and z (0 where s == 0), and a value is s * code + z.  160 instead of 96
+ * bytes per history token and KV head at quant_group 32.
+ *
+ *   pool     num_pages * Hk blocks of oscar_block_bytes_int4(shape) bytes
+ *            (10240 at g = 32, 9216 at 64, 8704 at 128); block (page, kv)
+ *            starts at (page*Hk + kv) * block_bytes and is two halves, K
+ *            then V, of 4096 + 256*ng bytes (ng = 128 / g):
+ *       K half   [0, 4096) codes, token-major: byte t*64 + 16a + 4k + i
+ *                (a, k, i in 0..3) holds stored positions 32k + 8a + 2i (low
+ *                nibble) and 32k + 8a + 2i + 1 (high nibble);
+ *                [4096, ...) scale/zero: at 4096 + t*4*ng + k*4, fp16 s, fp16 z
+ *       V half   [0, 4096) codes, byte-plane-major: byte j*64 + t holds
+ *                stored positions 2j (low) and 2j + 1 (high) of token t;
+ *                [4096, ...) scale/zero as for K
+ *            oscar_pool_layout gives its page table and page count (its
+ *            pool_bytes are those of a 2-bit pool).
+ *
+ * oscar_evict_quantize_int4: oscar_evict_quantize into a 4-bit pool, with
+ *   the same arguments.  Every decision (the clip threshold, s, z, the
+ *   codes) is taken from compensated pairs of about 2^-44 relative error.
+ * oscar_decode_attn_int4: oscar_decode_attn over a 4-bit pool, with the
+ *   same arguments and workspace convention, and `out` of type out_type:
+ *   OSCAR_OUT_F32 (fp32, 16-byte aligned) or OSCAR_OUT_BF16 (bf16 [B][Hq][d],
+ *   8-byte aligned, rounded once from the fp32 result).
+ * Errors: as the 2-bit calls; INVALID_ARG for an unknown out_type.
+ */
+#define OSCAR_OUT_F32 0
+#define OSCAR_OUT_BF16 1
+size_t oscar_block_bytes_int4(const oscar_shape* shape);
+oscar_status oscar_evict_quantize_int4(const oscar_shape* shape, int32_t n_tok, const void* src_kv,
+                                       int32_t src_rows, const int32_t* src_row, const int32_t* dst_seq,
+                                       const int32_t* dst_pos, const void* new_kv, const float* U,
+                                       const float* clip, uint8_t* pool, const int32_t* page_table,
+                                       int32_t batch, int32_t max_pages, int32_t num_pages,
+                                       int32_t* dev_status, void* stream);
+oscar_status oscar_decode_attn_int4(const oscar_shape* shape, int32_t batch, const void* q, const void* bf16_kv,
+                                    const int32_t* bf16_len, const uint8_t* pool, const int32_t* page_table,
+                                    int32_t max_pages, int32_t num_pages, const int32_t* hist_len, const float* U,
+                                    float sm_scale, void* out, int32_t out_type, void* workspace, size_t* ws_bytes,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * oscar_history_read -- stored history tokens back as rows: the values
+ * s * code + z that the codes stand for, in the rotated domain and stored
+ * order (row vector x of a token is stored as x . R).  For attention of
+ * several query tokens over the history by the caller's own kernels (queries
+ * multiplied by R_K, outputs by R_V^T), for moving a history to another
+ * format, and to look at what an eviction wrote.
+ *
+ *   bits     2 (pools of oscar_evict_quantize; the uniform levels) or 4
+ *   seq, pos (device int32 [n_tok]) sequence and history position of each row
+ *   out      (device) [n_tok][Hk][2][d] of out_type, 16-byte aligned; one
+ *            rounding to bf16 for OSCAR_OUT_BF16
+ * A row with a bad sequence, position or page id is left as it was and
+ * reported in dev_status.
+ * Errors: UNSUPPORTED for other bits; INVALID_ARG for bad sizes or pointers.
+ */
+oscar_status oscar_history_read(const oscar_shape* shape, int32_t bits, int32_t n_tok, const int32_t* seq,
+                                const int32_t* pos, const uint8_t* pool, const int32_t* page_table, int32_t batch,
+                                int32_t max_pages, int32_t num_pages, void* out, int32_t out_type,
+                                int32_t* dev_status, void* stream);
+
+/*
+ * oscar_history_gather -- compaction: the kept tokens of each sequence's
+ * history moved to positions 0, 1, ... of its row of dst_table, in the order
+ * of the list (codes and pairs copied bit by bit).  With the keep list of
+ * every position it forks a history; with a part of it, it drops the rest.
+ * The caller takes the destination pages from its allocator
+ * (oscar_pages_alloc), releases the old ones afterwards, and decodes with
+ * dst_table and n_keep as the history lengths.
+ *
+ *   bits      2 or 4 (block layout of the pool)
+ *   pool      source and destination pages; boost (nullable): the K boost
+ *             records of a 2-bit pool, moved along
+ *   src_table (device int32 [batch][src_max_pages]), dst_table (device int32
+ *             [batch][dst_max_pages])
+ *   keep      (device int32 [batch][keep_stride]) source positions; the first
+ *             n_keep[b] (device int32) of row b are read.  A position may
+ *             appear more than once.
+ * No destination page may be a source page of the same call, nor appear
+ * twice (contents are then undefined; nothing is accessed out of range).
+ * Slots behind the last kept token are left as they were.  A token with a
+ * bad position or page id, and a page with a bad destination id, is skipped
+ * and reported; n_keep outside [0, min(keep_stride, 64 dst_max_pages)] is
+ * clamped and reported.
+ */
+oscar_status oscar_history_gather(const oscar_shape* shape, int32_t bits, int32_t batch, uint8_t* pool,
+                                  uint8_t* boost, const int32_t* src_table, int32_t src_max_pages,
+                                  const int32_t* dst_table, int32_t dst_max_pages, const int32_t* keep,
+                                  int32_t keep_stride, const int32_t* n_keep, int32_t num_pages,
+                                  int32_t* dev_status, void* stream);
+
+/*
+ * oscar_pages_copy_device -- page src[i] copied to page dst[i], i < n_copies,
+ * in each of n_pools pools (the layers of a model: one page table serves
+ * them all), by one launch that reads the index arrays on the device, so
+ * that a captured graph copies whatever pages the arrays name at each
+ * replay.  oscar_pages_copy is the form for host index arrays and one pool.
+ *
+ *   page_bytes  bytes of a page: Hk * oscar_block_bytes(shape) or
+ *               _int4, Hk * OSCAR_BOOST_BLOCK_BYTES, ...; a multiple of 16
+ *   src, dst    (device int32 [n_copies]).  No dst page may also be a src
+ *               page of the call, nor appear twice (its contents are then
+ *               undefined); src[i] == dst[i] copies nothing.
+ *   pools       (host array of n_pools <= OSCAR_MAX_COPY_POOLS device
+ *               pointers, 16-byte aligned), read before the call returns;
+ *               num_pages pages each
+ * A pair with a bad page id is skipped and reported in dev_status.
+ */
+#define OSCAR_MAX_COPY_POOLS 128
+oscar_status oscar_pages_copy_device(size_t page_bytes, int32_t n_copies, const int32_t* src, const int32_t* dst,
+                                     uint8_t* const* pools, int32_t n_pools, int32_t num_pages, int32_t* dev_status,
+                                     void* stream);
 
 /*
  * oscar_calibrate_codebook -- offline Lloyd-Max fit of the inner level a of
