@@ -1,0 +1,692 @@
+// evict_bulk.cu -- eviction of many tokens at once into the 4-bit history (a
+// prompt's history): the same codes and pairs as evict_kernel<., 4>
+// (evict.cu), with the rotation on tensor cores.
+//
+// The mathematics.  A vector's decisions (s, z, codes) have to be those of the
+// exact rotated values, while a tensor-core product gives y within some
+// bound delta.  So every decision is taken from the product first, together with a
+// test whether an error of delta could change it; the few that could (about
+// one group in 25 for s or z, one code in 10^4) are taken again from exactly
+// summed values.
+//   Product: y = x . R, R = U . Hadamard . bit-reversal / sqrt(d) formed once
+// per block in 64-bit fixed point and kept as fp16 parts h1 + h2 (22 bits) and
+// a remainder r3 of 16 bits, all scaled by a power of two; x (bf16) is scaled per row into
+// fp16, exactly.  acc = x . h2 first, then x . h1: the second sum's eight
+// accumulation steps each lose at most 2^-23 of a partial sum, which is at
+// most |x| |R_j| (Cauchy-Schwarz): 2^-20, and r3 is below 2^-22 of R:
+// delta = 1.5 2^-20 |x| max_j |R_j|.
+//   Exact value of one element: x (h1 + h2) as an error-free product, x r3 exact
+// in fp32 (8 x 16 bits), added by the warp as pairs: the value of R to about
+// 2^-38.
+//
+// What bounds it: 512 bytes read and 160 written per token and KV head
+// (24 us for 15,104 tokens of eight KV heads), 256 tensor-core products per
+// 16 vectors, and about 1,300 instructions for their decisions.  Measured 141
+// us for that case (the per-vector kernel: 1832 us): 18 us for R, then per
+// 16-token tile a quarter of the time in the products (at the rate of
+// mma.sync), a sixth each in the exact sums and in the codes.  The kernel's
+// code is larger than the instruction caches hold: loops are kept rolled and
+// warps in step (below) for that reason.
+#include <algorithm>
+
+#include "pairs.cuh"
+
+namespace oscar {
+
+namespace {
+
+constexpr int kBulkWarps = 12;
+constexpr int kBulkThreads = 32 * kBulkWarps;
+constexpr int kGroupWarps = 6;              // warps that go through a tile together
+constexpr int kTile = 16;                   // tokens of a warp's tile (MMA rows)
+constexpr int kXPitch = kD * 2 + 16;        // bytes of a staged row: ldmatrix rows on distinct banks
+constexpr int kStgPitch = kD / 2 + 4;       // bytes of a staged code row
+
+// Fragment words of a k-step: [16 n-tiles][32 lanes], and four more, so that the
+// eight k-steps that a team of bulk_exact reads lie on distinct banks (without
+// them that phase took 66 of 302 thousand cycles, with them 30).
+constexpr int kStepWords = 16 * 32 + 4;
+
+struct BulkSmem {
+    static constexpr int kFrag = 0;                                  // [2 parts][8 k-steps][kStepWords] uint2
+    static constexpr int kR3 = kFrag + 2 * 8 * kStepWords * 8;       // [8][kStepWords] float4
+    static constexpr int kX = kR3 + 8 * kStepWords * 16;             // [warp][16][kXPitch]
+    static constexpr int kStg = kX + kBulkWarps * kTile * kXPitch;   // [warp][16][kStgPitch]: byte j = positions 2j, 2j + 1
+    static constexpr int kSz = kStg + kBulkWarps * kTile * kStgPitch;  // [warp][16][4] (s, z) word per 32-position block
+    static constexpr int kDst = kSz + kBulkWarps * kTile * 16;       // [warp][16] destination half, [warp][16] slot
+    static constexpr int kCol = kDst + kBulkWarps * kTile * 16;      // [128] column sums of squares, then scalars
+    static constexpr int kList = kCol + (kD + 4) * 4;                // open groups of the round
+    static constexpr int kBytes = kList + kBulkWarps * kTile * 4 * 8;
+};
+static_assert(BulkSmem::kBytes <= 227 * 1024, "one block per SM");
+
+__device__ __forceinline__ float pow2f_bits(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// R of this block's (KV head, K|V) into shared memory.  Row a of U times the
+// Hadamard matrix in fixed point, as two 32-bit integers (2^-44 of the largest
+// |U|; the additions are exact), then times 1 / sqrt(d) as a pair.  (64-bit
+// integers took 25 us: their conversions run on the slow 64-bit pipe.)  Returns the exponent q of the scale
+// (stored = R 2^q) and the largest column norm of the stored matrix.
+__device__ __forceinline__ void bulk_matrix(const float* U, uint8_t* smem, int& q, float& norm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* col = reinterpret_cast<float*>(smem + BulkSmem::kCol);
+    int* umax = reinterpret_cast<int*>(col + kD);
+    if (threadIdx.x < kD) col[threadIdx.x] = 0.f;
+    if (threadIdx.x == 0) *umax = 0;
+    __syncthreads();
+    float mx = 0.f;
+    for (int i = threadIdx.x; i < kD * kD / 4; i += kBulkThreads) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(U) + i);
+        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
+    if (lane == 0) atomicMax(umax, __float_as_int(mx));
+    __syncthreads();
+    const int e = min(60, max(-60, ((*umax >> 23) & 0xff) - 127));
+    q = 10 - e;  // |R| <= 128 |U| / sqrt(128) < 2^(e + 4.5): stored below 2^14.5
+    const float up = pow2f_bits(22 - e);  // |U| 2^(22 - e) < 2^23: sums of 128 below 2^30
+    // R 2^q = v 2^(e - 22 + q) / sqrt(128) = v 2^-12 / sqrt(128)
+    const float kc_hi = __uint_as_float(0x3db504f3u), kc_lo = __uint_as_float(0x30cfe77au), down = pow2f_bits(-12);
+    // Four rows at a time, the k indices of one fragment word pair (16 ks + 2 tq,
+    // + 1, + 8, + 9), so that a position's parts are stored as vectors.  (Loops
+    // rolled, with the sums in shared memory in between: this code runs three
+    // times per warp and would otherwise wait on its own instruction fetches.)
+    uint2* frag = reinterpret_cast<uint2*>(smem + BulkSmem::kFrag);
+    float4* r3 = reinterpret_cast<float4*>(smem + BulkSmem::kR3);
+    int4* sums = reinterpret_cast<int4*>(smem + BulkSmem::kX + warp * kTile * kXPitch);  // [4 rows][high, low][32 lanes]
+    float sq[4] = {0.f, 0.f, 0.f, 0.f};
+    float4 next[4];
+    auto load_rows = [&](int w) {
+        if (w >= kD / 4) return;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            next[i] = __ldg(reinterpret_cast<const float4*>(U + (size_t)(16 * (w >> 2) + 2 * (w & 3) + (i & 1) + 8 * (i >> 1)) * kD) + lane);
+    };
+    load_rows(warp);
+#pragma unroll 1
+    for (int w = warp; w < kD / 4; w += kBulkWarps) {
+        const int ks = w >> 2, tq = w & 3;
+        const float4 u[4] = {next[0], next[1], next[2], next[3]};
+        load_rows(w + kBulkWarps);
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const float4 ui = i == 0 ? u[0] : i == 1 ? u[1] : i == 2 ? u[2] : u[3];
+            const float x[4] = {ui.x * up, ui.y * up, ui.z * up, ui.w * up};
+            int v[2][4];  // x = v[0] + v[1] 2^-22
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[0][k] = __float2int_rn(x[k]);
+                v[1][k] = __float2int_rn((x[k] - __int2float_rn(v[0][k])) * 4194304.f);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int t0 = v[h][0] + v[h][1], t1 = v[h][0] - v[h][1], t2 = v[h][2] + v[h][3], t3 = v[h][2] - v[h][3];
+                v[h][0] = t0 + t2;
+                v[h][1] = t1 + t3;
+                v[h][2] = t0 - t2;
+                v[h][3] = t1 - t3;
+            }
+#pragma unroll 1
+            for (int m = 1; m < 32; m <<= 1) {
+                const bool upper = (lane & m) != 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int o = __shfl_xor_sync(kFull, v[h][k], m);
+                        v[h][k] = upper ? o - v[h][k] : v[h][k] + o;
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) sums[(2 * i + h) * 32 + lane] = make_int4(v[h][0], v[h][1], v[h][2], v[h][3]);
+        }
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            const int p = 32 * bitrev2(k) + bitrev5(lane);  // stored position of Hadamard output 4 lane + k
+            uint32_t h1[4], h2[4];
+            float r[4], ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int va = reinterpret_cast<const int*>(sums + (2 * i) * 32 + lane)[k];
+                const int vb = reinterpret_cast<const int*>(sums + (2 * i + 1) * 32 + lane)[k];
+                const float hi = __int2float_rn(va);
+                const float lo = __int2float_rn((va - __float2int_rn(hi)) * 4194304 + vb) * (1.f / 4194304.f);
+                float ph = __fmul_rn(hi, kc_hi);
+                float pe = __fmaf_rn(lo, kc_hi, __fmaf_rn(hi, kc_lo, __fmaf_rn(hi, kc_hi, -ph)));
+                ph = __fmul_rn(ph, down);
+                pe = __fmul_rn(pe, down);
+                // h1 + h2: the leading 22 bits (down to 2^-24), so that their fp32 sum is exact
+                const float lead = __uint_as_float(__float_as_uint(ph) & 0xfffffffcu);
+                const __half f1 = __float2half_rn(lead);
+                const float r1 = __half2float(f1);
+                const __half f2 = __float2half_rn(__fsub_rn(lead, r1));
+                h1[i] = __half_as_ushort(f1);
+                h2[i] = __half_as_ushort(f2);
+                // 16 bits, so that its products with bf16 are exact too
+                r[i] = __uint_as_float(
+                    __float_as_uint(__fadd_rn(__fsub_rn(__fsub_rn(ph, r1), __half2float(f2)), pe)) & 0xffffff00u);
+                ss = fmaf(ph, ph, ss);
+            }
+            const int at = ks * kStepWords + (p >> 3) * 32 + 4 * (p & 7) + tq;
+            frag[at] = make_uint2(h1[0] | (h1[1] << 16), h1[2] | (h1[3] << 16));
+            frag[8 * kStepWords + at] = make_uint2(h2[0] | (h2[1] << 16), h2[2] | (h2[3] << 16));
+            r3[at] = make_float4(r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sq[j] += j == k ? ss : 0.f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) atomicAdd(col + 32 * bitrev2(k) + bitrev5(lane), sq[k]);
+    __syncthreads();
+    float c2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c2 = fmaxf(c2, col[lane + 32 * i]);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) c2 = fmaxf(c2, __shfl_xor_sync(kFull, c2, m));
+    norm = sqrtf(c2) * 1.001f;
+}
+
+// Exact value of stored position p of a staged row, by teams of eight lanes
+// (each team its own row and position; every lane of the warp takes part):
+// lane ks of a team sums k indices 16 ks .. 16 ks + 15.
+__device__ __noinline__ df bulk_exact(const uint8_t* smem, const uint8_t* xrow, int p, float down) {
+    const int ks = threadIdx.x & 7;
+    const int at = ks * kStepWords + (p >> 3) * 32 + 4 * (p & 7);
+    const uint4* f1 = reinterpret_cast<const uint4*>(smem + BulkSmem::kFrag) + at / 2;
+    const uint4* f2 = f1 + 8 * kStepWords / 2;
+    const float4* f3 = reinterpret_cast<const float4*>(smem + BulkSmem::kR3) + at;
+    const uint4 xa = *reinterpret_cast<const uint4*>(xrow + 32 * ks), xb = *reinterpret_cast<const uint4*>(xrow + 32 * ks + 16);
+    const uint32_t xl[4] = {xa.x, xa.y, xa.z, xa.w}, xh[4] = {xb.x, xb.y, xb.z, xb.w};  // k = 2 tq, + 1; 8 + 2 tq, + 1
+    float s = 0.f, c = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint4 h1 = f1[half], h2 = f2[half];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // fragment word pair of quad member tq = 2 half + i
+            const uint32_t u1 = i ? h1.z : h1.x, v1 = i ? h1.w : h1.y, u2 = i ? h2.z : h2.x, v2 = i ? h2.w : h2.y;
+            const float4 r = f3[2 * half + i];
+            const uint32_t xi = xl[2 * half + i], xj = xh[2 * half + i];
+            const float x[4] = {bf16_lo(xi), bf16_hi(xi), bf16_lo(xj), bf16_hi(xj)};
+            const float h[4] = {half_lo(u1) + half_lo(u2), half_hi(u1) + half_hi(u2), half_lo(v1) + half_lo(v2),
+                                half_hi(v1) + half_hi(v2)};  // exact: 22 bits
+            const float q[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float pr = __fmul_rn(x[k], h[k]), pe = __fmaf_rn(x[k], h[k], -pr);  // exact product
+                const df t = two_sum(s, pr);
+                s = t.hi;
+                c = __fadd_rn(__fmaf_rn(x[k], q[k], c), __fadd_rn(pe, t.lo));
+            }
+        }
+    }
+    df y = two_sum(s, c);
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1)
+        y = df_add(y, df{__shfl_xor_sync(kFull, y.hi, m), __shfl_xor_sync(kFull, y.lo, m)});
+    return {__fmul_rn(y.hi, down), __fmul_rn(y.lo, down)};
+}
+
+// c max|y| of exact extremes, and the extremes clipped by it.
+__device__ __forceinline__ df bulk_clip(float cr, df& hi, df& lo) {
+    if (!(cr < 1.f)) return {INFINITY, 0.f};
+    const df nlo = df_neg(lo), a = df_less(hi, nlo) ? nlo : hi;
+    const float th = __fmul_rn(cr, a.hi);
+    const df t = fast_two_sum(th, __fmaf_rn(cr, a.lo, __fmaf_rn(cr, a.hi, -th))), nt = df_neg(t);
+    if (df_less(t, hi)) hi = t;
+    if (df_less(lo, nt)) lo = nt;
+    return t;
+}
+
+__device__ __forceinline__ uint32_t bulk_pair(df hi, df lo) {
+    return (uint32_t)df_to_f16(df_div15(df_add(hi, df_neg(lo)))) | ((uint32_t)df_to_f16(lo) << 16);
+}
+
+// A whole group from exact values: extremes, pair and codes of its 32-position
+// blocks b0 .. b0 + nb - 1, written over the staged ones.  For groups whose
+// extremes are not single elements within the bound.
+__device__ __noinline__ void bulk_group_exact(uint8_t* smem, const uint8_t* xrow, uint8_t* stg, uint32_t* sz, int b0, int nb,
+                                              float cr, float down) {
+    const int lane = threadIdx.x & 31;
+    df v[4], hi{-INFINITY, 0.f}, lo{INFINITY, 0.f};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        v[b] = {0.f, 0.f};
+        if (b >= nb) continue;
+        for (int e = 0; e < 8; ++e) {  // team j takes element 8 j + e
+            const df y = bulk_exact(smem, xrow, 32 * (b0 + b) + 8 * (lane >> 3) + e, down);
+            if ((lane & 7) == e) v[b] = y;
+        }
+        if (df_less(hi, v[b])) hi = v[b];
+        if (df_less(v[b], lo)) lo = v[b];
+    }
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const df h{__shfl_xor_sync(kFull, hi.hi, m), __shfl_xor_sync(kFull, hi.lo, m)};
+        const df l{__shfl_xor_sync(kFull, lo.hi, m), __shfl_xor_sync(kFull, lo.lo, m)};
+        if (df_less(hi, h)) hi = h;
+        if (df_less(l, lo)) lo = l;
+    }
+    const df t = bulk_clip(cr, hi, lo), nt = df_neg(t);
+    const uint32_t w = bulk_pair(hi, lo);
+    const float sf = half_lo(w), zf = half_hi(w);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        if (b >= nb) continue;
+        df y = v[b];
+        if (df_less(t, y)) y = t;
+        else if (df_less(y, nt)) y = nt;
+        const uint32_t code = sf != 0.f ? (uint32_t)code4_of(y, sf, zf) : 0u;
+        const uint32_t other = __shfl_xor_sync(kFull, code, 1);
+        if (!(lane & 1)) stg[16 * (b0 + b) + (lane >> 1)] = (uint8_t)(code | (other << 4));
+        if (lane == 0) sz[b0 + b] = w;
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void bulk_ldsm(uint32_t (&r)[4], const void* p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+
+// Block = one (KV head, K|V), blockIdx.x / pairs of the blocks that share it;
+// its warps take tiles of 16 listed tokens in turn.
+__global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gID = lane >> 2, tq = lane & 3;
+    const int pairs = 2 * p.hk, pair = blockIdx.x % pairs, kv = pair >> 1, which = pair & 1;
+    const int step = gridDim.x / pairs * kBulkWarps, tiles = (p.n_tok + kTile - 1) / kTile;
+    int q;
+    float rnorm;
+    bulk_matrix(p.U + ((size_t)kv * 2 + which) * kD * kD, smem, q, rnorm);
+    const float cr = __ldg(p.clip + kv * 2 + which), rdown = pow2f_bits(-q);
+    const int nb = 1 << p.gshift;  // 32-position blocks per group
+    uint8_t* xs = smem + BulkSmem::kX + warp * kTile * kXPitch;
+    uint8_t* stg = smem + BulkSmem::kStg + warp * kTile * kStgPitch;
+    uint32_t* sz = reinterpret_cast<uint32_t*>(smem + BulkSmem::kSz) + warp * kTile * 4;
+    uint8_t** dst = reinterpret_cast<uint8_t**>(smem + BulkSmem::kDst) + warp * kTile;
+    int* slots = reinterpret_cast<int*>(smem + BulkSmem::kDst + kBulkWarps * kTile * 8) + warp * kTile;
+    const uint2* frag = reinterpret_cast<const uint2*>(smem + BulkSmem::kFrag);
+    // the group's open quantisation groups: row of the block, 32-position block, positions of the extremes
+    ushort4* list = reinterpret_cast<ushort4*>(smem + BulkSmem::kList) + warp / kGroupWarps * (kGroupWarps * kTile * 4);
+    int* n_list = reinterpret_cast<int*>(smem + BulkSmem::kCol) + kD + 1 + warp / kGroupWarps;
+
+    // Lane r < 16 (and 16 + r) looks token r of a tile up: its row (-1: skipped)
+    // and where it goes.  Done a tile ahead, with the rows requested into L2.
+    struct Token {
+        int row, slot;
+        uint8_t* to;
+    };
+    auto look_up = [&](int tile) {
+        Token k{-1, 0, nullptr};
+        const int i = tile * kTile + (lane & 15);
+        if (i < p.n_tok) {
+            k.row = p.src_row ? __ldg(p.src_row + i) : i;
+            if (k.row < 0 || k.row >= p.src_rows) {
+                k.row = -1;
+                report(p.status, OSCAR_STATUS_BAD_POS);
+            } else {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.src_kv + ((size_t)k.row * pairs + pair) * kD + 64 * (lane >> 4)));
+                const int seq = __ldg(p.dst_seq + i), pos = __ldg(p.dst_pos + i);
+                if (pos < 0 || pos >= p.max_pages * kPage || seq < 0 || seq >= p.batch) {
+                    report(p.status, OSCAR_STATUS_BAD_POS);
+                } else {
+                    const int page = __ldg(p.page_table + (size_t)seq * p.max_pages + pos / kPage);
+                    if (page < 0 || page >= p.num_pages) report(p.status, OSCAR_STATUS_BAD_PAGE);
+                    else k.to = p.pool + ((size_t)page * p.hk + kv) * p.block_bytes + which * half_bytes4(p.gshift);
+                    k.slot = pos % kPage;
+                }
+            }
+        }
+        return k;
+    };
+    // Two groups of six warps, each going through a tile together (its own
+    // barrier): left to themselves the warps spread over the loop's code and
+    // wait for instruction fetches half of the time, and in one group the
+    // tensor cores idle while the codes are made.
+    auto group_sync = [&]() {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / kGroupWarps), "r"(32 * kGroupWarps) : "memory");
+    };
+    const int first = blockIdx.x / pairs * kBulkWarps, rounds = (tiles - first + step - 1) / step;
+    Token next = look_up(first + warp);
+    for (int round = 0; round < rounds; ++round) {
+        const int tile = first + warp + round * step;
+        group_sync();
+        if (lane == 0 && warp % kGroupWarps == 0) *n_list = 0;  // (added to after a further barrier)
+        const int row = next.row;
+        if (lane < kTile) {  // (the last tile's stores have read dst and slots)
+            dst[lane] = next.to;
+            slots[lane] = next.slot;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // two rows of 16 chunks at a time
+            const int r = 2 * c + (lane >> 4), ch = lane & 15;
+            const int rr = __shfl_sync(kFull, row, r);
+            uint8_t* to = xs + r * kXPitch + 16 * ch;
+            if (rr >= 0)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)),
+                             "l"(p.src_kv + ((size_t)rr * pairs + pair) * kD + 8 * ch)
+                             : "memory");
+            else
+                *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        next = look_up(tile + step);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncwarp();
+        if (p.new_kv) {  // fused ring append: overwrite the rows just read
+#pragma unroll 1
+            for (int r = 0; r < kTile; ++r) {
+                const int rr = __shfl_sync(kFull, row, r);
+                if (rr >= 0)
+                    reinterpret_cast<uint2*>(const_cast<__nv_bfloat16*>(p.src_kv) + ((size_t)rr * pairs + pair) * kD)[lane] =
+                        __ldg(reinterpret_cast<const uint2*>(p.new_kv + ((size_t)(tile * kTile + r) * pairs + pair) * kD) + lane);
+            }
+        }
+
+        // -- rows scaled by 2^k, k from the largest element
+        const uint8_t* xfrag = xs + ((lane & 7) + 8 * ((lane >> 3) & 1)) * kXPitch + 16 * (lane >> 4);
+        float mx[2] = {0.f, 0.f}, n2[2] = {0.f, 0.f}, fdown[2], up[2], delta[2];
+#pragma unroll 2
+        for (int ks = 0; ks < 8; ++ks) {
+            uint32_t a[4];
+            bulk_ldsm(a, xfrag + 32 * ks);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mx[e & 1] = fmaxf(mx[e & 1], fmaxf(fabsf(bf16_lo(a[e])), fabsf(bf16_hi(a[e]))));
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 2));
+            const int k = min(80, 14 - ((int)(__float_as_uint(mx[r]) >> 23) - 127));  // largest |x| 2^k below 2^15
+            up[r] = pow2f_bits(k);
+            fdown[r] = pow2f_bits(-k) * rdown;  // accumulator -> y
+        }
+
+        // -- y: n-tile n = stored positions 8 n .. 8 n + 7; rows gID (entries
+        //    0, 1) and gID + 8 (2, 3).  Steps 0-7: x . h2, 8-15: x . h1.  (A
+        //    loop, not unrolled: with every product unrolled the kernel waited
+        //    on instruction fetches for half of its time.)
+        float acc[16][4];
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll 1
+        for (int step16 = 0; step16 < 16; ++step16) {
+            const int ks = step16 & 7;
+            uint32_t a[4];
+            bulk_ldsm(a, xfrag + 32 * ks);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = bf16_lo(a[e]) * up[e & 1], v1 = bf16_hi(a[e]) * up[e & 1];
+                n2[e & 1] = fmaf(v0, v0, fmaf(v1, v1, n2[e & 1]));
+                a[e] = pack_f16x2_rn(v0, v1);
+            }
+            const uint2* fb = frag + (((step16 >> 3) ^ 1) * 8 + ks) * kStepWords + lane;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+                const uint2 b = fb[n * 32];
+                mma_f16_16816(acc[n], a[0], a[1], a[2], a[3], b.x, b.y);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            n2[r] += __shfl_xor_sync(kFull, n2[r], 1);
+            n2[r] += __shfl_xor_sync(kFull, n2[r], 2);  // every element twice: 2 |x|^2
+            delta[r] = 1.5f * 9.5367431640625e-7f * sqrtf(0.5f * n2[r]) * 1.001f * rnorm * fdown[r];
+        }
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] *= fdown[e >> 1];
+
+        // -- extremes, clip threshold and pair of every group (by 32-position block)
+        float gmx[2][4], gmn[2][4], clip[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float h = acc[4 * b][2 * r], l = h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h = fmaxf(h, fmaxf(acc[4 * b + i][2 * r], acc[4 * b + i][2 * r + 1]));
+                    l = fminf(l, fminf(acc[4 * b + i][2 * r], acc[4 * b + i][2 * r + 1]));
+                }
+                h = fmaxf(h, __shfl_xor_sync(kFull, h, 1));
+                l = fminf(l, __shfl_xor_sync(kFull, l, 1));
+                gmx[r][b] = fmaxf(h, __shfl_xor_sync(kFull, h, 2));
+                gmn[r][b] = fminf(l, __shfl_xor_sync(kFull, l, 2));
+            }
+            if (p.gshift >= 1) {
+                gmx[r][0] = gmx[r][1] = fmaxf(gmx[r][0], gmx[r][1]);
+                gmx[r][2] = gmx[r][3] = fmaxf(gmx[r][2], gmx[r][3]);
+                gmn[r][0] = gmn[r][1] = fminf(gmn[r][0], gmn[r][1]);
+                gmn[r][2] = gmn[r][3] = fminf(gmn[r][2], gmn[r][3]);
+            }
+            if (p.gshift >= 2) {
+                gmx[r][0] = gmx[r][1] = gmx[r][2] = gmx[r][3] = fmaxf(gmx[r][0], gmx[r][2]);
+                gmn[r][0] = gmn[r][1] = gmn[r][2] = gmn[r][3] = fminf(gmn[r][0], gmn[r][2]);
+            }
+        }
+        // Candidates for the extremes: elements within 2 delta of them; count (bits
+        // 0-7) and sum of positions per row and block, then per group.
+        uint32_t cx[2][4], cn[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float d2 = 2.02f * delta[r];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float bx = gmx[r][b] - d2, bn = gmn[r][b] + d2;
+                uint32_t x = 0, n = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = acc[4 * b + i][2 * r + e];
+                        const uint32_t one = 1u + ((uint32_t)(32 * b + 8 * i + 2 * tq + e) << 8);
+                        if (!(y < bx)) x += one;
+                        if (!(y > bn)) n += one;
+                    }
+                x += __shfl_xor_sync(kFull, x, 1);
+                n += __shfl_xor_sync(kFull, n, 1);
+                cx[r][b] = x + __shfl_xor_sync(kFull, x, 2);
+                cn[r][b] = n + __shfl_xor_sync(kFull, n, 2);
+            }
+            if (p.gshift >= 1) {
+                cx[r][0] += cx[r][1];
+                cx[r][2] += cx[r][3];
+                cn[r][0] += cn[r][1];
+                cn[r][2] += cn[r][3];
+            }
+            if (p.gshift >= 2) {
+                cx[r][0] += cx[r][2];
+                cn[r][0] += cn[r][2];
+            }
+        }
+        uint32_t whole[2] = {0u, 0u};  // bit 4 gID + b: the group of (row gID + 8 r, block b) is taken from exact values as a whole
+        group_sync();  // (the list's counter is zero)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float d = delta[r];
+                const float t = cr < 1.f ? cr * fmaxf(gmx[r][b], -gmn[r][b]) : INFINITY;
+                const float hi = fminf(gmx[r][b], t), lo = fmaxf(gmn[r][b], -t);
+                const float sp = (hi - lo) * (1.f / 15.f), es = d * (2.f / 15.f) + sp * 4.8e-7f, ez = d + fabsf(lo) * 2.4e-7f;
+                const uint32_t w0 = pack_f16x2_rn(sp - es, lo - ez), w1 = pack_f16x2_rn(sp + es, lo + ez);
+                clip[r][b] = t;
+                // (NaN bounds leave it open as well)
+                const bool open = (!(sp - es <= sp + es && lo - ez <= lo + ez) || w0 != w1) && tq == 0 && (b & (nb - 1)) == 0;
+                const bool single = (cx[r][b] & 0xffu) == 1u && (cn[r][b] & 0xffu) == 1u;
+                if (tq == 0) sz[(gID + 8 * r) * 4 + b] = w0;
+                whole[r] |= (__ballot_sync(kFull, open && !single) & 0x11111111u) << b;
+                if (open && single)
+                    list[atomicAdd(n_list, 1)] =
+                        make_ushort4((unsigned short)(warp * kTile + gID + 8 * r), (unsigned short)b,
+                                     (unsigned short)(cx[r][b] >> 8), (unsigned short)(cn[r][b] >> 8));
+            }
+        // The group's warps share the list (a tile opens about three groups,
+        // some six or more): half warps take an entry each, a team of eight
+        // lanes per extreme.
+        group_sync();
+        const int entries = *n_list;
+        for (int e0 = 2 * (warp % kGroupWarps); e0 < entries; e0 += 2 * kGroupWarps) {
+            const ushort4 en = list[min(e0 + (lane >> 4), entries - 1)];
+            const df y = bulk_exact(smem, smem + BulkSmem::kX + en.x * kXPitch, (lane & 8) ? en.w : en.z, rdown);
+            const df o{__shfl_xor_sync(kFull, y.hi, 8), __shfl_xor_sync(kFull, y.lo, 8)};
+            df hi = (lane & 8) ? o : y, lo = (lane & 8) ? y : o;
+            (void)bulk_clip(cr, hi, lo);
+            const uint32_t w = bulk_pair(hi, lo);
+            if ((lane & 15) < nb) reinterpret_cast<uint32_t*>(smem + BulkSmem::kSz)[en.x * 4 + en.y + (lane & 15)] = w;
+        }
+        group_sync();
+
+        // -- codes: byte 4 n + tq of a row; an undecided code's bit 2 n + e in `late`
+        uint32_t late[2] = {0u, 0u};
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t w = sz[(gID + 8 * r) * 4 + b];
+                const float sf = half_lo(w), zf = half_hi(w), t = clip[r][b];
+                const float inv = sf != 0.f ? __fdividef(1.f, sf) : 0.f;
+                // u is off by delta / s and the rounding of three fp32 operations on |u| < 16
+                const float edge = 0.5f - (delta[r] * inv * 1.01f + 8e-6f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = 4 * b + i;
+                    uint32_t c[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = fminf(fmaxf(acc[n][2 * r + e], -t), t);
+                        const float u = (y - zf) * inv, k = rintf(u);
+                        if (!(fabsf(u - k) < edge) && inv != 0.f) late[r] |= 1u << (2 * n + e);
+                        c[e] = (uint32_t)fminf(fmaxf(k, 0.f), 15.f);
+                    }
+                    stg[(gID + 8 * r) * kStgPitch + 4 * n + tq] = (uint8_t)(c[0] | (c[1] << 4));
+                }
+            }
+        __syncwarp();
+        for (;;) {
+            const uint32_t who = __ballot_sync(kFull, (late[0] | late[1]) != 0u);
+            if (!who) break;
+            const int src = __ffs(who) - 1;
+            const int r = late[0] ? 0 : 1;
+            int item = 64 * r + __ffs(r ? late[1] : late[0]) - 1;  // (of each lane; the chosen lane's is taken)
+            item = __shfl_sync(kFull, item, src);
+            const int rr = item >> 6, n = (item & 63) >> 1, e = item & 1, g = src >> 2;
+            if (lane == src) {
+                if (rr) late[1] &= late[1] - 1;
+                else late[0] &= late[0] - 1;
+            }
+            const int row16 = g + 8 * rr, pos = 8 * n + 2 * (src & 3) + e, b0 = (n >> 2) & ~(nb - 1);
+            if ((whole[rr] >> (4 * g + b0)) & 1u) continue;  // taken as a whole below
+            const df y = bulk_exact(smem, xs + row16 * kXPitch, pos, rdown);
+            float t = 0.f, d = 0.f;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b == b0) t = rr ? clip[1][b] : clip[0][b];
+            t = __shfl_sync(kFull, t, src);
+            d = __shfl_sync(kFull, rr ? delta[1] : delta[0], src);
+            if (!(fabsf(y.hi) < t - 2.f * d)) {  // at the clip threshold: its exact value is needed too
+                whole[rr] |= 1u << (4 * g + b0);
+                continue;
+            }
+            if (lane == src) {
+                const uint32_t w = sz[row16 * 4 + (n >> 2)];
+                const uint32_t code = (uint32_t)code4_of(y, half_lo(w), half_hi(w));
+                uint8_t* at = stg + row16 * kStgPitch + (pos >> 1);
+                *at = (uint8_t)(e ? (*at & 0x0f) | (code << 4) : (*at & 0xf0) | code);
+            }
+            __syncwarp();
+        }
+#pragma unroll 1
+        for (int r = 0; r < 2; ++r)
+            for (uint32_t m = r ? whole[1] : whole[0]; m; m &= m - 1) {
+                const int bit = __ffs(m) - 1, row16 = (bit >> 2) + 8 * r;
+                bulk_group_exact(smem, xs + row16 * kXPitch, stg + row16 * kStgPitch, sz + row16 * 4, bit & 3, nb, cr, rdown);
+            }
+        __syncwarp();
+
+        // -- stores
+        if (which == 0) {  // 16-byte chunk a of a token: word k = bytes 16 k + 4 a .. + 3
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                const int t = 8 * it + gID;
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(stg + t * kStgPitch) + tq;
+                if (dst[t])
+                    *reinterpret_cast<uint4*>(dst[t] + slots[t] * (kD / 2) + 16 * tq) = make_uint4(w[0], w[4], w[8], w[12]);
+            }
+        } else {  // plane j, four tokens at a time
+            const int t0 = 4 * tq;
+            uint8_t* const d0 = dst[t0];
+            const int s0 = slots[t0];
+            const bool joined = d0 && (s0 & 3) == 0 && dst[t0 + 1] == d0 && dst[t0 + 2] == d0 && dst[t0 + 3] == d0 &&
+                                slots[t0 + 1] == s0 + 1 && slots[t0 + 2] == s0 + 2 && slots[t0 + 3] == s0 + 3;
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {  // planes 4 (gID + 8 it) .. + 3
+                const int j4 = gID + 8 * it;
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint32_t*>(stg + (t0 + i) * kStgPitch)[j4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w01 = __byte_perm(v[0], v[1], 0x0040u + 0x0011u * i), w23 = __byte_perm(v[2], v[3], 0x0040u + 0x0011u * i);
+                    const uint32_t w = __byte_perm(w01, w23, 0x5410u);
+                    const int plane = (4 * j4 + i) * kPage;
+                    if (joined) {
+                        *reinterpret_cast<uint32_t*>(d0 + plane + s0) = w;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (dst[t0 + k]) dst[t0 + k][plane + slots[t0 + k]] = (uint8_t)(w >> (8 * k));
+                    }
+                }
+            }
+        }
+        if (lane < kTile && dst[lane]) {
+            const int ng = sz_pairs(p.gshift);
+            const uint32_t* w = sz + lane * 4;
+            uint8_t* to = dst[lane] + kCodes4 + slots[lane] * 4 * ng;
+            if (ng == 4) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if (ng == 2) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[2]);
+            else *reinterpret_cast<uint32_t*>(to) = w[0];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_evict_bulk(const EvictParams& p, cudaStream_t st) {
+    static int sms[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (sms[dev & 63] == 0) {
+        e = cudaFuncSetAttribute(evict_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BulkSmem::kBytes);
+        if (e != cudaSuccess) return e;
+        e = cudaDeviceGetAttribute(&sms[dev & 63], cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    const int pairs = 2 * p.hk, tiles = (p.n_tok + kTile - 1) / kTile;
+    const int share = std::max(1, std::min((tiles + kBulkWarps - 1) / kBulkWarps, sms[dev & 63] / pairs));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(pairs * share);
+    cfg.blockDim = dim3(kBulkThreads);
+    cfg.dynamicSmemBytes = BulkSmem::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, evict_bulk_kernel, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace oscar

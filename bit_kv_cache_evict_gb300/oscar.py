@@ -536,24 +536,78 @@ def oscar_calibrate_codebook(shape: oscar_shape, kv, U, clip, codebook, workspac
 OSCAR_OUT_F32, OSCAR_OUT_BF16 = 0, 1
 MAX_COPY_POOLS = 128
 
+# The calls below run once per layer and step, where a launch costs a few
+# microseconds: their checks touch each tensor once (_arg), sizes that depend
+# on the shape alone are kept per shape, and pointers go to ctypes as ints.
+_F32 = _BF16 = _I32 = _U8 = _raw_stream = None
 
-def _out_type(out, what: str = "out") -> int:
-    """OSCAR_OUT_* of an output tensor."""
+
+def _torch_names() -> None:
+    global _F32, _BF16, _I32, _U8, _raw_stream
     import torch
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{what}: expected float32 or bfloat16, got {out.dtype}")
-    return OSCAR_OUT_BF16 if out.dtype == torch.bfloat16 else OSCAR_OUT_F32
+    _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _room(t, need: int, what: str) -> None:
-    """A tensor that the device reads or writes up to element `need`."""
-    if t is not None and t.numel() < need:
-        raise ValueError(f"{what}: {t.numel()} elements, {need} are needed")
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _arg(t, what: str, dtype, need: int, dev: int):
+    """Address of a contiguous tensor of `dtype` on device `dev` with at least
+    `need` elements (None -> NULL)."""
+    if t is None:
+        return None
+    try:
+        if not t.is_cuda:
+            raise TypeError(f"{what}: expected a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: must be contiguous")
+        if t.numel() < need:
+            raise ValueError(f"{what}: {t.numel()} elements, {need} are needed")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: on device {t.get_device()}, the current device is {dev}")
+        return t.data_ptr()
+    except AttributeError:
+        raise TypeError(f"{what}: expected a CUDA tensor") from None
+
+
+def _stream_arg(stream, dev: int):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev)
+
+
+def _out_type(out) -> int:
+    """OSCAR_OUT_* of an output tensor."""
+    if _F32 is None:
+        _torch_names()
+    if out.dtype is _BF16:
+        return OSCAR_OUT_BF16
+    if out.dtype is _F32:
+        return OSCAR_OUT_F32
+    raise TypeError(f"out: expected float32 or bfloat16, got {out.dtype}")
+
+
+_BLOCK = {}
+
+
+def _pool_block(shape: oscar_shape, bits: int) -> int:
+    """Block bytes of a pool, kept per (bits, shape)."""
+    key = (bits, bytes(shape))
+    n = _BLOCK.get(key)
+    if n is None:
+        fn = lib().oscar_block_bytes_int4 if bits == 4 else lib().oscar_block_bytes
+        n = _BLOCK[key] = int(fn(ctypes.byref(shape)))
+    return n
 
 
 def block_bytes_int4(shape: oscar_shape) -> int:
     """Bytes of a (page, KV head) block of a 4-bit pool, 0 if unsupported."""
-    return int(lib().oscar_block_bytes_int4(ctypes.byref(shape)))
+    return _pool_block(shape, 4)
 
 
 def oscar_evict_quantize_int4(shape: oscar_shape, src_kv, dst_seq, dst_pos, U, clip, pool, page_table, batch: int,
@@ -561,23 +615,20 @@ def oscar_evict_quantize_int4(shape: oscar_shape, src_kv, dst_seq, dst_pos, U, c
                               stream=None) -> None:
     """oscar_evict_quantize into a 4-bit pool (num_pages * Hk blocks of
     block_bytes_int4(shape) bytes); see include/oscar.h."""
-    import torch
-    n_tok = int(dst_seq.numel())
-    row = shape.num_kv_heads * 2 * shape.head_dim
-    _room(dst_pos, n_tok, "dst_pos")
-    _room(src_row, n_tok, "src_row")
-    _room(new_kv, n_tok * row, "new_kv")
-    _room(src_kv, int(src_kv.shape[0]) * row, "src_kv")
-    _room(page_table, batch * max_pages, "page_table")
-    _room(pool, num_pages * shape.num_kv_heads * block_bytes_int4(shape), "pool")
+    if _F32 is None:
+        _torch_names()
+    dev, n, hk, d = _current_device(), dst_seq.numel(), shape.num_kv_heads, shape.head_dim
+    rows, row = src_kv.shape[0], hk * 2 * d
     st = lib().oscar_evict_quantize_int4(
-        ctypes.byref(shape), n_tok, _dptr(src_kv, "src_kv", torch.bfloat16), int(src_kv.shape[0]),
-        _dptr(src_row, "src_row", torch.int32), _dptr(dst_seq, "dst_seq", torch.int32),
-        _dptr(dst_pos, "dst_pos", torch.int32), _dptr(new_kv, "new_kv", torch.bfloat16),
-        _dptr(U, "U", torch.float32), _dptr(clip, "clip", torch.float32), _dptr(pool, "pool", torch.uint8),
-        _dptr(page_table, "page_table", torch.int32), batch, max_pages, num_pages,
-        _dptr(dev_status, "dev_status", torch.int32), _stream_ptr(stream))
-    _check("oscar_evict_quantize_int4", st)
+        ctypes.byref(shape), n, _arg(src_kv, "src_kv", _BF16, rows * row, dev), rows,
+        _arg(src_row, "src_row", _I32, n, dev), _arg(dst_seq, "dst_seq", _I32, n, dev),
+        _arg(dst_pos, "dst_pos", _I32, n, dev), _arg(new_kv, "new_kv", _BF16, n * row, dev),
+        _arg(U, "U", _F32, row * d, dev), _arg(clip, "clip", _F32, hk * 2, dev),
+        _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, 4), dev),
+        _arg(page_table, "page_table", _I32, batch * max_pages, dev), batch, max_pages, num_pages,
+        _arg(dev_status, "dev_status", _I32, 1, dev), _stream_arg(stream, dev))
+    if st:
+        _check("oscar_evict_quantize_int4", st)
 
 
 def oscar_decode_workspace_bytes_int4(shape: oscar_shape, batch: int, max_pages: int) -> int:
@@ -595,28 +646,20 @@ def oscar_decode_attn_int4(shape: oscar_shape, q, bf16_kv, bf16_len, pool, page_
     """oscar_decode_attn over a 4-bit pool; out may be float32 or bfloat16 (see
     include/oscar.h).  ``workspace``: CUDA uint8 tensor of at least
     oscar_decode_workspace_bytes_int4(shape, batch, max_pages) bytes."""
-    import torch
-    B = int(q.shape[0])
-    _room(q, B * shape.num_q_heads * shape.head_dim, "q")
-    _room(bf16_kv, B * (shape.sink + shape.recent) * shape.num_kv_heads * 2 * shape.head_dim, "bf16_kv")
-    _room(bf16_len, B, "bf16_len")
-    _room(hist_len, B, "hist_len")
-    _room(page_table, B * max_pages, "page_table")
-    _room(pool, num_pages * shape.num_kv_heads * block_bytes_int4(shape), "pool")
-    _room(out, B * shape.num_q_heads * shape.head_dim, "out")
-    ws = ctypes.c_size_t(int(workspace.numel()))
+    kind = _out_type(out)
+    dev, B, hk, d = _current_device(), q.shape[0], shape.num_kv_heads, shape.head_dim
+    rows, slots = B * shape.num_q_heads * d, shape.sink + shape.recent
     st = lib().oscar_decode_attn_int4(
-        ctypes.byref(shape), B, _dptr(q, "q", torch.bfloat16), _dptr(bf16_kv, "bf16_kv", torch.bfloat16),
-        _dptr(bf16_len, "bf16_len", torch.int32), _dptr(pool, "pool", torch.uint8),
-        _dptr(page_table, "page_table", torch.int32), max_pages, num_pages, _dptr(hist_len, "hist_len", torch.int32),
-        _dptr(U, "U", torch.float32), ctypes.c_float(sm_scale), _dptr(out, "out"), _out_type(out),
-        _dptr(workspace, "workspace", torch.uint8), ctypes.byref(ws), _dptr(dev_status, "dev_status", torch.int32),
-        _stream_ptr(stream))
-    _check("oscar_decode_attn_int4", st)
-
-
-def _pool_block(shape: oscar_shape, bits: int) -> int:
-    return block_bytes_int4(shape) if bits == 4 else block_bytes(shape)
+        ctypes.byref(shape), B, _arg(q, "q", _BF16, rows, dev),
+        _arg(bf16_kv, "bf16_kv", _BF16, B * slots * hk * 2 * d, dev), _arg(bf16_len, "bf16_len", _I32, B, dev),
+        _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, 4), dev),
+        _arg(page_table, "page_table", _I32, B * max_pages, dev), max_pages, num_pages,
+        _arg(hist_len, "hist_len", _I32, B, dev), _arg(U, "U", _F32, hk * 2 * d * d, dev), sm_scale,
+        _arg(out, "out", out.dtype, rows, dev), kind, _arg(workspace, "workspace", _U8, 0, dev),
+        ctypes.byref(ctypes.c_size_t(workspace.numel())), _arg(dev_status, "dev_status", _I32, 1, dev),
+        _stream_arg(stream, dev))
+    if st:
+        _check("oscar_decode_attn_int4", st)
 
 
 def oscar_history_read(shape: oscar_shape, bits: int, seq, pos, pool, page_table, batch: int, max_pages: int,
@@ -624,17 +667,16 @@ def oscar_history_read(shape: oscar_shape, bits: int, seq, pos, pool, page_table
     """Stored tokens (seq, pos: int32 [n]) as rows out [n][Hk][2][d] (float32 or
     bfloat16) in the rotated domain; bits: 2 or 4, the pool's codes; see
     include/oscar.h."""
-    import torch
-    n = int(seq.numel())
-    _room(pos, n, "pos")
-    _room(page_table, batch * max_pages, "page_table")
-    _room(pool, num_pages * shape.num_kv_heads * _pool_block(shape, bits), "pool")
-    _room(out, n * shape.num_kv_heads * 2 * shape.head_dim, "out")
+    kind = _out_type(out)
+    dev, n, hk = _current_device(), seq.numel(), shape.num_kv_heads
     st = lib().oscar_history_read(
-        ctypes.byref(shape), bits, n, _dptr(seq, "seq", torch.int32), _dptr(pos, "pos", torch.int32),
-        _dptr(pool, "pool", torch.uint8), _dptr(page_table, "page_table", torch.int32), batch, max_pages, num_pages,
-        _dptr(out, "out"), _out_type(out), _dptr(dev_status, "dev_status", torch.int32), _stream_ptr(stream))
-    _check("oscar_history_read", st)
+        ctypes.byref(shape), bits, n, _arg(seq, "seq", _I32, n, dev), _arg(pos, "pos", _I32, n, dev),
+        _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, bits), dev),
+        _arg(page_table, "page_table", _I32, batch * max_pages, dev), batch, max_pages, num_pages,
+        _arg(out, "out", out.dtype, n * hk * 2 * shape.head_dim, dev), kind,
+        _arg(dev_status, "dev_status", _I32, 1, dev), _stream_arg(stream, dev))
+    if st:
+        _check("oscar_history_read", st)
 
 
 def oscar_history_gather(shape: oscar_shape, bits: int, pool, src_table, dst_table, keep, n_keep, num_pages: int,
@@ -642,35 +684,37 @@ def oscar_history_gather(shape: oscar_shape, bits: int, pool, src_table, dst_tab
     """The kept tokens (keep: int32 [B][stride] source positions, the first
     n_keep[b] of row b) of each history moved to positions 0, 1, ... of its
     row of dst_table (int32 [B][pages], fresh pages); see include/oscar.h."""
-    import torch
-    B = int(src_table.shape[0])
-    if dst_table.shape[0] != B or keep.shape[0] != B:
+    if _F32 is None:
+        _torch_names()
+    (B, smax), (B2, dmax), (B3, stride) = src_table.shape, dst_table.shape, keep.shape
+    if B2 != B or B3 != B:
         raise ValueError("src_table, dst_table and keep: one row per sequence")
-    _room(n_keep, B, "n_keep")
-    _room(pool, num_pages * shape.num_kv_heads * _pool_block(shape, bits), "pool")
-    _room(boost, num_pages * shape.num_kv_heads * BOOST_BLOCK_BYTES, "boost")
+    dev, hk = _current_device(), shape.num_kv_heads
     st = lib().oscar_history_gather(
-        ctypes.byref(shape), bits, B, _dptr(pool, "pool", torch.uint8), _dptr(boost, "boost", torch.uint8),
-        _dptr(src_table, "src_table", torch.int32), int(src_table.shape[1]), _dptr(dst_table, "dst_table", torch.int32),
-        int(dst_table.shape[1]), _dptr(keep, "keep", torch.int32), int(keep.shape[1]),
-        _dptr(n_keep, "n_keep", torch.int32), num_pages, _dptr(dev_status, "dev_status", torch.int32),
-        _stream_ptr(stream))
-    _check("oscar_history_gather", st)
+        ctypes.byref(shape), bits, B, _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, bits), dev),
+        _arg(boost, "boost", _U8, num_pages * hk * BOOST_BLOCK_BYTES, dev), _arg(src_table, "src_table", _I32, 0, dev),
+        smax, _arg(dst_table, "dst_table", _I32, 0, dev), dmax, _arg(keep, "keep", _I32, 0, dev), stride,
+        _arg(n_keep, "n_keep", _I32, B, dev), num_pages, _arg(dev_status, "dev_status", _I32, 1, dev),
+        _stream_arg(stream, dev))
+    if st:
+        _check("oscar_history_gather", st)
+
+
+_COPY_POOLS = ctypes.c_void_p * MAX_COPY_POOLS
 
 
 def oscar_pages_copy_device(page_bytes: int, src, dst, pools, num_pages: int, dev_status=None, stream=None) -> None:
     """Page src[i] copied to page dst[i] (int32 CUDA tensors) in every pool of
     the list (uint8 CUDA tensors of num_pages pages of page_bytes each) by
     one launch; see include/oscar.h."""
-    import torch
-    n = int(src.numel())
-    _room(dst, n, "dst")
-    ptrs = (ctypes.c_void_p * max(len(pools), 1))()
-    for i, t in enumerate(pools):
-        _room(t, num_pages * page_bytes, f"pools[{i}]")
-        ptrs[i] = _dptr(t, f"pools[{i}]", torch.uint8)
+    if _F32 is None:
+        _torch_names()
+    dev, n, need = _current_device(), src.numel(), num_pages * page_bytes
+    if len(pools) > MAX_COPY_POOLS:
+        raise ValueError(f"pools: {len(pools)}, at most {MAX_COPY_POOLS}")
     st = lib().oscar_pages_copy_device(
-        page_bytes, n, _dptr(src, "src", torch.int32), _dptr(dst, "dst", torch.int32),
-        ctypes.cast(ptrs, _P), len(pools), num_pages, _dptr(dev_status, "dev_status", torch.int32),
-        _stream_ptr(stream))
-    _check("oscar_pages_copy_device", st)
+        page_bytes, n, _arg(src, "src", _I32, n, dev), _arg(dst, "dst", _I32, n, dev),
+        _COPY_POOLS(*[_arg(t, "pools", _U8, need, dev) for t in pools]), len(pools), num_pages,
+        _arg(dev_status, "dev_status", _I32, 1, dev), _stream_arg(stream, dev))
+    if st:
+        _check("oscar_pages_copy_device", st)

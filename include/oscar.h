@@ -471,7 +471,10 @@ oscar_status oscar_decode_attn_boost(const oscar_shape* shape, int32_t batch, co
  *
  * oscar_evict_quantize_int4: oscar_evict_quantize into a 4-bit pool, with
  *   the same arguments.  Every decision (the clip threshold, s, z, the
- *   codes) is taken from compensated pairs of about 2^-44 relative error.
+ *   codes) is that of values within 2^-36 |x| of the exact rotated ones, so
+ *   codes and pairs match a float64 evaluation except that close to a
+ *   border.  Calls with many tokens (a prompt's history) rotate on tensor
+ *   cores and take the few open decisions again from exact sums.
  * oscar_decode_attn_int4: oscar_decode_attn over a 4-bit pool, with the
  *   same arguments and workspace convention, and `out` of type out_type:
  *   OSCAR_OUT_F32 (fp32, 16-byte aligned) or OSCAR_OUT_BF16 (bf16 [B][Hq][d],

@@ -222,6 +222,81 @@ def test_eviction_appends_into_the_ring_and_skips_bad_indices(B_):
     assert np.array_equal(dkv.view(torch.int16).cpu().numpy().view(np.uint16), kv)
 
 
+def evict_in_calls(rows, U, clip, pos, seq, table, g, per_call, src_row=None, new=None, kv=None):
+    """A fresh pool after evicting the tokens `per_call` at a time (None: in one call)."""
+    n, hk = len(pos), rows.shape[1]
+    pages = int(table.max()) + 1
+    pool = torch.full((pages * hk * I.block_bytes(4, g),), 0xA5, dtype=torch.uint8, device="cuda")
+    sh, dt = O.make_shape(hk, hk, quant_group=g), H.i32_t(table)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    src = rows if kv is None else kv
+    for a in range(0, n, per_call or n):
+        s = slice(a, a + (per_call or n))
+        part = src[s].contiguous() if src_row is None else src
+        O.oscar_evict_quantize_int4(sh, part, seq[s].contiguous(), pos[s].contiguous(), U, clip, pool, dt, table.shape[0], table.shape[1], pages,
+                                    src_row=None if src_row is None else src_row[s].contiguous(),
+                                    new_kv=None if new is None else new[s].contiguous(), dev_status=status)
+    return pool, int(status)
+
+
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("kind", ["outliers", "flat", "scales", "offset", "grid", "wide_U"])
+def test_many_tokens_at_once_give_the_same_bytes(kind, g):
+    """The kernel for many tokens and the one for few agree in every byte, on
+    values that put many decisions next to a border (equal values, grids,
+    subnormal scales) as well."""
+    hk, n = 4, 1200
+    gen = torch.Generator("cuda").manual_seed(g)
+    x = torch.randn(n, hk, 2, D, device="cuda", generator=gen)
+    U = torch.from_numpy(rotation(np.random.default_rng(g), hk)).cuda()
+    clip = torch.tensor([0.95, 1.0, 0.6, 0.99] * (hk // 2), device="cuda").reshape(hk, 2)
+    if kind == "outliers":
+        x[..., [5, 90]] *= 20
+    elif kind == "scales":
+        x *= torch.exp2(torch.randint(-40, 14, (n, 1, 1, 1), device="cuda", generator=gen).float())
+        x[7], x[8, :, :, 1:] = 0.0, 0.0
+    elif kind == "offset":                                 # one direction far larger than the rest: |z| over the range
+        x = x * 0.01 + U.sum(-1).unsqueeze(0)
+    elif kind == "grid":                                   # R^T of a few levels: ties and equal values
+        x = torch.randint(-2, 3, x.shape, device="cuda", generator=gen).float()
+        U = torch.eye(D, device="cuda").expand(hk, 2, D, D).contiguous()
+    elif kind == "wide_U":
+        U = (U * 37.5).contiguous()
+    x = x.bfloat16()
+    table = np.random.default_rng(1).permutation(21).astype(np.int32).reshape(1, 21)
+    pos, seq = H.i32_t(np.arange(n) + 5), H.i32_t(np.zeros(n))
+    few, st1 = evict_in_calls(x, U, clip, pos, seq, table, g, 31)
+    many, st2 = evict_in_calls(x, U, clip, pos, seq, table, g, None)
+    assert st1 == 0 and st2 == 0
+    assert torch.equal(few, many), int((few != many).sum())
+
+
+@pytest.mark.parametrize("n", [96, 97, 111, 112, 333])
+def test_many_tokens_scattered_with_append_and_bad_indices(n):
+    rng = np.random.default_rng(n)
+    hk, g, pages = 24, 32, 12                              # 48 vectors a token: one call of n is bulk, calls of 13 are not
+    table = rng.permutation(pages).astype(np.int32).reshape(2, 6)
+    at = rng.permutation(2 * 384)[:n]
+    seq, pos = (at // 384).astype(np.int32), (at % 384).astype(np.int32)
+    row = rng.permutation(2 * n)[:n].astype(np.int32)
+    seq[3], pos[5], row[11] = 2, 384, 2 * n                # each skipped; the third one's row is not touched either
+    kv, new = kv_bits(rng, 2 * n, hk), kv_bits(rng, n, hk)
+    U, clip = H.f32_t(rotation(rng, hk)), torch.full((hk, 2), 0.95, device="cuda")
+    pools, states, rows = [], [], []
+    for per_call in (13, None):
+        dkv = H.bf16_t(kv)
+        p, st = evict_in_calls(dkv, U, clip, H.i32_t(pos), H.i32_t(seq), table, g, per_call, src_row=H.i32_t(row), new=H.bf16_t(new), kv=dkv)
+        pools.append(p)
+        states.append(st)
+        rows.append(dkv.view(torch.int16).cpu().numpy().view(np.uint16))
+    assert states == [O.OSCAR_STATUS_BAD_POS] * 2
+    assert torch.equal(pools[0], pools[1])
+    want = kv.copy()
+    ok = np.arange(n) != 11
+    want[row[ok]] = new[ok]
+    assert np.array_equal(rows[0], want) and np.array_equal(rows[1], want)
+
+
 # ---------------------------------------------------------------------------
 # decode
 # ---------------------------------------------------------------------------

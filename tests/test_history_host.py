@@ -131,19 +131,53 @@ def test_copy_refusals(lib):
     assert copy(lib, page_bytes=1 << 30, n=1 << 20) == BAD  # more pieces than a launch counts
 
 
-def test_binding_refuses_host_tensors_and_short_arrays(lib):
+class Fake:
+    """What the binding looks at of a CUDA tensor."""
+
+    def __init__(self, *shape, dtype=None, device=0, contiguous=True, at=4096):
+        import torch
+        self.shape, self.dtype, self.is_cuda, self._d, self._c, self._at = shape, dtype or torch.int32, True, device, contiguous, at
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def is_contiguous(self):
+        return self._c
+
+    def get_device(self):
+        return self._d
+
+    def data_ptr(self):
+        return self._at
+
+
+def test_binding_refuses_wrong_tensors(lib, monkeypatch):
     torch = pytest.importorskip("torch")
-    i = torch.zeros(2, dtype=torch.int32)
-    with pytest.raises(TypeError):
-        O.oscar_pages_copy_device(64, i, i, [torch.zeros(256, dtype=torch.uint8)], 4)
+    monkeypatch.setattr(O, "_current_device", lambda: 0)
+    u8, i = torch.uint8, Fake(2)
+    O._torch_names()
+    monkeypatch.setattr(O, "_raw_stream", lambda d: 0)
+
+    def copy(src=i, dst=i, pools=(Fake(256, dtype=u8),), n=4):
+        O.oscar_pages_copy_device(64, src, dst, list(pools), n)
+
+    for bad, what in ((dict(src=torch.zeros(2, dtype=torch.int32)), TypeError), (dict(dst=[0, 1]), TypeError),
+                      (dict(dst=Fake(2, dtype=torch.int64)), TypeError), (dict(dst=Fake(1)), ValueError),
+                      (dict(dst=Fake(2, device=1)), ValueError), (dict(src=Fake(2, contiguous=False)), ValueError),
+                      (dict(pools=[Fake(255, dtype=u8)]), ValueError), (dict(pools=[Fake(256)]), TypeError),
+                      (dict(pools=[Fake(256, dtype=u8)] * 129), ValueError)):
+        with pytest.raises(what):
+            copy(**bad)
+    with pytest.raises(O.OscarError):                       # the library's own refusal: a pool at an odd address
+        copy(pools=[Fake(256, dtype=u8, at=4104)])
+    out = Fake(2, 8, 2, 128, dtype=torch.float32)
+    pool = Fake(8 * 10240, dtype=u8)
+    for bad, what in ((dict(out=Fake(2, 8, 2, 128, dtype=torch.float16)), TypeError), (dict(out=Fake(2, 8, 2, 127, dtype=torch.bfloat16)), ValueError),
+                      (dict(pool=Fake(8 * 10240 - 1, dtype=u8)), ValueError), (dict(pos=Fake(1)), ValueError), (dict(table=Fake(0)), ValueError)):
+        k = dict(out=out, pool=pool, pos=i, table=Fake(1)) | bad
+        with pytest.raises(what):
+            O.oscar_history_read(sh(), 4, i, k["pos"], k["pool"], k["table"], 1, 1, 1, k["out"])
     with pytest.raises(ValueError):
-        O.oscar_pages_copy_device(64, i, i[:1], [], 4)
-    with pytest.raises(ValueError):                         # the pool is shorter than its pages
-        O.oscar_history_read(sh(), 4, i, i, torch.zeros(16, dtype=torch.uint8), i, 1, 1, 1, torch.zeros(1))
-    with pytest.raises(ValueError):
-        O.oscar_history_gather(sh(), 4, torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(2, 1, dtype=torch.int32),
-                               torch.zeros(1, 1, dtype=torch.int32), torch.zeros(2, 1, dtype=torch.int32), i, 1)
-    assert O._out_type(torch.zeros(1)) == O.OSCAR_OUT_F32
-    with pytest.raises(TypeError):
-        O._out_type(torch.zeros(1, dtype=torch.float16))
-    assert np.int32(O.MAX_COPY_POOLS) == 128
+        O.oscar_history_gather(sh(), 4, pool, Fake(2, 1), Fake(1, 1), Fake(2, 1), i, 1)
+    assert O._out_type(torch.zeros(1)) == O.OSCAR_OUT_F32 and O._out_type(torch.zeros(1, dtype=torch.bfloat16)) == O.OSCAR_OUT_BF16
+    assert O.block_bytes_int4(sh()) == 10240 and O.block_bytes_int4(sh(quant_group=128)) == 8704
