@@ -463,6 +463,7 @@ struct HistoryGatherParams {
     const int32_t* n_keep;     // [batch]
     int32_t* status;
     int batch, hk, src_max_pages, dst_max_pages, keep_stride, num_pages, gshift, block_bytes, bits4;
+    int heads;                 // KV heads per thread block (set by the launch)
 };
 cudaError_t launch_history_gather(const HistoryGatherParams& p, cudaStream_t st);
 

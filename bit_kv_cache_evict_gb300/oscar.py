@@ -560,6 +560,8 @@ def _arg(t, what: str, dtype, need: int, dev: int):
     if t is None:
         return None
     try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= need and t.is_contiguous():
+            return t.data_ptr()
         if not t.is_cuda:
             raise TypeError(f"{what}: expected a CUDA tensor")
         if t.dtype is not dtype:
@@ -568,9 +570,7 @@ def _arg(t, what: str, dtype, need: int, dev: int):
             raise ValueError(f"{what}: must be contiguous")
         if t.numel() < need:
             raise ValueError(f"{what}: {t.numel()} elements, {need} are needed")
-        if t.get_device() != dev:
-            raise ValueError(f"{what}: on device {t.get_device()}, the current device is {dev}")
-        return t.data_ptr()
+        raise ValueError(f"{what}: on device {t.get_device()}, the current device is {dev}")
     except AttributeError:
         raise TypeError(f"{what}: expected a CUDA tensor") from None
 
