@@ -68,11 +68,11 @@ static int tail_pages_of(int pps) { return pps > kShortItemPages ? 2 * kShortIte
 
 struct WsLayout {
     size_t counter, item_start, item_start2, qfrag, qsum, qkinv, qrot, part, bf_part, total;
-    int NT, pps, tail_pg, part_stride;
+    int NT, pps, tail_pg, part_stride, part_shift;
     int64_t max_items;   // split-K items at most (int64: batch x KV heads x splits can exceed int32)
 };
 
-static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages) {
+static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bits) {
     WsLayout w{};
     const int G = s->num_q_heads / s->num_kv_heads, hk = s->num_kv_heads;
     w.NT = (G + 3) / 4;
@@ -80,6 +80,11 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages) {
     w.part_stride = (int)round_up((size_t)G * (kD + 2), 4);
     w.tail_pg = tail_pages_of(w.pps);
     w.max_items = (int64_t)batch * hk * ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages);
+    w.part_shift = 0;
+    if (bits == 4) {  // items of at least pps pages, or at most one per thread block of any size
+        w.max_items += kMaxBlocks4;
+        w.part_shift = 2;
+    }
     size_t off = 0;
     w.counter = off;
     off += 256;
@@ -96,7 +101,7 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages) {
     w.qrot = off;
     off = round_up(off + (size_t)batch * hk * w.NT * 4 * kD * 4, 256);
     w.part = off;
-    off = round_up(off + (size_t)w.max_items * w.part_stride * 4, 256);
+    off = round_up(off + ((size_t)w.max_items << w.part_shift) * w.part_stride * 4, 256);
     w.bf_part = off;
     off = round_up(off + (size_t)batch * hk * bf16_items(s) * w.part_stride * 4, 256);
     w.total = off;
@@ -307,9 +312,10 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (batch < 0 || max_pages <= 0 || num_pages < 0 || !ws_bytes) return OSCAR_ERR_INVALID_ARG;
-    const WsLayout w = ws_layout(shape, batch, max_pages);
+    const WsLayout w = ws_layout(shape, batch, max_pages, bits);
     // item counts, item offsets and partial indices are int32 on the device
-    if (w.max_items > INT32_MAX || (double)w.max_items * w.part_stride > 4.0e9) return OSCAR_ERR_INVALID_ARG;
+    if (w.max_items << w.part_shift > INT32_MAX || (double)w.max_items * w.part_stride > 4.0e9)
+        return OSCAR_ERR_INVALID_ARG;
     if (!workspace) {
         *ws_bytes = w.total;
         return OSCAR_OK;
@@ -350,10 +356,14 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.nslot = shape->sink + shape->recent;
     p.bf_items = bf16_items(shape);
     {   // merge warps per row: more when rows are few and split-K partials many
-        const int splits = (max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages;
+        const int splits = ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages) << w.part_shift;
         const int rows = batch * p.G;
         int wpr = 1;
-        while (wpr < 8 && splits > 16 * wpr && rows * wpr < 4096) wpr *= 2;
+        // (4-bit, four partials per item: no more blocks than two per SM, each stages U_V)
+        if (bits == 4)
+            while (wpr < 8 && splits > 16 * wpr && (int64_t)rows * p.hk * wpr <= 4 * 304) wpr *= 2;
+        else
+            while (wpr < 8 && splits > 16 * wpr && rows * wpr < 4096) wpr *= 2;
         p.merge_wpr = wpr;
     }
     p.max_pages = max_pages;
@@ -365,6 +375,7 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.pps = w.pps;
     p.tail_pg = w.tail_pg;
     p.part_stride = w.part_stride;
+    p.part_shift = w.part_shift;
     p.qscale = sm_scale * kLog2e;
     p.codebook = codebook;
     p.boost = boost;

@@ -65,6 +65,57 @@ __global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(DecodeParams p) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) pdl_wait();
 }
 
+// Pages per long item and in short tail items of a 4-bit history, from the
+// lengths as they are (one warp).  The kernel's time is that of its busiest
+// block, and an item costs its pages and about one more for its start and
+// end.  If items of one size, one for each block at most, leave little idle
+// (equal lengths, or few sequences), they are taken: 8 x 508 pages of eight KV heads:
+// 448 items of 73 pages on 456 blocks.  Otherwise items of a quarter of a
+// block's share, with short ones queued last.  At most 64 items per
+// sequence and KV head in the first form: the merge reads four partials of each.
+__device__ __forceinline__ void plan4(const DecodeParams& p, int& pps, int& tail_pg) {
+    const int lane = threadIdx.x & 31;
+    auto pages_of = [&](int b) {
+        const int h = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+        return (h + kPage - 1) / kPage;
+    };
+    long total = 0;
+    int most = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const int n = pages_of(b);
+        total += n;
+        most = max(most, n);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        total += __shfl_xor_sync(kFull, total, m);
+        most = max(most, __shfl_xor_sync(kFull, most, m));
+    }
+    total *= p.hk;
+    auto items_at = [&](int size) {  // items of every sequence and KV head at this size
+        long n = 0;
+        for (int b = lane; b < p.B; b += 32) n += (pages_of(b) + size - 1) / size;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(kFull, n, m);
+        return n * p.hk;
+    };
+    int lo = max(4, (most + 63) / 64), hi = 256;  // four pages: one for each consumer warp
+    if (lo <= hi && items_at(hi) <= p.blocks4) {
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (items_at(mid) <= p.blocks4) hi = mid;
+            else lo = mid + 1;
+        }
+        if (lo <= 32 || (long)lo * p.blocks4 <= total + total / 4) {
+            pps = lo;
+            tail_pg = 0;
+            return;
+        }
+    }
+    pps = (int)min(256l, max((long)p.pps, total / (4 * p.blocks4)));
+    tail_pg = pps > kShortItemPages ? 2 * kShortItemPages : 0;
+}
+
 __device__ __forceinline__ void prep_body(const DecodeParams& p) {
     extern __shared__ __align__(16) float psm[];
     float* Us = psm;                       // [a][k] = U_K[a][k]
@@ -73,6 +124,14 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p) {
     if (blockIdx.x == gridDim.x - 1) {  // plan
         if (blockIdx.y != 0 || warp != 0) return;
         // long items of every sequence first, then the short tail items
+        int pps = p.pps, tail_pg = p.tail_pg;
+        if (p.bits4) {
+            plan4(p, pps, tail_pg);
+            if (lane == 0) {
+                p.counter[kPlanPps] = pps;
+                p.counter[kPlanTail] = tail_pg;
+            }
+        }
         int run_long = 0, run_short = 0;
         if (lane == 0) {
             p.item_start[0] = 0;
@@ -89,7 +148,7 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p) {
                     report(p.status, OSCAR_STATUS_BAD_POS);
                     h = min(max(h, 0), p.max_pages * kPage);
                 }
-                const SeqSplits sp = seq_splits((h + kPage - 1) / kPage, p.pps, p.tail_pg);
+                const SeqSplits sp = seq_splits((h + kPage - 1) / kPage, pps, tail_pg);
                 n_long = sp.n_long * p.hk;
                 n_short = sp.n_short * p.hk;
             }
@@ -1652,9 +1711,10 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
         const int s0 = __ldg(p.item_start + b), t0 = __ldg(p.item_start2 + b);
         n_long = (__ldg(p.item_start + b + 1) - s0) / p.hk;
         const int n_short = (__ldg(p.item_start2 + b + 1) - t0) / p.hk;
-        splits = n_long + n_short;
-        first = s0 + kv * n_long;
-        first2 = __ldg(p.item_start + p.B) + t0 + kv * n_short - n_long;
+        splits = (n_long + n_short) << p.part_shift;
+        first = (s0 + kv * n_long) << p.part_shift;
+        first2 = (__ldg(p.item_start + p.B) + t0 + kv * n_short - n_long) * (1 << p.part_shift);  // (may be negative)
+        n_long <<= p.part_shift;
     }
     pdl_wait();  // partials of int2_kernel and bf16_kernel
     const int r5 = bitrev5(lane);
@@ -1922,7 +1982,8 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
         if (e != cudaSuccess) return e;
     }
     DecodeParams p = pin;
-    {   // Fewer history pages (at most) than two waves of minimum items on
+    if (p.bits4) p.blocks4 = std::min(int4_blocks_per_sm(p.NT, p.gshift) * at.sms, kMaxBlocks4);
+    if (!p.bits4) {  // Fewer history pages (at most) than two waves of minimum items on
         // the INT2 grid (a batch of one or two long sequences): items of one
         // wave instead, so that no block takes a second item while others
         // idle.  Longer items only lower the item count the workspace was
@@ -1947,7 +2008,7 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
     if ((e = launch_pdl(prep_kernel, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
     if (ev_int2_start && (e = cudaEventRecord(ev_int2_start, st)) != cudaSuccess) return e;
     if (p.bits4)
-        e = launch_int4(p, st, dev, at.sms);
+        e = launch_int4(p, st, dev);
     else if (p.codebook)  // Lloyd-Max levels
         e = (p.NT == 1) ? launch_int2<1, true>(p, st, at.sms, at.setl) : launch_int2<2, true>(p, st, at.sms, at.setl2);
     else if (p.boost)  // K channel boost

@@ -4,23 +4,25 @@
 // query fragments and plan before, un-rotation and log-sum-exp merge after.
 //
 // The mathematics.  A stored value is s c + z (c in 0..15, one fp16 pair per
-// token and quantisation group).  With the codes centred, c' = c - 8 and
-// z' = z + 8 s, and b the 32-position blocks of a vector:
-//   logit_t = sum_b s_tb D_tb + z'_tb Q_b,  D_tb = sum_{j in b} c'_tj q'_j,
-//                                           Q_b = sum_{j in b} q'_j;
-//   o'_j    = sum_t W_tb(j) c'_tj + sum_t p_t z'_tb,  W_tb = p_t s_tb.
+// token and quantisation group b):
+//   logit_t = sum_b s_tb D_tb + z_tb Q_b,  D_tb = sum_{j in b} c_tj q'_j,
+//                                          Q_b = sum_{j in b} q'_j;
+//   o'_j    = sum_t W_tb(j) (c_tj - 8) + sum_t p_t z'_tb,  W_tb = p_t s_tb,
+//                                          z' = z + 8 s.
 // D and the W products are tensor-core products (mma.sync m16n8k16, fp16 in,
 // fp32 sums) with the codes as the A operand, exact in fp16; q' (times 2^e,
 // from prep) and W (times 2^w) enter as fp16 high and low parts, 22 bits.
-// The sums stay centred, so that a flat softmax over a long history does not
-// subtract two sums that are far larger than their difference (uncentred
-// codes give sums of 7.5 s against values of 4.6 s).
+// The V codes are centred so that a flat softmax over a long history does
+// not subtract two sums far larger than their difference (7.5 s against the
+// values' 4.6 s, both times sum p, where the result is of the order of 4.6 s
+// sqrt(sum p^2)), and their products are summed page by page (page_values).
+// A logit has 128 terms and no such difference: K codes stay as they are.
 //
-// Operands.  A 16-bit pattern 0x6400 | c is the fp16 1024 + c and
+// Operands of V.  A 16-bit pattern 0x6400 | c is the fp16 1024 + c and
 // 0x6400 | 16 c is 1024 + 16 c: one AND-OR on the code word in place and one
 // fp16 add (-1032) or fused multiply-add (/ 16, -72) give c - 8 exactly; a
 // shift by 8 serves the other two nibbles of each half: nine instructions
-// for a word of eight codes, five of them on the integer pipe.
+// for a word of eight codes, against seven for the K codes' in_place4.
 //
 // 2^w: W is scaled by a power of two per warp and item, from the largest V
 // scale seen so far, so that its fp16 parts keep 22 bits whatever the
@@ -42,33 +44,42 @@ struct PageInfo {  // one per page of a consumer warp; 16 bytes
     int item, b, kv, valid_flags;
 };
 
-template <int NT>
+// A probability or V-scale row of the value phase: the page's 64 tokens in 16
+// groups of four; k-step m of lane quad member tq covers group 4 tq + m (whose V
+// codes are bytes 16 tq + 4 m .. + 3 of every plane, so that one 16-byte load
+// per plane serves the four k-steps).  Group q lies at 20 (q / 4) + 4 (q % 4): the
+// skew of 20 keeps the lanes of a load on distinct banks and every k-step or
+// tile at a constant offset from the lane's own place; inside a group the
+// order is pv_slot (tokens 0, 2 | 1, 3: the two B-operand pairs).
+constexpr int kRow4 = 80;
+__device__ __forceinline__ int row_pos(int t) { return 20 * (t >> 4) + 4 * ((t >> 2) & 3) + pv_slot(t & 3); }
+
+template <int NT, int GS>
 struct Int4Smem {
     static constexpr int G4 = NT * 4;
-    // halves per consumer warp: three (one being read, two in flight) for up
-    // to four heads; for eight heads the larger scratch of three blocks per
-    // SM leaves two
-    static constexpr int NSW = NT == 1 ? 3 : 2;
-    // per-warp scratch.  Logit phase: K s [64] float4 | K z' [64] float4.
-    // Value phase: V s 2^w [4][kPvRow] (token order pv_pos) | V z' [64]
-    // float4, then P [G4][kPvRow] over the z'.  Item end: the warp's state
-    // [G4][kD + 2].
-    static constexpr int kWVs = 0, kWVz = 4 * kPvRow * 4, kWP = kWVz;
-    static constexpr int kWarp1 = 2 * kPage * 16, kWarp2 = kWP + G4 * kPvRow * 4, kWarp3 = G4 * (kD + 2) * 4;
-    static constexpr int kWarpBytes0 = kWarp1 > kWarp2 ? kWarp1 : kWarp2;
-    static constexpr int kWarpBytes = kWarpBytes0 > kWarp3 ? kWarpBytes0 : kWarp3;
+    // halves per consumer warp: three (one being read, two in flight); with
+    // the larger scratch of eight heads two where three blocks share an SM,
+    // four where two do
+    static constexpr int kBlocks = int4_blocks_per_sm(NT, GS);
+    static constexpr int NSW = NT == 1 ? 3 : kBlocks == 3 ? 2 : 4;
+    // per-warp scratch (NB groups per vector).  Logit phase: K s [64][NB] | K z
+    // [64][NB].  Value phase: V s 2^w [NB][kRow4] (token order row_pos) | V z'
+    // [64][NB], then P [G4][kRow4] over the z'.
+    static constexpr int kWVs = 0, kWVz = 4 * kRow4 * 4, kWP = kWVz;
+    static constexpr int kWarp1 = 2 * kPage * 16, kWarp2 = kWP + G4 * kRow4 * 4;
+    static constexpr int kWarpBytes = kWarp1 > kWarp2 ? kWarp1 : kWarp2;
     static constexpr int kStage = 0;
     static constexpr int kInfo = kStage + kConsumerWarps * NSW * kHalfMax;  // [4][2] PageInfo
     static constexpr int kWarp = kInfo + kConsumerWarps * 2 * 16;
     // two item buffers: q' fragments [NT][8][32] uint2, group sums [G4] float4, 2^-e
     static constexpr int kQbSum = NT * 8 * 32 * 8, kQbKinv = kQbSum + G4 * 16, kQbBytes = kQbKinv + 16;
     static constexpr int kQb = kWarp + kConsumerWarps * kWarpBytes;
-    // full / empty per half, qfull[2], qempty[2], merge
+    // full / empty per half, qfull[2], qempty[2]
     static constexpr int kBars = kQb + 2 * kQbBytes;
-    static constexpr int kBytes = kBars + (2 * kConsumerWarps * NSW + 5) * 8;
+    static constexpr int kBytes = kBars + (2 * kConsumerWarps * NSW + 4) * 8;
     static_assert(kWarp % 16 == 0 && kWarpBytes % 16 == 0 && kQb % 16 == 0 && kQbBytes % 16 == 0 && kBars % 8 == 0,
                   "16-byte vectors and bulk copies");
-    static_assert(3 * (kBytes + 1024) <= 228 * 1024, "three blocks per SM");
+    static_assert(kBlocks * (kBytes + 1024) <= 228 * 1024, "blocks per SM");
 };
 
 // Ring position: half `slot` of NSW, in its `phase`-th use.
@@ -103,63 +114,93 @@ __device__ __forceinline__ void unpack4(uint32_t x, uint32_t (&r)[4]) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(n3), "r"(0x2C002C00u), "r"(0xD480D480u));
 }
 
-// The (s, z) words of token t of a half, one per 32-position block.
-template <int GS>
-__device__ __forceinline__ void load_pairs(const uint8_t* half, int t, uint32_t (&w)[4]) {
-    const uint8_t* at = half + kCodes4 + t * (16 >> GS);
-    if constexpr (GS == 0) {
-        const uint4 v = *reinterpret_cast<const uint4*>(at);
-        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else if constexpr (GS == 1) {
-        const uint2 v = *reinterpret_cast<const uint2*>(at);
-        w[0] = w[1] = v.x; w[2] = w[3] = v.y;
+// N consecutive floats of shared memory (N = 1, 2, 4; aligned to them).
+template <int N>
+__device__ __forceinline__ void load_n(const float* at, float (&v)[N]) {
+    if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(at);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else if constexpr (N == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(at);
+        v[0] = x.x; v[1] = x.y;
     } else {
-        w[0] = w[1] = w[2] = w[3] = *reinterpret_cast<const uint32_t*>(at);
+        v[0] = *at;
     }
 }
-__device__ __forceinline__ void load_pairs(const uint8_t* half, int t, int gshift, uint32_t (&w)[4]) {
-    switch (gshift) {  // warp-uniform
-        case 0: load_pairs<0>(half, t, w); break;
-        case 1: load_pairs<1>(half, t, w); break;
-        default: load_pairs<2>(half, t, w); break;
+template <int N>
+__device__ __forceinline__ void store_n(float* at, const float (&v)[N]) {
+    if constexpr (N == 4) *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+    else if constexpr (N == 2) *reinterpret_cast<float2*>(at) = make_float2(v[0], v[1]);
+    else *at = v[0];
+}
+
+// The K codes stay uncentred and in place: a 16-bit pattern below 0x0400 is an
+// fp16 of value pattern 2^-24, so a nibble at bits 4-7 reads c 2^-20; three
+// shifts and four ANDs for eight codes.
+constexpr float kInPlaceUp = 1048576.f;  // 2^20
+__device__ __forceinline__ void in_place4(uint32_t x, uint32_t (&r)[4]) {
+    r[0] = (x << 4) & 0x00f000f0u;
+    r[1] = x & 0x00f000f0u;
+    r[2] = (x >> 4) & 0x00f000f0u;
+    r[3] = (x >> 8) & 0x00f000f0u;
+}
+
+// The (s, z) words of token t of a half, one per quantisation group.
+template <int NB>
+__device__ __forceinline__ void load_pairs(const uint8_t* half, int t, uint32_t (&w)[NB]) {
+    const uint8_t* at = half + kCodes4 + t * 4 * NB;
+    if constexpr (NB == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (NB == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(at);
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
     }
 }
 
 __device__ __forceinline__ float pow2_bits(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// State of one consumer warp inside an item.
-template <int NT>
+// State of one consumer warp inside an item.  NB = 4 >> GS quantisation groups
+// per vector, of 4 / NB 32-position blocks each.
+template <int NT, int GS>
 struct WarpState {
-    float m_run[NT], l_run[NT], zacc[NT][4];  // per head of the lane: max, sum, sum p z' per block (lane partials)
+    float m_run[NT], l_run[NT], zacc[NT][4 >> GS];  // per head of the lane: max, sum, sum p z' per group (lane partials)
     // [M tile][row gID: columns 2tq, 2tq+1; row gID+8]; up to four heads: columns = (hi, lo) of head tq; eight: heads 2tq, 2tq+1
     float acc[8][4];
-    int wexp;                                  // 2^wexp scales W; kNoScale before the first page
+    int wexp;                                       // 2^wexp scales W; kNoScale before the first page
 };
 constexpr int kNoScale = 64;
 
 // K half of a page: logits (base 2) of the lane's tokens 16m + gID and
 // 16m + gID + 8.  Up to four heads: lg[m][0], lg[m][1] = the two tokens of
 // head tq; eight heads: (token a, heads 2tq, 2tq+1), (token b, the same).
-template <int NT, bool FULL>
+template <int NT, int GS, bool FULL>
 __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint8_t* wbuf, const uint2* qf,
-                                            const float4 (&qsv)[NT], float kq, int gshift, float (&lg)[4][2 * NT]) {
+                                            const float (&qsv)[NT][4 >> GS], float kq, float (&lg)[4][2 * NT]) {
+    constexpr int NB = 4 >> GS;
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
-    float4* ksS = reinterpret_cast<float4*>(wbuf);
-    float4* kzS = ksS + kPage;
+    float* ksS = reinterpret_cast<float*>(wbuf);  // [64][NB]
+    float* kzS = ksS + kPage * NB;
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
         const int t = lane + 32 * it;
-        float4 sv = make_float4(0.f, 0.f, 0.f, 0.f), zv = sv;
+        float sv[NB], zv[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sv[b] = zv[b] = 0.f;
         if (FULL || t < valid) {
-            uint32_t w[4];
-            load_pairs(half, t, gshift, w);
-            const float s[4] = {half_lo(w[0]), half_lo(w[1]), half_lo(w[2]), half_lo(w[3])};
-            sv = make_float4(s[0] * kq, s[1] * kq, s[2] * kq, s[3] * kq);
-            zv = make_float4(fmaf(8.f, s[0], half_hi(w[0])), fmaf(8.f, s[1], half_hi(w[1])),
-                             fmaf(8.f, s[2], half_hi(w[2])), fmaf(8.f, s[3], half_hi(w[3])));
+            uint32_t w[NB];
+            load_pairs<NB>(half, t, w);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float s = half_lo(w[b]);
+                sv[b] = s * (kq * kInPlaceUp);
+                zv[b] = half_hi(w[b]);
+            }
         }
-        ksS[t] = sv;
-        kzS[t] = zv;
+        store_n<NB>(ksS + t * NB, sv);
+        store_n<NB>(kzS + t * NB, zv);
     }
     __syncwarp();
 #pragma unroll
@@ -171,57 +212,48 @@ __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint
         const uint4 xa = *reinterpret_cast<const uint4*>(half + ta * (kD / 2) + 16 * tq);
         const uint4 xb = *reinterpret_cast<const uint4*>(half + (ta + 8) * (kD / 2) + 16 * tq);
         const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-        float acc[4][4];
+        float acc[NB][4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
             uint32_t ra[4], rb[4];
-            unpack4(wa[b], ra);
-            unpack4(wb[b], rb);
+            in_place4(wa[b], ra);
+            in_place4(wb[b], rb);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {  // eight heads: the high, then the low parts
                     const uint2 q = qf[(nt * 8 + 2 * b + h) * 32 + lane];
-                    mma_f16_16816(acc[b], ra[2 * h], rb[2 * h], ra[2 * h + 1], rb[2 * h + 1], q.x, q.y);
+                    mma_f16_16816(acc[b >> GS], ra[2 * h], rb[2 * h], ra[2 * h + 1], rb[2 * h + 1], q.x, q.y);
                 }
         }
-        const float4 sA = ksS[ta], sB = ksS[ta + 8], zA = kzS[ta], zB = kzS[ta + 8];
-        const float sa[4] = {sA.x, sA.y, sA.z, sA.w}, za[4] = {zA.x, zA.y, zA.z, zA.w};
-        const float sb[4] = {sB.x, sB.y, sB.z, sB.w}, zb[4] = {zB.x, zB.y, zB.z, zB.w};
+        float sa[NB], za[NB], sb[NB], zb[NB];
+        load_n<NB>(ksS + ta * NB, sa);
+        load_n<NB>(ksS + (ta + 8) * NB, sb);
+        load_n<NB>(kzS + ta * NB, za);
+        load_n<NB>(kzS + (ta + 8) * NB, zb);
         const bool va = FULL || ta < valid, vb = FULL || ta + 8 < valid;
-        if constexpr (NT == 1) {
-            const float qg[4] = {qsv[0].x, qsv[0].y, qsv[0].z, qsv[0].w};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
             float x = 0.f, y = 0.f;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                x = fmaf(sa[b], acc[b][0] + acc[b][1], fmaf(za[b], qg[b], x));
-                y = fmaf(sb[b], acc[b][2] + acc[b][3], fmaf(zb[b], qg[b], y));
+            for (int b = 0; b < NB; ++b) {
+                x = fmaf(sa[b], NT == 1 ? acc[b][0] + acc[b][1] : acc[b][j], fmaf(za[b], qsv[j][b], x));
+                y = fmaf(sb[b], NT == 1 ? acc[b][2] + acc[b][3] : acc[b][2 + j], fmaf(zb[b], qsv[j][b], y));
             }
-            lg[m][0] = va ? x : -INFINITY;
-            lg[m][1] = vb ? y : -INFINITY;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float qg[4] = {qsv[j].x, qsv[j].y, qsv[j].z, qsv[j].w};
-                float x = 0.f, y = 0.f;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    x = fmaf(sa[b], acc[b][j], fmaf(za[b], qg[b], x));
-                    y = fmaf(sb[b], acc[b][2 + j], fmaf(zb[b], qg[b], y));
-                }
-                lg[m][j] = va ? x : -INFINITY;
-                lg[m][2 + j] = vb ? y : -INFINITY;
-            }
+            lg[m][j] = va ? x : -INFINITY;
+            lg[m][NT == 1 ? 1 : 2 + j] = vb ? y : -INFINITY;
         }
     }
 }
 
 // Online softmax of a page's logits: lg becomes p, l_run advances, alpha is
 // the factor that the older sums take.  Returns whether any lane's is not 1.
-template <int NT>
-__device__ __forceinline__ bool page_softmax(float (&lg)[4][2 * NT], WarpState<NT>& st, float (&alpha)[NT]) {
+template <int NT, int GS>
+__device__ __forceinline__ bool page_softmax(float (&lg)[4][2 * NT], WarpState<NT, GS>& st, float (&alpha)[NT]) {
     bool any = false;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {  // j: token pair entries (NT == 1: 0 and 1; NT == 2: j and 2 + j)
@@ -253,26 +285,27 @@ __device__ __forceinline__ bool page_softmax(float (&lg)[4][2 * NT], WarpState<N
 
 // V half of a page: the scales, the rescaling of the sums, sum p z', and the
 // products W . (c - 8).
-template <int NT, bool FULL>
+template <int NT, int GS, bool FULL>
 __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint8_t* wbuf, const float (&p)[4][2 * NT],
-                                            const float (&alpha)[NT], bool any, int gshift, const SplitSel& take_lo,
-                                            WarpState<NT>& st) {
-    using SM = Int4Smem<NT>;
+                                            const float (&alpha)[NT], bool any, const SplitSel& take_lo,
+                                            WarpState<NT, GS>& st) {
+    using SM = Int4Smem<NT, GS>;
+    constexpr int NB = 4 >> GS;
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
-    float* vsS = reinterpret_cast<float*>(wbuf + SM::kWVs);
-    float4* vzS = reinterpret_cast<float4*>(wbuf + SM::kWVz);
+    float* vsS = reinterpret_cast<float*>(wbuf + SM::kWVs);  // [NB][kRow4]
+    float* vzS = reinterpret_cast<float*>(wbuf + SM::kWVz);  // [64][NB]
     float* pS = reinterpret_cast<float*>(wbuf + SM::kWP);
     // -- pairs; the largest scale of the page picks 2^w: s 2^w < 2^14
-    uint32_t w[2][4];
+    uint32_t w[2][NB];
     uint32_t smax = 0;
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
         const int t = lane + 32 * it;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) w[it][b] = 0u;
-        if (FULL || t < valid) load_pairs(half, t, gshift, w[it]);
+        for (int b = 0; b < NB; ++b) w[it][b] = 0u;
+        if (FULL || t < valid) load_pairs<NB>(half, t, w[it]);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) smax = max(smax, w[it][b] & 0x7fffu);
+        for (int b = 0; b < NB; ++b) smax = max(smax, w[it][b] & 0x7fffu);
     }
     smax = __reduce_max_sync(kFull, smax);
     const int wexp = 13 - (max((int)(smax >> 10), 1) - 15);
@@ -285,7 +318,7 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) st.zacc[j][b] *= alpha[j];
+            for (int b = 0; b < NB; ++b) st.zacc[j][b] *= alpha[j];
         // column 2tq + e: up to four heads, both columns belong to head tq; eight: heads 2tq, 2tq + 1
         const float f0 = alpha[0] * down, f1 = alpha[NT - 1] * down;
 #pragma unroll
@@ -299,15 +332,15 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
     const float up = pow2_bits(st.wexp);
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
-        const int t = lane + 32 * it, ps = pv_pos(t);
-        float s[4], z[4];
+        const int t = lane + 32 * it, ps = row_pos(lane) + 40 * it;
+        float z[NB];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            s[b] = half_lo(w[it][b]);
-            z[b] = fmaf(8.f, s[b], half_hi(w[it][b]));
-            vsS[b * kPvRow + ps] = s[b] * up;
+        for (int b = 0; b < NB; ++b) {
+            const float s = half_lo(w[it][b]);
+            z[b] = fmaf(8.f, s, half_hi(w[it][b]));
+            vsS[b * kRow4 + ps] = s * up;
         }
-        vzS[t] = make_float4(z[0], z[1], z[2], z[3]);
+        store_n<NB>(vzS + t * NB, z);
     }
     __syncwarp();
     // -- sum p z'
@@ -315,62 +348,73 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
     for (int m = 0; m < 4; ++m) {
         if (!FULL && 16 * m >= valid) continue;
         const int ta = 16 * m + gID;
-        const float4 zA = vzS[ta], zB = vzS[ta + 8];
+        float zA[NB], zB[NB];
+        load_n<NB>(vzS + ta * NB, zA);
+        load_n<NB>(vzS + (ta + 8) * NB, zB);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const float pa = p[m][j], pb = p[m][NT == 1 ? 1 : 2 + j];
-            st.zacc[j][0] = fmaf(pa, zA.x, fmaf(pb, zB.x, st.zacc[j][0]));
-            st.zacc[j][1] = fmaf(pa, zA.y, fmaf(pb, zB.y, st.zacc[j][1]));
-            st.zacc[j][2] = fmaf(pa, zA.z, fmaf(pb, zB.z, st.zacc[j][2]));
-            st.zacc[j][3] = fmaf(pa, zA.w, fmaf(pb, zB.w, st.zacc[j][3]));
-        }
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                st.zacc[j][b] = fmaf(p[m][j], zA[b], fmaf(p[m][NT == 1 ? 1 : 2 + j], zB[b], st.zacc[j][b]));
     }
     __syncwarp();  // z' read: P takes its place
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            float* row = pS + (NT == 1 ? tq : 2 * tq + j) * kPvRow;
-            row[pv_pos(16 * m + gID)] = p[m][j];
-            row[pv_pos(16 * m + gID + 8)] = p[m][NT == 1 ? 1 : 2 + j];
+            float* row = pS + (NT == 1 ? tq : 2 * tq + j) * kRow4 + row_pos(gID) + 20 * m;
+            row[0] = p[m][j];
+            row[8] = p[m][NT == 1 ? 1 : 2 + j];
         }
     __syncwarp();
     // -- products: M tile mt = planes 8 mt + gID (rows gID: position
     //    16 mt + 2 gID, rows gID + 8: the next one), k-step m = token group
-    //    4 tq + m; two blocks (four M tiles) at a time
+    //    4 tq + m.  W of group b and k-step m: B registers (b0, b1), eight
+    //    heads also their low parts
+    auto weights = [&](int b, int m, uint32_t (&r)[2 * NT]) {
+        const int chunk = 20 * tq + 4 * m;
+        const float4 pp = *reinterpret_cast<const float4*>(pS + (NT == 1 ? gID >> 1 : gID) * kRow4 + chunk);
+        const float4 sg = *reinterpret_cast<const float4*>(vsS + b * kRow4 + chunk);
+        const float2 p0 = make_float2(pp.x, pp.y), p1 = make_float2(pp.z, pp.w);
+        const float2 s0 = make_float2(sg.x, sg.y), s1 = make_float2(sg.z, sg.w);
+        if constexpr (NT == 1) {
+            r[0] = split_w_pair_f16(p0, s0, take_lo);
+            r[1] = split_w_pair_f16(p1, s1, take_lo);
+        } else {
+            split_both(mul2(p0, s0), r[0], r[2]);
+            split_both(mul2(p1, s1), r[1], r[3]);
+        }
+    };
+    // One block (two M tiles) at a time, summed over the page from zero and then
+    // added to the running sums in fp32: the tensor core truncates its
+    // accumulator at every step, always toward zero, which over the
+    // hundreds of steps of an item shrinks a flat softmax's small result by
+    // 10^-5; four steps from zero and one rounded addition do not.
     const uint8_t* vb = half + gID * kPage + 16 * tq;
+    uint32_t r[4][2 * NT];  // the block's group's W
 #pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {
-        uint4 v4[4];
+    for (int b = 0; b < 4; ++b) {
+        if (GS == 0 || (b & ((1 << GS) - 1)) == 0)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v4[k] = *reinterpret_cast<const uint4*>(vb + (4 * hb + k) * 8 * kPage);
+            for (int m = 0; m < 4; ++m) weights(b >> GS, m, r[m]);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const int chunk = 4 * (4 * tq + (m ^ tq));
-            const float4 pp = *reinterpret_cast<const float4*>(pS + (NT == 1 ? gID >> 1 : gID) * kPvRow + chunk);
+        for (int k = 0; k < 2; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vb + (2 * b + k) * 8 * kPage);
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int bb = 0; bb < 2; ++bb) {
-                const float4 sg = *reinterpret_cast<const float4*>(vsS + (2 * hb + bb) * kPvRow + chunk);
-                const float2 p0 = make_float2(pp.x, pp.y), p1 = make_float2(pp.z, pp.w);
-                const float2 s0 = make_float2(sg.x, sg.y), s1 = make_float2(sg.z, sg.w);
-                uint32_t b0, b1, l0 = 0, l1 = 0;
-                if constexpr (NT == 1) {
-                    b0 = split_w_pair_f16(p0, s0, take_lo);
-                    b1 = split_w_pair_f16(p1, s1, take_lo);
-                } else {
-                    split_both(mul2(p0, s0), b0, l0);
-                    split_both(mul2(p1, s1), b1, l1);
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 v = v4[2 * bb + k];
-                    uint32_t r[4];
-                    unpack4(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w, r);
-                    float(&acc)[4] = st.acc[4 * hb + 2 * bb + k];
-                    mma_f16_16816(acc, r[0], r[1], r[2], r[3], b0, b1);
-                    if constexpr (NT == 2) mma_f16_16816(acc, r[0], r[1], r[2], r[3], l0, l1);
-                }
+            for (int m = 0; m < 4; ++m) {
+                uint32_t c[4];
+                unpack4(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w, c);
+                mma_f16_16816(t, c[0], c[1], c[2], c[3], r[m][0], r[m][1]);
+                if constexpr (NT == 2) mma_f16_16816(t, c[0], c[1], c[2], c[3], r[m][2], r[m][3]);
             }
+            float(&acc)[4] = st.acc[2 * b + k];
+            const float2 a0 = add2(make_float2(acc[0], acc[1]), make_float2(t[0], t[1]));
+            const float2 a1 = add2(make_float2(acc[2], acc[3]), make_float2(t[2], t[3]));
+            acc[0] = a0.x;
+            acc[1] = a0.y;
+            acc[2] = a1.x;
+            acc[3] = a1.y;
         }
     }
 }
@@ -378,21 +422,22 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
 // Persistent blocks: the producer warp takes split-K items from the work
 // counter and streams their pages, page i of an item to consumer warp i % 4,
 // as two halves (K, then V) into the warp's ring; in each round of four
-// pages the four K halves go first.  Every wait is bounded: on a timeout the
+// pages the four K halves go first.  A consumer warp writes its own partial
+// state at an item's end and goes on with the next item: a merge of the four
+// in shared memory cost about four pages' time per item.  Every wait is bounded: on a timeout the
 // block reports OSCAR_STATUS_TIMEOUT, lets its copies land and exits.
-template <int NT>
-__global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
+template <int NT, int GS>
+__global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_kernel(DecodeParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    using SM = Int4Smem<NT>;
-    constexpr int NSW = SM::NSW;
+    using SM = Int4Smem<NT, GS>;
+    constexpr int NSW = SM::NSW, NB = 4 >> GS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);  // [warp][NSW]
     uint64_t* empty = full + kConsumerWarps * NSW;
     uint64_t* qfull = empty + kConsumerWarps * NSW;
     uint64_t* qempty = qfull + 2;
-    uint64_t* merge_bar = qempty + 2;
     PageInfo* info = reinterpret_cast<PageInfo*>(smem + SM::kInfo);  // [warp][2]
-    const uint32_t half_bytes = (uint32_t)half_bytes4(p.gshift);
+    constexpr uint32_t half_bytes = kCodes4 + kPage * 4 * NB;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kConsumerWarps * NSW; ++s) {
@@ -403,7 +448,6 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
             mbar_init(&qfull[s], 1);
             mbar_init(&qempty[s], kConsumerWarps);
         }
-        mbar_init(merge_bar, kConsumerWarps);
         fence_mbar_init();
     }
     __syncthreads();
@@ -412,6 +456,7 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
 
     if (warp == kConsumerWarps) {
         // ------------------------------ producer ------------------------------
+        const int pps = p.counter[kPlanPps], tail_pg = p.counter[kPlanTail];  // from prep_kernel
         const int total_long = __ldg(p.item_start + p.B);
         const int total = total_long + __ldg(p.item_start2 + p.B);
         Ring<NSW> ring;       // the same for the four warps: every round gives each two halves
@@ -448,9 +493,9 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
             const int split = (rel - s0) % splits;
             const int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
             const int seq_pages = (hist + kPage - 1) / kPage;
-            const SeqSplits sp = seq_splits(seq_pages, p.pps, p.tail_pg);
-            const int pg0 = is_long ? split * p.pps : sp.long_pages + split * kShortItemPages;
-            const int npg = is_long ? min(p.pps, sp.long_pages - pg0) : min(kShortItemPages, seq_pages - pg0);
+            const SeqSplits sp = seq_splits(seq_pages, pps, tail_pg);
+            const int pg0 = is_long ? split * pps : sp.long_pages + split * kShortItemPages;
+            const int npg = is_long ? min(pps, sp.long_pages - pg0) : min(kShortItemPages, seq_pages - pg0);
             const int rounds = (npg + kConsumerWarps - 1) / kConsumerWarps;
             {   // the item's q' data into its buffer, once item k - 2 has left it
                 const uint32_t qs = pitem & 1u;
@@ -546,20 +591,12 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
     empty += warp * NSW;
     const SplitSel take_lo = split_sel(gID & 1);
 
-    uint32_t merge_phase = 0;
-    auto consumer_sync = [&]() -> bool {  // bounded rendezvous of the four consumer warps
-        __syncwarp();
-        if (lane == 0) mbar_arrive(merge_bar);
-        const bool w = mbar_wait_bounded(merge_bar, merge_phase & 1u, kWaitPolls);
-        ++merge_phase;
-        return __all_sync(kFull, w);
-    };
     auto give_up = [&]() {
         if (lane == 0) report(p.status, OSCAR_STATUS_TIMEOUT);
     };
 
-    WarpState<NT> st;
-    float4 qsv[NT];
+    WarpState<NT, GS> st;
+    float qsv[NT][NB];  // group sums of q'
     float kq = 1.f;
     uint32_t citem = 0, cur_qs = 0;
     const uint2* qf = nullptr;
@@ -579,11 +616,18 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
             kq = *reinterpret_cast<const float*>(qb + SM::kQbKinv);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                qsv[n] = reinterpret_cast<const float4*>(qb + SM::kQbSum)[NT == 1 ? tq : 2 * tq + n];
+                const float4 q4 = reinterpret_cast<const float4*>(qb + SM::kQbSum)[NT == 1 ? tq : 2 * tq + n];
+                const float q1[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    qsv[n][b] = q1[b << GS];
+#pragma unroll
+                    for (int i = 1; i < 1 << GS; ++i) qsv[n][b] += q1[(b << GS) + i];
+                }
                 st.m_run[n] = -INFINITY;
                 st.l_run[n] = 0.f;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) st.zacc[n][b] = 0.f;
+                for (int b = 0; b < NB; ++b) st.zacc[n][b] = 0.f;
             }
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
@@ -596,18 +640,18 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
         const bool on = !(flags & kFlagPad);
         if (on) {
             const uint8_t* half = stages + ring.slot * kHalfMax;
-            if (valid == kPage) page_logits<NT, true>(half, valid, wbuf, qf, qsv, kq, p.gshift, lg);
-            else page_logits<NT, false>(half, valid, wbuf, qf, qsv, kq, p.gshift, lg);
+            if (valid == kPage) page_logits<NT, GS, true>(half, valid, wbuf, qf, qsv, kq, lg);
+            else page_logits<NT, GS, false>(half, valid, wbuf, qf, qsv, kq, lg);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[ring.slot]);
         ring.step();
-        if (on) any = page_softmax<NT>(lg, st, alpha);
+        if (on) any = page_softmax<NT, GS>(lg, st, alpha);
         if (!__all_sync(kFull, mbar_wait_bounded(&full[ring.slot], ring.phase, kWaitPolls))) return give_up();
         if (on) {
             const uint8_t* half = stages + ring.slot * kHalfMax;
-            if (valid == kPage) page_values<NT, true>(half, valid, wbuf, lg, alpha, any, p.gshift, take_lo, st);
-            else page_values<NT, false>(half, valid, wbuf, lg, alpha, any, p.gshift, take_lo, st);
+            if (valid == kPage) page_values<NT, GS, true>(half, valid, wbuf, lg, alpha, any, take_lo, st);
+            else page_values<NT, GS, false>(half, valid, wbuf, lg, alpha, any, take_lo, st);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[ring.slot]);
@@ -615,87 +659,67 @@ __global__ void __launch_bounds__(kThreads4, 3) int4_kernel(DecodeParams p) {
 
         if (!(flags & kFlagLast)) continue;
         if (lane == 0) mbar_arrive(&qempty[cur_qs]);  // done with the item's q' data
-        // this warp's partial state -> its scratch
-        float* mw = reinterpret_cast<float*>(wbuf);
+        // this warp's partial state: part[4 item + warp] = o' [G][d], m [G], l [G]
+        float* part = p.part + ((size_t)item * kConsumerWarps + warp) * p.part_stride;
         const float down = st.wexp == kNoScale ? 0.f : pow2_bits(-st.wexp);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            const int head = NT == 1 ? tq : 2 * tq + n;
             float l = st.l_run[n];
             l += __shfl_xor_sync(kFull, l, 4);
             l += __shfl_xor_sync(kFull, l, 8);
             l += __shfl_xor_sync(kFull, l, 16);
-            float z[4];
+            float z[NB];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 z[b] = st.zacc[n][b];
                 z[b] += __shfl_xor_sync(kFull, z[b], 4);
                 z[b] += __shfl_xor_sync(kFull, z[b], 8);
                 z[b] += __shfl_xor_sync(kFull, z[b], 16);
             }
-            float* o = mw + (size_t)(NT == 1 ? tq : 2 * tq + n) * (kD + 2);
+            if (head >= p.G) continue;
+            float* o = part + (size_t)head * kD;
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
                 const float a = NT == 1 ? st.acc[mt][0] + st.acc[mt][1] : st.acc[mt][n];
                 const float c = NT == 1 ? st.acc[mt][2] + st.acc[mt][3] : st.acc[mt][2 + n];
                 *reinterpret_cast<float2*>(o + 16 * mt + 2 * gID) =
-                    make_float2(fmaf(a, down, z[mt >> 1]), fmaf(c, down, z[mt >> 1]));
+                    make_float2(fmaf(a, down, z[mt >> (1 + GS)]), fmaf(c, down, z[mt >> (1 + GS)]));
             }
             if (gID == 0) {
-                o[kD] = st.m_run[n];
-                o[kD + 1] = l;
+                part[(size_t)p.G * kD + head] = st.m_run[n];
+                part[(size_t)p.G * kD + p.G + head] = l;
             }
         }
-        if (!consumer_sync()) return give_up();
-        // merge the four warps: thread -> stored position, all heads
-        float* part = p.part + (size_t)item * p.part_stride;
-        const int d = threadIdx.x;  // 0..127
-        for (int hl = 0; hl < p.G; ++hl) {
-            float M = -INFINITY;
-#pragma unroll
-            for (int ww = 0; ww < kConsumerWarps; ++ww)
-                M = fmaxf(M, reinterpret_cast<const float*>(smem + SM::kWarp + ww * SM::kWarpBytes)[hl * (kD + 2) + kD]);
-            float acc = 0.f, L = 0.f;
-            if (M != -INFINITY) {
-#pragma unroll
-                for (int ww = 0; ww < kConsumerWarps; ++ww) {
-                    const float* src =
-                        reinterpret_cast<const float*>(smem + SM::kWarp + ww * SM::kWarpBytes) + hl * (kD + 2);
-                    const float sc = ex2(src[kD] - M);
-                    acc = fmaf(sc, src[d], acc);
-                    L = fmaf(sc, src[kD + 1], L);
-                }
-            }
-            part[(size_t)hl * kD + d] = acc;
-            if (d == 0) {
-                part[(size_t)p.G * kD + hl] = M;
-                part[(size_t)p.G * kD + p.G + hl] = L;
-            }
-        }
-        if (!consumer_sync()) return give_up();
     }
 }
 
-template <int NT>
-cudaError_t launch(const DecodeParams& p, cudaStream_t st, int sms, bool& attr_set) {
+template <int NT, int GS>
+cudaError_t launch(const DecodeParams& p, cudaStream_t st, bool& attr_set) {
     if (!attr_set) {
-        const cudaError_t e = set_smem(int4_kernel<NT>, Int4Smem<NT>::kBytes);
+        const cudaError_t e = set_smem(int4_kernel<NT, GS>, Int4Smem<NT, GS>::kBytes);
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    const int64_t max_items =
-        (int64_t)p.B * p.hk * ((p.max_pages + p.pps - 1) / p.pps + p.tail_pg / kShortItemPages);
-    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)3 * sms, max_items));
+    // no more blocks than items (of four pages at least)
+    const int64_t items = (int64_t)p.B * p.hk * ((p.max_pages + 3) / 4);
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(p.blocks4, items));
     const cudaError_t e =
-        launch_pdl(int4_kernel<NT>, dim3(blocks), dim3(kThreads4), Int4Smem<NT>::kBytes, st, p);
+        launch_pdl(int4_kernel<NT, GS>, dim3(blocks), dim3(kThreads4), Int4Smem<NT, GS>::kBytes, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev, int sms) {
-    static bool attr_set[64][2];
-    bool(&at)[2] = attr_set[dev & 63];
-    return p.NT == 1 ? launch<1>(p, st, sms, at[0]) : launch<2>(p, st, sms, at[1]);
+cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev) {
+    static bool attr_set[64][6];
+    bool(&at)[6] = attr_set[dev & 63];
+    if (p.NT == 1) {
+        if (p.gshift == 0) return launch<1, 0>(p, st, at[0]);
+        return p.gshift == 1 ? launch<1, 1>(p, st, at[1]) : launch<1, 2>(p, st, at[2]);
+    }
+    if (p.gshift == 0) return launch<2, 0>(p, st, at[3]);
+    return p.gshift == 1 ? launch<2, 1>(p, st, at[4]) : launch<2, 2>(p, st, at[5]);
 }
 
 }  // namespace oscar

@@ -16,6 +16,9 @@ constexpr int kGroup = 32;        // quantisation group
 constexpr int kNumGroups = kD / kGroup;
 constexpr int kPage = 64;         // tokens per page
 constexpr int kBfCounter = 32;      // index of the BF16 item queue's counter
+constexpr int kPlanPps = 8;         // 4-bit: index of the plan's pages per long item
+constexpr int kPlanTail = 9;        // 4-bit: index of the plan's pages in short tail items
+constexpr int kMaxBlocks4 = 512;    // 4-bit: blocks that the plan counts with at most (room for as many items is added)
 constexpr int kShortItemPages = 16; // pages per short split-K item (the queue's tail)
 constexpr int kBlock = OSCAR_BLOCK_BYTES;
 constexpr int kKCodes = 0;        // byte offsets inside a (page, kv) block
@@ -160,6 +163,12 @@ constexpr float kLmVDown = 0.5f;  // extra V-scale factor of the Lloyd-Max kerne
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 r;
     asm("{.reg .b64 A, B, C; mov.b64 A, {%2, %3}; mov.b64 B, {%4, %5}; mul.rn.f32x2 C, A, B; mov.b64 {%0, %1}, C;}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 A, B, C; mov.b64 A, {%2, %3}; mov.b64 B, {%4, %5}; add.rn.f32x2 C, A, B; mov.b64 {%0, %1}, C;}"
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
@@ -388,6 +397,8 @@ struct DecodeParams {
     const float* codebook;  // [hk][2] Lloyd-Max inner level a, or null (uniform levels)
     const uint8_t* boost;   // K boost records [num_pages][hk][kBoostBlock], or null (no boost)
     int bits4;     // 1: 4-bit history blocks (int4.cu), 0: 2-bit blocks
+    int blocks4;   // 4-bit: thread blocks of int4_kernel; the plan aims at one item for each (counter[kPlanPps, kPlanTail])
+    int part_shift; // log2 of the partials per split-K item: 2 for 4-bit (one per consumer warp), 0
     int out_bf16;  // 1: out is bf16
 };
 

@@ -91,7 +91,14 @@ inline cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, si
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Blocks per SM of the 4-bit history kernel: three (128 registers); two (168, and
+// four page halves per warp instead of two) for eight query heads per KV head
+// with two or four quantisation groups per vector, whose state would spill:
+// 32 x 32K, 64 query heads, groups of 32: 508 us with three blocks, 444 with two;
+// groups of 64: 363 and 354; groups of 128: 313 and 329.
+__host__ __device__ constexpr int int4_blocks_per_sm(int nt, int gshift) { return nt == 2 && gshift < 2 ? 2 : 3; }
+
 // the 4-bit history kernel (int4.cu), launched by launch_decode between prep_kernel and bf16_kernel
-cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev, int sms);
+cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev);
 
 }  // namespace oscar
