@@ -1456,8 +1456,9 @@ __device__ __forceinline__ void bf16_stage_rows(const DecodeParams& p, int b, in
 // head in rows.  MMA row h holds head h (rows G..15 are zero): S = Q.K^T,
 // then O += P.V twice into the same accumulators, with A = the bf16 high
 // part of P (its low 16 bits cleared, exact) and A = the rounded remainder,
-// so P keeps ~16 bits and each head's output is one accumulator row.
-template <int G>
+// so P keeps ~16 bits and each head's output is one accumulator row.  FINE (the
+// fp32 output of the 4-bit history) adds a third part: 24 bits.
+template <int G, bool FINE>
 __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, float qscale) {
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
     float* st = reinterpret_cast<float*>(rows);  // [G][kD + 2] at the end
@@ -1518,7 +1519,7 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
     la += __shfl_xor_sync(kFull, la, 2);
 
     // P as the A operand of O = P.V (k = the 16 tokens), high and low parts
-    uint32_t ph[2], pl[2];
+    uint32_t ph[2], pl[2], pt[2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
         const float w0 = sacc[nt][0], w1 = sacc[nt][1];
@@ -1526,6 +1527,8 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
         const float h1 = __uint_as_float(__float_as_uint(w1) & 0xffff0000u);
         ph[nt] = row_on ? pack_bf16x2_rn(h0, h1) : 0u;
         pl[nt] = row_on ? pack_bf16x2_rn(w0 - h0, w1 - h1) : 0u;
+        if constexpr (FINE)
+            pt[nt] = row_on ? pack_bf16x2_rn(w0 - h0 - bf16_lo(pl[nt]), w1 - h1 - bf16_hi(pl[nt])) : 0u;
     }
 
     // O = P.V over dims 8j .. 8j+7 (B via ldmatrix.trans: matrix i/8 = tokens
@@ -1542,6 +1545,10 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
         mma_bf16_16816(o[2 * jp], pl[0], 0u, pl[1], 0u, vf[0], vf[1]);
         mma_bf16_16816(o[2 * jp + 1], ph[0], 0u, ph[1], 0u, vf[2], vf[3]);
         mma_bf16_16816(o[2 * jp + 1], pl[0], 0u, pl[1], 0u, vf[2], vf[3]);
+        if constexpr (FINE) {
+            mma_bf16_16816(o[2 * jp], pt[0], 0u, pt[1], 0u, vf[0], vf[1]);
+            mma_bf16_16816(o[2 * jp + 1], pt[0], 0u, pt[1], 0u, vf[2], vf[3]);
+        }
     }
     __syncwarp();  // all row reads done: the tile now holds the warp's state
     if (row_on) {  // head gID: accumulator row gID
@@ -1562,6 +1569,7 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
 // results it does not read; its block 0 waits for int2_kernel's completion
 // before it exits (the others leave when their items are done), so this grid
 // completes after int2_kernel and the merge after it sees both.
+template <bool FINE>
 __global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
     extern __shared__ __align__(128) uint8_t bsm[];
     pdl_trigger();
@@ -1616,10 +1624,10 @@ __global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
         uint8_t* rows = rows_of(buf, warp);
         const __nv_bfloat16* qsm = reinterpret_cast<const __nv_bfloat16*>(q_of(buf));
         switch (p.G) {
-            case 1: bf16_tile<1>(n - t0, rows, qsm, p.qscale); break;
-            case 2: bf16_tile<2>(n - t0, rows, qsm, p.qscale); break;
-            case 4: bf16_tile<4>(n - t0, rows, qsm, p.qscale); break;
-            default: bf16_tile<8>(n - t0, rows, qsm, p.qscale); break;
+            case 1: bf16_tile<1, FINE>(n - t0, rows, qsm, p.qscale); break;
+            case 2: bf16_tile<2, FINE>(n - t0, rows, qsm, p.qscale); break;
+            case 4: bf16_tile<4, FINE>(n - t0, rows, qsm, p.qscale); break;
+            default: bf16_tile<8, FINE>(n - t0, rows, qsm, p.qscale); break;
         }
         __syncthreads();
         // merge the four warps: thread -> dimension
@@ -2019,12 +2027,14 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
     if (e != cudaSuccess) return e;
     if (ev_int2_stop && (e = cudaEventRecord(ev_int2_stop, st)) != cudaSuccess) return e;
     if (!at.setb) {
-        e = set_smem(bf16_kernel, kBfSmem);
+        e = set_smem(bf16_kernel<false>, kBfSmem);
+        if (e == cudaSuccess) e = set_smem(bf16_kernel<true>, kBfSmem);
         if (e != cudaSuccess) return e;
         at.setb = true;
     }
     const int bf_total = p.bf_items * p.B * p.hk;
-    e = launch_pdl(bf16_kernel, dim3(min(bf_total, 3 * at.sms)), dim3(kBfThreads), kBfSmem, st, p);
+    e = launch_pdl(p.bits4 && !p.out_bf16 ? bf16_kernel<true> : bf16_kernel<false>, dim3(min(bf_total, 3 * at.sms)),
+                   dim3(kBfThreads), kBfSmem, st, p);
     if (e != cudaSuccess) return e;
     if (!at.setm) {
         e = set_smem(merge_kernel, kMergeSmem);

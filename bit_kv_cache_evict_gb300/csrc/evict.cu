@@ -20,83 +20,12 @@
 
 namespace oscar {
 
-// merge two blocks' (max, min) into both: the extremes of their union
-__device__ __forceinline__ void df_group_extremes(df& hi_a, df& hi_b, df& lo_a, df& lo_b) {
-    const df h = df_less(hi_a, hi_b) ? hi_b : hi_a;
-    const df l = df_less(lo_b, lo_a) ? lo_b : lo_a;
-    hi_a = hi_b = h;
-    lo_a = lo_b = l;
-}
-
-// Codes and pairs of one vector into its 4-bit slot.  Value k of the lane is
-// in-group index j = bitrev5(lane) of 32-position block bitrev2(k); its
-// nibble partner (j ^ 1) is lane ^ 16.
-__device__ __forceinline__ void evict_store4(const EvictParams& p, const df (&yn)[4], const df (&hi)[4],
-                                             const df (&lo)[4], int i, int kv, int which) {
-    const int lane = threadIdx.x & 31;
-    const int seq = __ldg(p.dst_seq + i);
-    const int pos = __ldg(p.dst_pos + i);
-    if (pos < 0 || pos >= p.max_pages * kPage || seq < 0 || seq >= p.batch) {
-        if (lane == 0) report(p.status, OSCAR_STATUS_BAD_POS);
-        return;
-    }
-    const int page = __ldg(p.page_table + (size_t)seq * p.max_pages + pos / kPage);
-    if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) report(p.status, OSCAR_STATUS_BAD_PAGE);
-        return;
-    }
-    uint32_t w[4], nib = 0;  // (s, z) words in block order; nibble of block b in byte b
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int b = bitrev2(k);
-        const unsigned short sb = df_to_f16(df_div15(df_add(hi[k], df_neg(lo[k])))), zb = df_to_f16(lo[k]);
-        const float sf = __half2float(__ushort_as_half(sb)), zf = __half2float(__ushort_as_half(zb));
-        const int code = sf != 0.f ? code4_of(yn[k], sf, zf) : 0;
-        nib |= (uint32_t)code << (8 * b);
-        w[b >> p.gshift] = (uint32_t)sb | ((uint32_t)zb << 16);
-    }
-    const uint32_t other = __shfl_xor_sync(kFull, nib, 16);
-    const uint32_t bytes = lane < 16 ? nib | (other << 4) : other | (nib << 4);  // byte b: byte j / 2 of block b
-    const int slot = pos % kPage;
-    uint8_t* half = p.pool + ((size_t)page * p.hk + kv) * p.block_bytes + which * half_bytes4(p.gshift);
-    if (which == 0) {  // word (a, b) of the token: bytes j / 2 = 4 a .. 4 a + 3 of block b
-        uint32_t word = 0;
-        const int a = (lane >> 2) & 3, b = lane & 3;
-#pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-            const uint32_t v = __shfl_sync(kFull, bytes, bitrev5(2 * (4 * a + i4)));
-            word |= ((v >> (8 * b)) & 0xffu) << (8 * i4);
-        }
-        if (lane < 16) *reinterpret_cast<uint32_t*>(half + slot * (kD / 2) + 4 * lane) = word;
-    } else {  // plane 16 b + j / 2: the pair of lanes stores two blocks each
-        const int jj = bitrev5(lane & 15) >> 1, b0 = (lane >> 4) * 2;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-            half[(16 * (b0 + b) + jj) * kPage + slot] = (uint8_t)(bytes >> (8 * (b0 + b)));
-    }
-    if (lane == 0) {
-        const int ng = sz_pairs(p.gshift);
-        uint8_t* sz = half + kCodes4 + slot * 4 * ng;
-        if (ng == 4) *reinterpret_cast<uint4*>(sz) = make_uint4(w[0], w[1], w[2], w[3]);
-        else if (ng == 2) *reinterpret_cast<uint2*>(sz) = make_uint2(w[0], w[1]);
-        else *reinterpret_cast<uint32_t*>(sz) = w[0];
-    }
-}
-
 // Block = one (token, KV head, K|V) vector; warp w accumulates the terms
 // a in [w*128/W, (w+1)*128/W) of y = x . U, warp 0 adds the W partial sums
 // exactly and finishes the vector.  W = 8 when there are few vectors (a
 // decode step at small batch: shorter dependent chains per warp), 4 when
 // there are many.
-//
-// BITS = 4 writes the 4-bit blocks: 16 levels, s = (max - min) / 15, and
-// every decision (the clip threshold c max|y|, s and z to fp16, the codes)
-// taken from the pairs, so that codes and pairs are those of a float64
-// evaluation except where that lies within 2^-40 or so (relative) of a
-// border.  max |y| comes out of the max and min reductions (one reduction
-// fewer than the 2-bit form), and the exact comparison runs for one code in
-// 25,000.
-template <int kEvictWarps, int BITS>
+template <int kEvictWarps>
 __global__ void __launch_bounds__(32 * kEvictWarps) evict_kernel(EvictParams p) {
     constexpr int kEvictTerms = kD / kEvictWarps;
     __shared__ df part[kEvictWarps][kD];
@@ -186,6 +115,7 @@ __global__ void __launch_bounds__(32 * kEvictWarps) evict_kernel(EvictParams p) 
     const float cb_a = p.codebook ? __ldg(p.codebook + kv * 2 + which) : 0.f;
     const float kc_hi = __uint_as_float(0x3db504f3u), kc_lo = __uint_as_float(0x30cfe77au);
     df yn[4];
+    float amax[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float ph = __fmul_rn(y[k].hi, kc_hi);
@@ -193,36 +123,31 @@ __global__ void __launch_bounds__(32 * kEvictWarps) evict_kernel(EvictParams p) 
         e = __fmaf_rn(y[k].hi, kc_lo, e);
         e = __fmaf_rn(y[k].lo, kc_hi, e);
         yn[k] = fast_two_sum(ph, e);
+        amax[k] = fabsf(yn[k].hi);
     }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(kFull, amax[k], m));
+    // value k's 32-position block is bitrev2(k); a group of 64 (128) stored
+    // positions is blocks {0,1}, {2,3} (all four): k = {0,2}, {1,3} (all)
+    if (p.gshift >= 1) {
+        amax[0] = amax[2] = fmaxf(amax[0], amax[2]);
+        amax[1] = amax[3] = fmaxf(amax[1], amax[3]);
+    }
+    if (p.gshift >= 2) amax[0] = amax[1] = amax[2] = amax[3] = fmaxf(amax[0], amax[1]);
+    // clamp to +-t, t = c * max|y| (fp32: an error of 1 ulp in t moves the
+    // clipped values by 6e-8 relative)
     df lo[4], hi[4];
-    if constexpr (BITS == 2) {
-        float amax[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) amax[k] = fabsf(yn[k].hi);
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) amax[k] = fmaxf(amax[k], __shfl_xor_sync(kFull, amax[k], m));
-        // value k's 32-position block is bitrev2(k); a group of 64 (128) stored
-        // positions is blocks {0,1}, {2,3} (all four): k = {0,2}, {1,3} (all)
-        if (p.gshift >= 1) {
-            amax[0] = amax[2] = fmaxf(amax[0], amax[2]);
-            amax[1] = amax[3] = fmaxf(amax[1], amax[3]);
+    for (int k = 0; k < 4; ++k) {
+        if (cr < 1.f) {  // warp-uniform; c >= 1 clips nothing
+            const float t = __fmul_rn(cr, amax[k]);
+            if (yn[k].hi > t || (yn[k].hi == t && yn[k].lo > 0.f)) yn[k] = {t, 0.f};
+            else if (yn[k].hi < -t || (yn[k].hi == -t && yn[k].lo < 0.f)) yn[k] = {-t, 0.f};
         }
-        if (p.gshift >= 2) amax[0] = amax[1] = amax[2] = amax[3] = fmaxf(amax[0], amax[1]);
-        // clamp to +-t, t = c * max|y| (fp32: an error of 1 ulp in t moves the
-        // clipped values by 6e-8 relative)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (cr < 1.f) {  // warp-uniform; c >= 1 clips nothing
-                const float t = __fmul_rn(cr, amax[k]);
-                if (yn[k].hi > t || (yn[k].hi == t && yn[k].lo > 0.f)) yn[k] = {t, 0.f};
-                else if (yn[k].hi < -t || (yn[k].hi == -t && yn[k].lo < 0.f)) yn[k] = {-t, 0.f};
-            }
-        }
+        lo[k] = hi[k] = yn[k];
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) lo[k] = hi[k] = yn[k];
     // exact min / max of the pairs: reduce the high parts, then the low parts
     // of the lanes that hold the extreme high part
 #pragma unroll
@@ -251,22 +176,6 @@ __global__ void __launch_bounds__(32 * kEvictWarps) evict_kernel(EvictParams p) 
         df_group_extremes(hi[0], hi[1], lo[0], lo[1]);
         hi[2] = hi[3] = hi[0];
         lo[2] = lo[3] = lo[0];
-    }
-    if constexpr (BITS == 4) {  // clip by +-t, t = c max|y| = c max(max, -min)
-        if (cr < 1.f) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const df nlo = df_neg(lo[k]), a = df_less(hi[k], nlo) ? nlo : hi[k];
-                const float th = __fmul_rn(cr, a.hi);
-                const df t = fast_two_sum(th, __fmaf_rn(cr, a.lo, __fmaf_rn(cr, a.hi, -th))), nt = df_neg(t);
-                if (df_less(t, yn[k])) yn[k] = t;
-                else if (df_less(yn[k], nt)) yn[k] = nt;
-                if (df_less(t, hi[k])) hi[k] = t;
-                if (df_less(lo[k], nt)) lo[k] = nt;
-            }
-        }
-        evict_store4(p, yn, hi, lo, i, kv, which);
-        return;
     }
     unsigned short sb[4], zb[4];
     // value k of this lane is in-group index bitrev5(lane) of group bitrev2(k):
@@ -382,15 +291,8 @@ __global__ void __launch_bounds__(32 * kEvictWarps) evict_kernel(EvictParams p) 
 // split the decode's kernels (up to 213 KB per SM), launched early by the
 // programmatic dependency, could not start on an SM until its eviction
 // blocks had drained.
-// 4-bit calls with this many vectors (tokens x KV heads x 2) take the bulk
-// kernel: it starts with 18 us of forming R in every block and then needs
-// 0.5 ns per vector, this kernel 7.6 ns per vector (GB300, 8 KV heads: 192
-// tokens 29 us here and 31 us there, 256 tokens 37 and 31, 15,104 tokens 1832
-// and 141).
-constexpr int kBulkVectors = 3328;
-
-template <int BITS>
-static cudaError_t launch_evict_bits(const EvictParams& p, cudaStream_t st) {
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
+    if (p.bits4) return launch_evict4(p, st);
     const int vecs = p.n_tok * p.hk * 2;
     if (vecs == 0) return cudaSuccess;
     static bool carveout_set[64] = {};
@@ -398,10 +300,10 @@ static cudaError_t launch_evict_bits(const EvictParams& p, cudaStream_t st) {
     cudaError_t ce = cudaGetDevice(&dev);
     if (ce != cudaSuccess) return ce;
     if (!carveout_set[dev & 63]) {
-        ce = cudaFuncSetAttribute(evict_kernel<8, BITS>, cudaFuncAttributePreferredSharedMemoryCarveout,
+        ce = cudaFuncSetAttribute(evict_kernel<8>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                   (int)cudaSharedmemCarveoutMaxShared);
         if (ce == cudaSuccess)
-            ce = cudaFuncSetAttribute(evict_kernel<4, BITS>, cudaFuncAttributePreferredSharedMemoryCarveout,
+            ce = cudaFuncSetAttribute(evict_kernel<4>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                       (int)cudaSharedmemCarveoutMaxShared);
         if (ce != cudaSuccess) return ce;
         carveout_set[dev & 63] = true;
@@ -415,15 +317,9 @@ static cudaError_t launch_evict_bits(const EvictParams& p, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = vecs < 512 ? cudaLaunchKernelEx(&cfg, evict_kernel<8, BITS>, p)
-                                     : cudaLaunchKernelEx(&cfg, evict_kernel<4, BITS>, p);
+    const cudaError_t e = vecs < 512 ? cudaLaunchKernelEx(&cfg, evict_kernel<8>, p)
+                                     : cudaLaunchKernelEx(&cfg, evict_kernel<4>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
-    if (p.bits4 && p.n_tok * p.hk * 2 >= kBulkVectors && ((uintptr_t)p.src_kv & 15) == 0)  // (16-byte row copies)
-        return launch_evict_bulk(p, st);
-    return p.bits4 ? launch_evict_bits<4>(p, st) : launch_evict_bits<2>(p, st);
 }
 
 }  // namespace oscar

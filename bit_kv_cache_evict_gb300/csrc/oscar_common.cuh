@@ -490,6 +490,7 @@ int64_t pages_copy_pieces(size_t page_bytes);  // thread blocks per (pair, pool)
 cudaError_t launch_pages_copy(const PagesCopyParams& p, int n_pools, cudaStream_t st);
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
+cudaError_t launch_evict4(const EvictParams& p, cudaStream_t st);      // 4-bit blocks (evict4.cu)
 cudaError_t launch_evict_bulk(const EvictParams& p, cudaStream_t st);  // many tokens, 4-bit blocks (evict_bulk.cu)
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t st, cudaEvent_t ev_int2_start,
                           cudaEvent_t ev_int2_stop);

@@ -70,5 +70,12 @@ __device__ __forceinline__ int code4_of(df y, float sf, float zf) {
     }
     return (int)fminf(fmaxf(c, 0.f), 15.f);
 }
+// merge two blocks' (max, min) into both: the extremes of their union
+__device__ __forceinline__ void df_group_extremes(df& hi_a, df& hi_b, df& lo_a, df& lo_b) {
+    const df h = df_less(hi_a, hi_b) ? hi_b : hi_a;
+    const df l = df_less(lo_b, lo_a) ? lo_b : lo_a;
+    hi_a = hi_b = h;
+    lo_a = lo_b = l;
+}
 
 }  // namespace oscar

@@ -6,6 +6,7 @@ or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -537,21 +538,18 @@ OSCAR_OUT_F32, OSCAR_OUT_BF16 = 0, 1
 MAX_COPY_POOLS = 128
 
 # The calls below run once per layer and step, where a launch costs a few
-# microseconds: their checks touch each tensor once (_arg), sizes that depend
-# on the shape alone are kept per shape, and pointers go to ctypes as ints.
-_F32 = _BF16 = _I32 = _U8 = _raw_stream = None
+# microseconds: their checks touch each tensor once (_arg), and pointers go to
+# ctypes as ints.
+_F32 = _BF16 = _I32 = _U8 = _raw_stream = _current_device = None
 
 
 def _torch_names() -> None:
-    global _F32, _BF16, _I32, _U8, _raw_stream
+    global _F32, _BF16, _I32, _U8, _raw_stream, _current_device
     import torch
+    torch.cuda.current_device()                     # initialises CUDA once; the raw queries below do not
     _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
     _raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+    _current_device = torch._C._cuda_getDevice
 
 
 def _arg(t, what: str, dtype, need: int, dev: int):
@@ -592,22 +590,15 @@ def _out_type(out) -> int:
     raise TypeError(f"out: expected float32 or bfloat16, got {out.dtype}")
 
 
-_BLOCK = {}
-
-
 def _pool_block(shape: oscar_shape, bits: int) -> int:
-    """Block bytes of a pool, kept per (bits, shape)."""
-    key = (bits, bytes(shape))
-    n = _BLOCK.get(key)
-    if n is None:
-        fn = lib().oscar_block_bytes_int4 if bits == 4 else lib().oscar_block_bytes
-        n = _BLOCK[key] = int(fn(ctypes.byref(shape)))
-    return n
+    """Block bytes of a pool of a supported shape (the library refuses the
+    others): codes of 64 K and V vectors and their pairs."""
+    return bits * 2048 + 512 * (128 // max(shape.quant_group, 1))
 
 
 def block_bytes_int4(shape: oscar_shape) -> int:
     """Bytes of a (page, KV head) block of a 4-bit pool, 0 if unsupported."""
-    return _pool_block(shape, 4)
+    return int(lib().oscar_block_bytes_int4(ctypes.byref(shape)))
 
 
 def oscar_evict_quantize_int4(shape: oscar_shape, src_kv, dst_seq, dst_pos, U, clip, pool, page_table, batch: int,
@@ -700,7 +691,19 @@ def oscar_history_gather(shape: oscar_shape, bits: int, pool, src_table, dst_tab
         _check("oscar_history_gather", st)
 
 
-_COPY_POOLS = ctypes.c_void_p * MAX_COPY_POOLS
+def _pool_args(pools, need: int, dev: int) -> list:
+    """Addresses of the pools of a copy.  The usual case is checked by loops in
+    C (36 layers: half the time of as many _arg calls); anything else goes
+    through _arg, which says what is wrong."""
+    import torch
+    T = torch.Tensor
+    try:
+        if ({t.dtype for t in pools} <= {_U8} and set(map(T.get_device, pools)) <= {dev}
+                and min(map(T.numel, pools), default=need) >= need and all(map(T.is_contiguous, pools))):
+            return list(map(T.data_ptr, pools))
+    except (AttributeError, TypeError):
+        pass
+    return [_arg(t, "pools", _U8, need, dev) for t in pools]
 
 
 def oscar_pages_copy_device(page_bytes: int, src, dst, pools, num_pages: int, dev_status=None, stream=None) -> None:
@@ -712,9 +715,10 @@ def oscar_pages_copy_device(page_bytes: int, src, dst, pools, num_pages: int, de
     dev, n, need = _current_device(), src.numel(), num_pages * page_bytes
     if len(pools) > MAX_COPY_POOLS:
         raise ValueError(f"pools: {len(pools)}, at most {MAX_COPY_POOLS}")
+    ptrs = array.array("Q", _pool_args(pools, need, dev))
     st = lib().oscar_pages_copy_device(
         page_bytes, n, _arg(src, "src", _I32, n, dev), _arg(dst, "dst", _I32, n, dev),
-        _COPY_POOLS(*[_arg(t, "pools", _U8, need, dev) for t in pools]), len(pools), num_pages,
+        ptrs.buffer_info()[0], len(pools), num_pages,
         _arg(dev_status, "dev_status", _I32, 1, dev), _stream_arg(stream, dev))
     if st:
         _check("oscar_pages_copy_device", st)

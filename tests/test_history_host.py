@@ -153,10 +153,11 @@ class Fake:
 
 def test_binding_refuses_wrong_tensors(lib, monkeypatch):
     torch = pytest.importorskip("torch")
-    monkeypatch.setattr(O, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)   # (no GPU here)
     u8, i = torch.uint8, Fake(2)
     O._torch_names()
     monkeypatch.setattr(O, "_raw_stream", lambda d: 0)
+    monkeypatch.setattr(O, "_current_device", lambda: 0)
 
     def copy(src=i, dst=i, pools=(Fake(256, dtype=u8),), n=4):
         O.oscar_pages_copy_device(64, src, dst, list(pools), n)
@@ -180,4 +181,6 @@ def test_binding_refuses_wrong_tensors(lib, monkeypatch):
     with pytest.raises(ValueError):
         O.oscar_history_gather(sh(), 4, pool, Fake(2, 1), Fake(1, 1), Fake(2, 1), i, 1)
     assert O._out_type(torch.zeros(1)) == O.OSCAR_OUT_F32 and O._out_type(torch.zeros(1, dtype=torch.bfloat16)) == O.OSCAR_OUT_BF16
+    for g in (32, 64, 128):
+        assert [O._pool_block(sh(quant_group=g), b) for b in (2, 4)] == [O.block_bytes(sh(quant_group=g)), O.block_bytes_int4(sh(quant_group=g))]
     assert O.block_bytes_int4(sh()) == 10240 and O.block_bytes_int4(sh(quant_group=128)) == 8704
