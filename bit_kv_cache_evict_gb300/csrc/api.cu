@@ -68,7 +68,7 @@ static int tail_pages_of(int pps) { return pps > kShortItemPages ? 2 * kShortIte
 
 struct WsLayout {
     size_t counter, item_start, item_start2, qfrag, qsum, qkinv, qrot, part, bf_part, total;
-    int NT, pps, tail_pg, part_stride, part_shift;
+    int NT, pps, tail_pg, part_stride, parts;  // parts: partials per item
     int64_t max_items;   // split-K items at most (int64: batch x KV heads x splits can exceed int32)
 };
 
@@ -80,10 +80,10 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bi
     w.part_stride = (int)round_up((size_t)G * (kD + 2), 4);
     w.tail_pg = tail_pages_of(w.pps);
     w.max_items = (int64_t)batch * hk * ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages);
-    w.part_shift = 0;
+    w.parts = 1;
     if (bits == 4) {  // items of at least pps pages, or at most one per thread block of any size
         w.max_items += kMaxBlocks4;
-        w.part_shift = 2;
+        w.parts = kPartsPerItem4;
     }
     size_t off = 0;
     w.counter = off;
@@ -101,7 +101,7 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bi
     w.qrot = off;
     off = round_up(off + (size_t)batch * hk * w.NT * 4 * kD * 4, 256);
     w.part = off;
-    off = round_up(off + ((size_t)w.max_items << w.part_shift) * w.part_stride * 4, 256);
+    off = round_up(off + (size_t)w.max_items * w.parts * w.part_stride * 4, 256);
     w.bf_part = off;
     off = round_up(off + (size_t)batch * hk * bf16_items(s) * w.part_stride * 4, 256);
     w.total = off;
@@ -255,8 +255,8 @@ static oscar_status evict_impl(const oscar_shape* shape, int32_t n_tok, const vo
     p.num_pages = num_pages;
     p.gshift = gshift_of(shape);
     p.block_bytes = block_bytes_of(shape, bits);
-    p.bits4 = bits == 4;
-    const cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = bits == 4 ? launch_evict4(p, st) : launch_evict(p, st);
     return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
 }
 
@@ -314,7 +314,7 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     if (batch < 0 || max_pages <= 0 || num_pages < 0 || !ws_bytes) return OSCAR_ERR_INVALID_ARG;
     const WsLayout w = ws_layout(shape, batch, max_pages, bits);
     // item counts, item offsets and partial indices are int32 on the device
-    if (w.max_items << w.part_shift > INT32_MAX || (double)w.max_items * w.part_stride > 4.0e9)
+    if (w.max_items * w.parts > INT32_MAX || (double)w.max_items * w.part_stride > 4.0e9)
         return OSCAR_ERR_INVALID_ARG;
     if (!workspace) {
         *ws_bytes = w.total;
@@ -329,7 +329,7 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
         return OSCAR_ERR_INVALID_ARG;
     if (!(sm_scale == sm_scale)) return OSCAR_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    DecodeParams p{};
+    DecodeParams4 p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.bf16_kv = static_cast<const __nv_bfloat16*>(bf16_kv);
     p.bf16_len = bf16_len;
@@ -356,7 +356,7 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.nslot = shape->sink + shape->recent;
     p.bf_items = bf16_items(shape);
     {   // merge warps per row: more when rows are few and split-K partials many
-        const int splits = ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages) << w.part_shift;
+        const int splits = ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages) * w.parts;
         const int rows = batch * p.G;
         int wpr = 1;
         // (4-bit, four partials per item: no more blocks than two per SM, each stages U_V)
@@ -370,15 +370,17 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.num_pages = num_pages;
     p.gshift = gshift_of(shape);
     p.block_bytes = block_bytes_of(shape, bits);
-    p.bits4 = bits == 4;
     p.out_bf16 = out_type == OSCAR_OUT_BF16;
     p.pps = w.pps;
     p.tail_pg = w.tail_pg;
     p.part_stride = w.part_stride;
-    p.part_shift = w.part_shift;
     p.qscale = sm_scale * kLog2e;
     p.codebook = codebook;
     p.boost = boost;
+    if (bits == 4) {
+        const cudaError_t e = launch_decode4(p, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
+    }
     cudaEvent_t ev0 = g_int2_ev_start, ev1 = g_int2_ev_stop;
     g_int2_ev_start = g_int2_ev_stop = nullptr;
     if (!ev0 || !ev1) ev0 = ev1 = nullptr;

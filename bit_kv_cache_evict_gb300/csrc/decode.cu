@@ -31,6 +31,8 @@
 //       W_tb = p_t s_tb                                  (fp16 MMA, dims x heads).
 // q' 2^e and W are split into fp16 hi + lo (22 bits); codes are exact and
 // carry no offset.
+#include <type_traits>
+
 #include "oscar_common.cuh"
 #include "splitk.cuh"
 
@@ -49,7 +51,12 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepUnits = kPrepSeqs * 2 * 4;  // (b, nt, hh) units of a block at most
 constexpr int kPrepSmem = kD * kD * 4 + kPrepUnits * kD * 4 + kPrepUnits * 4;
 
-__device__ __forceinline__ void prep_body(const DecodeParams& p);
+// The parameters of a kernel that both histories use.
+template <bool INT4>
+using Params = std::conditional_t<INT4, DecodeParams4, DecodeParams>;
+
+template <bool INT4>
+__device__ __forceinline__ void prep_body(const Params<INT4>& p);
 
 // Launched as a programmatic dependent of the eviction (it reads neither the
 // pool nor the BF16 segment), so the two overlap.  One block waits for the
@@ -59,9 +66,10 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p);
 // slots go to the rest of the grid and to the INT2 kernel's blocks).
 // 40 registers, so that two blocks fit on an SM beside the eviction's blocks
 // (the grid is one wave there).
-__global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(DecodeParams p) {
+template <bool INT4>
+__global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4> p) {
     pdl_trigger();
-    prep_body(p);
+    prep_body<INT4>(p);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) pdl_wait();
 }
 
@@ -73,7 +81,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(DecodeParams p) {
 // 448 items of 73 pages on 456 blocks.  Otherwise items of a quarter of a
 // block's share, with short ones queued last.  At most 64 items per
 // sequence and KV head in the first form: the merge reads four partials of each.
-__device__ __forceinline__ void plan4(const DecodeParams& p, int& pps, int& tail_pg) {
+__device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tail_pg) {
     const int lane = threadIdx.x & 31;
     auto pages_of = [&](int b) {
         const int h = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
@@ -100,23 +108,24 @@ __device__ __forceinline__ void plan4(const DecodeParams& p, int& pps, int& tail
         return n * p.hk;
     };
     int lo = max(4, (most + 63) / 64), hi = 256;  // four pages: one for each consumer warp
-    if (lo <= hi && items_at(hi) <= p.blocks4) {
+    if (lo <= hi && items_at(hi) <= p.blocks) {
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
-            if (items_at(mid) <= p.blocks4) hi = mid;
+            if (items_at(mid) <= p.blocks) hi = mid;
             else lo = mid + 1;
         }
-        if (lo <= 32 || (long)lo * p.blocks4 <= total + total / 4) {
+        if (lo <= 32 || (long)lo * p.blocks <= total + total / 4) {
             pps = lo;
             tail_pg = 0;
             return;
         }
     }
-    pps = (int)min(256l, max((long)p.pps, total / (4 * p.blocks4)));
+    pps = (int)min(256l, max((long)p.pps, total / (4 * p.blocks)));
     tail_pg = pps > kShortItemPages ? 2 * kShortItemPages : 0;
 }
 
-__device__ __forceinline__ void prep_body(const DecodeParams& p) {
+template <bool INT4>
+__device__ __forceinline__ void prep_body(const Params<INT4>& p) {
     extern __shared__ __align__(16) float psm[];
     float* Us = psm;                       // [a][k] = U_K[a][k]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -125,7 +134,7 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p) {
         if (blockIdx.y != 0 || warp != 0) return;
         // long items of every sequence first, then the short tail items
         int pps = p.pps, tail_pg = p.tail_pg;
-        if (p.bits4) {
+        if constexpr (INT4) {
             plan4(p, pps, tail_pg);
             if (lane == 0) {
                 p.counter[kPlanPps] = pps;
@@ -303,8 +312,8 @@ __device__ __forceinline__ void prep_body(const DecodeParams& p) {
         // four codes of bytes 4(2tq+h)..4(2tq+h)+3 of group g's slot; column
         // 2hh = hi, 2hh+1 = lo.  (4-bit codes: in-group indices 8tq + 2h +
         // {0,4} and + {1,5}, the nibbles 2h, 2h+1 of both halves of word tq.)
-        const int second = p.bits4 ? 4 : 2;
-        const int base = 32 * (ks >> 1) + 8 * tq + (p.bits4 ? 2 : 4) * (ks & 1);
+        constexpr int second = INT4 ? 4 : 2;
+        const int base = 32 * (ks >> 1) + 8 * tq + (INT4 ? 2 : 4) * (ks & 1);
         const float v[4] = {qs[base] * up, qs[base + second] * up, qs[base + 1] * up, qs[base + second + 1] * up};
         uint32_t h01, h23, l01, l23;
         split_f16(v, h01, h23, l01, l23);
@@ -1690,7 +1699,10 @@ constexpr int kMergeSmem = (kD * kURow + 2 * kMergeWarps * kMergeRow) * 4;
 constexpr int kMergeBatch = 12;   // split-K partials per batch of loads
 constexpr int kMaxBfItems = 5;    // BF16 segment blocks per row: ceil(320 / 64)
 
-__global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p) {
+// INT4: the 4-bit history's form (four partials per item, rows scaled before
+// their fp16 split, fp32 or bf16 output).
+template <bool INT4>
+__global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p) {
     extern __shared__ __align__(16) float msm[];
     float* Us = msm;                  // [a][kURow] = U_V[a][j]
     float* Ws = msm + kD * kURow;     // [warp][kMergeRow]: a warp's share (y, M, L), then the row's w
@@ -1719,10 +1731,15 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
         const int s0 = __ldg(p.item_start + b), t0 = __ldg(p.item_start2 + b);
         n_long = (__ldg(p.item_start + b + 1) - s0) / p.hk;
         const int n_short = (__ldg(p.item_start2 + b + 1) - t0) / p.hk;
-        splits = (n_long + n_short) << p.part_shift;
-        first = (s0 + kv * n_long) << p.part_shift;
-        first2 = (__ldg(p.item_start + p.B) + t0 + kv * n_short - n_long) * (1 << p.part_shift);  // (may be negative)
-        n_long <<= p.part_shift;
+        splits = n_long + n_short;
+        first = s0 + kv * n_long;
+        first2 = __ldg(p.item_start + p.B) + t0 + kv * n_short - n_long;
+        if constexpr (INT4) {  // kPartsPerItem4 partials per item
+            splits *= kPartsPerItem4;
+            first *= kPartsPerItem4;
+            first2 *= kPartsPerItem4;
+            n_long *= kPartsPerItem4;
+        }
     }
     pdl_wait();  // partials of int2_kernel and bf16_kernel
     const int r5 = bitrev5(lane);
@@ -1830,7 +1847,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
         const float inv = (L > 0.f) ? 1.f / L : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = active ? y[k] * inv : 0.f;
-        if (p.bits4) {
+        if constexpr (INT4) {
             float mx = fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3])));
 #pragma unroll
             for (int m = 1; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
@@ -1923,19 +1940,21 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
     }
     const float Mx = fmaxf(L > 0.f ? M : -INFINITY, lb > 0.f ? mb : -INFINITY);
     const float wl = (L > 0.f) ? ex2(M - Mx) * L : 0.f;
-    const float wi = wl * wup;
+    const float wi = INT4 ? wl * wup : wl;
     const float wb = (lb > 0.f) ? ex2(mb - Mx) : 0.f;
     const float den = wl + wb * lb;
     const float inv = (den > 0.f) ? 1.f / den : 0.f;
     const size_t at = ((size_t)b * p.hq + kv * p.G + hh) * kD;
-    if (p.out_bf16) {  // a model's next product reads bf16: rounded once, here
-        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+    if constexpr (INT4) {
+        if (p.out_bf16) {  // a model's next product reads bf16: rounded once, here
+            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int a2 = lane + 32 * c;
-            o[a2] = __float2bfloat16_rn((wi * yrow[a2] + wb * ob[c]) * inv);
+            for (int c = 0; c < 4; ++c) {
+                const int a2 = lane + 32 * c;
+                o[a2] = __float2bfloat16_rn((wi * yrow[a2] + wb * ob[c]) * inv);
+            }
+            return;
         }
-        return;
     }
     float* o = p.out + at;
 #pragma unroll
@@ -1990,8 +2009,7 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
         if (e != cudaSuccess) return e;
     }
     DecodeParams p = pin;
-    if (p.bits4) p.blocks4 = std::min(int4_blocks_per_sm(p.NT, p.gshift) * at.sms, kMaxBlocks4);
-    if (!p.bits4) {  // Fewer history pages (at most) than two waves of minimum items on
+    {   // Fewer history pages (at most) than two waves of minimum items on
         // the INT2 grid (a batch of one or two long sequences): items of one
         // wave instead, so that no block takes a second item while others
         // idle.  Longer items only lower the item count the workspace was
@@ -2008,16 +2026,14 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
         }
     }
     if (!at.setp) {
-        e = set_smem(prep_kernel, kPrepSmem);
+        e = set_smem(prep_kernel<false>, kPrepSmem);
         if (e != cudaSuccess) return e;
         at.setp = true;
     }
     dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
-    if ((e = launch_pdl(prep_kernel, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
+    if ((e = launch_pdl(prep_kernel<false>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
     if (ev_int2_start && (e = cudaEventRecord(ev_int2_start, st)) != cudaSuccess) return e;
-    if (p.bits4)
-        e = launch_int4(p, st, dev);
-    else if (p.codebook)  // Lloyd-Max levels
+    if (p.codebook)  // Lloyd-Max levels
         e = (p.NT == 1) ? launch_int2<1, true>(p, st, at.sms, at.setl) : launch_int2<2, true>(p, st, at.sms, at.setl2);
     else if (p.boost)  // K channel boost
         e = (p.NT == 1) ? launch_int2<1, false, true>(p, st, at.sms, at.setk)
@@ -2028,22 +2044,52 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
     if (ev_int2_stop && (e = cudaEventRecord(ev_int2_stop, st)) != cudaSuccess) return e;
     if (!at.setb) {
         e = set_smem(bf16_kernel<false>, kBfSmem);
-        if (e == cudaSuccess) e = set_smem(bf16_kernel<true>, kBfSmem);
         if (e != cudaSuccess) return e;
         at.setb = true;
     }
     const int bf_total = p.bf_items * p.B * p.hk;
-    e = launch_pdl(p.bits4 && !p.out_bf16 ? bf16_kernel<true> : bf16_kernel<false>, dim3(min(bf_total, 3 * at.sms)),
-                   dim3(kBfThreads), kBfSmem, st, p);
+    e = launch_pdl(bf16_kernel<false>, dim3(min(bf_total, 3 * at.sms)), dim3(kBfThreads), kBfSmem, st, p);
     if (e != cudaSuccess) return e;
     if (!at.setm) {
-        e = set_smem(merge_kernel, kMergeSmem);
+        e = set_smem(merge_kernel<false>, kMergeSmem);
         if (e != cudaSuccess) return e;
         at.setm = true;
     }
     const int rpb = kMergeWarps / p.merge_wpr;
     dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
-    return launch_pdl(merge_kernel, mg, dim3(kMergeThreads), kMergeSmem, st, p);
+    return launch_pdl(merge_kernel<false>, mg, dim3(kMergeThreads), kMergeSmem, st, p);
+}
+
+// The chain over a 4-bit history: int4_kernel in int2_kernel's place.
+cudaError_t launch_decode4(const DecodeParams4& pin, cudaStream_t st) {
+    static bool attr_set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Int2Attr& at = attr_for_device(dev);
+    if (at.sms == 0) {
+        e = cudaDeviceGetAttribute(&at.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    if (!attr_set[dev & 63]) {
+        e = set_smem(prep_kernel<true>, kPrepSmem);
+        if (e == cudaSuccess) e = set_smem(bf16_kernel<true>, kBfSmem);
+        if (e == cudaSuccess) e = set_smem(bf16_kernel<false>, kBfSmem);
+        if (e == cudaSuccess) e = set_smem(merge_kernel<true>, kMergeSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev & 63] = true;
+    }
+    DecodeParams4 p = pin;
+    p.blocks = std::min(int4_blocks_per_sm(p.NT, p.gshift) * at.sms, kMaxBlocks4);
+    dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
+    if ((e = launch_pdl(prep_kernel<true>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
+    if ((e = launch_int4(p, st, dev)) != cudaSuccess) return e;
+    e = launch_pdl<DecodeParams>(p.out_bf16 ? bf16_kernel<false> : bf16_kernel<true>,
+                                 dim3(min(p.bf_items * p.B * p.hk, 3 * at.sms)), dim3(kBfThreads), kBfSmem, st, p);
+    if (e != cudaSuccess) return e;
+    const int rpb = kMergeWarps / p.merge_wpr;
+    dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
+    return launch_pdl(merge_kernel<true>, mg, dim3(kMergeThreads), kMergeSmem, st, p);
 }
 
 }  // namespace oscar

@@ -292,7 +292,6 @@ __global__ void __launch_bounds__(32 * kEvictWarps) evict_kernel(EvictParams p) 
 // programmatic dependency, could not start on an SM until its eviction
 // blocks had drained.
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
-    if (p.bits4) return launch_evict4(p, st);
     const int vecs = p.n_tok * p.hk * 2;
     if (vecs == 0) return cudaSuccess;
     static bool carveout_set[64] = {};

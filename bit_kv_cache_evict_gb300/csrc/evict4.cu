@@ -72,8 +72,8 @@ template <int W, int DEPTH>
 __global__ void __launch_bounds__(32 * W) evict4_kernel(EvictParams p) {
     constexpr int kTerms = kD / W;
     __shared__ df part[W][kD];
-    pdl_trigger();  // the decode's query preparation does not read what this kernel writes
     pdl_wait();     // launched early (programmatic serialization): the previous kernel's results first
+    pdl_trigger();  // the decode's query preparation reads nothing that this kernel writes (but what came before it)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int pairs = 2 * p.hk, pair = blockIdx.x % pairs, i = blockIdx.x / pairs;
     const float* Um = p.U + (size_t)pair * kD * kD + (size_t)kTerms * warp * kD;
@@ -274,7 +274,7 @@ cudaError_t launch(const EvictParams& p, cudaStream_t st) {
 // Calls with this many vectors (tokens x KV heads x 2) take the bulk kernel: it
 // starts with 18 us of forming R in every block and then needs 0.5 ns per
 // vector, this kernel 7.3 ns (GB300, 8 KV heads: 192 tokens 23 us here and 31
-// us there, 256 tokens 31 and 31, 15,104 tokens 1830 and 128).
+// us there, 256 tokens 31 and 31, 15,104 tokens 1830 and 120).
 constexpr int kBulkVectors = 4096;
 
 }  // namespace

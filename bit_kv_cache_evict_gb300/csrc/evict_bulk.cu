@@ -294,8 +294,8 @@ __device__ __forceinline__ void bulk_ldsm(uint32_t (&r)[4], const void* p) {
 // its warps take tiles of 16 listed tokens in turn.
 __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gID = lane >> 2, tq = lane & 3;
     const int pairs = 2 * p.hk, pair = blockIdx.x % pairs, kv = pair >> 1, which = pair & 1;
     const int step = gridDim.x / pairs * kBulkWarps, tiles = (p.n_tok + kTile - 1) / kTile;
@@ -473,14 +473,34 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
                 gmn[r][0] = gmn[r][1] = gmn[r][2] = gmn[r][3] = fminf(gmn[r][0], gmn[r][2]);
             }
         }
-        // Candidates for the extremes: elements within 2 delta of them; count (bits
-        // 0-7) and sum of positions per row and block, then per group.
+        // Clip threshold and pair of every group, and whether an error of delta
+        // leaves it open (bit 4 r + b; the same in a group's blocks and in a quad)
+        uint32_t open = 0;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float d = delta[r];
+                const float t = cr < 1.f ? cr * fmaxf(gmx[r][b], -gmn[r][b]) : INFINITY;
+                const float hi = fminf(gmx[r][b], t), lo = fmaxf(gmn[r][b], -t);
+                const float sp = (hi - lo) * (1.f / 15.f), es = d * (2.f / 15.f) + sp * 4.8e-7f, ez = d + fabsf(lo) * 2.4e-7f;
+                const uint32_t w0 = pack_f16x2_rn(sp - es, lo - ez), w1 = pack_f16x2_rn(sp + es, lo + ez);
+                clip[r][b] = t;
+                if (tq == 0) sz[(gID + 8 * r) * 4 + b] = w0;
+                // (NaN bounds leave it open as well)
+                if (!(sp - es <= sp + es && lo - ez <= lo + ez) || w0 != w1) open |= 1u << (4 * r + b);
+            }
+        // Candidates for the extremes of the open groups: elements within 2 delta of
+        // them; count (bits 0-7) and sum of positions per row and block, then per group
+        const uint32_t some = __reduce_or_sync(kFull, open);
         uint32_t cx[2][4], cn[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const float d2 = 2.02f * delta[r];
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
+                cx[r][b] = cn[r][b] = 0;
+                if (!((some >> (4 * r + b)) & 1u)) continue;  // warp-uniform
                 const float bx = gmx[r][b] - d2, bn = gmn[r][b] + d2;
                 uint32_t x = 0, n = 0;
 #pragma unroll
@@ -514,18 +534,11 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
         for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const float d = delta[r];
-                const float t = cr < 1.f ? cr * fmaxf(gmx[r][b], -gmn[r][b]) : INFINITY;
-                const float hi = fminf(gmx[r][b], t), lo = fmaxf(gmn[r][b], -t);
-                const float sp = (hi - lo) * (1.f / 15.f), es = d * (2.f / 15.f) + sp * 4.8e-7f, ez = d + fabsf(lo) * 2.4e-7f;
-                const uint32_t w0 = pack_f16x2_rn(sp - es, lo - ez), w1 = pack_f16x2_rn(sp + es, lo + ez);
-                clip[r][b] = t;
-                // (NaN bounds leave it open as well)
-                const bool open = (!(sp - es <= sp + es && lo - ez <= lo + ez) || w0 != w1) && tq == 0 && (b & (nb - 1)) == 0;
+                if (!((some >> (4 * r + b)) & 1u) || (b & (nb - 1))) continue;  // warp-uniform
+                const bool mine = ((open >> (4 * r + b)) & 1u) && tq == 0;
                 const bool single = (cx[r][b] & 0xffu) == 1u && (cn[r][b] & 0xffu) == 1u;
-                if (tq == 0) sz[(gID + 8 * r) * 4 + b] = w0;
-                whole[r] |= (__ballot_sync(kFull, open && !single) & 0x11111111u) << b;
-                if (open && single)
+                whole[r] |= (__ballot_sync(kFull, mine && !single) & 0x11111111u) << b;
+                if (mine && single)
                     list[atomicAdd(n_list, 1)] =
                         make_ushort4((unsigned short)(warp * kTile + gID + 8 * r), (unsigned short)b,
                                      (unsigned short)(cx[r][b] >> 8), (unsigned short)(cn[r][b] >> 8));
@@ -557,18 +570,20 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
                 const float inv = sf != 0.f ? __fdividef(1.f, sf) : 0.f;
                 // u is off by delta / s and the rounding of three fp32 operations on |u| < 16
                 const float edge = 0.5f - (delta[r] * inv * 1.01f + 8e-6f);
+                // u of the clip thresholds and of the codes' range, as one pair of bounds (s = 0: every code 0)
+                const float ulo = sf != 0.f ? fmaxf(0.f, (-t - zf) * inv) : 0.f, uhi = sf != 0.f ? fminf(15.f, (t - zf) * inv) : 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int n = 4 * b + i;
                     uint32_t c[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float y = fminf(fmaxf(acc[n][2 * r + e], -t), t);
-                        const float u = (y - zf) * inv, k = rintf(u);
-                        if (!(fabsf(u - k) < edge) && inv != 0.f) late[r] |= 1u << (2 * n + e);
-                        c[e] = (uint32_t)fminf(fmaxf(k, 0.f), 15.f);
+                        const float u = fminf(fmaxf((acc[n][2 * r + e] - zf) * inv, ulo), uhi);
+                        const float m = u + 12582912.f;  // 1.5 2^23: rounds u to an integer, in the low bits
+                        if (!(fabsf(u - (m - 12582912.f)) < edge)) late[r] |= 1u << (2 * n + e);
+                        c[e] = __float_as_uint(m);
                     }
-                    stg[(gID + 8 * r) * kStgPitch + 4 * n + tq] = (uint8_t)(c[0] | (c[1] << 4));
+                    stg[(gID + 8 * r) * kStgPitch + 4 * n + tq] = (uint8_t)(c[0] + (c[1] << 4));
                 }
             }
         __syncwarp();

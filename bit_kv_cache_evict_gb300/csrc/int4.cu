@@ -37,6 +37,7 @@ namespace oscar {
 
 namespace {
 
+static_assert(kPartsPerItem4 == kConsumerWarps, "a partial per consumer warp");
 constexpr int kThreads4 = (kConsumerWarps + 1) * 32;
 constexpr int kHalfMax = kCodes4 + kPage * 16;  // bytes of a half at g = 32
 
@@ -427,7 +428,7 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
 // in shared memory cost about four pages' time per item.  Every wait is bounded: on a timeout the
 // block reports OSCAR_STATUS_TIMEOUT, lets its copies land and exits.
 template <int NT, int GS>
-__global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_kernel(DecodeParams p) {
+__global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_kernel(DecodeParams4 p) {
     extern __shared__ __align__(128) uint8_t smem[];
     using SM = Int4Smem<NT, GS>;
     constexpr int NSW = SM::NSW, NB = 4 >> GS;
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
 }
 
 template <int NT, int GS>
-cudaError_t launch(const DecodeParams& p, cudaStream_t st, bool& attr_set) {
+cudaError_t launch(const DecodeParams4& p, cudaStream_t st, bool& attr_set) {
     if (!attr_set) {
         const cudaError_t e = set_smem(int4_kernel<NT, GS>, Int4Smem<NT, GS>::kBytes);
         if (e != cudaSuccess) return e;
@@ -703,7 +704,7 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t st, bool& attr_set) {
     }
     // no more blocks than items (of four pages at least)
     const int64_t items = (int64_t)p.B * p.hk * ((p.max_pages + 3) / 4);
-    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(p.blocks4, items));
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(p.blocks, items));
     const cudaError_t e =
         launch_pdl(int4_kernel<NT, GS>, dim3(blocks), dim3(kThreads4), Int4Smem<NT, GS>::kBytes, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -711,7 +712,7 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t st, bool& attr_set) {
 
 }  // namespace
 
-cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev) {
+cudaError_t launch_int4(const DecodeParams4& p, cudaStream_t st, int dev) {
     static bool attr_set[64][6];
     bool(&at)[6] = attr_set[dev & 63];
     if (p.NT == 1) {

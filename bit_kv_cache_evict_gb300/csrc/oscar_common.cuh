@@ -18,6 +18,7 @@ constexpr int kPage = 64;         // tokens per page
 constexpr int kBfCounter = 32;      // index of the BF16 item queue's counter
 constexpr int kPlanPps = 8;         // 4-bit: index of the plan's pages per long item
 constexpr int kPlanTail = 9;        // 4-bit: index of the plan's pages in short tail items
+constexpr int kPartsPerItem4 = 4;   // 4-bit: partials per split-K item, one per consumer warp
 constexpr int kMaxBlocks4 = 512;    // 4-bit: blocks that the plan counts with at most (room for as many items is added)
 constexpr int kShortItemPages = 16; // pages per short split-K item (the queue's tail)
 constexpr int kBlock = OSCAR_BLOCK_BYTES;
@@ -349,7 +350,6 @@ struct EvictParams {
     int n_tok, hk, src_rows, batch, max_pages, num_pages;
     int gshift;       // log2(quant_group / 32): 0, 1, 2
     int block_bytes;  // bytes per (page, KV head) block: 4096 + 512 * (4 >> gshift); 4-bit blocks 2 * half_bytes4
-    int bits4;        // 1: 4-bit blocks
 };
 
 // A 4-bit (page, KV head) block is two halves of the same size, K then V,
@@ -396,9 +396,11 @@ struct DecodeParams {
     float qscale;  // sm_scale * log2(e)
     const float* codebook;  // [hk][2] Lloyd-Max inner level a, or null (uniform levels)
     const uint8_t* boost;   // K boost records [num_pages][hk][kBoostBlock], or null (no boost)
-    int bits4;     // 1: 4-bit history blocks (int4.cu), 0: 2-bit blocks
-    int blocks4;   // 4-bit: thread blocks of int4_kernel; the plan aims at one item for each (counter[kPlanPps, kPlanTail])
-    int part_shift; // log2 of the partials per split-K item: 2 for 4-bit (one per consumer warp), 0
+};
+
+// The same for a 4-bit history (int4.cu), with what only its kernels read.
+struct DecodeParams4 : DecodeParams {
+    int blocks;    // thread blocks of int4_kernel; the plan aims at one item for each (counter[kPlanPps, kPlanTail])
     int out_bf16;  // 1: out is bf16
 };
 
@@ -494,5 +496,6 @@ cudaError_t launch_evict4(const EvictParams& p, cudaStream_t st);      // 4-bit 
 cudaError_t launch_evict_bulk(const EvictParams& p, cudaStream_t st);  // many tokens, 4-bit blocks (evict_bulk.cu)
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t st, cudaEvent_t ev_int2_start,
                           cudaEvent_t ev_int2_stop);
+cudaError_t launch_decode4(const DecodeParams4& p, cudaStream_t st);  // 4-bit history
 
 }  // namespace oscar

@@ -75,9 +75,8 @@ inline cudaError_t set_smem(void (*kernel)(Args...), int bytes, bool max_carveou
 
 // Launch with a programmatic dependency on the previous kernel in the stream
 // (the kernel itself decides where it waits, see pdl_wait).
-template <typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              const DecodeParams& p) {
+template <typename P>
+inline cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -98,7 +97,7 @@ inline cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, si
 // groups of 64: 363 and 354; groups of 128: 313 and 329.
 __host__ __device__ constexpr int int4_blocks_per_sm(int nt, int gshift) { return nt == 2 && gshift < 2 ? 2 : 3; }
 
-// the 4-bit history kernel (int4.cu), launched by launch_decode between prep_kernel and bf16_kernel
-cudaError_t launch_int4(const DecodeParams& p, cudaStream_t st, int dev);
+// the 4-bit history kernel (int4.cu), launched by launch_decode4 between prep_kernel and bf16_kernel
+cudaError_t launch_int4(const DecodeParams4& p, cudaStream_t st, int dev);
 
 }  // namespace oscar

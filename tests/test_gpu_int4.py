@@ -438,3 +438,53 @@ def test_every_output_row_is_written_and_nothing_else():
     c.decode(out=room[1:1 + c.B])
     assert (room[0] == 7).all() and (room[-1] == 7).all()
     check(room[1:1 + c.B], *c.want())
+
+
+def test_zero_queries_average_the_values():
+    c = Cache(27, [100, 5], 4, 1, 32)
+    c.q[:] = 0
+    check(c.decode(), *c.want())
+    c = Cache(28, [64 * 3], 8, 1, 64)
+    c.q[0, 1:] = 0                                        # one head of a KV group alone is not zero
+    check(c.decode(), *c.want())
+
+
+def test_eviction_then_decode_in_a_chain_without_waits():
+    """Eviction, decode, compaction, decode, copies, read: launched one behind
+    the other, each reading what the one before wrote."""
+    c = Cache(29, [640, 300], 8, 2, 32, spare=16, extra=1)
+    d = c.device()
+    rows = kv_bits(c.rng, c.B, c.hk, outlier=1.0)
+    clip = np.full((c.hk, 2), 0.95, np.float32)
+    src, seq, pos, dclip = H.bf16_t(rows), H.i32_t(np.arange(c.B)), H.i32_t(c.hist), H.f32_t(clip)
+    hist = H.i32_t(c.hist + 1)
+    keeps = [np.arange(0, 641, 3), np.arange(1, 301, 2)]
+    keep = np.zeros((2, 256), np.int32)
+    for b, k in enumerate(keeps):
+        keep[b, :len(k)] = k
+    n_keep = np.array([len(k) for k in keeps], np.int32)
+    fresh = np.full((2, 4), -1, np.int32)
+    fresh[0], fresh[1, :3] = c.spare[:4], c.spare[4:7]
+    dk, dn, df = H.i32_t(keep), H.i32_t(n_keep), H.i32_t(fresh)
+    copies = (H.i32_t(fresh[0]), H.i32_t(c.spare[8:12]))
+    moved = H.i32_t(np.stack([c.spare[8:12], fresh[1]]))
+    o1, o2, o3 = (torch.zeros(c.B, c.hq, D, device="cuda") for _ in range(3))
+    back = torch.zeros(n_keep[0], c.hk, 2, D, device="cuda")
+    ws = torch.zeros(O.oscar_decode_workspace_bytes_int4(c.sh, c.B, c.max_pages), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):                                     # (the same again changes nothing)
+        O.oscar_evict_quantize_int4(c.sh, src, seq, pos, d["U"], dclip, d["pool"], d["table"], c.B, c.max_pages, c.num_pages)
+        c.decode(out=o1, ws=ws, hist=hist)
+        O.oscar_history_gather(c.sh, 4, d["pool"], d["table"], df, dk, dn, c.num_pages)
+        c.decode(out=o2, ws=ws, hist=dn, table=df)
+        O.oscar_pages_copy_device(c.hk * I.block_bytes(4, 32), *copies, [d["pool"]], c.num_pages)
+        c.decode(out=o3, ws=ws, hist=dn, table=moved)
+        O.oscar_history_read(c.sh, 4, H.i32_t(np.zeros(n_keep[0])), H.i32_t(np.arange(n_keep[0])), d["pool"], moved, 2, 4, c.num_pages, back)
+    I.evict(c.pool, f64(rows), c.U, clip, c.table, np.arange(c.B), c.hist, 32)
+    check(o1, *c.want(hist=c.hist + 1))
+    c.pool = I.gather(c.pool, c.table, fresh, keep, n_keep, c.hk, 4, 32)
+    check(o2, *c.want(hist=n_keep, table=fresh))
+    assert (o3 - o2).abs().max() <= 1e-5 * o2.abs().max()
+    ref = np.stack([np.stack([I.values(c.pool, fresh, 0, np.arange(n_keep[0]), h, w, c.hk, 4, 32) for w in (0, 1)], 1)
+                    for h in range(c.hk)], 1)
+    assert np.array_equal(back.cpu().numpy(), ref.astype(np.float32))
