@@ -442,8 +442,8 @@ oscar_status oscar_history_read(const oscar_shape* shape, int32_t bits, int32_t 
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
-    if (n_tok < 0 || batch < 0 || max_pages <= 0 || max_pages > INT32_MAX / kPage || num_pages < 0 ||
-        (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) || shape->num_kv_heads > 65535)
+    if (n_tok < 0 || n_tok > INT32_MAX - kPage || batch < 0 || max_pages <= 0 || max_pages > INT32_MAX / kPage ||
+        num_pages < 0 || (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) || shape->num_kv_heads > 65535)
         return OSCAR_ERR_INVALID_ARG;
     if (n_tok == 0) return OSCAR_OK;
     if (!seq || !pos || !page_table || !out || (num_pages > 0 && !pool)) return OSCAR_ERR_INVALID_ARG;
@@ -511,7 +511,7 @@ oscar_status oscar_history_gather(const oscar_shape* shape, int32_t bits, int32_
 oscar_status oscar_pages_copy_device(size_t page_bytes, int32_t n_copies, const int32_t* src, const int32_t* dst,
                                      uint8_t* const* pools, int32_t n_pools, int32_t num_pages, int32_t* dev_status,
                                      void* stream) {
-    if (page_bytes == 0 || page_bytes % 16 != 0 || n_copies < 0 || n_pools < 0 || n_pools > OSCAR_MAX_COPY_POOLS ||
+    if (page_bytes == 0 || page_bytes % 16 != 0 || page_bytes / 16 > INT32_MAX || n_copies < 0 || n_pools < 0 || n_pools > OSCAR_MAX_COPY_POOLS ||
         num_pages < 0)
         return OSCAR_ERR_INVALID_ARG;
     const int64_t pieces = pages_copy_pieces(page_bytes);

@@ -68,6 +68,9 @@ __device__ __forceinline__ void prep_body(const Params<INT4>& p);
 // (the grid is one wave there).
 template <bool INT4>
 __global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4> p) {
+    // 4-bit history: q and the lengths may come from the kernel just before, so
+    // every block waits for it first.
+    if constexpr (INT4) pdl_wait();
     pdl_trigger();
     prep_body<INT4>(p);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) pdl_wait();

@@ -470,7 +470,9 @@ oscar_status oscar_decode_attn_boost(const oscar_shape* shape, int32_t batch, co
  *            pool_bytes are those of a 2-bit pool).
  *
  * oscar_evict_quantize_int4: oscar_evict_quantize into a 4-bit pool, with
- *   the same arguments.  Every decision (the clip threshold, s, z, the
+ *   the same arguments.  Two listed tokens with the same destination leave
+ *   either's codes or a mixture in that slot (the order is not fixed); no
+ *   other slot is touched.  Every decision (the clip threshold, s, z, the
  *   codes) is that of values within 2^-36 |x| of the exact rotated ones, so
  *   codes and pairs match a float64 evaluation except that close to a
  *   border.  Calls with many tokens (a prompt's history) rotate on tensor
@@ -555,7 +557,8 @@ oscar_status oscar_history_gather(const oscar_shape* shape, int32_t bits, int32_
  * replay.  oscar_pages_copy is the form for host index arrays and one pool.
  *
  *   page_bytes  bytes of a page: Hk * oscar_block_bytes(shape) or
- *               _int4, Hk * OSCAR_BOOST_BLOCK_BYTES, ...; a multiple of 16
+ *               _int4, Hk * OSCAR_BOOST_BLOCK_BYTES, ...; a multiple of 16,
+ *               at most 16 * INT32_MAX
  *   src, dst    (device int32 [n_copies]).  No dst page may also be a src
  *               page of the call, nor appear twice (its contents are then
  *               undefined); src[i] == dst[i] copies nothing.

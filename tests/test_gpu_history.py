@@ -250,3 +250,54 @@ def test_prompt_fork_compaction_and_decode_together():
     ref, mag = I.decode(f(q), f(kv), [320, 320], kept, fresh, n_keep, U, 1 / np.sqrt(D), g)
     tol = mag[..., 1:] * (4 * mag[..., :1] / np.log(2) * 2.0 ** -19 + 2.0 ** -15)
     assert (np.abs(out.cpu().numpy() - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+def test_offsets_past_32_bits(bits):
+    """Reads, compaction and copies at the end of a pool of 4.9 GB."""
+    hk, g, n, rng = 8, 32, 10, np.random.default_rng(bits)
+    page = hk * I.block_bytes(bits, g)
+    pages = 4_900_000_000 // page
+    base = pages - n
+    assert base * page > 1 << 32
+    sh, small = O.make_shape(hk, hk, quant_group=g), H.u8_t(random_pool(rng, n, hk, bits, g))
+    big = torch.zeros(pages, page, dtype=torch.uint8, device="cuda")
+    big[base:] = small.view(n, page)
+    src, dst = np.array([[3, 1, 4]], np.int32), np.array([[0, 5]], np.int32)
+    keep = np.sort(rng.permutation(192)[:100]).astype(np.int32)[None]
+    pos = rng.permutation(192).astype(np.int32)
+    outs = []
+    for pool, up, np_ in ((small, 0, n), (big.view(-1), base, pages)):
+        out = torch.zeros(192, hk, 2, D, device="cuda")
+        O.oscar_history_read(sh, bits, H.i32_t(np.zeros(192)), H.i32_t(pos), pool, H.i32_t(src + up), 1, 3, np_, out)
+        O.oscar_history_gather(sh, bits, pool, H.i32_t(src + up), H.i32_t(dst + up), H.i32_t(keep), H.i32_t([100]), np_)
+        O.oscar_pages_copy_device(page, H.i32_t([1 + up, 2 + up]), H.i32_t([8 + up, 9 + up]), [pool], np_)
+        outs.append(out)
+    assert torch.equal(*outs) and outs[0].any()
+    assert torch.equal(big[base:], small.view(n, page)) and not big[:base:997].any()
+
+
+def test_all_calls_on_a_side_stream():
+    """Each call given a stream orders with what that stream does, not the current one."""
+    rng = np.random.default_rng(5)
+    hk, g, n = 2, 32, 6
+    sh, page = O.make_shape(hk, hk, quant_group=g), hk * I.block_bytes(4, g)
+    host = random_pool(rng, n, hk, 4, g)
+    src, dst, keep, nk = H.i32_t([[0, 1]]), H.i32_t([[2, 3]]), H.i32_t(np.arange(0, 128, 2)[None]), H.i32_t([64])
+    zero, pos, cs, cd = H.i32_t(np.zeros(64)), H.i32_t(np.arange(64)), H.i32_t([2]), H.i32_t([5])
+    held, moved = H.u8_t(host), H.i32_t([[5, -1]])
+    pool, out = torch.zeros_like(held), torch.zeros(64, hk, 2, D, device="cuda")
+    big = torch.zeros(1 << 28, device="cuda")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(8):
+            big.add_(1)                                    # keeps the side stream busy before the pool is filled
+        pool.copy_(held)
+    O.oscar_history_gather(sh, 4, pool, src, dst, keep, nk, n, stream=st)
+    O.oscar_pages_copy_device(page, cs, cd, [pool], n, stream=st)
+    O.oscar_history_read(sh, 4, zero, pos, pool, moved, 1, 2, n, out, stream=st)
+    st.synchronize()
+    ref = np.stack([np.stack([I.values(host, np.array([[0, 1]]), 0, np.arange(0, 128, 2), h, w, hk, 4, g) for w in (0, 1)], 1)
+                    for h in range(hk)], 1)
+    assert np.array_equal(out.cpu().numpy(), ref.astype(np.float32))

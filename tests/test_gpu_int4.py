@@ -488,3 +488,74 @@ def test_eviction_then_decode_in_a_chain_without_waits():
     ref = np.stack([np.stack([I.values(c.pool, fresh, 0, np.arange(n_keep[0]), h, w, c.hk, 4, 32) for w in (0, 1)], 1)
                     for h in range(c.hk)], 1)
     assert np.array_equal(back.cpu().numpy(), ref.astype(np.float32))
+
+
+def test_queries_and_lengths_written_just_before_the_call():
+    """No wait between the kernels that write q and the lengths and the call."""
+    c = Cache(30, [700, 90, 1], 8, 2, 32)
+    d = c.device()
+    n, rng = 12, np.random.default_rng(2)
+    qs = H.bf16_t(S.bf16_bits(rng.standard_normal((n, c.B, c.hq, D))))
+    hists = H.i32_t(np.stack([rng.integers(0, c.hist + 1) for _ in range(n)]))
+    q, hist, alone = d["q"], d["hist"], []
+    ws = torch.zeros(O.oscar_decode_workspace_bytes_int4(c.sh, c.B, c.max_pages), dtype=torch.uint8, device="cuda")
+    for i in range(n):
+        q.copy_(qs[i])
+        hist.copy_(hists[i])
+        torch.cuda.synchronize()
+        alone.append(c.decode(ws=ws))
+        torch.cuda.synchronize()
+    outs = torch.zeros(n, c.B, c.hq, D, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(n):
+        hist.copy_(hists[i])
+        q.copy_(qs[i])
+        c.decode(out=outs[i], ws=ws)
+    assert torch.equal(outs, torch.stack(alone))
+
+
+def test_two_graphs_share_a_workspace():
+    a, b = Cache(31, [1500, 40], 8, 2, 32), Cache(32, [64, 900, 3], 8, 1, 128)
+    need = max(O.oscar_decode_workspace_bytes_int4(c.sh, c.B, c.max_pages) for c in (a, b))
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros(c.B, c.hq, D, device="cuda") for c in (a, b)]
+    graphs = []
+    for c, o in zip((a, b), outs):
+        c.device()
+        c.decode(out=o, ws=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.decode(out=o, ws=ws)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+    for c, o in zip((a, b), outs):
+        check(o, *c.want())
+
+
+def test_eviction_and_decode_past_32_bit_offsets():
+    """The same pages at the end of a pool of 4.9 GB: equal bytes and outputs."""
+    c = Cache(33, [300, 77], 32, 8, 32, extra=300)
+    d = c.device()
+    page = c.hk * I.block_bytes(4, 32)
+    pages, base = 60000, 60000 - c.num_pages
+    assert base * page > 1 << 32
+    big = torch.zeros(pages, page, dtype=torch.uint8, device="cuda")
+    big[base:] = d["pool"].view(-1, page)
+    up = H.i32_t(np.where(c.table >= 0, c.table + base, -1))
+    clip = torch.full((c.hk, 2), 0.95, device="cuda")
+    for n in (1, 260):                                     # one vector per block, tensor cores
+        rows = H.bf16_t(kv_bits(c.rng, 2 * n, c.hk))
+        seq, pos = H.i32_t(np.repeat([0, 1], n)), H.i32_t(np.concatenate([h + np.arange(n) for h in c.hist]))
+        for pool, table, np_ in ((d["pool"], d["table"], c.num_pages), (big.view(-1), up, pages)):
+            O.oscar_evict_quantize_int4(c.sh, rows, seq, pos, d["U"], clip, pool, table, c.B, c.max_pages, np_)
+    assert torch.equal(big[base:], d["pool"].view(-1, page)) and not big[:base:997].any()
+    hist = H.i32_t(c.hist + 260)
+    low = c.decode(hist=hist)
+    high = torch.zeros_like(low)
+    ws = torch.zeros(O.oscar_decode_workspace_bytes_int4(c.sh, c.B, c.max_pages), dtype=torch.uint8, device="cuda")
+    O.oscar_decode_attn_int4(c.sh, d["q"], d["kv"], d["len"], big.view(-1), up, c.max_pages, pages, hist, d["U"], SCALE, high, ws)
+    assert torch.equal(low, high) and low.isfinite().all()

@@ -89,6 +89,7 @@ def test_read_refusals(lib):
     for bits in (0, 1, 3, 8):
         assert read(lib, bits=bits) == UNSUP
     assert read(lib, n=-1) == BAD and read(lib, batch=-1) == BAD and read(lib, max_pages=0) == BAD
+    assert read(lib, n=(1 << 31) - 1) == BAD
     assert read(lib, max_pages=1 << 26) == BAD and read(lib, num_pages=-1) == BAD and read(lib, kind=7) == BAD
     assert read(lib, s=sh(head_dim=64)) == UNSUP
 
@@ -129,6 +130,8 @@ def test_copy_refusals(lib):
     assert copy(lib, n=-1) == BAD and copy(lib, n_pools=-1) == BAD and copy(lib, num_pages=-1) == BAD
     assert copy(lib, pools=tuple([4096] * 129)) == BAD and copy(lib, status=M) == BAD
     assert copy(lib, page_bytes=1 << 30, n=1 << 20) == BAD  # more pieces than a launch counts
+    for page_bytes in (1 << 35, (1 << 64) - 16, (1 << 64) - 16384):  # (a sum with them would wrap around)
+        assert copy(lib, page_bytes=page_bytes, n=1, pools=(4096,)) == BAD
 
 
 class Fake:
