@@ -177,7 +177,7 @@ constexpr int kNoScale = 64;
 // K half of a page: logits (base 2) of the lane's tokens 16m + gID and
 // 16m + gID + 8.  Up to four heads: lg[m][0], lg[m][1] = the two tokens of
 // head tq; eight heads: (token a, heads 2tq, 2tq+1), (token b, the same).
-template <int NT, int GS, bool FULL>
+template <int NT, int GS>
 __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint8_t* wbuf, const uint2* qf,
                                             const float (&qsv)[NT][4 >> GS], float kq, float (&lg)[4][2 * NT]) {
     constexpr int NB = 4 >> GS;
@@ -188,17 +188,13 @@ __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint
     for (int it = 0; it < 2; ++it) {
         const int t = lane + 32 * it;
         float sv[NB], zv[NB];
+        uint32_t w[NB];
+        load_pairs<NB>(half, t, w);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) sv[b] = zv[b] = 0.f;
-        if (FULL || t < valid) {
-            uint32_t w[NB];
-            load_pairs<NB>(half, t, w);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const float s = half_lo(w[b]);
-                sv[b] = s * (kq * kInPlaceUp);
-                zv[b] = half_hi(w[b]);
-            }
+        for (int b = 0; b < NB; ++b) {
+            const float s = half_lo(w[b]);
+            sv[b] = s * (kq * kInPlaceUp);
+            zv[b] = half_hi(w[b]);
         }
         store_n<NB>(ksS + t * NB, sv);
         store_n<NB>(kzS + t * NB, zv);
@@ -206,9 +202,6 @@ __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint
     __syncwarp();
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-#pragma unroll
-        for (int e = 0; e < 2 * NT; ++e) lg[m][e] = -INFINITY;
-        if (!FULL && 16 * m >= valid) continue;
         const int ta = 16 * m + gID;
         const uint4 xa = *reinterpret_cast<const uint4*>(half + ta * (kD / 2) + 16 * tq);
         const uint4 xb = *reinterpret_cast<const uint4*>(half + (ta + 8) * (kD / 2) + 16 * tq);
@@ -236,7 +229,6 @@ __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint
         load_n<NB>(ksS + (ta + 8) * NB, sb);
         load_n<NB>(kzS + ta * NB, za);
         load_n<NB>(kzS + (ta + 8) * NB, zb);
-        const bool va = FULL || ta < valid, vb = FULL || ta + 8 < valid;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             float x = 0.f, y = 0.f;
@@ -245,9 +237,18 @@ __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint
                 x = fmaf(sa[b], NT == 1 ? acc[b][0] + acc[b][1] : acc[b][j], fmaf(za[b], qsv[j][b], x));
                 y = fmaf(sb[b], NT == 1 ? acc[b][2] + acc[b][3] : acc[b][2 + j], fmaf(zb[b], qsv[j][b], y));
             }
-            lg[m][j] = va ? x : -INFINITY;
-            lg[m][NT == 1 ? 1 : 2 + j] = vb ? y : -INFINITY;
+            lg[m][j] = x;
+            lg[m][NT == 1 ? 1 : 2 + j] = y;
         }
+    }
+    if (valid < kPage) {  // whatever the slots behind the last token hold, NaN included
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                if (16 * m + gID >= valid) lg[m][j] = -INFINITY;
+                if (16 * m + gID + 8 >= valid) lg[m][NT == 1 ? 1 : 2 + j] = -INFINITY;
+            }
     }
 }
 
@@ -286,7 +287,7 @@ __device__ __forceinline__ bool page_softmax(float (&lg)[4][2 * NT], WarpState<N
 
 // V half of a page: the scales, the rescaling of the sums, sum p z', and the
 // products W . (c - 8).
-template <int NT, int GS, bool FULL>
+template <int NT, int GS>
 __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint8_t* wbuf, const float (&p)[4][2 * NT],
                                             const float (&alpha)[NT], bool any, const SplitSel& take_lo,
                                             WarpState<NT, GS>& st) {
@@ -302,9 +303,10 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
         const int t = lane + 32 * it;
+        load_pairs<NB>(half, t, w[it]);
+        if (valid < kPage && t >= valid)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) w[it][b] = 0u;
-        if (FULL || t < valid) load_pairs<NB>(half, t, w[it]);
+            for (int b = 0; b < NB; ++b) w[it][b] = 0u;
 #pragma unroll
         for (int b = 0; b < NB; ++b) smax = max(smax, w[it][b] & 0x7fffu);
     }
@@ -347,7 +349,6 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
     // -- sum p z'
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        if (!FULL && 16 * m >= valid) continue;
         const int ta = 16 * m + gID;
         float zA[NB], zB[NB];
         load_n<NB>(vzS + ta * NB, zA);
@@ -641,8 +642,7 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
         const bool on = !(flags & kFlagPad);
         if (on) {
             const uint8_t* half = stages + ring.slot * kHalfMax;
-            if (valid == kPage) page_logits<NT, GS, true>(half, valid, wbuf, qf, qsv, kq, lg);
-            else page_logits<NT, GS, false>(half, valid, wbuf, qf, qsv, kq, lg);
+            page_logits<NT, GS>(half, valid, wbuf, qf, qsv, kq, lg);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[ring.slot]);
@@ -651,8 +651,7 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
         if (!__all_sync(kFull, mbar_wait_bounded(&full[ring.slot], ring.phase, kWaitPolls))) return give_up();
         if (on) {
             const uint8_t* half = stages + ring.slot * kHalfMax;
-            if (valid == kPage) page_values<NT, GS, true>(half, valid, wbuf, lg, alpha, any, take_lo, st);
-            else page_values<NT, GS, false>(half, valid, wbuf, lg, alpha, any, take_lo, st);
+            page_values<NT, GS>(half, valid, wbuf, lg, alpha, any, take_lo, st);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[ring.slot]);
