@@ -62,94 +62,118 @@ static_assert(BulkSmem::kBytes <= 227 * 1024, "one block per SM");
 
 __device__ __forceinline__ float pow2f_bits(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
+// Place of k-step ks's fragment word pair (position p, quad member tq).  The quad
+// member is exchanged by the n-tile's low bits, so that the 32 positions that
+// a warp of bulk_matrix stores lie on distinct banks (8-way conflicts without).
+__device__ __forceinline__ int frag_at(int ks, int p, int tq) {
+    return ks * kStepWords + (p >> 3) * 32 + 4 * (p & 7) + (tq ^ ((p >> 3) & 3));
+}
+
 // R of this block's (KV head, K|V) into shared memory.  Row a of U times the
 // Hadamard matrix in fixed point, as two 32-bit integers (2^-44 of the largest
 // |U|; the additions are exact), then times 1 / sqrt(d) as a pair.  (64-bit
-// integers took 25 us: their conversions run on the slow 64-bit pipe.)  Returns the exponent q of the scale
-// (stored = R 2^q) and the largest column norm of the stored matrix.
+// integers took 25 us: their conversions run on the slow 64-bit pipe.)  A warp takes
+// the four rows of one fragment word pair (16 ks + 2 tq, + 1, + 8, + 9) at a time, eight
+// lanes to a row, lane c of them inputs 4 c + 32 j + k: four of the seven butterfly
+// stages stay in the lane.  Returns the exponent q of the scale (stored = R 2^q) and the largest
+// column norm of the stored matrix.
 __device__ __forceinline__ void bulk_matrix(const float* U, uint8_t* smem, int& q, float& norm) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kTurns = (kD / 4 + kBulkWarps - 1) / kBulkWarps;
+    // every load first, for the largest entry too
+    float4 u[kTurns][4];
+    float mx = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+        const int w = warp + kBulkWarps * t, i = lane >> 3;
+        const float* row = U + (size_t)(16 * (w >> 2) + 2 * (w & 3) + (i & 1) + 8 * (i >> 1)) * kD + 4 * (lane & 7);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            u[t][j] = w < kD / 4 ? __ldg(reinterpret_cast<const float4*>(row + 32 * j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float* col = reinterpret_cast<float*>(smem + BulkSmem::kCol);
     int* umax = reinterpret_cast<int*>(col + kD);
     if (threadIdx.x < kD) col[threadIdx.x] = 0.f;
     if (threadIdx.x == 0) *umax = 0;
     __syncthreads();
-    float mx = 0.f;
-    for (int i = threadIdx.x; i < kD * kD / 4; i += kBulkThreads) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(U) + i);
-        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(u.x), fabsf(u.y)), fmaxf(fabsf(u.z), fabsf(u.w))));
-    }
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            mx = fmaxf(mx, fmaxf(fmaxf(fabsf(u[t][j].x), fabsf(u[t][j].y)), fmaxf(fabsf(u[t][j].z), fabsf(u[t][j].w))));
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
     if (lane == 0) atomicMax(umax, __float_as_int(mx));
     __syncthreads();
     const int e = min(60, max(-60, ((*umax >> 23) & 0xff) - 127));
     q = 10 - e;  // |R| <= 128 |U| / sqrt(128) < 2^(e + 4.5): stored below 2^14.5
-    const float up = pow2f_bits(22 - e);  // |U| 2^(22 - e) < 2^23: sums of 128 below 2^30
-    // R 2^q = v 2^(e - 22 + q) / sqrt(128) = v 2^-12 / sqrt(128)
-    const float kc_hi = __uint_as_float(0x3db504f3u), kc_lo = __uint_as_float(0x30cfe77au), down = pow2f_bits(-12);
-    // Four rows at a time, the k indices of one fragment word pair (16 ks + 2 tq,
-    // + 1, + 8, + 9), so that a position's parts are stored as vectors.  (Loops
-    // rolled, with the sums in shared memory in between: this code runs three
-    // times per warp and would otherwise wait on its own instruction fetches.)
+    const float up = pow2f_bits(21 - e);  // |U| 2^(21 - e) < 2^22: sums of 128 below 2^29
+    // R 2^q = v 2^(e - 21 + q) / sqrt(128) = v 2^-11 / sqrt(128)
+    const float kc_hi = __uint_as_float(0x3db504f3u), kc_lo = __uint_as_float(0x30cfe77au), down = pow2f_bits(-11);
     uint2* frag = reinterpret_cast<uint2*>(smem + BulkSmem::kFrag);
     float4* r3 = reinterpret_cast<float4*>(smem + BulkSmem::kR3);
-    int4* sums = reinterpret_cast<int4*>(smem + BulkSmem::kX + warp * kTile * kXPitch);  // [4 rows][high, low][32 lanes]
+    // [high, low][4 rows][128 outputs]; output o at o ^ ((o >> 5) & 3), so that the outputs of 32 neighbouring
+    // positions lie on distinct banks
+    int* sums = reinterpret_cast<int*>(smem + BulkSmem::kX + warp * kTile * kXPitch);
+    static_assert(2 * 4 * kD * 4 <= kTile * kXPitch, "the sums fit in the warp's rows");
     float sq[4] = {0.f, 0.f, 0.f, 0.f};
-    float4 next[4];
-    auto load_rows = [&](int w) {
-        if (w >= kD / 4) return;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            next[i] = __ldg(reinterpret_cast<const float4*>(U + (size_t)(16 * (w >> 2) + 2 * (w & 3) + (i & 1) + 8 * (i >> 1)) * kD) + lane);
-    };
-    load_rows(warp);
+    // (Rolled, the loads moving up by a turn: this code runs three times per warp and
+    // would otherwise wait on its own instruction fetches.)
 #pragma unroll 1
     for (int w = warp; w < kD / 4; w += kBulkWarps) {
         const int ks = w >> 2, tq = w & 3;
-        const float4 u[4] = {next[0], next[1], next[2], next[3]};
-        load_rows(w + kBulkWarps);
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const float4 ui = i == 0 ? u[0] : i == 1 ? u[1] : i == 2 ? u[2] : u[3];
-            const float x[4] = {ui.x * up, ui.y * up, ui.z * up, ui.w * up};
-            int v[2][4];  // x = v[0] + v[1] 2^-22
+        int v[2][16];  // input = v[0] + v[1] 2^-22
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[0][k] = __float2int_rn(x[k]);
-                v[1][k] = __float2int_rn((x[k] - __int2float_rn(v[0][k])) * 4194304.f);
+        for (int j = 0; j < 4; ++j) {
+            const float x[4] = {u[0][j].x * up, u[0][j].y * up, u[0][j].z * up, u[0][j].w * up};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 1.5 2^23 added rounds to an integer, in the low bits
+                const float m0 = __fadd_rn(x[k], 12582912.f);
+                const float m1 = __fadd_rn(__fsub_rn(x[k], __fsub_rn(m0, 12582912.f)) * 4194304.f, 12582912.f);
+                v[0][4 * j + k] = __float_as_int(m0) - 0x4b400000;
+                v[1][4 * j + k] = __float_as_int(m1) - 0x4b400000;
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int t0 = v[h][0] + v[h][1], t1 = v[h][0] - v[h][1], t2 = v[h][2] + v[h][3], t3 = v[h][2] - v[h][3];
-                v[h][0] = t0 + t2;
-                v[h][1] = t1 + t3;
-                v[h][2] = t0 - t2;
-                v[h][3] = t1 - t3;
-            }
-#pragma unroll 1
-            for (int m = 1; m < 32; m <<= 1) {
-                const bool upper = (lane & m) != 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int o = __shfl_xor_sync(kFull, v[h][k], m);
-                        v[h][k] = upper ? o - v[h][k] : v[h][k] + o;
-                    }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) sums[(2 * i + h) * 32 + lane] = make_int4(v[h][0], v[h][1], v[h][2], v[h][3]);
         }
+#pragma unroll
+        for (int t = 0; t + 1 < kTurns; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[t][j] = u[t + 1][j];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!(i & m)) {
+                        const int x = v[h][i], y = v[h][i | m];
+                        v[h][i] = x + y;
+                        v[h][i | m] = x - y;
+                    }
+#pragma unroll 1
+        for (int m = 1; m < 8; m <<= 1) {
+            const int sign = (lane & m) ? -1 : 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[h][i] = v[h][i] * sign + __shfl_xor_sync(kFull, v[h][i], m);
+        }
+        __syncwarp();  // (the last turn's sums are read)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<int4*>(sums + (4 * h + (lane >> 3)) * kD + 32 * j + 4 * (lane & 7)) =
+                    make_int4(v[h][4 * j + j], v[h][4 * j + (1 ^ j)], v[h][4 * j + (2 ^ j)], v[h][4 * j + (3 ^ j)]);
+        __syncwarp();
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-            const int p = 32 * bitrev2(k) + bitrev5(lane);  // stored position of Hadamard output 4 lane + k
+            const int p = 32 * k + lane, l = bitrev5(lane);  // stored position p is output 4 l + bitrev2(k)
+            const int* from = sums + 4 * l + (bitrev2(k) ^ (l >> 3));
             uint32_t h1[4], h2[4];
             float r[4], ss = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int va = reinterpret_cast<const int*>(sums + (2 * i) * 32 + lane)[k];
-                const int vb = reinterpret_cast<const int*>(sums + (2 * i + 1) * 32 + lane)[k];
+                const int va = from[i * kD], vb = from[(4 + i) * kD];
                 const float hi = __int2float_rn(va);
                 const float lo = __int2float_rn((va - __float2int_rn(hi)) * 4194304 + vb) * (1.f / 4194304.f);
                 float ph = __fmul_rn(hi, kc_hi);
@@ -168,7 +192,7 @@ __device__ __forceinline__ void bulk_matrix(const float* U, uint8_t* smem, int& 
                     __float_as_uint(__fadd_rn(__fsub_rn(__fsub_rn(ph, r1), __half2float(f2)), pe)) & 0xffffff00u);
                 ss = fmaf(ph, ph, ss);
             }
-            const int at = ks * kStepWords + (p >> 3) * 32 + 4 * (p & 7) + tq;
+            const int at = frag_at(ks, p, tq);
             frag[at] = make_uint2(h1[0] | (h1[1] << 16), h1[2] | (h1[3] << 16));
             frag[8 * kStepWords + at] = make_uint2(h2[0] | (h2[1] << 16), h2[2] | (h2[3] << 16));
             r3[at] = make_float4(r[0], r[1], r[2], r[3]);
@@ -177,7 +201,7 @@ __device__ __forceinline__ void bulk_matrix(const float* U, uint8_t* smem, int& 
         }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) atomicAdd(col + 32 * bitrev2(k) + bitrev5(lane), sq[k]);
+    for (int k = 0; k < 4; ++k) atomicAdd(col + 32 * k + lane, sq[k]);
     __syncthreads();
     float c2 = 0.f;
 #pragma unroll
@@ -192,32 +216,27 @@ __device__ __forceinline__ void bulk_matrix(const float* U, uint8_t* smem, int& 
 // lane ks of a team sums k indices 16 ks .. 16 ks + 15.
 __device__ __noinline__ df bulk_exact(const uint8_t* smem, const uint8_t* xrow, int p, float down) {
     const int ks = threadIdx.x & 7;
-    const int at = ks * kStepWords + (p >> 3) * 32 + 4 * (p & 7);
-    const uint4* f1 = reinterpret_cast<const uint4*>(smem + BulkSmem::kFrag) + at / 2;
-    const uint4* f2 = f1 + 8 * kStepWords / 2;
-    const float4* f3 = reinterpret_cast<const float4*>(smem + BulkSmem::kR3) + at;
+    const uint2* f1 = reinterpret_cast<const uint2*>(smem + BulkSmem::kFrag);
+    const uint2* f2 = f1 + 8 * kStepWords;
+    const float4* f3 = reinterpret_cast<const float4*>(smem + BulkSmem::kR3);
     const uint4 xa = *reinterpret_cast<const uint4*>(xrow + 32 * ks), xb = *reinterpret_cast<const uint4*>(xrow + 32 * ks + 16);
     const uint32_t xl[4] = {xa.x, xa.y, xa.z, xa.w}, xh[4] = {xb.x, xb.y, xb.z, xb.w};  // k = 2 tq, + 1; 8 + 2 tq, + 1
     float s = 0.f, c = 0.f;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const uint4 h1 = f1[half], h2 = f2[half];
+    for (int tq = 0; tq < 4; ++tq) {  // fragment word pair of quad member tq
+        const int at = frag_at(ks, p, tq);
+        const uint2 u1 = f1[at], u2 = f2[at];
+        const float4 r = f3[at];
+        const float x[4] = {bf16_lo(xl[tq]), bf16_hi(xl[tq]), bf16_lo(xh[tq]), bf16_hi(xh[tq])};
+        const float h[4] = {half_lo(u1.x) + half_lo(u2.x), half_hi(u1.x) + half_hi(u2.x), half_lo(u1.y) + half_lo(u2.y),
+                            half_hi(u1.y) + half_hi(u2.y)};  // exact: 22 bits
+        const float q[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {  // fragment word pair of quad member tq = 2 half + i
-            const uint32_t u1 = i ? h1.z : h1.x, v1 = i ? h1.w : h1.y, u2 = i ? h2.z : h2.x, v2 = i ? h2.w : h2.y;
-            const float4 r = f3[2 * half + i];
-            const uint32_t xi = xl[2 * half + i], xj = xh[2 * half + i];
-            const float x[4] = {bf16_lo(xi), bf16_hi(xi), bf16_lo(xj), bf16_hi(xj)};
-            const float h[4] = {half_lo(u1) + half_lo(u2), half_hi(u1) + half_hi(u2), half_lo(v1) + half_lo(v2),
-                                half_hi(v1) + half_hi(v2)};  // exact: 22 bits
-            const float q[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float pr = __fmul_rn(x[k], h[k]), pe = __fmaf_rn(x[k], h[k], -pr);  // exact product
-                const df t = two_sum(s, pr);
-                s = t.hi;
-                c = __fadd_rn(__fmaf_rn(x[k], q[k], c), __fadd_rn(pe, t.lo));
-            }
+        for (int k = 0; k < 4; ++k) {
+            const float pr = __fmul_rn(x[k], h[k]), pe = __fmaf_rn(x[k], h[k], -pr);  // exact product
+            const df t = two_sum(s, pr);
+            s = t.hi;
+            c = __fadd_rn(__fmaf_rn(x[k], q[k], c), __fadd_rn(pe, t.lo));
         }
     }
     df y = two_sum(s, c);
@@ -427,10 +446,10 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
                 n2[e & 1] = fmaf(v0, v0, fmaf(v1, v1, n2[e & 1]));
                 a[e] = pack_f16x2_rn(v0, v1);
             }
-            const uint2* fb = frag + (((step16 >> 3) ^ 1) * 8 + ks) * kStepWords + lane;
+            const uint2* fb = frag + (((step16 >> 3) ^ 1) * 8 + ks) * kStepWords;
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-                const uint2 b = fb[n * 32];
+                const uint2 b = fb[n * 32 + (lane ^ (n & 3))];  // (frag_at)
                 mma_f16_16816(acc[n], a[0], a[1], a[2], a[3], b.x, b.y);
             }
         }
