@@ -28,6 +28,7 @@
 // code is larger than the instruction caches hold: loops are kept rolled and
 // warps in step (below) for that reason.
 #include <algorithm>
+#include <climits>
 
 #include "pairs.cuh"
 
@@ -333,53 +334,44 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
     ushort4* list = reinterpret_cast<ushort4*>(smem + BulkSmem::kList) + warp / kGroupWarps * (kGroupWarps * kTile * 4);
     int* n_list = reinterpret_cast<int*>(smem + BulkSmem::kCol) + kD + 1 + warp / kGroupWarps;
 
-    // Lane r < 16 (and 16 + r) looks token r of a tile up: its row (-1: skipped)
-    // and where it goes.  Done a tile ahead, with the rows requested into L2.
+    // Lane r < 16 (and 16 + r) looks token r of a tile up, in steps a tile
+    // apart so that nothing waits for a load: its indices two tiles ahead; the
+    // checks, the row's request into L2 and the page's load one tile ahead;
+    // the row's copy at the end of the tile before.
     struct Token {
-        int row, slot;
-        uint8_t* to;
+        int row, seq, pos;
     };
-    auto look_up = [&](int tile) {
-        Token k{-1, 0, nullptr};
+    auto fetch = [&](int tile) {
+        Token k{-1, -1, 0};
         const int i = tile * kTile + (lane & 15);
         if (i < p.n_tok) {
             k.row = p.src_row ? __ldg(p.src_row + i) : i;
-            if (k.row < 0 || k.row >= p.src_rows) {
-                k.row = -1;
-                report(p.status, OSCAR_STATUS_BAD_POS);
-            } else {
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.src_kv + ((size_t)k.row * pairs + pair) * kD + 64 * (lane >> 4)));
-                const int seq = __ldg(p.dst_seq + i), pos = __ldg(p.dst_pos + i);
-                if (pos < 0 || pos >= p.max_pages * kPage || seq < 0 || seq >= p.batch) {
-                    report(p.status, OSCAR_STATUS_BAD_POS);
-                } else {
-                    const int page = __ldg(p.page_table + (size_t)seq * p.max_pages + pos / kPage);
-                    if (page < 0 || page >= p.num_pages) report(p.status, OSCAR_STATUS_BAD_PAGE);
-                    else k.to = p.pool + ((size_t)page * p.hk + kv) * p.block_bytes + which * half_bytes4(p.gshift);
-                    k.slot = pos % kPage;
-                }
-            }
+            k.seq = __ldg(p.dst_seq + i);
+            k.pos = __ldg(p.dst_pos + i);
         }
         return k;
     };
-    // Two groups of six warps, each going through a tile together (its own
-    // barrier): left to themselves the warps spread over the loop's code and
-    // wait for instruction fetches half of the time, and in one group the
-    // tensor cores idle while the codes are made.
-    auto group_sync = [&]() {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / kGroupWarps), "r"(32 * kGroupWarps) : "memory");
+    struct Place {
+        int row, page, slot;  // row -1: skipped; page kNone: no destination
     };
-    const int first = blockIdx.x / pairs * kBulkWarps, rounds = (tiles - first + step - 1) / step;
-    Token next = look_up(first + warp);
-    for (int round = 0; round < rounds; ++round) {
-        const int tile = first + warp + round * step;
-        group_sync();
-        if (lane == 0 && warp % kGroupWarps == 0) *n_list = 0;  // (added to after a further barrier)
-        const int row = next.row;
-        if (lane < kTile) {  // (the last tile's stores have read dst and slots)
-            dst[lane] = next.to;
-            slots[lane] = next.slot;
+    constexpr int kNone = INT_MIN;
+    auto locate = [&](int tile, const Token& k) {
+        Place at{-1, kNone, k.pos % kPage};
+        if (tile * kTile + (lane & 15) < p.n_tok) {
+            if (k.row < 0 || k.row >= p.src_rows) {
+                report(p.status, OSCAR_STATUS_BAD_POS);
+            } else {
+                at.row = k.row;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.src_kv + ((size_t)k.row * pairs + pair) * kD + 64 * (lane >> 4)));
+                if (k.pos < 0 || k.pos >= p.max_pages * kPage || k.seq < 0 || k.seq >= p.batch)
+                    report(p.status, OSCAR_STATUS_BAD_POS);
+                else
+                    at.page = __ldg(p.page_table + (size_t)k.seq * p.max_pages + k.pos / kPage);
+            }
         }
+        return at;
+    };
+    auto copy_rows = [&](int row) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {  // two rows of 16 chunks at a time
             const int r = 2 * c + (lane >> 4), ch = lane & 15;
@@ -393,7 +385,31 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
                 *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        next = look_up(tile + step);
+    };
+    // Two groups of six warps, each going through a tile together (its own
+    // barrier): left to themselves the warps spread over the loop's code and
+    // wait for instruction fetches half of the time, and in one group the
+    // tensor cores idle while the codes are made.
+    auto group_sync = [&]() {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / kGroupWarps), "r"(32 * kGroupWarps) : "memory");
+    };
+    const int first = blockIdx.x / pairs * kBulkWarps, rounds = (tiles - first + step - 1) / step;
+    Place now = locate(first + warp, fetch(first + warp));
+    Token next = fetch(first + warp + step);
+    copy_rows(now.row);
+    for (int round = 0; round < rounds; ++round) {
+        const int tile = first + warp + round * step;
+        group_sync();
+        if (lane == 0 && warp % kGroupWarps == 0) *n_list = 0;  // (added to after a further barrier)
+        const int row = now.row;
+        if (lane < kTile) {  // (the last tile's stores have read dst and slots)
+            const bool ok = now.page >= 0 && now.page < p.num_pages;
+            if (!ok && now.page != kNone) report(p.status, OSCAR_STATUS_BAD_PAGE);
+            dst[lane] = ok ? p.pool + ((size_t)now.page * p.hk + kv) * p.block_bytes + which * half_bytes4(p.gshift) : nullptr;
+            slots[lane] = now.slot;
+        }
+        now = locate(tile + step, next);
+        next = fetch(tile + 2 * step);
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
         if (p.new_kv) {  // fused ring append: overwrite the rows just read
@@ -646,6 +662,7 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
                 bulk_group_exact(smem, xs + row16 * kXPitch, stg + row16 * kStgPitch, sz + row16 * 4, bit & 3, nb, cr, rdown);
             }
         __syncwarp();
+        copy_rows(now.row);  // the next tile's (these rows have been read for the last time)
 
         // -- stores
         if (which == 0) {  // 16-byte chunk a of a token: word k = bytes 16 k + 4 a .. + 3
