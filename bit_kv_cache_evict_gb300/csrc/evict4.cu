@@ -272,9 +272,10 @@ cudaError_t launch(const EvictParams& p, cudaStream_t st) {
 }
 
 // Calls with this many vectors (tokens x KV heads x 2) take the bulk kernel: it
-// starts with 18 us of forming R in every block and then needs 0.5 ns per
-// vector, this kernel 7.3 ns (GB300, 8 KV heads: 192 tokens 23 us here and 31
-// us there, 256 tokens 31 and 31, 15,104 tokens 1830 and 120).
+// starts with 11 us of forming R in every block and then needs 0.5 ns per
+// vector, this kernel 7.3 ns (GB300, 8 KV heads: 128 tokens 16 us here and 24
+// us there, 192 tokens 24 and 24, 256 tokens 26 and 24, 320 tokens 32 and 24,
+// 15,104 tokens 1830 and 125).
 constexpr int kBulkVectors = 4096;
 
 }  // namespace

@@ -1,6 +1,6 @@
 // evict_bulk.cu -- eviction of many tokens at once into the 4-bit history (a
-// prompt's history): the same codes and pairs as evict_kernel<., 4>
-// (evict.cu), with the rotation on tensor cores.
+// prompt's history): the same codes and pairs as evict4_kernel
+// (evict4.cu), with the rotation on tensor cores.
 //
 // The mathematics.  A vector's decisions (s, z, codes) have to be those of the
 // exact rotated values, while a tensor-core product gives y within some
@@ -9,7 +9,7 @@
 // one group in 25 for s or z, one code in 10^4) are taken again from exactly
 // summed values.
 //   Product: y = x . R, R = U . Hadamard . bit-reversal / sqrt(d) formed once
-// per block in 64-bit fixed point and kept as fp16 parts h1 + h2 (22 bits) and
+// per block in fixed point and kept as fp16 parts h1 + h2 (22 bits) and
 // a remainder r3 of 16 bits, all scaled by a power of two; x (bf16) is scaled per row into
 // fp16, exactly.  acc = x . h2 first, then x . h1: the second sum's eight
 // accumulation steps each lose at most 2^-23 of a partial sum, which is at
@@ -21,12 +21,14 @@
 //
 // What bounds it: 512 bytes read and 160 written per token and KV head
 // (24 us for 15,104 tokens of eight KV heads), 256 tensor-core products per
-// 16 vectors, and about 1,300 instructions for their decisions.  Measured 141
-// us for that case (the per-vector kernel: 1832 us): 18 us for R, then per
-// 16-token tile a quarter of the time in the products (at the rate of
-// mma.sync), a sixth each in the exact sums and in the codes.  The kernel's
+// 16 vectors, and their decisions: 4,900 instructions in all.  Measured 125 us
+// for that case (GB300; 0.65 TB/s; the per-vector kernel: 1832 us): 11 us for
+// R, then per 16-token tile a third of the time in the products (at the rate
+// of mma.sync), a sixth in the exact sums, an eighth in the codes; the
+// schedulers issue in 54 % of the cycles, the tensor cores run in 22 %.  The kernel's
 // code is larger than the instruction caches hold: loops are kept rolled and
-// warps in step (below) for that reason.
+// warps in step (below) for that reason.  (16 warps of 128 registers instead of
+// 12 of 168: 128 us; groups of four warps: 132.)
 #include <algorithm>
 #include <climits>
 
