@@ -182,6 +182,19 @@ struct WarpState {
 };
 constexpr int kNoScale = 64;
 
+// How the products of a page are laid out in the code: kTiles token tiles of 16
+// per turn of a loop (less code to fetch, against less to schedule), kSide of them
+// (logits) and kSideV M tiles (values) side by side, so that their chains of
+// products interleave and share the B fragments.  32 x 32K, eight KV heads, us, as (kTiles, kSide,
+// kSideV) for groups of 32, 64, 128:
+//            1,1,1          2,2,2          4,2,1          4,4,2
+// 4 heads    283 251 232    286 237 220    294 234 217    298 242 216
+// 8 heads    443 391 324    427 372 325    465 368 311    422 353 310
+template <int NT, int GS>
+struct Shape {
+    static constexpr int kTiles = NT == 1 && GS == 0 ? 1 : 4, kSide = NT == 2 ? 4 : GS == 0 ? 1 : 2, kSideV = NT;
+};
+
 // K half of a page: logits (base 2) of the lane's tokens 16m + gID and
 // 16m + gID + 8.  Up to four heads: lg[m][0], lg[m][1] = the two tokens of
 // head tq; eight heads: (token a, heads 2tq, 2tq+1), (token b, the same).
@@ -208,52 +221,63 @@ __device__ __forceinline__ void page_logits(const uint8_t* half, int valid, uint
         store_n<NB>(kzS + t * NB, zv);
     }
     __syncwarp();
-    // Token tiles of 16 in a rolled loop, one at a time up to four heads (all
-    // four: 334 us for the batch of 64; two: 329; one: 327: less code to fetch),
-    // unrolled for eight (one: 327 for 32 x 32K; two: 320; four: 317).
-    constexpr int kTiles = NT == 1 ? 1 : 4;
+    constexpr int kTiles = Shape<NT, GS>::kTiles, kSide = Shape<NT, GS>::kSide;
 #pragma unroll 1
     for (int m0 = 0; m0 < 4; m0 += kTiles) {
         float cur[kTiles][2 * NT];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-            const int ta = 16 * (m0 + m) + gID;
-            const uint4 xa = *reinterpret_cast<const uint4*>(half + ta * (kD / 2) + 16 * tq);
-            const uint4 xb = *reinterpret_cast<const uint4*>(half + (ta + 8) * (kD / 2) + 16 * tq);
-            const uint32_t wa[4] = {xa.x, xa.y, xa.z, xa.w}, wb[4] = {xb.x, xb.y, xb.z, xb.w};
-            float acc[NB][4];
+        for (int m1 = 0; m1 < kTiles; m1 += kSide) {
+            uint32_t wa[kSide][4], wb[kSide][4];
+            float acc[kSide][NB][4];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int i = 0; i < kSide; ++i) {
+                const int ta = 16 * (m0 + m1 + i) + gID;
+                const uint4 xa = *reinterpret_cast<const uint4*>(half + ta * (kD / 2) + 16 * tq);
+                const uint4 xb = *reinterpret_cast<const uint4*>(half + (ta + 8) * (kD / 2) + 16 * tq);
+                wa[i][0] = xa.x; wa[i][1] = xa.y; wa[i][2] = xa.z; wa[i][3] = xa.w;
+                wb[i][0] = xb.x; wb[i][1] = xb.y; wb[i][2] = xb.z; wb[i][3] = xb.w;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[b][e] = 0.f;
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][b][e] = 0.f;
+            }
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                uint32_t ra[4], rb[4];
-                in_place4(wa[b], ra);
-                in_place4(wb[b], rb);
+                uint32_t ra[kSide][4], rb[kSide][4];
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                    in_place4(wa[i][b], ra[i]);
+                    in_place4(wb[i][b], rb[i]);
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {  // eight heads: the high, then the low parts
                         const uint2 q = qf[(nt * 8 + 2 * b + h) * 32 + lane];
-                        mma_f16_16816(acc[b >> GS], ra[2 * h], rb[2 * h], ra[2 * h + 1], rb[2 * h + 1], q.x, q.y);
+#pragma unroll
+                        for (int i = 0; i < kSide; ++i)
+                            mma_f16_16816(acc[i][b >> GS], ra[i][2 * h], rb[i][2 * h], ra[i][2 * h + 1], rb[i][2 * h + 1], q.x, q.y);
                     }
             }
-            float sa[NB], za[NB], sb[NB], zb[NB];
-            load_n<NB>(ksS + ta * NB, sa);
-            load_n<NB>(ksS + (ta + 8) * NB, sb);
-            load_n<NB>(kzS + ta * NB, za);
-            load_n<NB>(kzS + (ta + 8) * NB, zb);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float x = 0.f, y = 0.f;
+            for (int i = 0; i < kSide; ++i) {
+                const int m = m1 + i, ta = 16 * (m0 + m) + gID;
+                float sa[NB], za[NB], sb[NB], zb[NB];
+                load_n<NB>(ksS + ta * NB, sa);
+                load_n<NB>(ksS + (ta + 8) * NB, sb);
+                load_n<NB>(kzS + ta * NB, za);
+                load_n<NB>(kzS + (ta + 8) * NB, zb);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    x = fmaf(sa[b], NT == 1 ? acc[b][0] + acc[b][1] : acc[b][j], fmaf(za[b], qsv[j][b], x));
-                    y = fmaf(sb[b], NT == 1 ? acc[b][2] + acc[b][3] : acc[b][2 + j], fmaf(zb[b], qsv[j][b], y));
+                for (int j = 0; j < NT; ++j) {
+                    float x = 0.f, y = 0.f;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        x = fmaf(sa[b], NT == 1 ? acc[i][b][0] + acc[i][b][1] : acc[i][b][j], fmaf(za[b], qsv[j][b], x));
+                        y = fmaf(sb[b], NT == 1 ? acc[i][b][2] + acc[i][b][3] : acc[i][b][2 + j], fmaf(zb[b], qsv[j][b], y));
+                    }
+                    cur[m][j] = x;
+                    cur[m][NT == 1 ? 1 : 2 + j] = y;
                 }
-                cur[m][j] = x;
-                cur[m][NT == 1 ? 1 : 2 + j] = y;
             }
         }
         // the tiles move up: tile m ends in lg[m] after the last turn
@@ -420,24 +444,37 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
         if (GS == 0 || (b & ((1 << GS) - 1)) == 0)
 #pragma unroll
             for (int m = 0; m < 4; ++m) weights(b >> GS, m, r[m]);
+        constexpr int kSideV = Shape<NT, GS>::kSideV;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4*>(vb + (2 * b + k) * 8 * kPage);
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k0 = 0; k0 < 2; k0 += kSideV) {
+            uint4 v[kSideV];
+            float t[kSideV][4];
+#pragma unroll
+            for (int k = 0; k < kSideV; ++k) {
+                v[k] = *reinterpret_cast<const uint4*>(vb + (2 * b + k0 + k) * 8 * kPage);
+                t[k][0] = t[k][1] = t[k][2] = t[k][3] = 0.f;
+            }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                uint32_t c[4];
-                unpack4(m == 0 ? v.x : m == 1 ? v.y : m == 2 ? v.z : v.w, c);
-                mma_f16_16816(t, c[0], c[1], c[2], c[3], r[m][0], r[m][1]);
-                if constexpr (NT == 2) mma_f16_16816(t, c[0], c[1], c[2], c[3], r[m][2], r[m][3]);
+                uint32_t c[kSideV][4];
+#pragma unroll
+                for (int k = 0; k < kSideV; ++k) unpack4(m == 0 ? v[k].x : m == 1 ? v[k].y : m == 2 ? v[k].z : v[k].w, c[k]);
+#pragma unroll
+                for (int k = 0; k < kSideV; ++k) mma_f16_16816(t[k], c[k][0], c[k][1], c[k][2], c[k][3], r[m][0], r[m][1]);
+                if constexpr (NT == 2)
+#pragma unroll
+                    for (int k = 0; k < kSideV; ++k) mma_f16_16816(t[k], c[k][0], c[k][1], c[k][2], c[k][3], r[m][2], r[m][3]);
             }
-            float(&acc)[4] = st.acc[2 * b + k];
-            const float2 a0 = add2(make_float2(acc[0], acc[1]), make_float2(t[0], t[1]));
-            const float2 a1 = add2(make_float2(acc[2], acc[3]), make_float2(t[2], t[3]));
-            acc[0] = a0.x;
-            acc[1] = a0.y;
-            acc[2] = a1.x;
-            acc[3] = a1.y;
+#pragma unroll
+            for (int k = 0; k < kSideV; ++k) {
+                float(&acc)[4] = st.acc[2 * b + k0 + k];
+                const float2 a0 = add2(make_float2(acc[0], acc[1]), make_float2(t[k][0], t[k][1]));
+                const float2 a1 = add2(make_float2(acc[2], acc[3]), make_float2(t[k][2], t[k][3]));
+                acc[0] = a0.x;
+                acc[1] = a0.y;
+                acc[2] = a1.x;
+                acc[3] = a1.y;
+            }
         }
     }
 }

@@ -93,8 +93,8 @@ inline cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t s
 // Blocks per SM of the 4-bit history kernel: three (128 registers); two (168, and
 // four page halves per warp instead of two) for eight query heads per KV head
 // with two or four quantisation groups per vector, whose state would spill:
-// 32 x 32K, 64 query heads, groups of 32: 508 us with three blocks, 444 with two;
-// groups of 64: 363 and 354; groups of 128: 313 and 329.
+// 32 x 32K, 64 query heads, groups of 32: 470 us with three blocks, 422 with two;
+// groups of 64: 373 and 353; groups of 128: 310 and 343.
 __host__ __device__ constexpr int int4_blocks_per_sm(int nt, int gshift) { return nt == 2 && gshift < 2 ? 2 : 3; }
 
 // the 4-bit history kernel (int4.cu), launched by launch_decode4 between prep_kernel and bf16_kernel
