@@ -33,10 +33,10 @@
 // warp owns a ring of halves and gives one back as soon as it has read it).
 // Measured (GB300, copy peak 6.79 TB/s): batch 64, 4K-32K, four heads per KV
 // head, groups of 32: 282 us for 1.44 GB, 5.1 TB/s; 32 x 32K, eight heads,
-// groups of 128: 282 us for 1.13 GB, 4.0 TB/s.  The first is bound by its
+// groups of 128: 275 us for 1.13 GB, 4.1 TB/s.  The first is bound by its
 // instructions (about 360 per 16-token tile, issued in 63 % of the cycles by
-// 12 consumer warps per SM), the second by the latency of its chained
-// products (51 %).  The code of a page is kept small for the same reason: with
+// 12 consumer warps per SM), the second by its products (tensor pipe 42 %) and
+// their latency (issue 52 %).  The code of a page is kept small for the same reason: with
 // separate code for partial pages and every tile unrolled the warps waited on
 // instruction fetches, 295 us.
 #include "splitk.cuh"
