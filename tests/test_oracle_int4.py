@@ -127,3 +127,14 @@ def test_gather_moves_whole_vectors():
         same = np.ones(4, bool)
         same[1] = False
         assert np.array_equal(out.reshape(4, bb)[same], pool.reshape(4, bb)[same])
+
+
+def test_decode_of_the_window_alone_is_exact():
+    rng = np.random.default_rng(9)
+    hk, g, m = 2, 32, 6
+    U = np.linalg.qr(rng.standard_normal((hk, 2, D, D)))[0]
+    kv, q = rng.standard_normal((1, 8, hk, 2, D)), rng.standard_normal((1, 4, D))
+    out, _ = I.decode(q, kv, [m], np.zeros(hk * I.block_bytes(4, g), np.uint8), np.array([[0]]), [0], U, 0.3, g)
+    for h in range(4):
+        p = np.exp(0.3 * kv[0, :m, h // 2, 0] @ q[0, h])
+        assert np.allclose(out[0, h], p @ kv[0, :m, h // 2, 1] / p.sum(), rtol=0, atol=1e-13)
