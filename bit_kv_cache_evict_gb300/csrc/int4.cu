@@ -104,6 +104,12 @@ struct Ring {
     }
 };
 
+// mbar_wait_bounded by a whole warp: one branch per poll, the same for every lane
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity, kWaitPolls));
+}
+
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
@@ -663,13 +669,13 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
     Ring<NSW> ring;
 
     for (uint32_t j = 0;; ++j) {
-        if (!__all_sync(kFull, mbar_wait_bounded(&full[ring.slot], ring.phase, kWaitPolls))) return give_up();
+        if (!warp_wait(&full[ring.slot], ring.phase)) return give_up();
         const int4 sraw = *reinterpret_cast<const int4*>(&info[warp * 2 + (j & 1u)]);
         const int item = sraw.x, flags = sraw.w >> 8, valid = sraw.w & 0xff;
         if (item < 0) break;
         if (flags & kFlagFirst) {
             cur_qs = citem & 1u;
-            if (!__all_sync(kFull, mbar_wait_bounded(&qfull[cur_qs], (citem >> 1) & 1u, kWaitPolls))) return give_up();
+            if (!warp_wait(&qfull[cur_qs], (citem >> 1) & 1u)) return give_up();
             ++citem;
             const uint8_t* qb = smem + SM::kQb + cur_qs * SM::kQbBytes;
             qf = reinterpret_cast<const uint2*>(qb);
@@ -695,21 +701,21 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
                 for (int e = 0; e < 4; ++e) st.acc[mt][e] = 0.f;
             st.wexp = kNoScale;
         }
-        float lg[4][2 * NT], alpha[NT];
-        bool any = false;
-        const bool on = !(flags & kFlagPad);
-        if (on) {
-            const uint8_t* half = stages + ring.slot * kHalfMax;
+        const uint8_t* half = stages + ring.slot * kHalfMax;
+        if (flags & kFlagPad) {  // no page: give both halves back
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[ring.slot]);
+            ring.step();
+            if (!warp_wait(&full[ring.slot], ring.phase)) return give_up();
+        } else {
+            float lg[4][2 * NT], alpha[NT];
             page_logits<NT, GS>(half, valid, wbuf, qf, qsv, kq, lg);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[ring.slot]);
-        ring.step();
-        if (on) any = page_softmax<NT, GS>(lg, st, alpha);
-        if (!__all_sync(kFull, mbar_wait_bounded(&full[ring.slot], ring.phase, kWaitPolls))) return give_up();
-        if (on) {
-            const uint8_t* half = stages + ring.slot * kHalfMax;
-            page_values<NT, GS>(half, valid, wbuf, lg, alpha, any, take_lo, st);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[ring.slot]);
+            ring.step();
+            const bool any = page_softmax<NT, GS>(lg, st, alpha);
+            if (!warp_wait(&full[ring.slot], ring.phase)) return give_up();
+            page_values<NT, GS>(stages + ring.slot * kHalfMax, valid, wbuf, lg, alpha, any, take_lo, st);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[ring.slot]);
