@@ -32,13 +32,13 @@
 // stream of the pages, so K and V halves travel separately (each consumer
 // warp owns a ring of halves and gives one back as soon as it has read it).
 // Measured (GB300, copy peak 6.79 TB/s): batch 64, 4K-32K, four heads per KV
-// head, groups of 32: 282 us for 1.44 GB, 5.1 TB/s; 32 x 32K, eight heads,
-// groups of 128: 275 us for 1.13 GB, 4.1 TB/s.  The first is bound by its
-// instructions (about 360 per 16-token tile, issued in 63 % of the cycles by
-// 12 consumer warps per SM), the second by its products (tensor pipe 42 %) and
-// their latency (issue 52 %).  The code of a page is kept small for the same reason: with
-// separate code for partial pages and every tile unrolled the warps waited on
-// instruction fetches, 295 us.
+// head, groups of 32: 275 us for 1.44 GB, 5.2 TB/s; 32 x 32K, eight heads,
+// groups of 128: 266 us for 1.13 GB, 4.2 TB/s.  The first is bound by its
+// instructions (about 350 per 16-token tile, issued in 63 % of the cycles by
+// 12 consumer warps per SM), the second by its products (tensor pipe 44 %) and
+// their latency (issue 52 %).  The code of a page is kept small and free of
+// divergent branches for the same reason: with separate code for partial pages,
+// every tile unrolled and the waits polled lane by lane it took 295 and 282 us.
 #include "splitk.cuh"
 
 namespace oscar {
@@ -194,11 +194,11 @@ constexpr int kNoScale = 64;
 // products interleave and share the B fragments.  32 x 32K, eight KV heads, us, as (kTiles, kSide,
 // kSideV) for groups of 32, 64, 128:
 //            1,1,1          2,2,2          4,2,1          4,4,2
-// 4 heads    283 251 232    286 237 220    294 234 217    298 242 216
-// 8 heads    443 391 324    427 372 325    465 368 311    422 353 310
+// 4 heads    275 239 226    283 232 216    291 229 213    289 247 219
+// 8 heads    422 370 315    411 358 318    435 333 295    407 345 300
 template <int NT, int GS>
 struct Shape {
-    static constexpr int kTiles = NT == 1 && GS == 0 ? 1 : 4, kSide = NT == 2 ? 4 : GS == 0 ? 1 : 2, kSideV = NT;
+    static constexpr int kTiles = NT == 1 && GS == 0 ? 1 : 4, kSide = GS > 0 ? 2 : NT == 1 ? 1 : 4, kSideV = GS > 0 ? 1 : NT;
 };
 
 // K half of a page: logits (base 2) of the lane's tokens 16m + gID and

@@ -92,10 +92,10 @@ inline cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t s
 
 // Blocks per SM of the 4-bit history kernel: three (128 registers); two (168, and
 // four page halves per warp instead of two) for eight query heads per KV head
-// with two or four quantisation groups per vector, whose state would spill:
-// 32 x 32K, 64 query heads, groups of 32: 470 us with three blocks, 422 with two;
-// groups of 64: 373 and 353; groups of 128: 310 and 343.
-__host__ __device__ constexpr int int4_blocks_per_sm(int nt, int gshift) { return nt == 2 && gshift < 2 ? 2 : 3; }
+// with four quantisation groups per vector, whose state would spill: 32 x
+// 32K, 64 query heads, groups of 32: 437 us with three blocks, 407 with two;
+// groups of 64: 333 and 339; groups of 128: 295 and 321.
+__host__ __device__ constexpr int int4_blocks_per_sm(int nt, int gshift) { return nt == 2 && gshift == 0 ? 2 : 3; }
 
 // the 4-bit history kernel (int4.cu), launched by launch_decode4 between prep_kernel and bf16_kernel
 cudaError_t launch_int4(const DecodeParams4& p, cudaStream_t st, int dev);
