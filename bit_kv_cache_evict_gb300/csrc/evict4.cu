@@ -272,7 +272,7 @@ cudaError_t launch(const EvictParams& p, cudaStream_t st) {
 }
 
 // Calls with this many vectors (tokens x KV heads x 2) take the bulk kernel: it
-// starts with 11 us of forming R in every block and then needs 0.5 ns per
+// starts with 9 us of forming R in every block and then needs 0.5 ns per
 // vector, this kernel 7.3 ns (GB300, 8 KV heads: 128 tokens 16 us here and 24
 // us there, 192 tokens 24 and 24, 256 tokens 26 and 24, 320 tokens 32 and 24,
 // 15,104 tokens 1830 and 125).

@@ -559,3 +559,53 @@ def test_eviction_and_decode_past_32_bit_offsets():
     ws = torch.zeros(O.oscar_decode_workspace_bytes_int4(c.sh, c.B, c.max_pages), dtype=torch.uint8, device="cuda")
     O.oscar_decode_attn_int4(c.sh, d["q"], d["kv"], d["len"], big.view(-1), up, c.max_pages, pages, hist, d["U"], SCALE, high, ws)
     assert torch.equal(low, high) and low.isfinite().all()
+
+
+@pytest.mark.parametrize("hk,n", [(5, 450), (80, 40), (1, 2111)])
+def test_many_tokens_with_other_counts_of_kv_heads(hk, n):
+    """More (KV head, K|V) pairs than SMs, one, and a count that divides nothing."""
+    rng = np.random.default_rng(hk)
+    x, U = H.bf16_t(kv_bits(rng, n, hk)), H.f32_t(rotation(rng, hk))
+    clip = torch.full((hk, 2), 0.9, device="cuda")
+    pages = (n + 63) // 64
+    table = rng.permutation(pages).astype(np.int32)[None]
+    pos, seq = H.i32_t(rng.permutation(n)), H.i32_t(np.zeros(n))
+    few, st1 = evict_in_calls(x, U, clip, pos, seq, table, 64, max(1, 2000 // hk))
+    many, st2 = evict_in_calls(x, U, clip, pos, seq, table, 64, None)
+    assert st1 == 0 and st2 == 0 and torch.equal(few, many)
+
+
+def test_rows_with_nan_and_infinity_leave_the_others_alone():
+    rng = np.random.default_rng(8)
+    hk, n, g = 8, 300, 32
+    x = H.bf16_t(kv_bits(rng, n, hk))
+    U, clip = H.f32_t(rotation(rng, hk)), torch.full((hk, 2), 0.9, device="cuda")
+    table, pos, seq = np.arange(5, dtype=np.int32)[None], H.i32_t(np.arange(n)), H.i32_t(np.zeros(n))
+    clean, _ = evict_in_calls(x, U, clip, pos, seq, table, g, None)
+    bad = [3, 17, 40, 41, 299]
+    x[3, 0, 0, 5], x[17], x[40, :, 1, 0], x[41, 2, 0] = float("nan"), float("inf"), -float("inf"), float("nan")
+    x[299, :, :, ::2] = 3e38
+    for per_call in (None, 7):
+        pool, status = evict_in_calls(x, U, clip, pos, seq, table, g, per_call)
+        assert status == 0
+        a, b = (p.view(5, hk, -1).cpu().numpy() for p in (clean, pool))
+        for t in sorted(set(range(n)) - set(bad)):
+            for w in (0, 1):
+                at = np.concatenate([I.pair_bytes(4, g, w, t % 64).ravel(), I.code_bytes(4, g, w, t % 64)[0]])
+                assert np.array_equal(a[t // 64][:, at], b[t // 64][:, at]), (t, w)
+
+
+@pytest.mark.parametrize("hq,hk,g", [(4, 1, 32), (16, 2, 128)])
+def test_a_sequence_with_nan_leaves_the_others_alone(hq, hk, g):
+    c = Cache(40, [500, 700, 130, 64], hq, hk, g)
+    want = c.want()
+    pool = c.pool.reshape(c.num_pages, hk, -1)
+    nan = np.full(2 * (D // g), 0x7E00, np.uint16).view(np.uint8)
+    for page in c.table[1, :3]:
+        for w in (0, 1):
+            pool[page][:, I.pair_bytes(4, g, w, 9).ravel()] = nan
+    c.q[1, 1], c.kv[1, 7] = 0x7FC0, 0x7F80
+    out = c.decode()
+    keep = [0, 2, 3]
+    check(out[keep], *[x[keep] for x in want])
+    assert out[1].isnan().any()
