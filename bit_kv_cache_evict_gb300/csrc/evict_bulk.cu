@@ -224,7 +224,7 @@ __device__ __noinline__ df bulk_exact(const uint8_t* smem, const uint8_t* xrow, 
     const float4* f3 = reinterpret_cast<const float4*>(smem + BulkSmem::kR3);
     const uint4 xa = *reinterpret_cast<const uint4*>(xrow + 32 * ks), xb = *reinterpret_cast<const uint4*>(xrow + 32 * ks + 16);
     const uint32_t xl[4] = {xa.x, xa.y, xa.z, xa.w}, xh[4] = {xb.x, xb.y, xb.z, xb.w};  // k = 2 tq, + 1; 8 + 2 tq, + 1
-    float s = 0.f, c = 0.f;
+    float s[4], c[4];  // four chains
 #pragma unroll
     for (int tq = 0; tq < 4; ++tq) {  // fragment word pair of quad member tq
         const int at = frag_at(ks, p, tq);
@@ -237,12 +237,19 @@ __device__ __noinline__ df bulk_exact(const uint8_t* smem, const uint8_t* xrow, 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float pr = __fmul_rn(x[k], h[k]), pe = __fmaf_rn(x[k], h[k], -pr);  // exact product
-            const df t = two_sum(s, pr);
-            s = t.hi;
-            c = __fadd_rn(__fmaf_rn(x[k], q[k], c), __fadd_rn(pe, t.lo));
+            if (tq == 0) {
+                s[k] = pr;
+                c[k] = __fmaf_rn(x[k], q[k], pe);
+            } else {
+                const df t = two_sum(s[k], pr);
+                s[k] = t.hi;
+                c[k] = __fadd_rn(__fmaf_rn(x[k], q[k], c[k]), __fadd_rn(pe, t.lo));
+            }
         }
     }
-    df y = two_sum(s, c);
+    const df s01 = two_sum(s[0], s[1]), s23 = two_sum(s[2], s[3]), sa = two_sum(s01.hi, s23.hi);
+    const float rest = __fadd_rn(__fadd_rn(__fadd_rn(c[0], c[1]), __fadd_rn(c[2], c[3])), __fadd_rn(s01.lo, s23.lo));
+    df y = two_sum(sa.hi, __fadd_rn(sa.lo, rest));
 #pragma unroll
     for (int m = 1; m < 8; m <<= 1)
         y = df_add(y, df{__shfl_xor_sync(kFull, y.hi, m), __shfl_xor_sync(kFull, y.lo, m)});
@@ -453,29 +460,37 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
         for (int n = 0; n < 16; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll 1
-        for (int step16 = 0; step16 < 16; ++step16) {
-            const int ks = step16 & 7;
-            uint32_t a[4];
-            bulk_ldsm(a, xfrag + 32 * ks);
+        uint32_t raw[4], a[4];
+        auto scale = [&](bool sum) {  // raw to fp16; the sum of squares
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float v0 = bf16_lo(a[e]) * up[e & 1], v1 = bf16_hi(a[e]) * up[e & 1];
-                n2[e & 1] = fmaf(v0, v0, fmaf(v1, v1, n2[e & 1]));
+                const float v0 = bf16_lo(raw[e]) * up[e & 1], v1 = bf16_hi(raw[e]) * up[e & 1];
+                if (sum) n2[e & 1] = fmaf(v0, v0, fmaf(v1, v1, n2[e & 1]));
                 a[e] = pack_f16x2_rn(v0, v1);
             }
-            const uint2* fb = frag + (((step16 >> 3) ^ 1) * 8 + ks) * kStepWords;
+        };
+        bulk_ldsm(raw, xfrag);
+        uint2 b[16];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) b[n] = frag[8 * kStepWords + n * 32 + (lane ^ (n & 3))];  // (frag_at)
+        scale(true);
+#pragma unroll 1
+        for (int step16 = 0; step16 < 16; ++step16) {  // (the next step's operands are loaded and made while the products run)
+            const int next16 = (step16 + 1) & 15;
+            bulk_ldsm(raw, xfrag + 32 * (next16 & 7));
+            const uint2* fn = frag + (((next16 >> 3) ^ 1) * 8 + (next16 & 7)) * kStepWords;
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-                const uint2 b = fb[n * 32 + (lane ^ (n & 3))];  // (frag_at)
-                mma_f16_16816(acc[n], a[0], a[1], a[2], a[3], b.x, b.y);
+                mma_f16_16816(acc[n], a[0], a[1], a[2], a[3], b[n].x, b[n].y);
+                b[n] = fn[n * 32 + (lane ^ (n & 3))];
             }
+            scale(step16 < 7);
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             n2[r] += __shfl_xor_sync(kFull, n2[r], 1);
-            n2[r] += __shfl_xor_sync(kFull, n2[r], 2);  // every element twice: 2 |x|^2
-            delta[r] = 1.5f * 9.5367431640625e-7f * sqrtf(0.5f * n2[r]) * 1.001f * rnorm * fdown[r];
+            n2[r] += __shfl_xor_sync(kFull, n2[r], 2);
+            delta[r] = 1.5f * 9.5367431640625e-7f * sqrtf(n2[r]) * 1.001f * rnorm * fdown[r];
         }
 #pragma unroll
         for (int n = 0; n < 16; ++n)
@@ -605,22 +620,22 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
                 const uint32_t w = sz[(gID + 8 * r) * 4 + b];
                 const float sf = half_lo(w), zf = half_hi(w), t = clip[r][b];
                 const float inv = sf != 0.f ? __fdividef(1.f, sf) : 0.f;
-                // u is off by delta / s and the rounding of three fp32 operations on |u| < 16
-                const float edge = 0.5f - (delta[r] * inv * 1.01f + 8e-6f);
+                // u = y / s - z / s, two elements an instruction: off by delta / s, by the rounding of z / s (|z| is at most
+                // |x| |R|, so a tenth of that) and by that of three fp32 operations on |u| < 16
+                const float nz = -zf * inv, edge = 0.5f - (delta[r] * inv * 1.01f + fabsf(nz) * 1.2e-7f + 8e-6f);
+                const float2 inv2 = make_float2(inv, inv), nz2 = make_float2(nz, nz), round2 = make_float2(12582912.f, 12582912.f);
                 // u of the clip thresholds and of the codes' range, as one pair of bounds (s = 0: every code 0)
                 const float ulo = sf != 0.f ? fmaxf(0.f, (-t - zf) * inv) : 0.f, uhi = sf != 0.f ? fminf(15.f, (t - zf) * inv) : 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int n = 4 * b + i;
-                    uint32_t c[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float u = fminf(fmaxf((acc[n][2 * r + e] - zf) * inv, ulo), uhi);
-                        const float m = u + 12582912.f;  // 1.5 2^23: rounds u to an integer, in the low bits
-                        if (!(fabsf(u - (m - 12582912.f)) < edge)) late[r] |= 1u << (2 * n + e);
-                        c[e] = __float_as_uint(m);
-                    }
-                    stg[(gID + 8 * r) * kStgPitch + 4 * n + tq] = (uint8_t)(c[0] + (c[1] << 4));
+                    float2 u = fma2(make_float2(acc[n][2 * r], acc[n][2 * r + 1]), inv2, nz2);
+                    u = make_float2(fminf(fmaxf(u.x, ulo), uhi), fminf(fmaxf(u.y, ulo), uhi));
+                    const float2 m = add2(u, round2);  // 1.5 2^23: rounds u to an integer, in the low bits
+                    const float2 off = sub2(u, sub2(m, round2));
+                    if (!(fabsf(off.x) < edge)) late[r] |= 1u << (2 * n);
+                    if (!(fabsf(off.y) < edge)) late[r] |= 2u << (2 * n);
+                    stg[(gID + 8 * r) * kStgPitch + 4 * n + tq] = (uint8_t)(__float_as_uint(m.x) + (__float_as_uint(m.y) << 4));
                 }
             }
         __syncwarp();
