@@ -275,7 +275,7 @@ cudaError_t launch(const EvictParams& p, cudaStream_t st) {
 // starts with 9 us of forming R in every block and then needs 0.5 ns per
 // vector, this kernel 7.3 ns (GB300, 8 KV heads: 128 tokens 16 us here and 24
 // us there, 192 tokens 24 and 24, 256 tokens 26 and 24, 320 tokens 32 and 24,
-// 15,104 tokens 1830 and 125).
+// 15,104 tokens 1830 and 120).
 constexpr int kBulkVectors = 4096;
 
 }  // namespace
