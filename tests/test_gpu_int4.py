@@ -609,3 +609,17 @@ def test_a_sequence_with_nan_leaves_the_others_alone(hq, hk, g):
     keep = [0, 2, 3]
     check(out[keep], *[x[keep] for x in want])
     assert out[1].isnan().any()
+
+
+def test_many_tokens_from_rows_at_an_eight_byte_address():
+    rng = np.random.default_rng(41)
+    hk, n = 8, 280
+    x, U = H.bf16_t(kv_bits(rng, n, hk)), H.f32_t(rotation(rng, hk))
+    moved = torch.zeros(x.numel() + 4, dtype=torch.bfloat16, device="cuda")[4:].view(x.shape)
+    moved.copy_(x)
+    assert moved.data_ptr() % 16 == 8
+    clip = torch.full((hk, 2), 0.9, device="cuda")
+    table, pos, seq = np.arange(5, dtype=np.int32)[None], H.i32_t(np.arange(n)), H.i32_t(np.zeros(n))
+    a, _ = evict_in_calls(x, U, clip, pos, seq, table, 32, None)
+    b, status = evict_in_calls(moved, U, clip, pos, seq, table, 32, None)
+    assert status == 0 and torch.equal(a, b)
