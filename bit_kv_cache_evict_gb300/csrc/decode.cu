@@ -1468,9 +1468,10 @@ __device__ __forceinline__ void bf16_stage_rows(const DecodeParams& p, int b, in
 // head in rows.  MMA row h holds head h (rows G..15 are zero): S = Q.K^T,
 // then O += P.V twice into the same accumulators, with A = the bf16 high
 // part of P (its low 16 bits cleared, exact) and A = the rounded remainder,
-// so P keeps ~16 bits and each head's output is one accumulator row.  FINE (the
-// fp32 output of the 4-bit history) adds a third part: 24 bits.
-template <int G, bool FINE>
+// so P keeps ~16 bits and each head's output is one accumulator row.  INT4 (the
+// 4-bit history's chain) adds a third part: 24 bits, for either output type, so
+// that a bf16 output is the fp32 one rounded.
+template <int G, bool INT4>
 __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, float qscale) {
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
     float* st = reinterpret_cast<float*>(rows);  // [G][kD + 2] at the end
@@ -1539,7 +1540,7 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
         const float h1 = __uint_as_float(__float_as_uint(w1) & 0xffff0000u);
         ph[nt] = row_on ? pack_bf16x2_rn(h0, h1) : 0u;
         pl[nt] = row_on ? pack_bf16x2_rn(w0 - h0, w1 - h1) : 0u;
-        if constexpr (FINE)
+        if constexpr (INT4)
             pt[nt] = row_on ? pack_bf16x2_rn(w0 - h0 - bf16_lo(pl[nt]), w1 - h1 - bf16_hi(pl[nt])) : 0u;
     }
 
@@ -1557,7 +1558,7 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
         mma_bf16_16816(o[2 * jp], pl[0], 0u, pl[1], 0u, vf[0], vf[1]);
         mma_bf16_16816(o[2 * jp + 1], ph[0], 0u, ph[1], 0u, vf[2], vf[3]);
         mma_bf16_16816(o[2 * jp + 1], pl[0], 0u, pl[1], 0u, vf[2], vf[3]);
-        if constexpr (FINE) {
+        if constexpr (INT4) {
             mma_bf16_16816(o[2 * jp], pt[0], 0u, pt[1], 0u, vf[0], vf[1]);
             mma_bf16_16816(o[2 * jp + 1], pt[0], 0u, pt[1], 0u, vf[2], vf[3]);
         }
@@ -1581,7 +1582,7 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
 // results it does not read; its block 0 waits for int2_kernel's completion
 // before it exits (the others leave when their items are done), so this grid
 // completes after int2_kernel and the merge after it sees both.
-template <bool FINE>
+template <bool INT4>
 __global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
     extern __shared__ __align__(128) uint8_t bsm[];
     pdl_trigger();
@@ -1636,10 +1637,10 @@ __global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
         uint8_t* rows = rows_of(buf, warp);
         const __nv_bfloat16* qsm = reinterpret_cast<const __nv_bfloat16*>(q_of(buf));
         switch (p.G) {
-            case 1: bf16_tile<1, FINE>(n - t0, rows, qsm, p.qscale); break;
-            case 2: bf16_tile<2, FINE>(n - t0, rows, qsm, p.qscale); break;
-            case 4: bf16_tile<4, FINE>(n - t0, rows, qsm, p.qscale); break;
-            default: bf16_tile<8, FINE>(n - t0, rows, qsm, p.qscale); break;
+            case 1: bf16_tile<1, INT4>(n - t0, rows, qsm, p.qscale); break;
+            case 2: bf16_tile<2, INT4>(n - t0, rows, qsm, p.qscale); break;
+            case 4: bf16_tile<4, INT4>(n - t0, rows, qsm, p.qscale); break;
+            default: bf16_tile<8, INT4>(n - t0, rows, qsm, p.qscale); break;
         }
         __syncthreads();
         // merge the four warps: thread -> dimension
@@ -2077,7 +2078,6 @@ cudaError_t launch_decode4(const DecodeParams4& pin, cudaStream_t st) {
     if (!attr_set[dev & 63]) {
         e = set_smem(prep_kernel<true>, kPrepSmem);
         if (e == cudaSuccess) e = set_smem(bf16_kernel<true>, kBfSmem);
-        if (e == cudaSuccess) e = set_smem(bf16_kernel<false>, kBfSmem);
         if (e == cudaSuccess) e = set_smem(merge_kernel<true>, kMergeSmem);
         if (e != cudaSuccess) return e;
         attr_set[dev & 63] = true;
@@ -2087,8 +2087,8 @@ cudaError_t launch_decode4(const DecodeParams4& pin, cudaStream_t st) {
     dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
     if ((e = launch_pdl(prep_kernel<true>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
     if ((e = launch_int4(p, st, dev)) != cudaSuccess) return e;
-    e = launch_pdl<DecodeParams>(p.out_bf16 ? bf16_kernel<false> : bf16_kernel<true>,
-                                 dim3(min(p.bf_items * p.B * p.hk, 3 * at.sms)), dim3(kBfThreads), kBfSmem, st, p);
+    e = launch_pdl<DecodeParams>(bf16_kernel<true>, dim3(min(p.bf_items * p.B * p.hk, 3 * at.sms)), dim3(kBfThreads),
+                                 kBfSmem, st, p);
     if (e != cudaSuccess) return e;
     const int rpb = kMergeWarps / p.merge_wpr;
     dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
