@@ -1463,6 +1463,18 @@ __device__ __forceinline__ void bf16_stage_rows(const DecodeParams& p, int b, in
     }
 }
 
+// Partials (o, m, l): sums of p v and of p = 2^(logit - m).  A NaN or +infinite
+// logit makes l NaN, and m may then be -infinity (a maximum passes NaN over): the
+// 4-bit chain carries that l through every merge to the output, as the
+// definition has it, and takes a partial as empty only where l is 0.  (The 2-bit
+// chain takes such a partial as empty.)  With finite_max a merge needs no
+// case for empty ones: their factor 2^(-inf - sub) is 0.
+template <bool INT4>
+__device__ __forceinline__ bool holds(float l) {
+    return INT4 ? l != 0.f : l > 0.f;
+}
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
 // One warp's 16-token tile from staged rows and the staged query rows of
 // its KV group (qsm: [G][kD] bf16); leaves the warp's state (o, m, l) per
 // head in rows.  MMA row h holds head h (rows G..15 are zero): S = Q.K^T,
@@ -1520,12 +1532,13 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
         }
     ma = fmaxf(ma, __shfl_xor_sync(kFull, ma, 1));
     ma = fmaxf(ma, __shfl_xor_sync(kFull, ma, 2));
+    const float sub = INT4 ? finite_max(ma) : ma;
     float la = 0.f;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            sacc[nt][e] = ex2(sacc[nt][e] - ma);
+            sacc[nt][e] = ex2(sacc[nt][e] - sub);
             la += sacc[nt][e];
         }
     la += __shfl_xor_sync(kFull, la, 1);
@@ -1652,11 +1665,12 @@ __global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
             for (int w = 0; w < kBfWarps; ++w)
                 M = fmaxf(M, reinterpret_cast<const float*>(rows_of(buf, w))[h * (kD + 2) + kD]);
             float acc = 0.f, L = 0.f;
-            if (M != -INFINITY) {
+            if (INT4 || M != -INFINITY) {
+                const float sub = INT4 ? finite_max(M) : M;
 #pragma unroll
                 for (int w = 0; w < kBfWarps; ++w) {
                     const float* src = reinterpret_cast<const float*>(rows_of(buf, w)) + h * (kD + 2);
-                    const float sc = ex2(src[kD] - M);
+                    const float sc = ex2(src[kD] - sub);
                     acc = fmaf(sc, src[d], acc);
                     L = fmaf(sc, src[kD + 1], L);
                 }
@@ -1796,15 +1810,16 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
             float mb = M;
 #pragma unroll
             for (int i = 0; i < kMergeBatch; ++i)
-                if (ls[i] > 0.f) mb = fmaxf(mb, ms[i]);
-            if (mb != -INFINITY) {
-                const float a = (M == -INFINITY) ? 0.f : ex2(M - mb);
+                if (INT4 || ls[i] > 0.f) mb = fmaxf(mb, ms[i]);
+            if (INT4 || mb != -INFINITY) {
+                const float sub = INT4 ? finite_max(mb) : mb;
+                const float a = (M == -INFINITY) ? 0.f : ex2(M - sub);
                 L *= a;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[k] *= a;
 #pragma unroll
                 for (int i = 0; i < kMergeBatch; ++i) {
-                    const float sc = (ls[i] > 0.f) ? ex2(ms[i] - mb) : 0.f;
+                    const float sc = (INT4 || ls[i] > 0.f) ? ex2(ms[i] - sub) : 0.f;
                     L = fmaf(sc, ls[i], L);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) y[k] = fmaf(sc, ov[i][k], y[k]);
@@ -1825,11 +1840,12 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
             float Mt = -INFINITY;
             for (int i = 0; i < wpr; ++i) Mt = fmaxf(Mt, Ws[(size_t)(warp + i) * kMergeRow + kD]);
             float Lt = 0.f, yt[4] = {0.f, 0.f, 0.f, 0.f};
-            if (Mt != -INFINITY) {
+            if (INT4 || Mt != -INFINITY) {
+                const float sub = INT4 ? finite_max(Mt) : Mt;
                 for (int i = 0; i < wpr; ++i) {
                     const float* wi = Ws + (size_t)(warp + i) * kMergeRow;
-                    if (wi[kD] == -INFINITY) continue;
-                    const float sc = ex2(wi[kD] - Mt);
+                    if (!INT4 && wi[kD] == -INFINITY) continue;
+                    const float sc = ex2(wi[kD] - sub);
                     Lt = fmaf(sc, wi[kD + 1], Lt);
                     const float4 v = *reinterpret_cast<const float4*>(wi + 4 * lane);
                     yt[0] = fmaf(sc, v.x, yt[0]);
@@ -1848,7 +1864,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
     const bool lead = active && sub == 0;
     float wup = 1.f;  // 4-bit history: w is split as w * 2^e, e from its largest entry, so that small rows keep 22 bits too
     if (sub == 0) {  // the row's w (zero for rows past the batch)
-        const float inv = (L > 0.f) ? 1.f / L : 0.f;
+        const float inv = holds<INT4>(L) ? 1.f / L : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = active ? y[k] * inv : 0.f;
         if constexpr (INT4) {
@@ -1929,25 +1945,27 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
     float mb = -INFINITY;
 #pragma unroll
     for (int it = 0; it < kMaxBfItems; ++it)
-        if (bl[it] > 0.f) mb = fmaxf(mb, bm[it]);
+        if (holds<INT4>(bl[it])) mb = fmaxf(mb, bm[it]);
     float lb = 0.f, ob[4] = {0.f, 0.f, 0.f, 0.f};
-    if (mb != -INFINITY) {
+    if (INT4 || mb != -INFINITY) {
+        const float sub = INT4 ? finite_max(mb) : mb;
 #pragma unroll
         for (int it = 0; it < kMaxBfItems; ++it) {
-            if (bl[it] > 0.f) {
-                const float sc = ex2(bm[it] - mb);
+            if (holds<INT4>(bl[it])) {
+                const float sc = ex2(bm[it] - sub);
                 lb = fmaf(sc, bl[it], lb);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) ob[c] = fmaf(sc, bo[it][c], ob[c]);
             }
         }
     }
-    const float Mx = fmaxf(L > 0.f ? M : -INFINITY, lb > 0.f ? mb : -INFINITY);
-    const float wl = (L > 0.f) ? ex2(M - Mx) * L : 0.f;
+    const float Mr = fmaxf(holds<INT4>(L) ? M : -INFINITY, holds<INT4>(lb) ? mb : -INFINITY);
+    const float Mx = INT4 ? finite_max(Mr) : Mr;
+    const float wl = holds<INT4>(L) ? ex2(M - Mx) * L : 0.f;
     const float wi = INT4 ? wl * wup : wl;
-    const float wb = (lb > 0.f) ? ex2(mb - Mx) : 0.f;
+    const float wb = holds<INT4>(lb) ? ex2(mb - Mx) : 0.f;
     const float den = wl + wb * lb;
-    const float inv = (den > 0.f) ? 1.f / den : 0.f;
+    const float inv = holds<INT4>(den) ? 1.f / den : 0.f;
     const size_t at = ((size_t)b * p.hq + kv * p.G + hh) * kD;
     if constexpr (INT4) {
         if (p.out_bf16) {  // a model's next product reads bf16: rounded once, here
