@@ -153,3 +153,15 @@ def test_what_an_eviction_stores_for_a_nan_row_is_seen_by_the_decode():
                                 c.max_pages, c.num_pages)
     out = c.decode()
     assert out[:2].isnan().all() and out[2].isfinite().all()
+
+
+@pytest.mark.parametrize("hq,hk,g", SHAPES[1:])
+def test_a_query_that_overflows_leaves_the_other_heads(hq, hk, g):
+    """1e38 along a column of U_K: the rotated query passes fp32's range, to infinity or NaN."""
+    c = Cache(57, [700, 20], hq, hk, g)
+    for b in (0, 1):
+        c.q[b, 1] = S.bf16_bits(1e38 * np.sign(c.U[0, 0, :, 5]))
+    want, mag = c.want()
+    keep = np.arange(hq) != 1
+    out = c.decode()[:, torch.from_numpy(keep).cuda()]
+    check(out, want[:, keep], mag[:, keep])
