@@ -48,7 +48,7 @@ static oscar_status check_shape(const oscar_shape* s) {
     if (s->head_dim != kD || s->page_size != kPage) return OSCAR_ERR_UNSUPPORTED;
     if (s->quant_group != 32 && s->quant_group != 64 && s->quant_group != 128) return OSCAR_ERR_UNSUPPORTED;
     if (G != 1 && G != 2 && G != 4 && G != 8) return OSCAR_ERR_UNSUPPORTED;
-    if (s->sink + s->recent > 320) return OSCAR_ERR_UNSUPPORTED;
+    if (s->sink > 320 || s->recent > 320 || s->sink + s->recent > 320) return OSCAR_ERR_UNSUPPORTED;
     return OSCAR_OK;
 }
 
@@ -322,7 +322,8 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     }
     if (*ws_bytes < w.total) return OSCAR_ERR_WORKSPACE;
     if (batch == 0) return OSCAR_OK;
-    if (!q || !bf16_kv || !bf16_len || !hist_len || !U || !out || !page_table) return OSCAR_ERR_INVALID_ARG;
+    if (!q || !bf16_len || !hist_len || !U || !out || !page_table) return OSCAR_ERR_INVALID_ARG;
+    if (!bf16_kv && shape->sink + shape->recent > 0) return OSCAR_ERR_INVALID_ARG;  // (without windows nothing reads it)
     if (num_pages > 0 && !pool) return OSCAR_ERR_INVALID_ARG;
     if (!aligned(q, 8) || !aligned(bf16_kv, 16) || !aligned(U, 16) || !aligned(pool, 16) ||
         !aligned(out, out_type == OSCAR_OUT_BF16 ? 8 : 16) || !aligned(workspace, 16) || !aligned(dev_status, 4))

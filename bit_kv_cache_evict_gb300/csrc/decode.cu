@@ -2022,6 +2022,12 @@ static cudaError_t launch_int2(const DecodeParams& p, cudaStream_t st, int sms, 
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Thread blocks of bf16_kernel: one at least, as block 0 waits for the history
+// kernel on the merge's behalf (a shape without windows has no items).
+static int bf16_blocks(const DecodeParams& p, int sms) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)p.bf_items * p.B * p.hk, 3 * sms));
+}
+
 cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t ev_int2_start,
                           cudaEvent_t ev_int2_stop) {
     int dev = 0;
@@ -2071,8 +2077,7 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
         if (e != cudaSuccess) return e;
         at.setb = true;
     }
-    const int bf_total = p.bf_items * p.B * p.hk;
-    e = launch_pdl(bf16_kernel<false>, dim3(min(bf_total, 3 * at.sms)), dim3(kBfThreads), kBfSmem, st, p);
+    e = launch_pdl(bf16_kernel<false>, dim3(bf16_blocks(p, at.sms)), dim3(kBfThreads), kBfSmem, st, p);
     if (e != cudaSuccess) return e;
     if (!at.setm) {
         e = set_smem(merge_kernel<false>, kMergeSmem);
@@ -2107,8 +2112,7 @@ cudaError_t launch_decode4(const DecodeParams4& pin, cudaStream_t st) {
     dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
     if ((e = launch_pdl(prep_kernel<true>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
     if ((e = launch_int4(p, st, dev)) != cudaSuccess) return e;
-    e = launch_pdl<DecodeParams>(bf16_kernel<true>, dim3(min(p.bf_items * p.B * p.hk, 3 * at.sms)), dim3(kBfThreads),
-                                 kBfSmem, st, p);
+    e = launch_pdl<DecodeParams>(bf16_kernel<true>, dim3(bf16_blocks(p, at.sms)), dim3(kBfThreads), kBfSmem, st, p);
     if (e != cudaSuccess) return e;
     const int rpb = kMergeWarps / p.merge_wpr;
     dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);

@@ -216,7 +216,8 @@ oscar_status oscar_evict_quantize(const oscar_shape* shape, int32_t n_tok, const
  * log-sum-exp.  An empty context gives a zero output.
  *
  *   q        (device) bf16 [B][Hq][d], 8-byte aligned
- *   bf16_kv  (device) see layouts, 16-byte aligned
+ *   bf16_kv  (device) see layouts, 16-byte aligned; nullable for a shape
+ *            without windows (sink = recent = 0)
  *   bf16_len (device int32 [B], each in [0, sink+recent])
  *   pool, page_table (device), max_pages, num_pages (pool extent)
  *   hist_len (device int32 [B]) history tokens at positions [0, hist_len)

@@ -1,6 +1,7 @@
 """The 4-bit decode where the listed scenes of test_gpu_int4.py do not come:
 items in which a warp takes several pages, and queues with short items behind
-the long ones; and its bf16 output, which is the fp32 output rounded once.
+the long ones, shapes without BF16 windows; and its bf16 output, which is the
+fp32 output rounded once.
 
 Tolerances are test_gpu_int4.check's.  Its share for the value sums, 2^-15 of the
 largest value, holds here too: a page's four tensor-core steps from zero lose 2^-19 of
@@ -164,3 +165,34 @@ def test_the_same_call_gives_the_same_bits():
     for _ in range(5):
         assert torch.equal(a.decode(), first)
 
+
+# ---------------------------------------------------------------------------
+# shapes without BF16 windows
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,hk,g", [(4, 1, 32), (16, 2, 128)])
+def test_a_shape_without_windows(hq, hk, g, dtype):
+    c = Cache(17, [500, 0, 64, 1], hq, hk, g)
+    c.sh, c.len = O.make_shape(hq, hk, quant_group=g, sink=0, recent=0), np.zeros(4, np.int32)
+    want, mag = c.want()
+    c.kv = np.zeros((4, 0, hk, 2, D), np.uint16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = c.decode(dtype=dtype, status=status)
+    assert int(status) == 0 and (out[1] == 0).all()
+    check(out, want, mag, dtype=dtype)
+
+
+def test_the_2bit_decode_of_a_shape_without_windows():
+    """History tokens alone: equal to the float64 attention over the values that oscar_history_read gives."""
+    from test_gpu_history import random_pool
+    rng = np.random.default_rng(18)
+    hq, hk, g, n = 4, 1, 32, 300
+    sh = O.make_shape(hq, hk, quant_group=g, sink=0, recent=0)
+    pool, table, U = random_pool(rng, 6, hk, 2, g), np.arange(5, dtype=np.int32)[None], rotation(rng, hk)
+    q = S.bf16_bits(rng.standard_normal((1, hq, D)))
+    out = torch.full((1, hq, D), float("nan"), device="cuda")
+    ws = torch.zeros(O.oscar_decode_workspace_bytes(sh, 1, 5), dtype=torch.uint8, device="cuda")
+    kv = torch.zeros(1, 0, hk, 2, D, dtype=torch.bfloat16, device="cuda")
+    O.oscar_decode_attn(sh, H.bf16_t(q), kv, H.i32_t([0]), H.u8_t(pool), H.i32_t(table), 5, 6, H.i32_t([n]), H.f32_t(U), SCALE, out, ws)
+    want, mag = I.decode(f64(q), np.zeros((1, 0, hk, 2, D)), [0], pool, table, [n], U, SCALE, g, bits=2)
+    check(out, want, mag)
