@@ -1,5 +1,6 @@
 // api.cu -- the liboscar C ABI (include/oscar.h): argument checks, the
 // workspace plan, the host page-table layout and kernel launches.
+#include <algorithm>
 #include <cstdio>
 #include <cstring>
 #include <vector>
@@ -72,6 +73,20 @@ struct WsLayout {
     int64_t max_items;   // split-K items at most (int64: batch x KV heads x splits can exceed int32)
 };
 
+// Most split-K items that the 4-bit plan (plan4, decode.cu) makes of `pairs`
+// (sequence, KV head) pairs, whatever their lengths:
+//   one size for all: one item for each block at most, each of four pages but the last;
+//   else items of pps pages, 16 <= pps <= 256, pps = floor(total / (4 blocks)) between those,
+//   and two short ones per pair: total / pps <= 17/16 of 4 blocks below 256 pages, and one
+//   more per pair for each kind's rounding up; or, as no full item has fewer than 16
+//   pages, one for every 16 pages.
+static int64_t items4_bound(int64_t pairs, int max_pages) {
+    auto per_pair = [&](int size) { return (int64_t)(max_pages + size - 1) / size; };
+    const int64_t even = std::min<int64_t>(kMaxBlocks4, pairs * per_pair(4));
+    const int64_t share = std::max<int64_t>(17 * kMaxBlocks4 / 4, (pairs * max_pages + kMaxItemPages4 - 1) / kMaxItemPages4) + 3 * pairs;
+    return std::max(even, std::min(share, pairs * per_pair(kMinItemPages4)));
+}
+
 static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bits) {
     WsLayout w{};
     const int G = s->num_q_heads / s->num_kv_heads, hk = s->num_kv_heads;
@@ -81,8 +96,8 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bi
     w.tail_pg = tail_pages_of(w.pps);
     w.max_items = (int64_t)batch * hk * ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages);
     w.parts = 1;
-    if (bits == 4) {  // items of at least pps pages, or at most one per thread block of any size
-        w.max_items += kMaxBlocks4;
+    if (bits == 4) {
+        w.max_items = items4_bound((int64_t)batch * hk, max_pages);
         w.parts = kPartsPerItem4;
     }
     size_t off = 0;
@@ -312,6 +327,7 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (batch < 0 || max_pages <= 0 || num_pages < 0 || !ws_bytes) return OSCAR_ERR_INVALID_ARG;
+    if ((int64_t)batch * shape->num_kv_heads > INT32_MAX) return OSCAR_ERR_INVALID_ARG;
     const WsLayout w = ws_layout(shape, batch, max_pages, bits);
     // item counts, item offsets and partial indices are int32 on the device
     if (w.max_items * w.parts > INT32_MAX || (double)w.max_items * w.part_stride > 4.0e9)
@@ -357,7 +373,8 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.nslot = shape->sink + shape->recent;
     p.bf_items = bf16_items(shape);
     {   // merge warps per row: more when rows are few and split-K partials many
-        const int splits = ((max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages) * w.parts;
+        const int splits = bits == 4 ? std::min(64, (max_pages + 3) / 4) * w.parts  // (plan4's most, with items of one size)
+                                     : (max_pages + w.pps - 1) / w.pps + w.tail_pg / kShortItemPages;
         const int rows = batch * p.G;
         int wpr = 1;
         // (4-bit, four partials per item: no more blocks than two per SM, each stages U_V)

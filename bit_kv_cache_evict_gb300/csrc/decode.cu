@@ -82,8 +82,12 @@ __global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4> p) {
 // end.  If items of one size, one for each block at most, leave little idle
 // (equal lengths, or few sequences), they are taken: 8 x 508 pages of eight KV heads:
 // 448 items of 73 pages on 456 blocks.  Otherwise items of a quarter of a
-// block's share, with short ones queued last.  At most 64 items per
-// sequence and KV head in the first form: the merge reads four partials of each.
+// block's share, sixteen pages at least, with short ones queued last.  Neither
+// depends on the width of the page table: with a floor taken from it, 64 sequences
+// of 4K to 32K took 400 us in a table of 2048 pages and 343 in one of 508 (now 343
+// in both, one call's data over and over).  At most 64 items per sequence and KV head in the first form: the
+// merge reads four partials of each.  items4_bound (api.cu) is the most items that
+// either form makes.
 __device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tail_pg) {
     const int lane = threadIdx.x & 31;
     auto pages_of = [&](int b) {
@@ -110,7 +114,7 @@ __device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tai
         for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(kFull, n, m);
         return n * p.hk;
     };
-    int lo = max(4, (most + 63) / 64), hi = 256;  // four pages: one for each consumer warp
+    int lo = max(kConsumerWarps, (most + 63) / 64), hi = kMaxItemPages4;  // a page for each consumer warp
     if (lo <= hi && items_at(hi) <= p.blocks) {
         while (lo < hi) {
             const int mid = (lo + hi) / 2;
@@ -123,7 +127,7 @@ __device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tai
             return;
         }
     }
-    pps = (int)min(256l, max((long)p.pps, total / (4 * p.blocks)));
+    pps = (int)min((long)kMaxItemPages4, max((long)kMinItemPages4, total / (4 * p.blocks)));
     tail_pg = pps > kShortItemPages ? 2 * kShortItemPages : 0;
 }
 

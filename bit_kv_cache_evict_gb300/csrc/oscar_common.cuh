@@ -19,7 +19,8 @@ constexpr int kBfCounter = 32;      // index of the BF16 item queue's counter
 constexpr int kPlanPps = 8;         // 4-bit: index of the plan's pages per long item
 constexpr int kPlanTail = 9;        // 4-bit: index of the plan's pages in short tail items
 constexpr int kPartsPerItem4 = 4;   // 4-bit: partials per split-K item, one per consumer warp
-constexpr int kMaxBlocks4 = 512;    // 4-bit: blocks that the plan counts with at most (room for as many items is added)
+constexpr int kMaxBlocks4 = 512;    // 4-bit: blocks that the plan counts with at most
+constexpr int kMinItemPages4 = 16, kMaxItemPages4 = 256;  // 4-bit: pages of a long item, where items are not one for each block
 constexpr int kShortItemPages = 16; // pages per short split-K item (the queue's tail)
 constexpr int kBlock = OSCAR_BLOCK_BYTES;
 constexpr int kKCodes = 0;        // byte offsets inside a (page, kv) block

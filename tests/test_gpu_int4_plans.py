@@ -1,7 +1,7 @@
 """The 4-bit decode where the listed scenes of test_gpu_int4.py do not come:
 items in which a warp takes several pages, and queues with short items behind
-the long ones, shapes without BF16 windows; and its bf16 output, which is the
-fp32 output rounded once.
+the long ones, tables wider than the histories, shapes without BF16 windows; and
+its bf16 output, which is the fp32 output rounded once.
 
 Tolerances are test_gpu_int4.check's.  Its share for the value sums, 2^-15 of the
 largest value, holds here too: a page's four tensor-core steps from zero lose 2^-19 of
@@ -26,6 +26,7 @@ from bit_kv_cache_evict_gb300 import build as B  # noqa: E402
 from bit_kv_cache_evict_gb300 import oscar as O  # noqa: E402
 from bit_kv_cache_evict_gb300 import synth as S  # noqa: E402
 from oracle import int4 as I  # noqa: E402
+from test_int4_plan_host import plan4  # noqa: E402
 from test_gpu_int4 import SCALE, Cache, check, f64, rotation  # noqa: E402
 
 D = 128
@@ -63,14 +64,17 @@ class Aliased:
         self.kv = S.bf16_bits(rng.standard_normal((self.B, S.NSLOT, hk, 2, D)))
         self.len = rng.integers(1, S.NSLOT + 1, self.B).astype(np.int32)
 
-    def decode(self, dtype=torch.float32):
+    def decode(self, dtype=torch.float32, wide=0):
         d = dict(q=H.bf16_t(self.q), kv=H.bf16_t(self.kv), len=H.i32_t(self.len), pool=H.u8_t(self.pool), hist=H.i32_t(self.hist), U=H.f32_t(self.U))
+        table = np.full((self.B, max(wide, self.max_pages)), -1, np.int32)
+        table[:, :self.max_pages] = self.table
         out = torch.full((self.B, self.hq, D), float("nan"), dtype=dtype, device="cuda")
-        ws = torch.full((O.oscar_decode_workspace_bytes_int4(self.sh, self.B, self.max_pages),), 0xFF, dtype=torch.uint8, device="cuda")
+        ws = torch.full((O.oscar_decode_workspace_bytes_int4(self.sh, self.B, table.shape[1]),), 0xFF, dtype=torch.uint8, device="cuda")
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        O.oscar_decode_attn_int4(self.sh, d["q"], d["kv"], d["len"], d["pool"], H.i32_t(self.table), self.max_pages, self.num_pages, d["hist"], d["U"],
+        O.oscar_decode_attn_int4(self.sh, d["q"], d["kv"], d["len"], d["pool"], H.i32_t(table), table.shape[1], self.num_pages, d["hist"], d["U"],
                                  SCALE, out, ws, dev_status=status)
         assert int(status) == 0
+        self.plan = ws[:256].view(torch.int32)[8:10].tolist()   # pages of a long item, pages in short ones
         return out
 
     def want(self):
@@ -149,6 +153,20 @@ def test_equal_lengths_of_one_item_size():
     c = Aliased(12, [64 * 130] * 8, 32, 8, 32, pages=16)
     want, mag = c.want()
     check(c.decode(), want, mag)
+
+
+@pytest.mark.parametrize("hist,hq,hk", [(RAGGED, 32, 8), ([700, 90, 1, 0], 4, 1), ([64 * 300], 8, 1), ([64 * 100] * 8, 64, 8)])
+@pytest.mark.parametrize("wide", [512, 4096])
+def test_a_wider_table_changes_nothing(hist, hq, hk, wide):
+    """Unused entries behind the histories: the plan goes by the lengths.  (Outputs may
+    differ by the merge's order: it has as many warps to a row as the table may need.)"""
+    c = Aliased(13, hist, hq, hk, 32)
+    want, mag = c.want()
+    narrow, plan = c.decode(), c.plan
+    out = c.decode(wide=wide)
+    check(out, want, mag)
+    assert c.plan == plan == list(plan4(c.hist, hk, 152 * (2 if hq // hk == 8 else 3)))
+    assert (out - narrow).abs().max() <= 4e-6 * narrow.abs().max()
 
 
 @pytest.mark.parametrize("hq,hk,g", [(1, 1, 32), (4, 1, 32), (16, 8, 64), (64, 8, 128)])
