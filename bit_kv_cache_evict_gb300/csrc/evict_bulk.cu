@@ -11,10 +11,21 @@
 //   Product: y = x . R, R = U . Hadamard . bit-reversal / sqrt(d) formed once
 // per block in fixed point and kept as fp16 parts h1 + h2 (22 bits) and
 // a remainder r3 of 16 bits, all scaled by a power of two; x (bf16) is scaled per row into
-// fp16, exactly.  acc = x . h2 first, then x . h1: the second sum's eight
-// accumulation steps each lose at most 2^-23 of a partial sum, which is at
-// most |x| |R_j| (Cauchy-Schwarz): 2^-20, and r3 is below 2^-22 of R:
-// delta = 1.5 2^-20 |x| max_j |R_j|.
+// fp16, exactly but for elements below 2^-31 of the row's largest (2^-35 |x| |R_j| of y in all).
+//   delta.  One MMA aligns its sixteen exact products and the accumulator to
+// the largest of them, cuts each off two bits below fp32's last (2^-25 of the largest),
+// adds, and cuts the sum off to 24 bits: it loses at most (17 / 4) 2^-23 M + 2^-23
+// |sum|, M the largest addend (tests/test_gpu_evict4_product.py measures
+// single MMAs against this: at most 0.79 of it).  A chain of eight k-steps would
+// lose 8 (17 / 4 + 1) 2^-23 |x| |R_j| in all, as M can be as large as the whole
+// (measured: 1.6 times the 1.5 2^-20 that was once allowed).  So each k-step s
+// is summed from zero: M and the sum are at most |x_s| |R_sj|
+// (Cauchy-Schwarz, over the step's indices), and the sum of those over the steps
+// at most |x| |R_j| (the same again): 5.25 2^-23.  The seven rounded
+// fp32 additions lose at most 2^-24 of a partial sum each: 3.5 2^-23; r3 is below
+// 3.5 2^-23 of R (two of 24 bits cut off, and the pair's low part).  In all 12.25 2^-23 and
+// less than 0.05 2^-23 for h2's own product: delta = 1.6 2^-20 |x| max_j |R_j|
+// is 12.8 2^-23 (measured: errors up to 0.40 delta on rows made for it).
 //   Exact value of one element: x (h1 + h2) as an error-free product, x r3 exact
 // in fp32 (8 x 16 bits), added by the warp as pairs: the value of R to about
 // 2^-38.
@@ -319,6 +330,115 @@ __device__ __forceinline__ void bulk_ldsm(uint32_t (&r)[4], const void* p) {
                  : "r"(smem_u32(p)));
 }
 
+// n-tiles whose products run side by side, and whose operands are loaded ahead
+// (15,104 tokens of eight KV heads, us: 2, 4: 124.5; 2, 8: 124.6; 4, 4: 124.8; 4, 8: 126).
+constexpr int kSide = 2, kAhead = 4;
+
+// y = x . R of a warp's tile of 16 staged rows: acc[n][e] is stored position
+// 8 n + 2 tq + (e & 1) of row gID + 8 (e >> 1), delta[r] the bound of its error for row gID + 8 r.
+__device__ __forceinline__ void bulk_product(const uint8_t* smem, const uint8_t* xs, float rdown, float rnorm,
+                                             float (&acc)[16][4], float (&delta)[2]) {
+    const int lane = threadIdx.x & 31;
+    const uint2* frag = reinterpret_cast<const uint2*>(smem + BulkSmem::kFrag);
+    // -- rows scaled by 2^k, k from the largest element
+    const uint8_t* xfrag = xs + ((lane & 7) + 8 * ((lane >> 3) & 1)) * kXPitch + 16 * (lane >> 4);
+    float mx[2] = {0.f, 0.f}, n2[2] = {0.f, 0.f}, fdown[2], up[2];
+#pragma unroll 2
+    for (int ks = 0; ks < 8; ++ks) {
+        uint32_t a[4];
+        bulk_ldsm(a, xfrag + 32 * ks);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            mx[e & 1] = fmaxf(mx[e & 1], fmaxf(fabsf(bf16_lo(a[e])), fabsf(bf16_hi(a[e]))));
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 2));
+        // largest |x| 2^k below 2^15; or k = 110, where every bf16 value (a multiple of 2^-133) is a multiple of 2^-23
+        const int k = min(110, 14 - ((int)(__float_as_uint(mx[r]) >> 23) - 127));
+        up[r] = pow2f_bits(k);
+        fdown[r] = pow2f_bits(-k) * rdown;  // accumulator -> y
+    }
+
+    // -- y: n-tile n = stored positions 8 n .. 8 n + 7; rows gID (entries
+    //    0, 1) and gID + 8 (2, 3).  A k-step's sum starts from zero, x . h2
+    //    then x . h1, and is added to acc in fp32 (for the bound's sake, see above).  (A
+    //    loop, not unrolled: with every product unrolled the kernel waited on
+    //    instruction fetches for half of its time.)
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    uint32_t raw[4], a[4];
+    auto scale = [&](bool sum) {  // raw to fp16; the sum of squares
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float v0 = bf16_lo(raw[e]) * up[e & 1], v1 = bf16_hi(raw[e]) * up[e & 1];
+            if (sum) n2[e & 1] = fmaf(v0, v0, fmaf(v1, v1, n2[e & 1]));
+            a[e] = pack_f16x2_rn(v0, v1);
+        }
+    };
+    auto operand = [&](int ks, int n, int part) {  // (frag_at)
+        return frag[(part * 8 + ks) * kStepWords + n * 32 + (lane ^ (n & 3))];
+    };
+    bulk_ldsm(raw, xfrag);
+    uint2 b[kAhead][2];  // operands of the next kAhead n-tiles: h1, h2
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n)
+#pragma unroll
+        for (int part = 0; part < 2; ++part) b[n][part] = operand(0, n, part);
+    scale(true);
+#pragma unroll 1
+    for (int ks = 0; ks < 8; ++ks) {  // (the next step's operands are loaded and made while the products run)
+        const int next = (ks + 1) & 7;
+        bulk_ldsm(raw, xfrag + 32 * next);
+        float t[2][kSide][4];  // the sums of kSide n-tiles, and of the kSide before them
+#pragma unroll
+        for (int n0 = 0; n0 < 16 + kSide; n0 += kSide) {
+            const int now = (n0 / kSide) & 1;
+            if (n0 < 16) {
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                    uint2& u = b[(n0 + i) % kAhead][1];
+                    mma_f16_16816_zero(t[now][i], a[0], a[1], a[2], a[3], u.x, u.y);
+                    u = operand(n0 + i + kAhead < 16 ? ks : next, (n0 + i + kAhead) & 15, 1);
+                }
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                    uint2& u = b[(n0 + i) % kAhead][0];
+                    mma_f16_16816(t[now][i], a[0], a[1], a[2], a[3], u.x, u.y);
+                    u = operand(n0 + i + kAhead < 16 ? ks : next, (n0 + i + kAhead) & 15, 0);
+                }
+            }
+            if (n0 > 0) {
+#pragma unroll
+                for (int i = 0; i < kSide; ++i) {
+                    float(&y)[4] = acc[n0 - kSide + i];
+                    const float(&u)[4] = t[now ^ 1][i];
+                    const float2 y0 = add2(make_float2(y[0], y[1]), make_float2(u[0], u[1]));
+                    const float2 y1 = add2(make_float2(y[2], y[3]), make_float2(u[2], u[3]));
+                    y[0] = y0.x;
+                    y[1] = y0.y;
+                    y[2] = y1.x;
+                    y[3] = y1.y;
+                }
+            }
+        }
+        scale(ks < 7);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        n2[r] += __shfl_xor_sync(kFull, n2[r], 1);
+        n2[r] += __shfl_xor_sync(kFull, n2[r], 2);
+        delta[r] = 1.6f * 9.5367431640625e-7f * sqrtf(n2[r]) * 1.001f * rnorm * fdown[r];
+    }
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] *= fdown[e >> 1];
+}
+
 // Block = one (KV head, K|V), blockIdx.x / pairs of the blocks that share it;
 // its warps take tiles of 16 listed tokens in turn.
 __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams p) {
@@ -338,7 +458,6 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
     uint32_t* sz = reinterpret_cast<uint32_t*>(smem + BulkSmem::kSz) + warp * kTile * 4;
     uint8_t** dst = reinterpret_cast<uint8_t**>(smem + BulkSmem::kDst) + warp * kTile;
     int* slots = reinterpret_cast<int*>(smem + BulkSmem::kDst + kBulkWarps * kTile * 8) + warp * kTile;
-    const uint2* frag = reinterpret_cast<const uint2*>(smem + BulkSmem::kFrag);
     // the group's open quantisation groups: row of the block, 32-position block, positions of the extremes
     ushort4* list = reinterpret_cast<ushort4*>(smem + BulkSmem::kList) + warp / kGroupWarps * (kGroupWarps * kTile * 4);
     int* n_list = reinterpret_cast<int*>(smem + BulkSmem::kCol) + kD + 1 + warp / kGroupWarps;
@@ -431,71 +550,8 @@ __global__ void __launch_bounds__(kBulkThreads, 1) evict_bulk_kernel(EvictParams
             }
         }
 
-        // -- rows scaled by 2^k, k from the largest element
-        const uint8_t* xfrag = xs + ((lane & 7) + 8 * ((lane >> 3) & 1)) * kXPitch + 16 * (lane >> 4);
-        float mx[2] = {0.f, 0.f}, n2[2] = {0.f, 0.f}, fdown[2], up[2], delta[2];
-#pragma unroll 2
-        for (int ks = 0; ks < 8; ++ks) {
-            uint32_t a[4];
-            bulk_ldsm(a, xfrag + 32 * ks);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                mx[e & 1] = fmaxf(mx[e & 1], fmaxf(fabsf(bf16_lo(a[e])), fabsf(bf16_hi(a[e]))));
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(kFull, mx[r], 2));
-            const int k = min(80, 14 - ((int)(__float_as_uint(mx[r]) >> 23) - 127));  // largest |x| 2^k below 2^15
-            up[r] = pow2f_bits(k);
-            fdown[r] = pow2f_bits(-k) * rdown;  // accumulator -> y
-        }
-
-        // -- y: n-tile n = stored positions 8 n .. 8 n + 7; rows gID (entries
-        //    0, 1) and gID + 8 (2, 3).  Steps 0-7: x . h2, 8-15: x . h1.  (A
-        //    loop, not unrolled: with every product unrolled the kernel waited
-        //    on instruction fetches for half of its time.)
-        float acc[16][4];
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-        uint32_t raw[4], a[4];
-        auto scale = [&](bool sum) {  // raw to fp16; the sum of squares
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float v0 = bf16_lo(raw[e]) * up[e & 1], v1 = bf16_hi(raw[e]) * up[e & 1];
-                if (sum) n2[e & 1] = fmaf(v0, v0, fmaf(v1, v1, n2[e & 1]));
-                a[e] = pack_f16x2_rn(v0, v1);
-            }
-        };
-        bulk_ldsm(raw, xfrag);
-        uint2 b[16];
-#pragma unroll
-        for (int n = 0; n < 16; ++n) b[n] = frag[8 * kStepWords + n * 32 + (lane ^ (n & 3))];  // (frag_at)
-        scale(true);
-#pragma unroll 1
-        for (int step16 = 0; step16 < 16; ++step16) {  // (the next step's operands are loaded and made while the products run)
-            const int next16 = (step16 + 1) & 15;
-            bulk_ldsm(raw, xfrag + 32 * (next16 & 7));
-            const uint2* fn = frag + (((next16 >> 3) ^ 1) * 8 + (next16 & 7)) * kStepWords;
-#pragma unroll
-            for (int n = 0; n < 16; ++n) {
-                mma_f16_16816(acc[n], a[0], a[1], a[2], a[3], b[n].x, b[n].y);
-                b[n] = fn[n * 32 + (lane ^ (n & 3))];
-            }
-            scale(step16 < 7);
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            n2[r] += __shfl_xor_sync(kFull, n2[r], 1);
-            n2[r] += __shfl_xor_sync(kFull, n2[r], 2);
-            delta[r] = 1.5f * 9.5367431640625e-7f * sqrtf(n2[r]) * 1.001f * rnorm * fdown[r];
-        }
-#pragma unroll
-        for (int n = 0; n < 16; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] *= fdown[e >> 1];
+        float acc[16][4], delta[2];
+        bulk_product(smem, xs, rdown, rnorm, acc, delta);
 
         // -- extremes, clip threshold and pair of every group (by 32-position block)
         float gmx[2][4], gmn[2][4], clip[2][4];
