@@ -547,9 +547,10 @@ def _torch_names() -> None:
     global _F32, _BF16, _I32, _U8, _raw_stream, _current_device
     import torch
     torch.cuda.current_device()                     # initialises CUDA once; the raw queries below do not
-    _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
     _raw_stream = torch._C._cuda_getCurrentRawStream
     _current_device = torch._C._cuda_getDevice
+    _BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+    _F32 = torch.float32                            # last: other threads take it for the sign that all are set
 
 
 def _arg(t, what: str, dtype, need: int, dev: int):
