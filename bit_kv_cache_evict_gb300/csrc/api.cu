@@ -245,7 +245,8 @@ static oscar_status evict_impl(const oscar_shape* shape, int32_t n_tok, const vo
     if (n_tok == 0) return OSCAR_OK;
     if (!src_kv || !dst_seq || !dst_pos || !U || !clip || !pool || !page_table) return OSCAR_ERR_INVALID_ARG;
     if (!aligned(src_kv, 8) || (new_kv && !aligned(new_kv, 8)) || !aligned(U, 16) || !aligned(pool, 16) ||
-        !aligned(clip, 4) || !aligned(dev_status, 4))
+        !aligned(clip, 4) || !aligned(dev_status, 4) || !aligned(src_row, 4) || !aligned(dst_seq, 4) ||
+        !aligned(dst_pos, 4) || !aligned(page_table, 4))
         return OSCAR_ERR_INVALID_ARG;
     if (!src_row && src_rows < n_tok) return OSCAR_ERR_INVALID_ARG;
     if ((int64_t)n_tok * shape->num_kv_heads * 2 > INT32_MAX) return OSCAR_ERR_INVALID_ARG;
@@ -342,7 +343,8 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     if (!bf16_kv && shape->sink + shape->recent > 0) return OSCAR_ERR_INVALID_ARG;  // (without windows nothing reads it)
     if (num_pages > 0 && !pool) return OSCAR_ERR_INVALID_ARG;
     if (!aligned(q, 8) || !aligned(bf16_kv, 16) || !aligned(U, 16) || !aligned(pool, 16) ||
-        !aligned(out, out_type == OSCAR_OUT_BF16 ? 8 : 16) || !aligned(workspace, 16) || !aligned(dev_status, 4))
+        !aligned(out, out_type == OSCAR_OUT_BF16 ? 8 : 16) || !aligned(workspace, 16) || !aligned(dev_status, 4) ||
+        !aligned(bf16_len, 4) || !aligned(hist_len, 4) || !aligned(page_table, 4))
         return OSCAR_ERR_INVALID_ARG;
     if (!(sm_scale == sm_scale)) return OSCAR_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
