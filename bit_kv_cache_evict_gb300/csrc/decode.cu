@@ -79,15 +79,21 @@ __global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4> p) {
 // Pages per long item and in short tail items of a 4-bit history, from the
 // lengths as they are (one warp).  The kernel's time is that of its busiest
 // block, and an item costs its pages and about one more for its start and
-// end.  If items of one size, one for each block at most, leave little idle
-// (equal lengths, or few sequences), they are taken: 8 x 508 pages of eight KV heads:
-// 448 items of 73 pages on 456 blocks.  Otherwise items of a quarter of a
-// block's share, sixteen pages at least, with short ones queued last.  Neither
-// depends on the width of the page table: with a floor taken from it, 64 sequences
-// of 4K to 32K took 400 us in a table of 2048 pages and 343 in one of 508 (now 343
-// in both, one call's data over and over).  At most 64 items per sequence and KV head in the first form: the
-// merge reads four partials of each.  items4_bound (api.cu) is the most items that
-// either form makes.
+// end.  Items of one size, one for each block at most, are taken if they leave
+// a fifth of the blocks' time idle at most (8 x 508 pages of eight KV heads: 448
+// items of 73 pages on 456 blocks), or are no longer than the other form's
+// smallest (one sequence of one KV head: 30,000 tokens 19.8 us in 59 items of 8
+// pages, 22.2 in items of 16; 100,000 tokens 38.7 in 63 items of 25 pages, 31.8 in
+// the other form).  Otherwise items of a quarter of a block's share, sixteen pages
+// at least, with short ones queued last.
+//   Neither depends on the width of the page table: with a floor taken from it, 64
+// sequences of 4K to 32K took 400 us in a table of 2048 pages and 343 in one of
+// 508 (now 343 in both, one call's data over and over).
+//   At most 64 items per sequence and KV head in the first form, as the merge
+// reads four partials of each (one sequence of 100,000, 60,000, 30,000 tokens and
+// four of up to 100,000, one KV head, us: 31.8, 25.9, 19.8, 35.6; with at most
+// 128: 31.3, 23.2, 19.5, 37.0; 256: 30.3, 25.8, 19.5, 37.1).
+//   items4_bound (api.cu) is the most items that either form makes.
 __device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tail_pg) {
     const int lane = threadIdx.x & 31;
     auto pages_of = [&](int b) {
@@ -121,7 +127,7 @@ __device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tai
             if (items_at(mid) <= p.blocks) hi = mid;
             else lo = mid + 1;
         }
-        if (lo <= 32 || (long)lo * p.blocks <= total + total / 4) {
+        if (lo <= kMinItemPages4 || (long)lo * p.blocks <= total + total / 4) {
             pps = lo;
             tail_pg = 0;
             return;

@@ -155,7 +155,7 @@ def test_equal_lengths_of_one_item_size():
     check(c.decode(), want, mag)
 
 
-@pytest.mark.parametrize("hist,hq,hk", [(RAGGED, 32, 8), ([700, 90, 1, 0], 4, 1), ([64 * 300], 8, 1), ([64 * 100] * 8, 64, 8)])
+@pytest.mark.parametrize("hist,hq,hk", [(RAGGED, 32, 8), ([700, 90, 1, 0], 4, 1), ([64 * 300], 8, 1), ([100000], 4, 1), ([64 * 100] * 8, 64, 8)])
 @pytest.mark.parametrize("wide", [512, 4096])
 def test_a_wider_table_changes_nothing(hist, hq, hk, wide):
     """Unused entries behind the histories: the plan goes by the lengths.  (Outputs may

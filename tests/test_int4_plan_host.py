@@ -25,7 +25,7 @@ def plan4(hist, hk, blocks):
         while lo < hi:
             mid = (lo + hi) // 2
             lo, hi = (lo, mid) if items(mid) <= blocks else (mid + 1, hi)
-        if lo <= 32 or lo * blocks <= total + total // 4:
+        if lo <= 16 or lo * blocks <= total + total // 4:
             return lo, 0
     pps = min(256, max(16, total // (4 * blocks)))
     return pps, 32 if pps > 16 else 0
@@ -61,6 +61,8 @@ def test_a_plan_of_known_lengths():
     assert plan4([0], 1, 456) == (4, 0)
     assert plan4([64 * 40] * 64, 8, 456) == (16, 0)        # sixteen pages at least
     assert plan4([64 * 508] * 64, 8, 456) == (142, 32)
+    assert plan4([30000], 1, 456) == (8, 0)                # no longer than the other form's smallest items
+    assert plan4([100000], 1, 456) == (16, 0)              # 25 pages would leave six of seven blocks idle
 
 
 def test_sizes_past_32_bits_are_refused(lib):
