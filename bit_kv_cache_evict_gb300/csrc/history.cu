@@ -115,22 +115,24 @@ __device__ __forceinline__ void store_eight(T* out, const float (&v)[8]) {
     }
 }
 
-// Block = TOK listed tokens of one KV head (64: 33.5 us for 32,448 tokens of
+// Block = kTok listed tokens of one KV head (64: 33.5 us for 32,448 tokens of
 // eight heads; 32: 36.8, the look-up of the tokens then weighs more).  Thread (token, c) makes the eight values of
 // positions 8 c .. 8 c + 7, so that a row is stored by 16 neighbouring lanes: K
 // straight from global memory, V through shared memory, where the plane
 // bytes are laid token by token.  Every load of a thread is issued before the
 // first is used.
-template <int BITS, typename T, int TOK>
+constexpr int kTok = 64;
+
+template <int BITS, typename T>
 __global__ void __launch_bounds__(kHistThreads) read_kernel(HistoryReadParams p) {
     using L = Layout<BITS>;
     constexpr int kRow = L::kVec + 4;  // bytes of a staged token: words of distinct tokens on distinct banks
-    constexpr int kPlanes = L::kVec * (TOK / 4) / kHistThreads;  // planes per thread: 2 (4 bits, 32 tokens)
-    __shared__ Source src[TOK];
-    __shared__ __align__(16) uint8_t vS[TOK * kRow];
-    const int t0 = blockIdx.x * TOK, kv = blockIdx.y;
+    constexpr int kPlanes = L::kVec * (kTok / 4) / kHistThreads;  // planes per thread: 4 (4 bits), 2
+    __shared__ Source src[kTok];
+    __shared__ __align__(16) uint8_t vS[kTok * kRow];
+    const int t0 = blockIdx.x * kTok, kv = blockIdx.y;
     pdl_wait();
-    if (threadIdx.x < TOK) {
+    if (threadIdx.x < kTok) {
         Source s{nullptr, 0};
         const int i = t0 + threadIdx.x;
         if (i < p.n_tok) {
@@ -142,11 +144,11 @@ __global__ void __launch_bounds__(kHistThreads) read_kernel(HistoryReadParams p)
         src[threadIdx.x] = s;
     }
     __syncthreads();
-    const int quad = threadIdx.x % (TOK / 4), plane = threadIdx.x / (TOK / 4) * kPlanes;
+    const int quad = threadIdx.x % (kTok / 4), plane = threadIdx.x / (kTok / 4) * kPlanes;
     uint32_t vw[kPlanes];
     Quad(src + 4 * quad, L::v_codes(p.gshift)).load(plane, vw);
     const int c = threadIdx.x & 15, k = c >> 2, a = c & 3, ng = sz_pairs(p.gshift);
-    constexpr int kIt = TOK / 16;
+    constexpr int kIt = kTok / 16;
     uint32_t kw[kIt][2], ksz[kIt], vsz[kIt];
 #pragma unroll
     for (int it = 0; it < kIt; ++it) {
@@ -332,19 +334,18 @@ static cudaError_t launch_history(void (*kernel)(P), dim3 grid, const P& p, cuda
 }
 
 cudaError_t launch_history_read(const HistoryReadParams& p, cudaStream_t st) {
-    constexpr int TOK = 64;
-    const dim3 grid((p.n_tok + TOK - 1) / TOK, p.hk);
-    if (p.bits4)
-        return launch_history(p.out_bf16 ? read_kernel<4, __nv_bfloat16, TOK> : read_kernel<4, float, TOK>, grid, p, st);
-    return launch_history(p.out_bf16 ? read_kernel<2, __nv_bfloat16, TOK> : read_kernel<2, float, TOK>, grid, p, st);
+    const dim3 grid((p.n_tok + kTok - 1) / kTok, p.hk);
+    if (p.bits4) return launch_history(p.out_bf16 ? read_kernel<4, __nv_bfloat16> : read_kernel<4, float>, grid, p, st);
+    return launch_history(p.out_bf16 ? read_kernel<2, __nv_bfloat16> : read_kernel<2, float>, grid, p, st);
 }
 
 cudaError_t launch_history_gather(const HistoryGatherParams& p, cudaStream_t st) {
     HistoryGatherParams q = p;
-    // Four KV heads per block once that still leaves more blocks than the GPU
-    // holds (912): 2032 pages of eight heads 88 us with one head, 81 with four;
-    // fewer pages want every block they can get.
-    q.heads = (int64_t)p.batch * p.dst_max_pages * p.hk >= 8192 ? 4 : 1;
+    // Four KV heads per block once that still leaves as many blocks as the GPU
+    // holds (912).  Pages x KV heads, us with one head and with four: 16256 89.1,
+    // 81.8; 8128 47.0, 44.0; 7616 (nearly all tokens kept) 38.8, 35.9; 4064 as 508 x 8
+    // 25.6, 25.0 and as 2032 x 2 26.2, 24.6; 2048 15.0, 15.4.
+    q.heads = (int64_t)p.batch * p.dst_max_pages * p.hk >= 4 * 912 ? 4 : 1;
     const dim3 grid(p.batch * p.dst_max_pages * ((p.hk + q.heads - 1) / q.heads));
     return launch_history(p.bits4 ? gather_kernel<4> : gather_kernel<2>, grid, q, st);
 }
