@@ -31,6 +31,7 @@
 //       W_tb = p_t s_tb                                  (fp16 MMA, dims x heads).
 // q' 2^e and W are split into fp16 hi + lo (22 bits); codes are exact and
 // carry no offset.
+#include <algorithm>
 #include <type_traits>
 
 #include "oscar_common.cuh"
@@ -442,6 +443,20 @@ __device__ __forceinline__ void v_operands(uint32_t r0, uint32_t r1, uint32_t r0
     a2 = code_pair_hi<G>(r0, r0s);
     a3 = code_pair_hi<G>(r1, r1s);
 }
+
+// Position of token t (0..63) in the warp's probability and V-scale rows.
+// The P.V products take the page's tokens in 16 groups of four: k-step m of
+// lane quad tq covers group q = 4 tq + m (tokens 4q .. 4q+3, whose V codes
+// are bytes 4q .. 4q+3 of every code plane, so one 16-byte load per plane
+// serves all four k-steps).  Group q sits in 16-byte chunk 4 tq + (m ^ tq)
+// of a row, which keeps the lanes of one shared-memory wavefront on
+// distinct banks; inside a chunk the order is pv_slot (tokens 4q, 4q+2 |
+// 4q+1, 4q+3 as the two B-operand pairs).
+__device__ __forceinline__ int pv_pos(int t) {
+    const int q = t >> 2, tq = q >> 2, m = q & 3;
+    return 4 * (4 * tq + (m ^ tq)) + pv_slot(t & 3);
+}
+constexpr int kPvRow = 72;  // floats per probability / V-scale row (64 + 8: conflict-free stores)
 
 // The page's scales into the warp's scratch: for each token row and each
 // 32-position block b (quantisation group b >> GS), fp32 s scaled by the

@@ -258,16 +258,7 @@ cudaError_t launch(const EvictParams& p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         carveout_set[dev & 63] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_tok * 2 * p.hk);
-    cfg.blockDim = dim3(32 * W);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict4_kernel<W, DEPTH>, p);
+    e = launch_pdl(evict4_kernel<W, DEPTH>, dim3(p.n_tok * 2 * p.hk), dim3(32 * W), 0, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -799,17 +799,7 @@ cudaError_t launch_evict_bulk(const EvictParams& p, cudaStream_t st) {
     }
     const int pairs = 2 * p.hk, tiles = (p.n_tok + kTile - 1) / kTile;
     const int share = std::max(1, std::min((tiles + kBulkWarps - 1) / kBulkWarps, sms[dev & 63] / pairs));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pairs * share);
-    cfg.blockDim = dim3(kBulkThreads);
-    cfg.dynamicSmemBytes = BulkSmem::kBytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_bulk_kernel, p);
+    e = launch_pdl(evict_bulk_kernel, dim3(pairs * share), dim3(kBulkThreads), BulkSmem::kBytes, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -14,7 +14,7 @@
 // eight 32K histories kept, 81 us (4.1 TB/s of 2 x 160 bytes; a random half of
 // a page's V plane costs its whole sectors, so 400 bytes move: 5.1 TB/s);
 // 2048 pages copied in 50.7 us (6.6 TB/s).
-#include "splitk.cuh"
+#include "oscar_common.cuh"
 
 namespace oscar {
 
@@ -320,16 +320,7 @@ static_assert(kCopyPiece == kHistThreads * 16 * 4, "four vectors per thread");
 // completion first.
 template <typename P>
 static cudaError_t launch_history(void (*kernel)(P), dim3 grid, const P& p, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kHistThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    const cudaError_t e = launch_pdl(kernel, grid, dim3(kHistThreads), 0, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -39,6 +39,8 @@
 // their latency (issue 52 %).  The code of a page is kept small and free of
 // divergent branches for the same reason: with separate code for partial pages,
 // every tile unrolled and the waits polled lane by lane it took 295 and 282 us.
+#include <algorithm>
+
 #include "splitk.cuh"
 
 namespace oscar {

@@ -500,6 +500,41 @@ struct PagesCopyParams {
 int64_t pages_copy_pieces(size_t page_bytes);  // thread blocks per (pair, pool)
 cudaError_t launch_pages_copy(const PagesCopyParams& p, int n_pools, cudaStream_t st);
 
+// ------------------------------------------------------------------
+// launches
+// ------------------------------------------------------------------
+// Dynamic shared memory of a kernel, and the largest L1 / shared carveout:
+// an SM changes its split only when idle, so every kernel of the chain asks
+// for the same split and a programmatically launched kernel can start on SMs
+// where its predecessor still runs.  (Not for the eight-head Lloyd-Max INT2
+// kernel: its register spills go through L1, which the largest split leaves
+// at 28 KB; it took 9 % longer with it.)
+template <typename... Args>
+inline cudaError_t set_smem(void (*kernel)(Args...), int bytes, bool max_carveout = true) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && max_carveout)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 (int)cudaSharedmemCarveoutMaxShared);
+    return e;
+}
+
+// Launch with a programmatic dependency on the previous kernel in the stream
+// (the kernel itself decides where it waits, see pdl_wait).
+template <typename P>
+inline cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
 cudaError_t launch_evict4(const EvictParams& p, cudaStream_t st);      // 4-bit blocks (evict4.cu)
 cudaError_t launch_evict_bulk(const EvictParams& p, cudaStream_t st);  // many tokens, 4-bit blocks (evict_bulk.cu)
