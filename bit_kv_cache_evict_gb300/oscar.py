@@ -647,7 +647,7 @@ def oscar_decode_attn_int4(shape: oscar_shape, q, bf16_kv, bf16_len, pool, page_
         _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, 4), dev),
         _arg(page_table, "page_table", _I32, B * max_pages, dev), max_pages, num_pages,
         _arg(hist_len, "hist_len", _I32, B, dev), _arg(U, "U", _F32, hk * 2 * d * d, dev), sm_scale,
-        _arg(out, "out", out.dtype, rows, dev), kind, _arg(workspace, "workspace", _U8, 0, dev),
+        _arg(out, "out", out.dtype, rows, dev), kind, _arg(workspace, "workspace", _U8, 1 if B else 0, dev),
         ctypes.byref(ctypes.c_size_t(workspace.numel())), _arg(dev_status, "dev_status", _I32, 1, dev),
         _stream_arg(stream, dev))
     if st:
