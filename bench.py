@@ -50,15 +50,30 @@ DEFAULT_WORKLOAD = "qwen3_8b_36l"
 # DRAM traffic of int2_kernel from one ncu capture (dram__bytes_read.sum +
 # dram__bytes_write.sum of one launch: the one-layer version of the
 # workload, the bench's own launch configuration, captured with
-# `ncu --set full -k regex:int2_kernel -c 1`), with the algorithmic bytes of
+# `ncu -k regex:int2_kernel -s 3 -c 1`), with the algorithmic bytes of
 # the captured launch.  Reported, scaled to the bench's mean launch by the
 # units processed, only while the kernel source is the one captured.
 INT2_TRAFFIC_CAPTURE = {
     "workload": "qwen3_8b_36l",
-    "source_sha256_16": "f069882ad321dc5c",     # csrc/decode.cu + csrc/oscar_common.cuh, comments removed
-    "traffic_bytes": 917.42e6 + 11.56e6,
+    "source_sha256_16": "b92e4e7774d2da6f",     # int2_sources(), comments removed
+    "traffic_bytes": 917.39e6 + 10.76e6,
     "algorithmic_bytes": 911.11e6,
 }
+
+
+def int2_sources() -> dict:
+    """Source texts of the INT2 kernel by file name: csrc/decode.cu and the
+    library headers that it includes, in the order of inclusion."""
+    import re
+    texts, todo = {}, ["decode.cu"]
+    while todo:
+        f = todo.pop(0)
+        if f in texts:
+            continue
+        with open(os.path.join(ROOT, "bit_kv_cache_evict_gb300", "csrc", f), encoding="utf-8") as fh:
+            texts[f] = fh.read()
+        todo += re.findall(r'^\s*#include "([^"/]+)"', texts[f], re.M)
+    return texts
 
 
 def kernel_source_hash() -> str:
@@ -68,9 +83,7 @@ def kernel_source_hash() -> str:
     import hashlib
     import re
     h = hashlib.sha256()
-    for f in ("decode.cu", "oscar_common.cuh"):
-        with open(os.path.join(ROOT, "bit_kv_cache_evict_gb300", "csrc", f), encoding="utf-8") as fh:
-            text = fh.read()
+    for text in int2_sources().values():
         for line in text.splitlines():
             code = re.sub(r"//.*$", "", line).rstrip()
             if code:
