@@ -5,13 +5,14 @@
 // run on float pairs; 16 levels, and every decision (the clip threshold c
 // max|y|, s and z to fp16, the codes) is taken from the pairs: codes and
 // pairs are those of a float64 evaluation except where that lies within
-// 2^-36 |x| of a border.
+// 2^-36 |x| of a border (the arithmetic replayed on the host over random and
+// aligned rows: at most 2^-39.5 |x|; if every rounding were of one sign, 2^-29).
 //
 // The sum y = x . U takes four instructions a term instead of the ten of a
 // compensated product and sum: the accumulator starts at M = 1.5 2^E, far
 // enough above every partial sum that it never leaves [2^E, 2^(E+1)), so its
 // steps are multiples of one unit, and
-//   n = fma(x, u, acc),  d = n - acc (exact),  lo += fma(x, u, -d) (exact)
+//   n = fma(x, u, acc),  d = n - acc (exact),  lo += fma(x, u, -d) (exact to 2^-49 2^E)
 // keep what each step rounds away.  E comes from sum|x| of the warp's terms and
 // |u| < 2 (an orthogonal U has |u| <= 1); a matrix with a larger entry is
 // summed the long way.  1024 vectors took 13.2 us with compensated sums

@@ -31,12 +31,13 @@
 // 2^-38.
 //
 // What bounds it: 512 bytes read and 160 written per token and KV head
-// (24 us for 15,104 tokens of eight KV heads), 256 tensor-core products per
-// 16 vectors, and their decisions: 4,700 instructions in all.  Measured 120 us
-// for that case (GB300; 0.67 TB/s; the per-vector kernel: 1832 us): 9 us for
+// (12 us for 15,104 tokens of eight KV heads), 256 tensor-core products per
+// 16 vectors, and their decisions: 4,800 instructions in all.  Measured 125 us
+// for that case (GB300; 0.65 TB/s; the per-vector kernel: 1832 us; 120 with the
+// products in chains, see delta): 9 us for
 // R, then per 16-token tile a third of the time in the products (at half of
 // mma.sync's rate), a sixth in the exact sums, an eighth in the codes; the
-// schedulers issue in 53 % of the cycles, the tensor cores run in 23 %.  The kernel's
+// schedulers issue in 52 % of the cycles, the tensor cores run in 22 %.  The kernel's
 // code is larger than the instruction caches hold: loops are kept rolled and
 // warps in step (below) for that reason.  (16 warps of 128 registers instead of
 // 12 of 168 cost 3 us, groups of four warps 7, two barriers fewer per tile 5.)

@@ -18,7 +18,8 @@
 // sqrt(sum p^2)), and their products are summed page by page (page_values).
 // A logit has 128 terms and no such difference: K codes stay as they are.
 //
-// Operands of V.  A 16-bit pattern 0x6400 | c is the fp16 1024 + c and
+// Operands of V, by the method of Kim, Henry, Fahim and Hassan Awadalla, "Who
+// Says Elephants Can't Run" (2022): a 16-bit pattern 0x6400 | c is the fp16 1024 + c and
 // 0x6400 | 16 c is 1024 + 16 c: one AND-OR on the code word in place and one
 // fp16 add (-1032) or fused multiply-add (/ 16, -72) give c - 8 exactly; a
 // shift by 8 serves the other two nibbles of each half: nine instructions

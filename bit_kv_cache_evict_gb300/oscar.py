@@ -657,8 +657,8 @@ def oscar_decode_attn_int4(shape: oscar_shape, q, bf16_kv, bf16_len, pool, page_
 def oscar_history_read(shape: oscar_shape, bits: int, seq, pos, pool, page_table, batch: int, max_pages: int,
                        num_pages: int, out, dev_status=None, stream=None) -> None:
     """Stored tokens (seq, pos: int32 [n]) as rows out [n][Hk][2][d] (float32 or
-    bfloat16) in the rotated domain; bits: 2 or 4, the pool's codes; see
-    include/oscar.h."""
+    bfloat16) in the rotated domain; bits: 2 (uniform levels: not for a Lloyd-Max
+    pool) or 4, the pool's codes; see include/oscar.h."""
     kind = _out_type(out)
     dev, n, hk = _current_device(), seq.numel(), shape.num_kv_heads
     st = lib().oscar_history_read(

@@ -476,12 +476,23 @@ oscar_status oscar_decode_attn_boost(const oscar_shape* shape, int32_t batch, co
  *   other slot is touched.  Every decision (the clip threshold, s, z, the
  *   codes) is that of values within 2^-36 |x| of the exact rotated ones, so
  *   codes and pairs match a float64 evaluation except that close to a
- *   border.  Calls with many tokens (a prompt's history) rotate on tensor
- *   cores and take the few open decisions again from exact sums.
+ *   border (the sign of a z of 0 is such a decision).  Calls with many
+ *   tokens (a prompt's history) rotate on tensor cores and take the few open
+ *   decisions again from exact sums.  A vector with NaN or infinity, or whose
+ *   rotated values pass fp32's range, gets codes and pairs that are not
+ *   specified but for this: every value that they stand for is NaN or
+ *   infinite.
  * oscar_decode_attn_int4: oscar_decode_attn over a 4-bit pool, with the
  *   same arguments and workspace convention, and `out` of type out_type:
  *   OSCAR_OUT_F32 (fp32, 16-byte aligned) or OSCAR_OUT_BF16 (bf16 [B][Hq][d],
- *   8-byte aligned, rounded once from the fp32 result).
+ *   8-byte aligned, rounded once from the fp32 result).  Sums, softmax
+ *   statistics and partials are fp32; rotated queries, weights times scales
+ *   and the un-rotation enter their products as two fp16 parts (22 bits).
+ *   The query heads of a KV head share the power of two of those parts: a
+ *   logit is off by about 2^-20 of its terms' sum, and by 2^-38 of what it
+ *   would be with the group's largest rotated query entry.  A NaN or
+ *   +infinite logit makes its output row NaN, as in the definition; a token
+ *   with a -infinite one has weight 0.
  * Errors: as the 2-bit calls; INVALID_ARG for an unknown out_type.
  */
 #define OSCAR_OUT_F32 0
@@ -507,7 +518,10 @@ oscar_status oscar_decode_attn_int4(const oscar_shape* shape, int32_t batch, con
  * multiplied by R_K, outputs by R_V^T), for moving a history to another
  * format, and to look at what an eviction wrote.
  *
- *   bits     2 (pools of oscar_evict_quantize; the uniform levels) or 4
+ *   bits     2 or 4.  For 2 bits the values are those of the uniform levels:
+ *            a pool of oscar_evict_quantize_codebook is not told apart and
+ *            comes back with the wrong ones, and of a boosted pool the
+ *            records are not read (the values are its 2-bit ones).
  *   seq, pos (device int32 [n_tok]) sequence and history position of each row
  *   out      (device) [n_tok][Hk][2][d] of out_type, 16-byte aligned; one
  *            rounding to bf16 for OSCAR_OUT_BF16

@@ -165,3 +165,25 @@ def test_a_query_that_overflows_leaves_the_other_heads(hq, hk, g):
     keep = np.arange(hq) != 1
     out = c.decode()[:, torch.from_numpy(keep).cuda()]
     check(out, want[:, keep], mag[:, keep])
+
+
+@pytest.mark.parametrize("g", [32, 128])
+@pytest.mark.parametrize("per_call", [None, 7])            # tensor cores; one vector per block
+def test_rows_that_are_not_finite_stand_for_no_finite_value(g, per_call):
+    """Whatever codes and pairs such a vector gets, what is read back of it is NaN or
+    infinite throughout, and finite of every other vector."""
+    from test_gpu_int4 import evict_in_calls, kv_bits, rotation
+    rng = np.random.default_rng(58)
+    hk, n = 8, 300
+    x = H.bf16_t(kv_bits(rng, n, hk))
+    nan, inf = float("nan"), float("inf")
+    bad = torch.zeros(n, hk, 2, dtype=torch.bool, device="cuda")
+    for at, v in (((3, 0, 0, 5), nan), ((17,), inf), ((40, slice(None), 1, 0), -inf), ((41, 2, 0), nan), ((299, 1, 1), 3e38), ((64, 7, 0, 127), inf)):
+        x[at] = v
+        bad[at[:3]] = True
+    table, pos, seq = np.arange(5, dtype=np.int32)[None], H.i32_t(np.arange(n)), H.i32_t(np.zeros(n))
+    pool, status = evict_in_calls(x, H.f32_t(rotation(rng, hk)), torch.full((hk, 2), 0.9, device="cuda"), pos, seq, table, g, per_call)
+    out = torch.zeros(n, hk, 2, D, device="cuda")
+    O.oscar_history_read(O.make_shape(hk, hk, quant_group=g), 4, seq, pos, pool, H.i32_t(table), 1, 5, 5, out)
+    assert status == 0
+    assert torch.equal(out.isfinite().all(-1), ~bad) and torch.equal(out.isfinite().any(-1), ~bad)
