@@ -266,13 +266,13 @@ cudaError_t launch(const EvictParams& p, cudaStream_t st) {
 // Calls with this many vectors (tokens x KV heads x 2) take the bulk kernel: it
 // starts with 9 us of forming R in every block and then needs 0.5 ns per
 // vector, this kernel 5 ns.  (GB300, us here and there, a graph of 20 calls:
-//                3072 vectors   4096         6000         8192
-//   1 KV head    19.6  23.1     24.9  23.5   34.0  23.5   44.5  24.3
-//   8            20.0  23.3     25.3  23.5   30.4  23.4*  45.1  24.0
-//   40           20.3  21.1     25.7  21.7   30.6  21.6*  46.0  22.4
-//   80           16.5* 38.2     25.8  38.2   36.0  38.9   46.0  38.8
-// (*) 5120 vectors, 2080 with 80 heads, whose 160 (KV head, K|V) pairs make two
-// waves of bulk blocks: from 77 heads up the border would lie near 6800.
+//                2048 vectors   4096         6000         8192
+//   1 KV head    15.7  22.8     24.9  23.5   34.0  23.5   44.5  24.3
+//   8            16.2  22.1     25.3  23.5   30.4  23.4*  45.1  24.0
+//   40           16.4  21.2     25.7  21.7   30.6  21.6*  46.0  22.4
+//   80           16.5  38.2     25.8  38.2   36.0  38.9   46.0  38.8
+// (*) 5120 vectors.  With 80 heads 160 (KV head, K|V) pairs make two waves of bulk
+// blocks: from 77 heads up the border would lie near 6800.
 // 15,104 tokens of eight heads: 1830 and 124.)
 constexpr int kBulkVectors = 4096;
 
