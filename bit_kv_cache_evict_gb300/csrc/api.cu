@@ -69,6 +69,8 @@ static int tail_pages_of(int pps) { return pps > kShortItemPages ? 2 * kShortIte
 
 struct WsLayout {
     size_t counter, item_start, item_start2, qfrag, qsum, qkinv, qrot, part, bf_part, total;
+    size_t logits, slot_logits, norm;  // kModeWeights
+    size_t skip, sref, member, groups, qrow, sh_part;  // kModeShared
     int NT, pps, tail_pg, part_stride, parts;  // parts: partials per item
     int64_t max_items;   // split-K items at most (int64: batch x KV heads x splits can exceed int32)
 };
@@ -87,7 +89,19 @@ static int64_t items4_bound(int64_t pairs, int max_pages) {
     return std::max(even, std::min(share, pairs * per_pair(kMinItemPages4)));
 }
 
-static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bits) {
+// Most partials (member, KV head, split) of the shared pages that group_kernel's
+// plan makes: an item is a KV head, up to `rows` rows and a run of pages.
+//   one item for each block at most; or, where whole groups are more, four times
+//   that and one per KV head and row tile for the rounding; runs have
+//   kMinSharedPages pages at least but for one per group and KV head.
+static int64_t shared_parts_bound(const oscar_shape* s, int batch, int max_pages, int n_groups) {
+    const int64_t hk = s->num_kv_heads, G = s->num_q_heads / hk, rows = 256;
+    const int64_t tiles = (batch * G + 127) / 128 + std::min(n_groups, batch / 2 + 1);
+    const int64_t items = 17 * kMaxSharedBlocks / 4 + hk * tiles;  // (runs of 16 pages at least, rounded down)
+    return std::min(items * (rows / G), batch * hk * ((max_pages + kMinSharedPages - 1) / kMinSharedPages));
+}
+
+static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bits, Mode mode = kModePlain, int n_groups = 0) {
     WsLayout w{};
     const int G = s->num_q_heads / s->num_kv_heads, hk = s->num_kv_heads;
     w.NT = (G + 3) / 4;
@@ -119,6 +133,29 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bi
     off = round_up(off + (size_t)w.max_items * w.parts * w.part_stride * 4, 256);
     w.bf_part = off;
     off = round_up(off + (size_t)batch * hk * bf16_items(s) * w.part_stride * 4, 256);
+    if (mode == kModeWeights) {
+        const size_t rows = (size_t)batch * s->num_q_heads;
+        w.logits = off;
+        off = round_up(off + rows * max_pages * kPage * 4, 256);
+        w.slot_logits = off;
+        off = round_up(off + rows * (s->sink + s->recent) * 4, 256);
+        w.norm = off;
+        off = round_up(off + rows * 8, 256);
+    }
+    if (mode == kModeShared) {
+        w.skip = off;
+        off = round_up(off + (size_t)batch * 4, 256);
+        w.sref = off;
+        off = round_up(off + (size_t)batch * 16, 256);
+        w.member = off;
+        off = round_up(off + (size_t)batch * 4, 256);
+        w.groups = off;
+        off = round_up(off + (size_t)n_groups * sizeof(SharedGroup), 256);
+        w.qrow = off;
+        off = round_up(off + (size_t)2 * batch * s->num_q_heads * kD * 2, 256);
+        w.sh_part = off;
+        off = round_up(off + (size_t)shared_parts_bound(s, batch, max_pages, n_groups) * w.part_stride * 4, 256);
+    }
     w.total = off;
     return w;
 }
@@ -319,20 +356,34 @@ oscar_status oscar_evict_quantize_int4(const oscar_shape* shape, int32_t n_tok, 
                       nullptr, page_table, batch, max_pages, num_pages, dev_status, stream, 4);
 }
 
+// What a call of another mode adds to a decode's arguments.
+struct DecodeExtra {
+    Mode mode;
+    float* weight;
+    int32_t weight_stride;
+    float* slot_weight;
+    float decay;
+    const int32_t* prefix_group;
+    const int32_t* group_pages;
+    int32_t n_groups;
+};
+
 static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const void* q, const void* bf16_kv,
                                 const int32_t* bf16_len, const uint8_t* pool, const int32_t* page_table,
                                 int32_t max_pages, int32_t num_pages, const int32_t* hist_len, const float* U,
                                 const float* codebook, const uint8_t* boost, float sm_scale, float* out,
                                 void* workspace, size_t* ws_bytes, int32_t* dev_status, void* stream,
-                                int bits = 2, int out_type = OSCAR_OUT_F32) {
+                                int bits = 2, int out_type = OSCAR_OUT_F32, const DecodeExtra* extra = nullptr) {
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (batch < 0 || max_pages <= 0 || num_pages < 0 || !ws_bytes) return OSCAR_ERR_INVALID_ARG;
     if ((int64_t)batch * shape->num_kv_heads > INT32_MAX) return OSCAR_ERR_INVALID_ARG;
-    const WsLayout w = ws_layout(shape, batch, max_pages, bits);
+    const Mode mode = extra ? extra->mode : kModePlain;
+    const WsLayout w = ws_layout(shape, batch, max_pages, bits, mode, extra ? extra->n_groups : 0);
     // item counts, item offsets and partial indices are int32 on the device
     if (w.max_items * w.parts > INT32_MAX || (double)w.max_items * w.part_stride > 4.0e9)
         return OSCAR_ERR_INVALID_ARG;
+    if (mode == kModeShared && shared_parts_bound(shape, batch, max_pages, extra->n_groups) > INT32_MAX) return OSCAR_ERR_INVALID_ARG;
     if (!workspace) {
         *ws_bytes = w.total;
         return OSCAR_OK;
@@ -347,6 +398,16 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
         !aligned(bf16_len, 4) || !aligned(hist_len, 4) || !aligned(page_table, 4))
         return OSCAR_ERR_INVALID_ARG;
     if (!(sm_scale == sm_scale)) return OSCAR_ERR_INVALID_ARG;
+    if (mode == kModeWeights) {
+        if (!extra->weight || !aligned(extra->weight, 4) || !aligned(extra->slot_weight, 4) ||
+            extra->weight_stride < (int64_t)max_pages * kPage || !(extra->decay >= 0.f) || !(extra->decay <= 1.f))
+            return OSCAR_ERR_INVALID_ARG;
+        // (thread blocks of weights_kernel)
+        if ((double)batch * ((double)max_pages * kPage / 256 + 4) > 2.0e9) return OSCAR_ERR_INVALID_ARG;
+    }
+    if (mode == kModeShared && (!extra->prefix_group || (extra->n_groups > 0 && !extra->group_pages) ||
+                                !aligned(extra->prefix_group, 4) || !aligned(extra->group_pages, 4)))
+        return OSCAR_ERR_INVALID_ARG;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     DecodeParams4 p{};
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -397,6 +458,29 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
     p.qscale = sm_scale * kLog2e;
     p.codebook = codebook;
     p.boost = boost;
+    if (extra) {
+        DecodeParamsX x{};
+        static_cast<DecodeParams4&>(x) = p;
+        x.logits = reinterpret_cast<float*>(ws + w.logits);
+        x.slot_logits = reinterpret_cast<float*>(ws + w.slot_logits);
+        x.norm = reinterpret_cast<float2*>(ws + w.norm);
+        x.weight = extra->weight;
+        x.slot_weight = extra->slot_weight;
+        x.weight_stride = extra->weight_stride;
+        x.decay = extra->decay;
+        x.prefix_group = extra->prefix_group;
+        x.group_pages = extra->group_pages;
+        x.n_groups = extra->n_groups;
+        x.skip = reinterpret_cast<int32_t*>(ws + w.skip);
+        x.sref = reinterpret_cast<int4*>(ws + w.sref);
+        x.member = reinterpret_cast<int32_t*>(ws + w.member);
+        x.groups = reinterpret_cast<SharedGroup*>(ws + w.groups);
+        x.qrow = reinterpret_cast<uint16_t*>(ws + w.qrow);
+        x.sh_part = reinterpret_cast<float*>(ws + w.sh_part);
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        const cudaError_t e = mode == kModeWeights ? launch_decode_weights(x, bits, st) : launch_decode_shared(x, bits, st);
+        return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
+    }
     if (bits == 4) {
         const cudaError_t e = launch_decode4(p, static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
@@ -453,6 +537,78 @@ oscar_status oscar_decode_attn_int4(const oscar_shape* shape, int32_t batch, con
     return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
                        nullptr, nullptr, sm_scale, static_cast<float*>(out), workspace, ws_bytes, dev_status, stream,
                        4, out_type);
+}
+
+oscar_status oscar_decode_attn_weights(const oscar_shape* shape, int32_t bits, int32_t batch, const void* q,
+                                       const void* bf16_kv, const int32_t* bf16_len, const uint8_t* pool,
+                                       const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                                       const int32_t* hist_len, const float* U, float sm_scale, void* out,
+                                       int32_t out_type, float* weight, int32_t weight_stride, float* slot_weight,
+                                       float decay, void* workspace, size_t* ws_bytes, int32_t* dev_status,
+                                       void* stream) {
+    const oscar_status sst = check_shape(shape);
+    if (sst != OSCAR_OK) return sst;
+    if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
+    if (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) return OSCAR_ERR_INVALID_ARG;
+    if (max_pages > INT32_MAX / kPage) return OSCAR_ERR_INVALID_ARG;  // positions are int32
+    const DecodeExtra extra{kModeWeights, weight, weight_stride, slot_weight, decay, nullptr, nullptr, 0};
+    return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
+                       nullptr, nullptr, sm_scale, static_cast<float*>(out), workspace, ws_bytes, dev_status, stream,
+                       bits, out_type, &extra);
+}
+
+oscar_status oscar_decode_attn_shared(const oscar_shape* shape, int32_t bits, int32_t batch, const void* q,
+                                      const void* bf16_kv, const int32_t* bf16_len, const uint8_t* pool,
+                                      const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                                      const int32_t* hist_len, const int32_t* prefix_group, int32_t n_groups,
+                                      const int32_t* group_pages, const float* U, float sm_scale, void* out,
+                                      int32_t out_type, void* workspace, size_t* ws_bytes, int32_t* dev_status,
+                                      void* stream) {
+    const oscar_status sst = check_shape(shape);
+    if (sst != OSCAR_OK) return sst;
+    if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
+    if (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) return OSCAR_ERR_INVALID_ARG;
+    if (max_pages > INT32_MAX / kPage) return OSCAR_ERR_INVALID_ARG;  // positions are int32
+    if (n_groups < 0 || n_groups > kMaxSharedGroups) return OSCAR_ERR_INVALID_ARG;
+    const DecodeExtra extra{kModeShared, nullptr, 0, nullptr, 1.f, prefix_group, group_pages, n_groups};
+    return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
+                       nullptr, nullptr, sm_scale, static_cast<float*>(out), workspace, ws_bytes, dev_status, stream,
+                       bits, out_type, &extra);
+}
+
+oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t weight_stride, const int32_t* hist_len,
+                                  const int32_t* budget, int32_t protect, int32_t* keep, int32_t keep_stride,
+                                  int32_t* n_keep, float* kept_weight, int32_t kept_stride, int32_t* dev_status,
+                                  void* stream) {
+    constexpr int32_t kMost = INT32_MAX - (1 << 16);  // positions rounded up to a thread block's parts are int32
+    if (batch < 0 || weight_stride < 0 || weight_stride > kMost || protect < 0 || keep_stride < 0 || kept_stride < 0 ||
+        batch > INT32_MAX / 8)
+        return OSCAR_ERR_INVALID_ARG;
+    if (batch == 0) return OSCAR_OK;
+    if (!hist_len || !budget || !n_keep || (weight_stride > 0 && !weight) || (keep_stride > 0 && !keep))
+        return OSCAR_ERR_INVALID_ARG;
+    if (!aligned(weight, 4) || !aligned(hist_len, 4) || !aligned(budget, 4) || !aligned(keep, 4) || !aligned(n_keep, 4) ||
+        !aligned(kept_weight, 4) || !aligned(dev_status, 4))
+        return OSCAR_ERR_INVALID_ARG;
+    // (thread blocks of a sequence write its kept scores while others still read)
+    const uintptr_t a0 = (uintptr_t)weight, a1 = a0 + (size_t)batch * weight_stride * 4;
+    const uintptr_t k0 = (uintptr_t)kept_weight, k1 = k0 + (size_t)batch * kept_stride * 4;
+    if (kept_weight && a0 < k1 && k0 < a1) return OSCAR_ERR_INVALID_ARG;
+    HistorySelectParams p{};
+    p.weight = weight;
+    p.hist_len = hist_len;
+    p.budget = budget;
+    p.keep = keep;
+    p.n_keep = n_keep;
+    p.kept_weight = kept_weight;
+    p.status = dev_status;
+    p.batch = batch;
+    p.stride = weight_stride;
+    p.protect = protect;
+    p.keep_stride = keep_stride;
+    p.kept_stride = kept_stride;
+    const cudaError_t e = launch_history_select(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? OSCAR_OK : cuda_fail(e);
 }
 
 oscar_status oscar_history_read(const oscar_shape* shape, int32_t bits, int32_t n_tok, const int32_t* seq,

@@ -53,11 +53,11 @@ constexpr int kPrepUnits = kPrepSeqs * 2 * 4;  // (b, nt, hh) units of a block a
 constexpr int kPrepSmem = kD * kD * 4 + kPrepUnits * kD * 4 + kPrepUnits * 4;
 
 // The parameters of a kernel that both histories use.
-template <bool INT4>
-using Params = std::conditional_t<INT4, DecodeParams4, DecodeParams>;
+template <bool INT4, Mode MODE>
+using Params = std::conditional_t<MODE == kModePlain, std::conditional_t<INT4, DecodeParams4, DecodeParams>, DecodeParamsX>;
 
-template <bool INT4>
-__device__ __forceinline__ void prep_body(const Params<INT4>& p);
+template <bool INT4, Mode MODE>
+__device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p);
 
 // Launched as a programmatic dependent of the eviction (it reads neither the
 // pool nor the BF16 segment), so the two overlap.  One block waits for the
@@ -67,13 +67,13 @@ __device__ __forceinline__ void prep_body(const Params<INT4>& p);
 // slots go to the rest of the grid and to the INT2 kernel's blocks).
 // 40 registers, so that two blocks fit on an SM beside the eviction's blocks
 // (the grid is one wave there).
-template <bool INT4>
-__global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4> p) {
-    // 4-bit history: q and the lengths may come from the kernel just before, so
-    // every block waits for it first.
-    if constexpr (INT4) pdl_wait();
+template <bool INT4, Mode MODE = kModePlain>
+__global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4, MODE> p) {
+    // 4-bit history, and the modes: q and the lengths may come from the kernel just
+    // before, so every block waits for it first.
+    if constexpr (INT4 || MODE != kModePlain) pdl_wait();
     pdl_trigger();
-    prep_body<INT4>(p);
+    prep_body<INT4, MODE>(p);
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) pdl_wait();
 }
 
@@ -95,11 +95,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6) prep_kernel(Params<INT4> p) {
 // four of up to 100,000, one KV head, us: 31.8, 25.9, 19.8, 35.6; with at most
 // 128: 31.3, 23.2, 19.5, 37.0; 256: 30.3, 25.8, 19.5, 37.1).
 //   items4_bound (api.cu) is the most items that either form makes.
-__device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tail_pg) {
+__device__ __forceinline__ void plan4(const DecodeParams4& p, const int32_t* skip, int& pps, int& tail_pg) {
     const int lane = threadIdx.x & 31;
-    auto pages_of = [&](int b) {
+    auto pages_of = [&](int b) {  // (behind the pages that its group attends, where there are such)
         const int h = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
-        return (h + kPage - 1) / kPage;
+        return (h + kPage - 1) / kPage - (skip ? __ldg(skip + b) : 0);
     };
     long total = 0;
     int most = 0;
@@ -138,8 +138,8 @@ __device__ __forceinline__ void plan4(const DecodeParams4& p, int& pps, int& tai
     tail_pg = pps > kShortItemPages ? 2 * kShortItemPages : 0;
 }
 
-template <bool INT4>
-__device__ __forceinline__ void prep_body(const Params<INT4>& p) {
+template <bool INT4, Mode MODE>
+__device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
     extern __shared__ __align__(16) float psm[];
     float* Us = psm;                       // [a][k] = U_K[a][k]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -149,7 +149,9 @@ __device__ __forceinline__ void prep_body(const Params<INT4>& p) {
         // long items of every sequence first, then the short tail items
         int pps = p.pps, tail_pg = p.tail_pg;
         if constexpr (INT4) {
-            plan4(p, pps, tail_pg);
+            const int32_t* skip = nullptr;
+            if constexpr (MODE == kModeShared) skip = p.skip;
+            plan4(p, skip, pps, tail_pg);
             if (lane == 0) {
                 p.counter[kPlanPps] = pps;
                 p.counter[kPlanTail] = tail_pg;
@@ -171,6 +173,7 @@ __device__ __forceinline__ void prep_body(const Params<INT4>& p) {
                     report(p.status, OSCAR_STATUS_BAD_POS);
                     h = min(max(h, 0), p.max_pages * kPage);
                 }
+                if constexpr (MODE == kModeShared) h -= p.skip[b] * kPage;
                 const SeqSplits sp = seq_splits((h + kPage - 1) / kPage, pps, tail_pg);
                 n_long = sp.n_long * p.hk;
                 n_short = sp.n_short * p.hk;
@@ -333,6 +336,11 @@ __device__ __forceinline__ void prep_body(const Params<INT4>& p) {
         const float v[4] = {qs[base] * up, qs[base + second] * up, qs[base + 1] * up, qs[base + second + 1] * up};
         uint32_t h01, h23, l01, l23;
         split_f16(v, h01, h23, l01, l23);
+        if constexpr (MODE == kModeShared) {  // the row of the shared pages' products, positions in the same order
+            uint16_t* row = const_cast<uint16_t*>(p.qrow) + ((size_t)b * p.hq + kv * p.G + hl) * kD + 8 * (4 * (ks >> 1) + tq) + 4 * (ks & 1);
+            *reinterpret_cast<uint2*>(row) = make_uint2(h01, h23);
+            *reinterpret_cast<uint2*>(row + (size_t)p.B * p.hq * kD) = make_uint2(l01, l23);
+        }
         if (p.NT == 2) {
             // eight heads: column = head, hi and lo parts in two fragment sets
             uint32_t* fr = p.qfrag + (size_t)bk * 2 * 8 * 32 * 2;  // [part][ks][32] uint2
@@ -370,7 +378,7 @@ constexpr int kInt2Threads = (kConsumerWarps + 1) * 32;
 
 struct StageInfo {
     int item, b, kv, valid_flags;  // valid tokens in bits 0-7, flags above
-    int pid, pad[3];               // page id (read by the boost variant)
+    int pid, page, pad[2];         // page id (read by the boost variant); page of the history (-1: none; kModeWeights)
 };
 
 // Blocks per SM and ring stages of an int2_kernel instantiation: three
@@ -463,7 +471,8 @@ constexpr int kPvRow = 72;  // floats per probability / V-scale row (64 + 8: con
 // block's power of two (K: k_scale_up) and z; rows past the
 // valid tokens are zero.  K rows: s~ and z as float4 per token; V rows: z per
 // token, and s~ in the P.V token order (pv_pos).
-template <bool FULL, int GS>
+// CENTRE: V z + 1.5 s in place of z (the codes then count from 1.5).
+template <bool FULL, int GS, bool CENTRE>
 __device__ __forceinline__ void page_scales_g(const uint8_t* blk, int valid, float4* ksS, float4* kzS, float4* vzS,
                                               float* vsS, float kmul, float vmul) {
     constexpr int NG = 4 >> GS;  // (s, z) pairs per token vector
@@ -493,7 +502,7 @@ __device__ __forceinline__ void page_scales_g(const uint8_t* blk, int valid, flo
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 sv[b] = s_g[b >> GS] * (which ? vmul : k_scale_up(b) * kmul);
-                zz[b] = z_g[b >> GS];
+                zz[b] = CENTRE && which ? fmaf(1.5f, s_g[b >> GS], z_g[b >> GS]) : z_g[b >> GS];
             }
         } else {
 #pragma unroll
@@ -513,13 +522,13 @@ __device__ __forceinline__ void page_scales_g(const uint8_t* blk, int valid, flo
 
 // kmul / vmul multiply the K / V scales (K: the item's 2^-e, times the
 // Lloyd-Max inner level a; V: a; 1 for the uniform levels)
-template <bool FULL>
+template <bool FULL, bool CENTRE = false>
 __device__ __forceinline__ void page_scales(const uint8_t* blk, int valid, int gshift, float4* ksS, float4* kzS,
                                             float4* vzS, float* vsS, float kmul = 1.f, float vmul = 1.f) {
     switch (gshift) {  // warp-uniform, once per page
-        case 0: page_scales_g<FULL, 0>(blk, valid, ksS, kzS, vzS, vsS, kmul, vmul); break;
-        case 1: page_scales_g<FULL, 1>(blk, valid, ksS, kzS, vzS, vsS, kmul, vmul); break;
-        default: page_scales_g<FULL, 2>(blk, valid, ksS, kzS, vzS, vsS, kmul, vmul); break;
+        case 0: page_scales_g<FULL, 0, CENTRE>(blk, valid, ksS, kzS, vzS, vsS, kmul, vmul); break;
+        case 1: page_scales_g<FULL, 1, CENTRE>(blk, valid, ksS, kzS, vzS, vsS, kmul, vmul); break;
+        default: page_scales_g<FULL, 2, CENTRE>(blk, valid, ksS, kzS, vzS, vsS, kmul, vmul); break;
     }
 }
 
@@ -568,17 +577,87 @@ __device__ __forceinline__ uint2 scaled_fragment(uint2 f, float kappa, int is_lo
     return is_lo ? make_uint2(l01, l23) : make_uint2(h01, h23);
 }
 
+// V code operands counted from the middle of the levels: (c - 1.5) 2^(P - 9) of a
+// register of codes c 2^(P - 24), exact in fp16 and never subnormal.
+template <int SLOT>
+__device__ __forceinline__ uint32_t centred(uint32_t a) {
+    constexpr uint32_t off = (uint32_t)(0x8000 | ((slot_bit(SLOT) - 9 + 15) << 10) | 0x200) * 0x10001u;  // -1.5 2^(P - 9)
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0x78007800u), "r"(off));  // 2^15
+    return r;
+}
+__device__ __forceinline__ constexpr float v_out_scale_centred(int slot) { return pow2f(9 - slot_bit(slot)); }
+
+// The P.V products of a page in the modes with fp32 output.  A flat softmax over a long history
+// leaves a result far smaller than sum p s c, so the codes are centred (z + 1.5 s
+// in the place of z), and each M tile is summed over the page from zero and
+// then added in fp32: the tensor core truncates its accumulator at every step.
+// 32 x 8K, eight heads, groups of 128, a flat softmax: the output within 2.7e-5 of float64
+// (2-norm) with the products of the plain decode, 1.4e-6 with these.  They cost 20 % (8 x
+// 32K, 32:8 heads: 96 -> 114 us), so a bf16 output, whose rounding is 2^-9, goes without.
+template <int NT>
+__device__ __forceinline__ void page_values_centred(const uint8_t* blk, const float* pS, const float* vsS,
+                                                    const SplitSel& take_lo, float (&acc_o)[8][4]) {
+    const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
+    uint32_t pv[4][4];  // [plane 8 k + gID][m]
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint4 v = *reinterpret_cast<const uint4*>(blk + kVCodes + (gID + 8 * k) * kPage + 16 * tq);
+        pv[k][0] = v.x; pv[k][1] = v.y; pv[k][2] = v.z; pv[k][3] = v.w;
+    }
+    auto slot_tiles = [&](auto slot) {
+        constexpr int g = decltype(slot)::value;
+        uint32_t w[4][2 * NT];  // k-step m: B registers, eight heads also their low parts
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int chunk = 4 * (4 * tq + (m ^ tq));
+            const float4 pp = *reinterpret_cast<const float4*>(pS + (NT == 1 ? gID >> 1 : gID) * kPvRow + chunk);
+            const float4 sg = *reinterpret_cast<const float4*>(vsS + g * kPvRow + chunk);
+            if constexpr (NT == 1) {
+                w[m][0] = split_w_pair_f16(make_float2(pp.x, pp.y), make_float2(sg.x, sg.y), take_lo);
+                w[m][1] = split_w_pair_f16(make_float2(pp.z, pp.w), make_float2(sg.z, sg.w), take_lo);
+            } else {
+                split_both(mul2(make_float2(pp.x, pp.y), make_float2(sg.x, sg.y)), w[m][0], w[m][2]);
+                split_both(mul2(make_float2(pp.z, pp.w), make_float2(sg.z, sg.w)), w[m][1], w[m][3]);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t r0 = pv[2 * half][m], r1 = pv[2 * half + 1][m];
+                uint32_t a0, a1, a2, a3;
+                v_operands<g>(r0, r1, code_swap(r0), code_swap(r1), a0, a1, a2, a3);
+                a0 = centred<g>(a0);
+                a1 = centred<g>(a1);
+                a2 = centred<g>(a2);
+                a3 = centred<g>(a3);
+                mma_f16_16816(t, a0, a1, a2, a3, w[m][0], w[m][1]);
+                if constexpr (NT == 2) mma_f16_16816(t, a0, a1, a2, a3, w[m][2], w[m][3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc_o[2 * g + half][e] += t[e];
+        }
+    };
+    slot_tiles(std::integral_constant<int, 0>{});
+    slot_tiles(std::integral_constant<int, 1>{});
+    slot_tiles(std::integral_constant<int, 2>{});
+    slot_tiles(std::integral_constant<int, 3>{});
+}
+
 // One page of INT2 history for one consumer warp: the page's scales, the
 // logits of its four 16-token tiles, one online-softmax update, and the P.V
 // products.  FULL (all 64 tokens valid, the common case) removes the
 // per-tile conditions of the logit phase so that the four tiles' work can
 // interleave.
-template <int NT, bool FULL, bool LM = false, bool BOOST = false>
+template <int NT, bool FULL, bool LM = false, bool BOOST = false, Mode MODE = kModePlain, bool CENTRE = false>
 __device__ __forceinline__ void attend_page(const uint8_t* blk, int valid, uint8_t* wbuf, const uint2* qfS,
                                             const float4 (&qsv)[NT], float kq, float (&m_run)[NT],
                                             float (&l_run)[NT], float (&zacc)[NT][4], float (&acc_o)[NT][8][4],
                                             const SplitSel& take_lo, int gshift, const Codebook& cbk = {},
-                                            const float4* qbS = nullptr, const uint8_t* brec = nullptr) {
+                                            const float4* qbS = nullptr, const uint8_t* brec = nullptr,
+                                            float* keep = nullptr, int keep_g = 0) {
     using SM = Int2Smem<NT>;
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
     if (FULL) valid = kPage;
@@ -596,7 +675,7 @@ __device__ __forceinline__ void attend_page(const uint8_t* blk, int valid, uint8
 
     // K scales times 2^-e (the power of two of the q' fragments)
     if constexpr (LM) page_scales<FULL>(blk, valid, gshift, ksS, kzS, vzS, vsS, cbk.ka * kq, cbk.va * kLmVDown);
-    else page_scales<FULL>(blk, valid, gshift, ksS, kzS, vzS, vsS, kq);
+    else page_scales<FULL, CENTRE>(blk, valid, gshift, ksS, kzS, vzS, vsS, kq);
     __syncwarp();
 
     // -- logits of the page's tiles: A rows gID / gID+8 = tokens 16m+gID /
@@ -714,6 +793,17 @@ __device__ __forceinline__ void attend_page(const uint8_t* blk, int valid, uint8
         __syncwarp();
     }
 
+    if constexpr (MODE == kModeWeights) {
+        static_assert(NT == 1, "eight heads: attend_page_g8");
+        float lg[4][2];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            lg[m][0] = la[m][0];
+            lg[m][1] = lb[m][0];
+        }
+        store_logits<1>(keep, keep_g, lg);
+    }
+
     // -- online softmax (base 2), once per page; every token's p is written
     //    (0 for the invalid ones)
 #pragma unroll
@@ -758,6 +848,10 @@ __device__ __forceinline__ void attend_page(const uint8_t* blk, int valid, uint8
     // -- values: A rows = dims (m-tile (g, half): in-group index 16 half +
     //    row, code plane 16 half + row, slot g), k = token group 4 tq + m
     //    (tokens 4q, 4q+2 | 4q+1, 4q+3), columns = heads (hi, lo)
+    if constexpr (CENTRE) {
+        page_values_centred<1>(blk, pS, vsS, take_lo, acc_o[0]);
+        return;
+    }
     uint4 pv4[4];  // bytes 16 tq .. 16 tq + 15 of planes gID, 8 + gID, 16 + gID, 24 + gID
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -830,13 +924,14 @@ __device__ __forceinline__ void attend_page(const uint8_t* blk, int valid, uint8
 // heads, and the hi / lo parts of q' and of P*s enter as two MMAs on the
 // same A fragment (accumulating into the same registers).  Lane (gID, tq)
 // holds heads 2tq and 2tq + 1.
-template <bool FULL, bool BOOST = false, bool LM = false>
+template <bool FULL, bool BOOST = false, bool LM = false, Mode MODE = kModePlain, bool CENTRE = false>
 __device__ __forceinline__ void attend_page_g8(const uint8_t* blk, int valid, uint8_t* wbuf, const uint2* qfS,
                                                const float4 (&qsv)[2], float kq, float (&m_run)[2],
                                                float (&l_run)[2],
                                                float (&zacc)[2][4], float (&acc_o)[8][4],
                                                int gshift, const float4* qbS = nullptr,
-                                               const uint8_t* brec = nullptr, const Codebook& cbk = {}) {
+                                               const uint8_t* brec = nullptr, const Codebook& cbk = {},
+                                               float* keep = nullptr) {
     using SM = Int2Smem<2>;
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
     if (FULL) valid = kPage;
@@ -854,7 +949,7 @@ __device__ __forceinline__ void attend_page_g8(const uint8_t* blk, int valid, ui
 
     // K scales times 2^-e (the power of two of the q' fragments)
     if constexpr (LM) page_scales<FULL>(blk, valid, gshift, ksS, kzS, vzS, vsS, cbk.ka * kq, cbk.va * kLmVDown);
-    else page_scales<FULL>(blk, valid, gshift, ksS, kzS, vzS, vsS, kq);
+    else page_scales<FULL, CENTRE>(blk, valid, gshift, ksS, kzS, vzS, vsS, kq);
     __syncwarp();
 
     // -- logits: lg[m] = (token a, head 2tq), (a, 2tq+1), (b, 2tq), (b, 2tq+1)
@@ -974,6 +1069,8 @@ __device__ __forceinline__ void attend_page_g8(const uint8_t* blk, int valid, ui
         __syncwarp();
     }
 
+    if constexpr (MODE == kModeWeights) store_logits<2>(keep, 8, lg);
+
     // -- online softmax per head (j: head 2tq + j)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -1016,6 +1113,10 @@ __device__ __forceinline__ void attend_page_g8(const uint8_t* blk, int valid, ui
     __syncwarp();
 
     // -- values: as attend_page, with B column gID = head gID (hi, then lo)
+    if constexpr (CENTRE) {
+        page_values_centred<2>(blk, pS, vsS, SplitSel{}, acc_o);
+        return;
+    }
     uint4 pv4[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -1075,8 +1176,11 @@ __device__ __forceinline__ void attend_page_g8(const uint8_t* blk, int valid, ui
     }
 }
 
-template <int NT, bool LM = false, bool BOOST = false>
-__global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOST>())) int2_kernel(DecodeParams p) {
+// CENTRE: the P.V products of page_values_centred.
+template <int NT, bool LM = false, bool BOOST = false, Mode MODE = kModePlain, bool CENTRE = false>
+__global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOST>()))
+int2_kernel(Params<false, MODE> p) {
+    static_assert(MODE == kModePlain || !(LM || BOOST), "the modes are for the uniform levels");
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int NS = int2_stages<NT, LM, BOOST>();  // ring stages
     using SM = Int2Smem<NT, NS>;
@@ -1116,7 +1220,7 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
         uint32_t pitem = 0;  // items started (QP: item k's q' data goes to buffer k % 2)
         bool ok = true;
         // one slot: wait for the stage, then publish its info (and copy)
-        auto post = [&](int item, int b, int kv, int pid, int valid, int flags) -> bool {
+        auto post = [&](int item, int b, int kv, int pid, int valid, int flags, int page = -1) -> bool {
             const uint32_t s = n % NS;
             if (n >= (uint32_t)NS) {
                 const bool w = mbar_wait_bounded(&empty[s], ((n / NS) - 1) & 1u, kWaitPolls);
@@ -1133,6 +1237,7 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
                 }
                 si.valid_flags = valid | (flags << 8);
                 si.pid = pid;
+                if constexpr (MODE == kModeWeights) si.page = page;
                 if (item < 0 || (flags & kFlagPad)) {
                     mbar_arrive(&full[s]);
                 } else {
@@ -1163,7 +1268,13 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
             const int splits = (__ldg(starts + b + 1) - s0) / p.hk;
             const int kv = (rel - s0) / splits;
             const int split = (rel - s0) % splits;
-            const int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+            int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+            const int32_t* table = p.page_table + (size_t)b * p.max_pages;
+            if constexpr (MODE == kModeShared) {  // the pages behind the shared ones
+                const int skip = __ldg(p.skip + b);
+                hist -= skip * kPage;
+                table += skip;
+            }
             const int seq_pages = (hist + kPage - 1) / kPage;
             const SeqSplits sp = seq_splits(seq_pages, p.pps, p.tail_pg);
             const int pg0 = is_long ? split * p.pps : sp.long_pages + split * kShortItemPages;
@@ -1192,7 +1303,7 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
             for (int c = 0; c < nslots && ok; c += 32) {
                 // page ids of the next 32 slots, one per lane
                 int pid = -1;
-                if (c + lane < npg) pid = __ldg(p.page_table + (size_t)b * p.max_pages + pg0 + c + lane);
+                if (c + lane < npg) pid = __ldg(table + pg0 + c + lane);
                 const int cnt = min(32, nslots - c);
                 for (int i = 0; i < cnt && ok; ++i) {
                     const int pl = c + i;
@@ -1200,7 +1311,7 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
                     const int flags = (pl < kConsumerWarps ? kFlagFirst : 0) |
                                       (pl >= nslots - kConsumerWarps ? kFlagLast : 0) | (pl >= npg ? kFlagPad : 0);
                     const int valid = pl < npg ? min(kPage, hist - (pg0 + pl) * kPage) : 0;
-                    ok = post(item, b, kv, pi, valid, flags);
+                    ok = post(item, b, kv, pi, valid, flags, pl < npg ? pg0 + pl : -1);
                 }
             }
             if (!ok) break;
@@ -1328,23 +1439,36 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
             }
         }
 
+        float* keep = nullptr;  // kModeWeights: where the page's logits go
+        if constexpr (MODE == kModeWeights) {
+            const int page = info[s].page;
+            if (page >= 0) keep = page_logits_at(p, sraw.y * p.hk + sraw.z, page);
+            if (keep && (flags & kFlagPad)) {  // a page that cannot be read: its tokens have weight 0
+                float none[4][2 * NT];
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2 * NT; ++e) none[m][e] = -INFINITY;
+                store_logits<NT>(keep, p.G, none);
+            }
+        }
         if (!(flags & kFlagPad)) {
             const uint8_t* brec = nullptr;
             if constexpr (BOOST) brec = p.boost + ((size_t)info[s].pid * p.hk + sraw.z) * kBoostBlock;
             if constexpr (NT == 2) {
                 if (valid == kPage)
-                    attend_page_g8<true, BOOST, LM>(blk, valid, wbuf, qfS, qsv, kq, m_run, l_run, zacc, acc_o[0],
-                                                    p.gshift, qbS, brec, cbk);
+                    attend_page_g8<true, BOOST, LM, MODE, CENTRE>(blk, valid, wbuf, qfS, qsv, kq, m_run, l_run, zacc, acc_o[0],
+                                                          p.gshift, qbS, brec, cbk, keep);
                 else
-                    attend_page_g8<false, BOOST, LM>(blk, valid, wbuf, qfS, qsv, kq, m_run, l_run, zacc, acc_o[0],
-                                                     p.gshift, qbS, brec, cbk);
+                    attend_page_g8<false, BOOST, LM, MODE, CENTRE>(blk, valid, wbuf, qfS, qsv, kq, m_run, l_run, zacc, acc_o[0],
+                                                           p.gshift, qbS, brec, cbk, keep);
             } else {
                 if (valid == kPage)
-                    attend_page<NT, true, LM, BOOST>(blk, valid, wbuf, qcur, qsv, kq, m_run, l_run, zacc, acc_o,
-                                                     take_lo, p.gshift, cbk, qbS, brec);
+                    attend_page<NT, true, LM, BOOST, MODE, CENTRE>(blk, valid, wbuf, qcur, qsv, kq, m_run, l_run, zacc, acc_o,
+                                                           take_lo, p.gshift, cbk, qbS, brec, keep, p.G);
                 else
-                    attend_page<NT, false, LM, BOOST>(blk, valid, wbuf, qcur, qsv, kq, m_run, l_run, zacc, acc_o,
-                                                      take_lo, p.gshift, cbk, qbS, brec);
+                    attend_page<NT, false, LM, BOOST, MODE, CENTRE>(blk, valid, wbuf, qcur, qsv, kq, m_run, l_run, zacc, acc_o,
+                                                            take_lo, p.gshift, cbk, qbS, brec, keep, p.G);
             }
         }
         __syncwarp();
@@ -1356,8 +1480,10 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
             float* mw = reinterpret_cast<float*>(wbuf);
             // P.V accumulator scales of the four slots (see v_out_scale)
             constexpr float kLmUp = LM ? 1.f / kLmVDown : 1.f;
-            const float vout[4] = {v_out_scale(0) * kLmUp, v_out_scale(1) * kLmUp, v_out_scale(2) * kLmUp,
-                                   v_out_scale(3) * kLmUp};
+            const float vout[4] = {CENTRE ? v_out_scale_centred(0) : v_out_scale(0) * kLmUp,
+                                   CENTRE ? v_out_scale_centred(1) : v_out_scale(1) * kLmUp,
+                                   CENTRE ? v_out_scale_centred(2) : v_out_scale(2) * kLmUp,
+                                   CENTRE ? v_out_scale_centred(3) : v_out_scale(3) * kLmUp};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float l = l_run[nt];
@@ -1415,12 +1541,13 @@ __global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOS
                 for (int ww = 0; ww < kConsumerWarps; ++ww)
                     M = fmaxf(M, reinterpret_cast<const float*>(smem + SM::kWarp + ww * SM::kWarpBytes)[hl * (kD + 2) + kD]);
                 float acc = 0.f, L = 0.f;
-                if (M != -INFINITY) {
+                if (MODE != kModePlain || M != -INFINITY) {  // (the modes pass NaN on, as the 4-bit chain)
+                    const float sub = MODE != kModePlain ? finite_max(M) : M;
 #pragma unroll
                     for (int ww = 0; ww < kConsumerWarps; ++ww) {
                         const float* src =
                             reinterpret_cast<const float*>(smem + SM::kWarp + ww * SM::kWarpBytes) + hl * (kD + 2);
-                        const float sc = ex2(src[kD] - M);
+                        const float sc = ex2(src[kD] - sub);
                         acc = fmaf(sc, src[d], acc);
                         L = fmaf(sc, src[kD + 1], L);
                     }
@@ -1500,7 +1627,6 @@ template <bool INT4>
 __device__ __forceinline__ bool holds(float l) {
     return INT4 ? l != 0.f : l > 0.f;
 }
-__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
 
 // One warp's 16-token tile from staged rows and the staged query rows of
 // its KV group (qsm: [G][kD] bf16); leaves the warp's state (o, m, l) per
@@ -1510,8 +1636,9 @@ __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0
 // so P keeps ~16 bits and each head's output is one accumulator row.  INT4 (the
 // 4-bit history's chain) adds a third part: 24 bits, for either output type, so
 // that a bf16 output is the fp32 one rounded.
-template <int G, bool INT4>
-__device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, float qscale) {
+// keep (kModeWeights): the tile's logits go to keep[token][G].
+template <int G, bool INT4, Mode MODE>
+__device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, float qscale, float* keep) {
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
     float* st = reinterpret_cast<float*>(rows);  // [G][kD + 2] at the end
     if (nvalid <= 0) {
@@ -1555,6 +1682,8 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
         for (int e = 0; e < 2; ++e) {
             const int tok = 8 * nt + 2 * tq + e;
             sacc[nt][e] = (tok < nvalid) ? sacc[nt][e] * qscale : -INFINITY;
+            if constexpr (MODE == kModeWeights)
+                if (row_on && tok < nvalid) keep[tok * G + gID] = sacc[nt][e];
             ma = fmaxf(ma, sacc[nt][e]);
         }
     ma = fmaxf(ma, __shfl_xor_sync(kFull, ma, 1));
@@ -1622,8 +1751,9 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
 // results it does not read; its block 0 waits for int2_kernel's completion
 // before it exits (the others leave when their items are done), so this grid
 // completes after int2_kernel and the merge after it sees both.
-template <bool INT4>
-__global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
+template <bool INT4, Mode MODE = kModePlain>
+__global__ void __launch_bounds__(kBfThreads, 3)
+bf16_kernel(std::conditional_t<MODE == kModeWeights, DecodeParamsX, DecodeParams> p) {
     extern __shared__ __align__(128) uint8_t bsm[];
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1676,11 +1806,13 @@ __global__ void __launch_bounds__(kBfThreads, 3) bf16_kernel(DecodeParams p) {
         const int t0 = item * kBfItemTok + 16 * warp;
         uint8_t* rows = rows_of(buf, warp);
         const __nv_bfloat16* qsm = reinterpret_cast<const __nv_bfloat16*>(q_of(buf));
+        float* keep = nullptr;
+        if constexpr (MODE == kModeWeights) keep = p.slot_logits + ((size_t)bk * p.nslot + t0) * p.G;
         switch (p.G) {
-            case 1: bf16_tile<1, INT4>(n - t0, rows, qsm, p.qscale); break;
-            case 2: bf16_tile<2, INT4>(n - t0, rows, qsm, p.qscale); break;
-            case 4: bf16_tile<4, INT4>(n - t0, rows, qsm, p.qscale); break;
-            default: bf16_tile<8, INT4>(n - t0, rows, qsm, p.qscale); break;
+            case 1: bf16_tile<1, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
+            case 2: bf16_tile<2, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
+            case 4: bf16_tile<4, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
+            default: bf16_tile<8, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
         }
         __syncthreads();
         // merge the four warps: thread -> dimension
@@ -1744,10 +1876,12 @@ constexpr int kMergeSmem = (kD * kURow + 2 * kMergeWarps * kMergeRow) * 4;
 constexpr int kMergeBatch = 12;   // split-K partials per batch of loads
 constexpr int kMaxBfItems = 5;    // BF16 segment blocks per row: ceil(320 / 64)
 
-// INT4: the 4-bit history's form (four partials per item, rows scaled before
-// their fp16 split, fp32 or bf16 output).
-template <bool INT4>
-__global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p) {
+// BITS4: four partials per item.  INT4: the 4-bit history's form, and the modes'
+// (rows scaled before their fp16 split, fp32 or bf16 output, NaN passed on).  kModeWeights: the row's maximum and 1 /
+// sum are kept for weights_kernel.
+template <bool BITS4, Mode MODE = kModePlain>
+__global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<BITS4, MODE> p) {
+    constexpr bool INT4 = BITS4 || MODE != kModePlain;
     extern __shared__ __align__(16) float msm[];
     float* Us = msm;                  // [a][kURow] = U_V[a][j]
     float* Ws = msm + kD * kURow;     // [warp][kMergeRow]: a warp's share (y, M, L), then the row's w
@@ -1772,6 +1906,9 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
     // int2_kernel passed its wait, i.e. before this grid could start: read it
     // before the wait, so that only the partials' loads follow it.
     int splits = 0, first = 0, first2 = 0, n_long = 0;
+    int n_shared = 0;                 // kModeShared: partials of the shared pages, before the others
+    const float* shared = nullptr;    // the first, and the step to the next
+    size_t shared_step = 0;
     if (active) {
         const int s0 = __ldg(p.item_start + b), t0 = __ldg(p.item_start2 + b);
         n_long = (__ldg(p.item_start + b + 1) - s0) / p.hk;
@@ -1779,11 +1916,18 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
         splits = n_long + n_short;
         first = s0 + kv * n_long;
         first2 = __ldg(p.item_start + p.B) + t0 + kv * n_short - n_long;
-        if constexpr (INT4) {  // kPartsPerItem4 partials per item
+        if constexpr (BITS4) {  // kPartsPerItem4 partials per item
             splits *= kPartsPerItem4;
             first *= kPartsPerItem4;
             first2 *= kPartsPerItem4;
             n_long *= kPartsPerItem4;
+        }
+        if constexpr (MODE == kModeShared) {
+            const int4 r = __ldg(p.sref + b);
+            n_shared = r.y;
+            splits += n_shared;
+            shared = p.sh_part + ((size_t)r.x + (size_t)kv * r.y * r.z + r.w) * p.part_stride;
+            shared_step = (size_t)r.z * p.part_stride;
         }
     }
     pdl_wait();  // partials of int2_kernel and bf16_kernel
@@ -1825,9 +1969,14 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) ov[i][k] = 0.f;
                 if (i0 + i < nmine) {
-                    const int sp = sub + wpr * (i0 + i);
-                    const float* pt =
-                        p.part + (size_t)(sp < n_long ? first + sp : first2 + sp) * p.part_stride;
+                    int sp = sub + wpr * (i0 + i);
+                    const float* pt;
+                    if (MODE == kModeShared && sp < n_shared) {
+                        pt = shared + sp * shared_step;
+                    } else {
+                        if constexpr (MODE == kModeShared) sp -= n_shared;
+                        pt = p.part + (size_t)(sp < n_long ? first + sp : first2 + sp) * p.part_stride;
+                    }
                     ms[i] = pt[(size_t)p.G * kD + hh];
                     ls[i] = pt[(size_t)p.G * kD + p.G + hh];
 #pragma unroll
@@ -1994,6 +2143,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
     const float den = wl + wb * lb;
     const float inv = holds<INT4>(den) ? 1.f / den : 0.f;
     const size_t at = ((size_t)b * p.hq + kv * p.G + hh) * kD;
+    if constexpr (MODE == kModeWeights)
+        if (lane == 0) p.norm[at / kD] = make_float2(finite_max(Mr), inv);
     if constexpr (INT4) {
         if (p.out_bf16) {  // a model's next product reads bf16: rounded once, here
             __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
@@ -2014,6 +2165,67 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(Params<INT4> p)
 }
 
 // ---------------------------------------------------------------------------
+// attention weights (kModeWeights)
+// ---------------------------------------------------------------------------
+// weight[b][t] = decay weight[b][t] + sum over heads of 2^(logit - m) / l, from
+// the logits that the history and BF16 kernels kept and the merge's (m, 1 / l):
+// the weights need the final maximum and sum, so either the logits are kept (4
+// bytes written and read per head and token, against 24 or 40 bytes of history per
+// head and token at four heads per KV head) or K is read and multiplied again.
+// Thread = token: its heads are summed in one order whatever the launch, so the
+// same call gives the same bits.  Blocks [0, chunks) of a sequence serve its
+// history, the others its slots.
+constexpr int kWeightThreads = 256;
+
+template <int G>
+__device__ __forceinline__ float head_weights(const float* lg, size_t kv_stride, int hk, const float2* norm) {
+    float sum = 0.f;
+#pragma unroll 4
+    for (int kv = 0; kv < hk; ++kv, lg += kv_stride, norm += G) {
+        float x[G];
+        if constexpr (G >= 4) {
+#pragma unroll
+            for (int i = 0; i < G; i += 4) {
+                const float4 v = __ldcs(reinterpret_cast<const float4*>(lg + i));
+                x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+            }
+        } else if constexpr (G == 2) {
+            const float2 v = __ldcs(reinterpret_cast<const float2*>(lg));
+            x[0] = v.x; x[1] = v.y;
+        } else {
+            x[0] = __ldcs(lg);
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) sum = fmaf(ex2(x[i] - norm[i].x), norm[i].y, sum);
+    }
+    return sum;
+}
+
+__global__ void __launch_bounds__(kWeightThreads) weights_kernel(DecodeParamsX p, int chunks, int slot_chunks) {
+    const int b = blockIdx.x / (chunks + slot_chunks), c = blockIdx.x % (chunks + slot_chunks);
+    const bool slots = c >= chunks;
+    const int t = (slots ? c - chunks : c) * kWeightThreads + threadIdx.x;
+    pdl_wait();
+    const int n = slots ? min(max(__ldg(p.bf16_len + b), 0), p.nslot)
+                        : min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+    if (t >= n) return;
+    float* w = slots ? p.slot_weight + (size_t)b * p.nslot + t : p.weight + (size_t)b * p.weight_stride + t;
+    // (a decay of 0 replaces the old weight, whatever it is)
+    const float old = p.decay != 0.f ? p.decay * *w : 0.f;
+    const size_t stride = (size_t)(slots ? p.nslot : p.max_pages * kPage) * p.G;
+    const float* lg = (slots ? p.slot_logits : p.logits) + (size_t)b * p.hk * stride + (size_t)t * p.G;
+    const float2* norm = p.norm + (size_t)b * p.hq;
+    float sum;
+    switch (p.G) {
+        case 1: sum = head_weights<1>(lg, stride, p.hk, norm); break;
+        case 2: sum = head_weights<2>(lg, stride, p.hk, norm); break;
+        case 4: sum = head_weights<4>(lg, stride, p.hk, norm); break;
+        default: sum = head_weights<8>(lg, stride, p.hk, norm); break;
+    }
+    *w = old + sum;
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 struct Int2Attr {
@@ -2027,14 +2239,14 @@ static Int2Attr& attr_for_device(int dev) {
     return attrs[dev & 63];
 }
 
-template <int NT, bool LM = false, bool BOOST = false>
-static cudaError_t launch_int2(const DecodeParams& p, cudaStream_t st, int sms, bool& attr_set) {
+template <int NT, bool LM = false, bool BOOST = false, Mode MODE = kModePlain, bool CENTRE = false>
+static cudaError_t launch_int2(const Params<false, MODE>& p, cudaStream_t st, int sms, bool& attr_set) {
     using SM = Int2Smem<NT, int2_stages<NT, LM, BOOST>()>;
     constexpr int smem = int2_q_prefetch<NT, LM, BOOST>() ? SM::kBytesQP : ((LM || BOOST) ? SM::kBytesLM : SM::kBytes);
     // the blocks of one SM share its 228 KB (1 KB of it reserved per block)
     static_assert(int2_blocks_per_sm<NT, LM, BOOST>() * (smem + 1024) <= 228 * 1024, "blocks per SM must fit");
     if (!attr_set) {
-        cudaError_t e = set_smem(int2_kernel<NT, LM, BOOST>, smem, !(NT == 2 && LM));
+        cudaError_t e = set_smem(int2_kernel<NT, LM, BOOST, MODE, CENTRE>, smem, !(NT == 2 && LM));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
@@ -2043,7 +2255,7 @@ static cudaError_t launch_int2(const DecodeParams& p, cudaStream_t st, int sms, 
         (int64_t)p.B * p.hk * ((p.max_pages + p.pps - 1) / p.pps + p.tail_pg / kShortItemPages);
     int blocks = (int)std::min<int64_t>((int64_t)per_sm * sms, max_items);
     if (blocks < 1) blocks = 1;
-    cudaError_t e = launch_pdl(int2_kernel<NT, LM, BOOST>, dim3(blocks), dim3(kInt2Threads), smem, st, p);
+    cudaError_t e = launch_pdl(int2_kernel<NT, LM, BOOST, MODE, CENTRE>, dim3(blocks), dim3(kInt2Threads), smem, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -2051,6 +2263,23 @@ static cudaError_t launch_int2(const DecodeParams& p, cudaStream_t st, int sms, 
 // kernel on the merge's behalf (a shape without windows has no items).
 static int bf16_blocks(const DecodeParams& p, int sms) {
     return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)p.bf_items * p.B * p.hk, 3 * sms));
+}
+
+// Fewer history pages (at most) than two waves of minimum items on the INT2
+// grid (a batch of one or two long sequences): items of one wave instead, so that
+// no block takes a second item while others idle.  Longer items only lower
+// the item count the workspace was sized for.
+static void one_wave_items(DecodeParams& p, int sms) {
+    const int per_sm = (p.NT == 1 || !(p.codebook || p.boost)) ? 3 : 2;  // as int2_blocks_per_sm
+    const int64_t blocks = (int64_t)per_sm * sms;
+    const int64_t line = (int64_t)p.B * p.hk * p.max_pages;
+    if (p.pps == kShortItemPages && line < 2 * kShortItemPages * blocks) {
+        const int pps = (int)std::min<int64_t>(256, ((line + blocks - 1) / blocks + 3) & ~3ll);
+        if (pps > p.pps) {
+            p.pps = pps;
+            p.tail_pg = 2 * kShortItemPages;
+        }
+    }
 }
 
 cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t ev_int2_start,
@@ -2064,22 +2293,7 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
         if (e != cudaSuccess) return e;
     }
     DecodeParams p = pin;
-    {   // Fewer history pages (at most) than two waves of minimum items on
-        // the INT2 grid (a batch of one or two long sequences): items of one
-        // wave instead, so that no block takes a second item while others
-        // idle.  Longer items only lower the item count the workspace was
-        // sized for.
-        const int per_sm = (p.NT == 1 || !(p.codebook || p.boost)) ? 3 : 2;  // as int2_blocks_per_sm
-        const int64_t blocks = (int64_t)per_sm * at.sms;
-        const int64_t line = (int64_t)p.B * p.hk * p.max_pages;
-        if (p.pps == kShortItemPages && line < 2 * kShortItemPages * blocks) {
-            const int pps = (int)std::min<int64_t>(256, ((line + blocks - 1) / blocks + 3) & ~3ll);
-            if (pps > p.pps) {
-                p.pps = pps;
-                p.tail_pg = 2 * kShortItemPages;
-            }
-        }
-    }
+    one_wave_items(p, at.sms);
     if (!at.setp) {
         e = set_smem(prep_kernel<false>, kPrepSmem);
         if (e != cudaSuccess) return e;
@@ -2142,6 +2356,99 @@ cudaError_t launch_decode4(const DecodeParams4& pin, cudaStream_t st) {
     const int rpb = kMergeWarps / p.merge_wpr;
     dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
     return launch_pdl(merge_kernel<true>, mg, dim3(kMergeThreads), kMergeSmem, st, p);
+}
+
+// Device attributes of a mode's kernels, set once per device.
+template <bool INT4, Mode MODE>
+static cudaError_t mode_attributes(int dev) {
+    static bool set[64];
+    if (set[dev & 63]) return cudaSuccess;
+    cudaError_t e = set_smem(prep_kernel<INT4, MODE>, kPrepSmem);
+    if (e == cudaSuccess) e = set_smem(bf16_kernel<true, MODE>, kBfSmem);
+    if (e == cudaSuccess) e = set_smem(merge_kernel<INT4, MODE>, kMergeSmem);
+    if (e == cudaSuccess) set[dev & 63] = true;
+    return e;
+}
+
+// The 2-bit history kernel of a mode: centred products for an fp32 output.
+template <Mode MODE>
+static cudaError_t launch_int2_mode(const DecodeParamsX& p, cudaStream_t st, int sms, int dev) {
+    static bool set[64][4];
+    bool(&at)[4] = set[dev & 63];
+    if (p.out_bf16)
+        return p.NT == 1 ? launch_int2<1, false, false, MODE, false>(p, st, sms, at[0])
+                         : launch_int2<2, false, false, MODE, false>(p, st, sms, at[1]);
+    return p.NT == 1 ? launch_int2<1, false, false, MODE, true>(p, st, sms, at[2])
+                     : launch_int2<2, false, false, MODE, true>(p, st, sms, at[3]);
+}
+
+// The chain that keeps the logits, and the attention weights behind it.
+template <bool INT4>
+static cudaError_t decode_weights(const DecodeParamsX& pin, cudaStream_t st) {
+    constexpr Mode MODE = kModeWeights;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Int2Attr& at = attr_for_device(dev);
+    if (at.sms == 0) {
+        e = cudaDeviceGetAttribute(&at.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    if ((e = mode_attributes<INT4, MODE>(dev)) != cudaSuccess) return e;
+    DecodeParamsX p = pin;
+    if constexpr (INT4) p.blocks = std::min(int4_blocks_per_sm(p.NT, p.gshift) * at.sms, kMaxBlocks4);
+    else one_wave_items(p, at.sms);
+    dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
+    if ((e = launch_pdl(prep_kernel<INT4, MODE>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
+    if constexpr (INT4) e = launch_int4(p, MODE, st, dev);
+    else e = launch_int2_mode<MODE>(p, st, at.sms, dev);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(bf16_kernel<true, MODE>, dim3(bf16_blocks(p, at.sms)), dim3(kBfThreads), kBfSmem, st, p);
+    if (e != cudaSuccess) return e;
+    const int rpb = kMergeWarps / p.merge_wpr;
+    dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
+    if ((e = launch_pdl(merge_kernel<INT4, MODE>, mg, dim3(kMergeThreads), kMergeSmem, st, p)) != cudaSuccess) return e;
+    const int chunks = (p.max_pages * kPage + kWeightThreads - 1) / kWeightThreads;
+    const int slot_chunks = p.slot_weight ? (p.nslot + kWeightThreads - 1) / kWeightThreads : 0;
+    return launch_pdl(weights_kernel, dim3((unsigned)p.B * (chunks + slot_chunks)), dim3(kWeightThreads), 0, st, p, chunks, slot_chunks);
+}
+
+// The chain in which groups of sequences attend their shared pages together.
+template <bool INT4>
+static cudaError_t decode_shared(const DecodeParamsX& pin, cudaStream_t st) {
+    constexpr Mode MODE = kModeShared;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Int2Attr& at = attr_for_device(dev);
+    if (at.sms == 0) {
+        e = cudaDeviceGetAttribute(&at.sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+    }
+    if ((e = mode_attributes<INT4, MODE>(dev)) != cudaSuccess) return e;
+    DecodeParamsX p = pin;
+    p.shared_blocks = std::min(at.sms, kMaxSharedBlocks);
+    if constexpr (INT4) p.blocks = std::min(int4_blocks_per_sm(p.NT, p.gshift) * at.sms, kMaxBlocks4);
+    if ((e = launch_shared_plan(p, st, dev)) != cudaSuccess) return e;
+    dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
+    if ((e = launch_pdl(prep_kernel<INT4, MODE>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
+    if ((e = launch_shared(p, INT4 ? 4 : 2, st, dev)) != cudaSuccess) return e;
+    if constexpr (INT4) e = launch_int4(p, MODE, st, dev);
+    else e = launch_int2_mode<MODE>(p, st, at.sms, dev);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl<DecodeParams>(bf16_kernel<true, MODE>, dim3(bf16_blocks(p, at.sms)), dim3(kBfThreads), kBfSmem, st, p);
+    if (e != cudaSuccess) return e;
+    const int rpb = kMergeWarps / p.merge_wpr;
+    dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
+    return launch_pdl(merge_kernel<INT4, MODE>, mg, dim3(kMergeThreads), kMergeSmem, st, p);
+}
+
+cudaError_t launch_decode_shared(const DecodeParamsX& p, int bits, cudaStream_t st) {
+    return bits == 4 ? decode_shared<true>(p, st) : decode_shared<false>(p, st);
+}
+
+cudaError_t launch_decode_weights(const DecodeParamsX& p, int bits, cudaStream_t st) {
+    return bits == 4 ? decode_weights<true>(p, st) : decode_weights<false>(p, st);
 }
 
 }  // namespace oscar

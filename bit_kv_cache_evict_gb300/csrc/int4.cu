@@ -41,6 +41,7 @@
 // divergent branches for the same reason: with separate code for partial pages,
 // every tile unrolled and the waits polled lane by lane it took 295 and 282 us.
 #include <algorithm>
+#include <type_traits>
 
 #include "splitk.cuh"
 
@@ -53,8 +54,11 @@ constexpr int kThreads4 = (kConsumerWarps + 1) * 32;
 constexpr int kHalfMax = kCodes4 + kPage * 16;  // bytes of a half at g = 32
 
 struct PageInfo {  // one per page of a consumer warp; 16 bytes
-    int item, b, kv, valid_flags;
+    int item, bk, page, valid_flags;  // (sequence, KV head) and page of its history (-1: none): kModeWeights
 };
+
+template <Mode MODE>
+using Params4 = std::conditional_t<MODE == kModePlain, DecodeParams4, DecodeParamsX>;
 
 // A probability or V-scale row of the value phase: the page's 64 tokens in 16
 // groups of four; k-step m of lane quad member tq covers group 4 tq + m (whose V
@@ -495,8 +499,8 @@ __device__ __forceinline__ void page_values(const uint8_t* half, int valid, uint
 // state at an item's end and goes on with the next item: a merge of the four
 // in shared memory cost about four pages' time per item.  Every wait is bounded: on a timeout the
 // block reports OSCAR_STATUS_TIMEOUT, lets its copies land and exits.
-template <int NT, int GS>
-__global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_kernel(DecodeParams4 p) {
+template <int NT, int GS, Mode MODE>
+__global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_kernel(Params4<MODE> p) {
     extern __shared__ __align__(128) uint8_t smem[];
     using SM = Int4Smem<NT, GS>;
     constexpr int NSW = SM::NSW, NB = 4 >> GS;
@@ -560,7 +564,13 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
             const int splits = (__ldg(starts + b + 1) - s0) / p.hk;
             const int kv = (rel - s0) / splits;
             const int split = (rel - s0) % splits;
-            const int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+            int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
+            const int32_t* table = p.page_table + (size_t)b * p.max_pages;
+            if constexpr (MODE == kModeShared) {  // the pages behind the shared ones
+                const int skip = __ldg(p.skip + b);
+                hist -= skip * kPage;
+                table += skip;
+            }
             const int seq_pages = (hist + kPage - 1) / kPage;
             const SeqSplits sp = seq_splits(seq_pages, pps, tail_pg);
             const int pg0 = is_long ? split * pps : sp.long_pages + split * kShortItemPages;
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
             for (int r = 0; r < rounds && ok; ++r, ++round) {
                 if ((r & 7) == 0) {  // page ids of the next eight rounds, one per lane
                     const int pl = 4 * r + lane;
-                    pid = pl < npg ? __ldg(p.page_table + (size_t)b * p.max_pages + pg0 + pl) : -1;
+                    pid = pl < npg ? __ldg(table + pg0 + pl) : -1;
                 }
                 // lane w < 4 serves warp w: page 4 r + w of the item
                 const int pl = 4 * r + (lane & 3);
@@ -606,8 +616,10 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
                     const int flags = (r == 0 ? kFlagFirst : 0) | (r == rounds - 1 ? kFlagLast : 0) | (pad ? kFlagPad : 0);
                     PageInfo& pi = info[lane * 2 + (round & 1u)];
                     pi.item = item;
-                    pi.b = b;
-                    pi.kv = kv;
+                    if constexpr (MODE == kModeWeights) {
+                        pi.bk = b * p.hk + kv;
+                        pi.page = pl < npg ? pg0 + pl : -1;
+                    }
                     pi.valid_flags = (pad ? 0 : min(kPage, hist - (pg0 + pl) * kPage)) | (flags << 8);
                     uint64_t* bar = &full[lane * NSW + ring.slot];
                     if (pad) {
@@ -706,6 +718,16 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
         }
         const uint8_t* half = stages + ring.slot * kHalfMax;
         if (flags & kFlagPad) {  // no page: give both halves back
+            if constexpr (MODE == kModeWeights) {
+                if (sraw.z >= 0) {  // a page that cannot be read: its tokens have weight 0
+                    float none[4][2 * NT];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int e = 0; e < 2 * NT; ++e) none[m][e] = -INFINITY;
+                    store_logits<NT>(page_logits_at(p, sraw.y, sraw.z), p.G, none);
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[ring.slot]);
             ring.step();
@@ -713,6 +735,7 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
         } else {
             float lg[4][2 * NT], alpha[NT];
             page_logits<NT, GS>(half, valid, wbuf, qf, qsv, kq, lg);
+            if constexpr (MODE == kModeWeights) store_logits<NT>(page_logits_at(p, sraw.y, sraw.z), p.G, lg);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[ring.slot]);
             ring.step();
@@ -761,10 +784,10 @@ __global__ void __launch_bounds__(kThreads4, int4_blocks_per_sm(NT, GS)) int4_ke
     }
 }
 
-template <int NT, int GS>
-cudaError_t launch(const DecodeParams4& p, cudaStream_t st, bool& attr_set) {
+template <int NT, int GS, Mode MODE>
+cudaError_t launch(const Params4<MODE>& p, cudaStream_t st, bool& attr_set) {
     if (!attr_set) {
-        const cudaError_t e = set_smem(int4_kernel<NT, GS>, Int4Smem<NT, GS>::kBytes);
+        const cudaError_t e = set_smem(int4_kernel<NT, GS, MODE>, Int4Smem<NT, GS>::kBytes);
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
@@ -772,21 +795,27 @@ cudaError_t launch(const DecodeParams4& p, cudaStream_t st, bool& attr_set) {
     const int64_t items = (int64_t)p.B * p.hk * ((p.max_pages + 3) / 4);
     const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(p.blocks, items));
     const cudaError_t e =
-        launch_pdl(int4_kernel<NT, GS>, dim3(blocks), dim3(kThreads4), Int4Smem<NT, GS>::kBytes, st, p);
+        launch_pdl(int4_kernel<NT, GS, MODE>, dim3(blocks), dim3(kThreads4), Int4Smem<NT, GS>::kBytes, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <Mode MODE>
+cudaError_t launch_mode(const Params4<MODE>& p, cudaStream_t st, int dev) {
+    static bool attr_set[64][6];
+    bool(&at)[6] = attr_set[dev & 63];
+    if (p.NT == 1) {
+        if (p.gshift == 0) return launch<1, 0, MODE>(p, st, at[0]);
+        return p.gshift == 1 ? launch<1, 1, MODE>(p, st, at[1]) : launch<1, 2, MODE>(p, st, at[2]);
+    }
+    if (p.gshift == 0) return launch<2, 0, MODE>(p, st, at[3]);
+    return p.gshift == 1 ? launch<2, 1, MODE>(p, st, at[4]) : launch<2, 2, MODE>(p, st, at[5]);
 }
 
 }  // namespace
 
-cudaError_t launch_int4(const DecodeParams4& p, cudaStream_t st, int dev) {
-    static bool attr_set[64][6];
-    bool(&at)[6] = attr_set[dev & 63];
-    if (p.NT == 1) {
-        if (p.gshift == 0) return launch<1, 0>(p, st, at[0]);
-        return p.gshift == 1 ? launch<1, 1>(p, st, at[1]) : launch<1, 2>(p, st, at[2]);
-    }
-    if (p.gshift == 0) return launch<2, 0>(p, st, at[3]);
-    return p.gshift == 1 ? launch<2, 1>(p, st, at[4]) : launch<2, 2>(p, st, at[5]);
+cudaError_t launch_int4(const DecodeParams4& p, cudaStream_t st, int dev) { return launch_mode<kModePlain>(p, st, dev); }
+cudaError_t launch_int4(const DecodeParamsX& p, Mode mode, cudaStream_t st, int dev) {
+    return mode == kModeWeights ? launch_mode<kModeWeights>(p, st, dev) : launch_mode<kModeShared>(p, st, dev);
 }
 
 }  // namespace oscar

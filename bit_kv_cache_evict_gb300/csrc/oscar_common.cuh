@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -413,6 +414,41 @@ struct DecodeParams4 : DecodeParams {
     int out_bf16;  // 1: out is bf16
 };
 
+// What a decode chain does besides: nothing; keep the logits, for the tokens'
+// attention weights (oscar_decode_attn_weights); leave out the pages that a
+// group of sequences shares, which another kernel attends (oscar_decode_attn_shared).
+enum Mode { kModePlain = 0, kModeWeights = 1, kModeShared = 2 };
+
+constexpr int kSharedItems = 10;        // index of the shared pages' item count in the counters
+constexpr int kMinSharedPages = 4;      // pages of an item of a group at least (but for its last)
+constexpr int kMaxSharedGroups = 8192;
+constexpr int kMaxSharedBlocks = 160;   // thread blocks of shared_kernel, one per SM, at most
+struct SharedGroup {
+    int pages, members, first_member, splits, first_part, first_item, tiles, pad;
+};
+
+// The parameters of the chains of the last two modes, for 2 and 4 bits.
+struct DecodeParamsX : DecodeParams4 {
+    // kModeWeights
+    float* logits;       // [B*Hk][max_pages * 64][G] base-2 logits of the history
+    float* slot_logits;  // [B*Hk][nslot][G] of the BF16 segment
+    float2* norm;        // [B*Hq] (m, 1 / l): a token's weight is 2^(logit - m) / l
+    float* weight;       // [B][weight_stride], in and out
+    float* slot_weight;  // [B][nslot], in and out, or null
+    int weight_stride;
+    float decay;
+    // kModeShared
+    const int32_t* prefix_group;  // [B] group of each sequence; negative: none
+    const int32_t* group_pages;   // [n_groups] first pages that a group shares
+    int32_t* skip;                // [B] pages that the sequence's group attends
+    int4* sref;                   // [B] its partials of them: (first, splits, members, index)
+    int32_t* member;              // [B] sequences by group
+    SharedGroup* groups;          // [n_groups]
+    const uint16_t* qrow;         // [2][B*Hq][kD] fp16 q' (times 2^e), high and low parts, in the products' order
+    float* sh_part;               // partials [part_stride]: (KV head, split, member) of each group
+    int n_groups, shared_blocks;
+};
+
 // Split-K geometry of one sequence with npg history pages: the last
 // min(npg, tail_pg) pages go to short items of kShortItemPages, the rest to
 // long items of pps pages.
@@ -489,6 +525,19 @@ struct HistoryGatherParams {
 };
 cudaError_t launch_history_gather(const HistoryGatherParams& p, cudaStream_t st);
 
+// history tokens chosen by their scores (select.cu)
+struct HistorySelectParams {
+    const float* weight;       // [batch][stride]
+    const int32_t* hist_len;   // [batch]
+    const int32_t* budget;     // [batch]
+    int32_t* keep;             // [batch][keep_stride]
+    int32_t* n_keep;           // [batch]
+    float* kept_weight;        // [batch][kept_stride], or null
+    int32_t* status;
+    int batch, stride, protect, keep_stride, kept_stride;
+};
+cudaError_t launch_history_select(const HistorySelectParams& p, cudaStream_t st);
+
 struct PagesCopyParams {
     const int32_t* src;        // [n]
     const int32_t* dst;        // [n]
@@ -520,8 +569,9 @@ inline cudaError_t set_smem(void (*kernel)(Args...), int bytes, bool max_carveou
 
 // Launch with a programmatic dependency on the previous kernel in the stream
 // (the kernel itself decides where it waits, see pdl_wait).
-template <typename P>
-inline cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const P& p) {
+template <typename... P>
+inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                              const std::common_type_t<P>&... p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -532,7 +582,7 @@ inline cudaError_t launch_pdl(void (*kernel)(P), dim3 grid, dim3 block, size_t s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, p...);
 }
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
@@ -541,5 +591,9 @@ cudaError_t launch_evict_bulk(const EvictParams& p, cudaStream_t st);  // many t
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t st, cudaEvent_t ev_int2_start,
                           cudaEvent_t ev_int2_stop);
 cudaError_t launch_decode4(const DecodeParams4& p, cudaStream_t st);  // 4-bit history
+cudaError_t launch_decode_weights(const DecodeParamsX& p, int bits, cudaStream_t st);
+cudaError_t launch_decode_shared(const DecodeParamsX& p, int bits, cudaStream_t st);
+cudaError_t launch_shared_plan(const DecodeParamsX& p, cudaStream_t st, int dev);       // shared.cu
+cudaError_t launch_shared(const DecodeParamsX& p, int bits, cudaStream_t st, int dev);
 
 }  // namespace oscar

@@ -27,6 +27,10 @@ __device__ __forceinline__ int find_seq(const int32_t* item_start, int B, int it
     return lo;
 }
 
+// The maximum that a merge subtracts: that of nothing is taken as 0, so that the
+// factors 2^(-inf - 0) are 0.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.f : m; }
+
 // Split two fp32 values into f16x2 registers of their high parts (the
 // values with the low 13 bits cleared, see split_pair_f16) and of the
 // rounded remainders.
@@ -38,6 +42,34 @@ __device__ __forceinline__ void split_both(float2 w, uint32_t& hi, uint32_t& lo)
     lo = pack_f16x2_rn(r.x, r.y);
 }
 
+// kModeWeights: where the logits [64][G] of a history page go, and their store
+// from a consumer warp's lanes: up to four heads (NT = 1): lg[m][0], lg[m][1] =
+// tokens 16 m + gID and + 8 of head tq; eight: (token, heads 2 tq, 2 tq + 1), (token
+// + 8, the same).  Token-major, so that a store of the warp covers whole lines
+// and the kernel that reads them takes a token's heads in one load.
+__device__ __forceinline__ float* page_logits_at(const DecodeParamsX& p, int bk, int page) {
+    return p.logits + ((size_t)bk * p.max_pages + page) * kPage * p.G;
+}
+template <int NT>
+__device__ __forceinline__ void store_logits(float* at, int G, const float (&lg)[4][2 * NT]) {
+    const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
+    if constexpr (NT == 2) {
+        float* to = at + gID * 8 + 2 * tq;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            *reinterpret_cast<float2*>(to + m * 128) = make_float2(lg[m][0], lg[m][1]);
+            *reinterpret_cast<float2*>(to + m * 128 + 64) = make_float2(lg[m][2], lg[m][3]);
+        }
+    } else if (tq < G) {
+        float* to = at + gID * G + tq;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            to[16 * m * G] = lg[m][0];
+            to[(16 * m + 8) * G] = lg[m][1];
+        }
+    }
+}
+
 // Blocks per SM of the 4-bit history kernel: three (128 registers); two (168, and
 // four page halves per warp instead of two) for eight query heads per KV head
 // with four quantisation groups per vector, whose state would spill: 32 x
@@ -47,5 +79,6 @@ __host__ __device__ constexpr int int4_blocks_per_sm(int nt, int gshift) { retur
 
 // the 4-bit history kernel (int4.cu), launched by launch_decode4 between prep_kernel and bf16_kernel
 cudaError_t launch_int4(const DecodeParams4& p, cudaStream_t st, int dev);
+cudaError_t launch_int4(const DecodeParamsX& p, Mode mode, cudaStream_t st, int dev);
 
 }  // namespace oscar

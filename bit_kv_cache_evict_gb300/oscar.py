@@ -127,6 +127,15 @@ def lib() -> ctypes.CDLL:
         L.oscar_history_gather.argtypes = [S, I32, I32, _P, _P, _P, I32, _P, I32, _P, I32, _P, I32, _P, _P]
         L.oscar_pages_copy_device.restype = ctypes.c_int
         L.oscar_pages_copy_device.argtypes = [ctypes.c_size_t, I32, _P, _P, _P, I32, I32, _P, _P]
+        F32 = ctypes.c_float
+        L.oscar_decode_attn_weights.restype = ctypes.c_int
+        L.oscar_decode_attn_weights.argtypes = [S, I32, I32, _P, _P, _P, _P, _P, I32, I32, _P, _P, F32, _P, I32, _P, I32, _P,
+                                                F32, _P, ctypes.POINTER(ctypes.c_size_t), _P, _P]
+        L.oscar_decode_attn_shared.restype = ctypes.c_int
+        L.oscar_decode_attn_shared.argtypes = [S, I32, I32, _P, _P, _P, _P, _P, I32, I32, _P, _P, I32, _P, _P, F32, _P, I32, _P,
+                                               ctypes.POINTER(ctypes.c_size_t), _P, _P]
+        L.oscar_history_select.restype = ctypes.c_int
+        L.oscar_history_select.argtypes = [I32, _P, I32, _P, _P, I32, _P, I32, _P, _P, I32, _P, _P]
         L.oscar_calibrate_codebook.restype = ctypes.c_int
         L.oscar_calibrate_codebook.argtypes = [S, ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.POINTER(ctypes.c_size_t),
                                                _P]
@@ -723,3 +732,98 @@ def oscar_pages_copy_device(page_bytes: int, src, dst, pools, num_pages: int, de
         _arg(dev_status, "dev_status", _I32, 1, dev), _stream_arg(stream, dev))
     if st:
         _check("oscar_pages_copy_device", st)
+
+
+def oscar_decode_workspace_bytes_weights(shape: oscar_shape, bits: int, batch: int, max_pages: int) -> int:
+    ws = ctypes.c_size_t(0)
+    st = lib().oscar_decode_attn_weights(ctypes.byref(shape), bits, batch, None, None, None, None, None, max_pages, 0,
+                                         None, None, 1.0, None, OSCAR_OUT_F32, None, 0, None, 1.0, None,
+                                         ctypes.byref(ws), None, None)
+    _check("oscar_decode_attn_weights", st)
+    return int(ws.value)
+
+
+def oscar_decode_attn_weights(shape: oscar_shape, bits: int, q, bf16_kv, bf16_len, pool, page_table, max_pages: int,
+                              num_pages: int, hist_len, U, sm_scale: float, out, weight, workspace, slot_weight=None,
+                              decay: float = 1.0, dev_status=None, stream=None) -> None:
+    """oscar_decode_attn (bits 2) or oscar_decode_attn_int4 (bits 4) with each
+    token's attention weight, summed over the query heads, added to decay times
+    its score: weight float32 [B][>= 64 max_pages] for the history,
+    slot_weight float32 [B][sink + recent] for the windows; see
+    include/oscar.h.  ``workspace``: CUDA uint8 tensor of at least
+    oscar_decode_workspace_bytes_weights(shape, bits, batch, max_pages) bytes."""
+    kind = _out_type(out)
+    dev, B, hk, d = _current_device(), q.shape[0], shape.num_kv_heads, shape.head_dim
+    rows, slots = B * shape.num_q_heads * d, shape.sink + shape.recent
+    if weight.dim() != 2 or weight.shape[0] != B:
+        raise ValueError("weight: one row per sequence")
+    st = lib().oscar_decode_attn_weights(
+        ctypes.byref(shape), bits, B, _arg(q, "q", _BF16, rows, dev),
+        _arg(bf16_kv, "bf16_kv", _BF16, B * slots * hk * 2 * d, dev), _arg(bf16_len, "bf16_len", _I32, B, dev),
+        _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, bits), dev),
+        _arg(page_table, "page_table", _I32, B * max_pages, dev), max_pages, num_pages,
+        _arg(hist_len, "hist_len", _I32, B, dev), _arg(U, "U", _F32, hk * 2 * d * d, dev), sm_scale,
+        _arg(out, "out", out.dtype, rows, dev), kind, _arg(weight, "weight", _F32, 0, dev), weight.shape[1],
+        _arg(slot_weight, "slot_weight", _F32, B * slots, dev), decay,
+        _arg(workspace, "workspace", _U8, 1 if B else 0, dev), ctypes.byref(ctypes.c_size_t(workspace.numel())),
+        _arg(dev_status, "dev_status", _I32, 1, dev), _stream_arg(stream, dev))
+    if st:
+        _check("oscar_decode_attn_weights", st)
+
+
+def oscar_history_select(weight, hist_len, budget, keep, n_keep, protect: int = 0, kept_weight=None, dev_status=None,
+                         stream=None) -> None:
+    """The tokens of each history that stay under budget (int32 [B]) by their
+    scores weight (float32 [B][stride]), the newest ``protect`` first: their
+    positions in increasing order into keep (int32 [B][stride]), their number
+    into n_keep (int32 [B]), their scores into kept_weight (float32 [B][stride]);
+    see include/oscar.h.  The lists are those that oscar_history_gather takes."""
+    if _F32 is None:
+        _torch_names()
+    (B, stride), (B2, kstride) = weight.shape, keep.shape
+    if B2 != B or (kept_weight is not None and (kept_weight.dim() != 2 or kept_weight.shape[0] != B)):
+        raise ValueError("weight, keep and kept_weight: one row per sequence")
+    dev = _current_device()
+    st = lib().oscar_history_select(
+        B, _arg(weight, "weight", _F32, 0, dev), stride, _arg(hist_len, "hist_len", _I32, B, dev),
+        _arg(budget, "budget", _I32, B, dev), protect, _arg(keep, "keep", _I32, 0, dev), kstride,
+        _arg(n_keep, "n_keep", _I32, B, dev), _arg(kept_weight, "kept_weight", _F32, 0, dev),
+        0 if kept_weight is None else kept_weight.shape[1], _arg(dev_status, "dev_status", _I32, 1, dev),
+        _stream_arg(stream, dev))
+    if st:
+        _check("oscar_history_select", st)
+
+
+def oscar_decode_workspace_bytes_shared(shape: oscar_shape, bits: int, batch: int, max_pages: int, n_groups: int) -> int:
+    ws = ctypes.c_size_t(0)
+    st = lib().oscar_decode_attn_shared(ctypes.byref(shape), bits, batch, None, None, None, None, None, max_pages, 0, None,
+                                        None, n_groups, None, None, 1.0, None, OSCAR_OUT_F32, None, ctypes.byref(ws), None,
+                                        None)
+    _check("oscar_decode_attn_shared", st)
+    return int(ws.value)
+
+
+def oscar_decode_attn_shared(shape: oscar_shape, bits: int, q, bf16_kv, bf16_len, pool, page_table, max_pages: int,
+                             num_pages: int, hist_len, prefix_group, group_pages, U, sm_scale: float, out, workspace,
+                             dev_status=None, stream=None) -> None:
+    """oscar_decode_attn (bits 2) or oscar_decode_attn_int4 (bits 4) with the
+    first group_pages[g] (int32 [n_groups]) pages of the sequences whose
+    prefix_group (int32 [B]; negative: none) is g read once for all of them;
+    out may be float32 or bfloat16; see include/oscar.h.  ``workspace``: CUDA
+    uint8 tensor of at least oscar_decode_workspace_bytes_shared(shape, bits,
+    batch, max_pages, n_groups) bytes."""
+    kind = _out_type(out)
+    dev, B, hk, d = _current_device(), q.shape[0], shape.num_kv_heads, shape.head_dim
+    rows, slots, n_groups = B * shape.num_q_heads * d, shape.sink + shape.recent, group_pages.numel()
+    st = lib().oscar_decode_attn_shared(
+        ctypes.byref(shape), bits, B, _arg(q, "q", _BF16, rows, dev),
+        _arg(bf16_kv, "bf16_kv", _BF16, B * slots * hk * 2 * d, dev), _arg(bf16_len, "bf16_len", _I32, B, dev),
+        _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, bits), dev),
+        _arg(page_table, "page_table", _I32, B * max_pages, dev), max_pages, num_pages,
+        _arg(hist_len, "hist_len", _I32, B, dev), _arg(prefix_group, "prefix_group", _I32, B, dev), n_groups,
+        _arg(group_pages, "group_pages", _I32, n_groups, dev), _arg(U, "U", _F32, hk * 2 * d * d, dev), sm_scale,
+        _arg(out, "out", out.dtype, rows, dev), kind, _arg(workspace, "workspace", _U8, 1 if B else 0, dev),
+        ctypes.byref(ctypes.c_size_t(workspace.numel())), _arg(dev_status, "dev_status", _I32, 1, dev),
+        _stream_arg(stream, dev))
+    if st:
+        _check("oscar_decode_attn_shared", st)

@@ -58,6 +58,9 @@
  *   oscar_history_read                     stored tokens back as rows
  *   oscar_history_gather                   kept tokens into fresh pages
  *   oscar_pages_copy_device                pages copied in every layer's pool
+ *   oscar_decode_attn_weights              decode that accumulates attention weight
+ *   oscar_history_select                   the tokens kept under a budget
+ *   oscar_decode_attn_shared               decode with shared first pages attended once
  *   oscar_calibrate_codebook               offline fit of the Lloyd-Max levels
  *   oscar_calibrate_rotation               offline U_K, U_V
  *   oscar_calibrate_clip                   offline clip ratios
@@ -586,6 +589,104 @@ oscar_status oscar_history_gather(const oscar_shape* shape, int32_t bits, int32_
 oscar_status oscar_pages_copy_device(size_t page_bytes, int32_t n_copies, const int32_t* src, const int32_t* dst,
                                      uint8_t* const* pools, int32_t n_pools, int32_t num_pages, int32_t* dev_status,
                                      void* stream);
+
+/*
+ * oscar_decode_attn_weights -- a decode step that also says what it attended
+ * to: oscar_decode_attn (bits 2, uniform levels) or oscar_decode_attn_int4
+ * (bits 4), and each token's attention weight of the step, summed over the
+ * query heads, added to a running score:
+ *   weight[b][t]      <- decay * weight[b][t]      + sum_h p[b, h, t]
+ *   slot_weight[b][s] <- decay * slot_weight[b][s] + sum_h p[b, h, s]
+ * for the history positions t < hist_len[b] and the BF16 slots s <
+ * bf16_len[b], p the softmax over the whole context.  The scores that
+ * oscar_history_select chooses by.  One page table serves every layer, so a
+ * model accumulates all its layers into one array: the first layer's call with
+ * the step's decay, the others with decay 1.
+ *
+ *   out           (device) [B][Hq][d] of out_type, for 2 bits too: as
+ *                 oscar_decode_attn_int4
+ *   weight        (device fp32 [B][weight_stride], weight_stride >= 64 *
+ *                 max_pages); entries behind hist_len are left as they were
+ *   slot_weight   (device fp32 [B][sink+recent], or NULL: not wanted), in the
+ *                 order of the slots.  When a slot's token is evicted, the
+ *                 caller moves its score to weight at the token's position.
+ *   decay         in [0, 1]; 0 replaces the old scores without reading them
+ *   workspace     as oscar_decode_attn, with room for the logits: 4 * Hq
+ *                 bytes for each of the batch's 64 * max_pages positions
+ * Sums are fp32, over the heads in order: the same call gives the same bits.
+ * Tokens of a page that is skipped (a bad id) have weight 0.  A row that is
+ * NaN in the output gives its weights NaN (4 bits; for 2 bits, whose decode
+ * drops parts with a NaN sum, the weights of such a row are not specified).
+ * Errors: as the decode calls; UNSUPPORTED for other bits.
+ */
+oscar_status oscar_decode_attn_weights(const oscar_shape* shape, int32_t bits, int32_t batch, const void* q,
+                                       const void* bf16_kv, const int32_t* bf16_len, const uint8_t* pool,
+                                       const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                                       const int32_t* hist_len, const float* U, float sm_scale, void* out,
+                                       int32_t out_type, float* weight, int32_t weight_stride, float* slot_weight,
+                                       float decay, void* workspace, size_t* ws_bytes, int32_t* dev_status,
+                                       void* stream);
+
+/*
+ * oscar_history_select -- the history tokens that stay under a budget, by
+ * their scores: of the n = hist_len[b] tokens of sequence b, m = min(n,
+ * budget[b]) stay: the newest min(protect, m) (they have been attended to by
+ * few queries so far), and the greatest scores of the others, ties to the lower
+ * position.  The list is in increasing order, as oscar_history_gather takes it.
+ *
+ *   weight       (device fp32 [batch][weight_stride]) scores, e.g. of
+ *                oscar_decode_attn_weights.  -0 counts as 0; NaN counts as the
+ *                greatest.
+ *   hist_len, budget (device int32 [batch])
+ *   keep         (device int32 [batch][keep_stride], out) the first m entries
+ *                of a row are written, the others left as they were
+ *   n_keep       (device int32 [batch], out) m
+ *   kept_weight  (device fp32 [batch][kept_stride], out, or NULL) the kept
+ *                tokens' scores at their new positions 0 .. m - 1; may not
+ *                overlap weight
+ * hist_len outside [0, weight_stride], a negative budget and an m beyond
+ * keep_stride (or kept_stride) are clamped and reported as BAD_POS.
+ */
+oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t weight_stride, const int32_t* hist_len,
+                                  const int32_t* budget, int32_t protect, int32_t* keep, int32_t keep_stride,
+                                  int32_t* n_keep, float* kept_weight, int32_t kept_stride, int32_t* dev_status,
+                                  void* stream);
+
+/*
+ * oscar_decode_attn_shared -- oscar_decode_attn (bits 2, uniform levels) or
+ * oscar_decode_attn_int4 (bits 4) for a batch in which groups of sequences
+ * share the first pages of their histories (oscar_pool_layout's prefix groups,
+ * pages adopted from the radix cache): the shared pages are read and
+ * dequantised once for all members.  The result is that of the plain decode.
+ *
+ *   prefix_group  (device int32 [batch]) the group of each sequence, in [0,
+ *                 n_groups); negative: none
+ *   group_pages   (device int32 [n_groups]) the number of pages that the
+ *                 group's sequences share: the first entries of their
+ *                 page-table rows, read from the row of its first sequence.
+ *                 Pages that a row shares with some members only do not count.
+ *   n_groups      at most 8192
+ *   out           as oscar_decode_attn_int4, for 2 bits too
+ *   workspace     as oscar_decode_attn; the size depends on n_groups too
+ * Both arrays are read on the device, so that a captured graph follows them.  A
+ * sequence whose history ends inside its group's pages attends by itself, as
+ * do groups of one.  A prefix_group of n_groups or more (no group) and
+ * group_pages outside [0, max_pages] (clamped) are reported as BAD_POS.
+ * Precision: fp32 output as oscar_decode_attn_int4.  For a bf16 output the
+ * shared pages' queries, values s * code + z and weights enter their products
+ * as fp16, one rounding of 2^-11 (relative) each; the rest as for fp32, but that 2-bit
+ * pages of a sequence's own are summed as in oscar_decode_attn.  Shared
+ * values s * code + z have to be finite in fp16 (|value| < 65520); NaN, and
+ * what overflows, reaches the rows that attend it as NaN.
+ * Errors: as the decode calls; UNSUPPORTED for other bits.
+ */
+oscar_status oscar_decode_attn_shared(const oscar_shape* shape, int32_t bits, int32_t batch, const void* q,
+                                      const void* bf16_kv, const int32_t* bf16_len, const uint8_t* pool,
+                                      const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                                      const int32_t* hist_len, const int32_t* prefix_group, int32_t n_groups,
+                                      const int32_t* group_pages, const float* U, float sm_scale, void* out,
+                                      int32_t out_type, void* workspace, size_t* ws_bytes, int32_t* dev_status,
+                                      void* stream);
 
 /*
  * oscar_calibrate_codebook -- offline Lloyd-Max fit of the inner level a of
