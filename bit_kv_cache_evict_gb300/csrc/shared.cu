@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
     int32_t* count = gsm;                 // [n_groups] members
     int32_t* first = gsm + p.n_groups;    // [n_groups] first member's place
     __shared__ int32_t chunk_group[kPlanThreads], chunk_index[kPlanThreads];
-    __shared__ int sh_pps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) count[g] = 0;
     pdl_wait();
@@ -149,7 +148,6 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
         }
         if (lane == 0) {
             p.counter[kSharedItems] = run_item;
-            sh_pps = pps;
         }
     }
     __syncthreads();
@@ -181,19 +179,29 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t on, uint64_t* bar) {
+    asm volatile("{ .reg .pred e; setp.ne.b32 e, %0, 0; @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1]; }" ::"r"(on),
+                 "r"(smem_u32(bar))
+                 : "memory");
 }
-// D[128 x N] (+)= A B^T, A and B K-major in shared memory (128-byte swizzle), 16 deep
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+// One lane of the warp, the same every time.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r;
+}
+// D[128 x N] (+)= A B^T, A and B K-major in shared memory (128-byte swizzle), 16 deep.  The
+// whole warp calls, the elected lane issues: under a branch of one lane the
+// operands are not uniform for the compiler and an issue took about 180 cycles.
+__device__ __forceinline__ void tc_mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{ .reg .pred e, p; setp.ne.b32 e, %0, 0; setp.ne.b32 p, %5, 0; @e tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p; }" ::"r"(on),
+                 "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
                  : "memory");
 }
 // the same with A in tensor memory
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+__device__ __forceinline__ void tc_mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{ .reg .pred e, p; setp.ne.b32 e, %0, 0; setp.ne.b32 p, %5, 0; @e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p; }" ::"r"(on),
+                 "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
                  : "memory");
 }
 // Instruction descriptor: fp16 operands, fp32 sums, both K-major, M = 128.
@@ -280,6 +288,8 @@ __device__ __forceinline__ void value_pair(uint32_t s, uint32_t c, uint32_t z, u
 // ---------------------------------------------------------------------------
 // kernel
 // ---------------------------------------------------------------------------
+constexpr int kDequantWarps = 8;
+
 template <int BITS, int PARTS>
 struct SharedSmem {
     static constexpr int T = PARTS == 1 ? 2 : 1;        // 128-row tiles of an item
@@ -292,14 +302,23 @@ struct SharedSmem {
     static constexpr int kK = kQ + T * PARTS * kQTile;  // [kStages][PARTS], each two atoms [64 rows][128 bytes]
     static constexpr int kV = kK + kStages * PARTS * kOperand;  // [kStages][PARTS] [128 rows][128 bytes]
     static constexpr int kRawAt = kV + kStages * PARTS * kOperand;
-    static constexpr int kPairs = kRawAt + kRawStages * kRaw;  // [4 warps][s, z][4 groups][64] fp16
-    static constexpr int kBars = kPairs + 4 * 2 * 4 * kPage * 2;
+    static constexpr int kPairs = kRawAt + kRawStages * kRaw;  // [kDequantWarps][groups][s, z][64] fp16
+    static constexpr int kPairGroups = BITS == 4 ? 1 : 4;      // groups that a warp's rows of V belong to, at most
+    static constexpr int kPairBytes = kPairGroups * 2 * kPage * 2;
+    static constexpr int kBars = kPairs + kDequantWarps * kPairBytes;
     static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 4 + T + 1;
     static constexpr int kBytes = kBars + kNumBars * 8 + 32;
     static constexpr int kAlloc = kBytes + 1024;        // the swizzled operands start on 1024 bytes
     static_assert(kAlloc <= 227 * 1024, "shared memory of a block");
+    // warps by role, in whole warpgroups: softmax, dequantisation, then the warp of the
+    // products, the producer and two that are idle
     static constexpr int kSoftWarps = 4 * T;
-    static constexpr int kThreads = (kSoftWarps + 4 + 2) * 32;
+    static constexpr int kMmaWarp = kSoftWarps + kDequantWarps, kThreads = (kMmaWarp + 4) * 32;
+    // registers per thread: of the launch, then of each role (their sum is within the launch's)
+    static constexpr int kLaunchRegs = PARTS == 1 ? 96 : 128;
+    static constexpr int kSoftRegs = PARTS == 1 ? 136 : 216, kDequantRegs = PARTS == 1 ? 80 : 112, kOtherRegs = PARTS == 1 ? 40 : 56;
+    static_assert(kSoftWarps * kSoftRegs + kDequantWarps * kDequantRegs + 4 * kOtherRegs <= (kMmaWarp + 4) * kLaunchRegs, "registers");
+    static_assert(kThreads * kLaunchRegs <= 65536, "registers of the SM");
     // tensor memory, columns: PARTS = 1: per tile S [2][64] (P in the first 32 columns
     // of its S) and O [128]; PARTS = 2: S [2][64], P [2][64] (hi, lo), O [2][128]
     static constexpr int kTileCols = 256;
@@ -307,10 +326,57 @@ struct SharedSmem {
     static constexpr int kCols = 512;
 };
 
-// log2 of the factor that P carries, so that small weights are not subnormal
-// fp16, and how far a row's logits may pass the subtracted maximum before its
-// sums are rescaled: P stays below 2^(kShift + kSlack + 1)
-constexpr float kShift = 6.f, kSlack = 8.f;
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void block_sync() { asm volatile("bar.sync 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// How far a row's logits may pass the subtracted maximum before its sums are
+// rescaled (log2): P stays at 2^15 at most, and the weights of a page whose
+// maximum is the one subtracted are fp16 normals down to 2^-14 of the largest,
+// 2^-25 off at most below.  A warp rescales when one of its 32 rows asks for it, so
+// with 8 every second page of logits of deviation 5 did, at 2000 cycles each.
+constexpr float kSlack = 15.f;
+
+// An item: a group's KV head, row tile(s) and run of pages.
+struct SharedItem {
+    SharedGroup g;
+    const int32_t* members;
+    const int32_t* table;  // of the group's first sequence
+    int kv, split, row0, rows, pg0, pg1, n;  // rows: of the item's tiles; n: pages that can be read
+};
+
+__device__ __forceinline__ SharedItem find_item(const DecodeParamsX& p, int item, int tile_rows) {
+    SharedItem r;
+    int lo = 0, hi = p.n_groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(&p.groups[mid].first_item) <= item) lo = mid;
+        else hi = mid;
+    }
+    r.g = p.groups[lo];
+    const int rel = item - r.g.first_item;
+    r.split = rel % r.g.splits;
+    r.kv = rel / r.g.splits % p.hk;
+    r.row0 = rel / r.g.splits / p.hk * tile_rows;
+    r.rows = min(tile_rows, r.g.members * p.G - r.row0);
+    r.pg0 = (int)((long)r.g.pages * r.split / r.g.splits);
+    r.pg1 = (int)((long)r.g.pages * (r.split + 1) / r.g.splits);
+    r.members = p.member + r.g.first_member;
+    r.table = p.page_table + (size_t)__ldg(r.members) * p.max_pages;
+    r.n = 0;
+    const int lane = threadIdx.x & 31;
+    for (int q0 = r.pg0; q0 < r.pg1; q0 += 128) {
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = q0 + 32 * i + lane < r.pg1 ? __ldg(r.table + q0 + 32 * i + lane) : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.n += __popc(__ballot_sync(kFull, id[i] >= 0 && id[i] < p.num_pages));
+    }
+    return r;
+}
 
 template <int BITS, int PARTS>
 __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_kernel(DecodeParamsX p) {
@@ -330,17 +396,17 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     uint64_t* drain = o_done + T;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);  // (uniform for the compiler)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 4);
+            mbar_init(&raw_empty[i], kDequantWarps);
         }
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&k_full[i], 4);
+            mbar_init(&k_full[i], kDequantWarps);
             mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 4);
+            mbar_init(&v_full[i], kDequantWarps);
             mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < 2 * T; ++i) {
@@ -354,7 +420,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     }
     if (warp == 0) tmem_alloc(tmem_at, SM::kCols);
     tc_before();
-    __syncthreads();
+    block_sync();
     tc_after();
     const uint32_t tmem = *tmem_at;
     pdl_wait();     // plan and Q' rows
@@ -370,70 +436,60 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         }
         return false;
     };
+    // Every role walks the block's items by itself; two barriers of the block per
+    // item: Q' is in place, and the item is done (with a timeout: the last one).
     bool ok = true;
-    uint32_t done = 0;          // pages of earlier items (rings of the pages)
-    uint32_t tile_done[T] = {};  // the same of each row tile's barriers (an item may have one tile only)
+    uint32_t done = 0;   // pages of earlier items: the rings of the pages, and tile 0
+    uint32_t done1 = 0;  // the same of tile 1, which an item may lack
 
-    for (int item = blockIdx.x; item < total; item += gridDim.x) {
-        // ---- the item: group, KV head, row tile, run of pages
-        int lo = 0, hi = p.n_groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldg(&p.groups[mid].first_item) <= item) lo = mid;
-            else hi = mid;
-        }
-        const SharedGroup gi = p.groups[lo];
-        const int rel = item - gi.first_item;
-        const int split = rel % gi.splits, kv = rel / gi.splits % p.hk, rt = rel / gi.splits / p.hk;
-        const int pg0 = (int)((long)gi.pages * split / gi.splits), pg1 = (int)((long)gi.pages * (split + 1) / gi.splits);
-        const int32_t* members = p.member + gi.first_member;
-        const int32_t* table = p.page_table + (size_t)__ldg(members) * p.max_pages;
-        const int row0 = rt * T * 128, rows_left = gi.members * p.G - row0;
-        const int tiles = T == 2 && rows_left > 128 ? 2 : 1;
-        int n = 0;  // pages that can be read
-        for (int q0 = pg0; q0 < pg1; q0 += 32) {
-            const int q = q0 + lane;
-            const int id = q < pg1 ? __ldg(table + q) : -1;
-            n += __popc(__ballot_sync(kFull, id >= 0 && id < p.num_pages));
-        }
-
-        // ---- Q' rows into their tiles (zeros behind the last row)
-        if (warp < SM::kSoftWarps) {
-            for (int i = threadIdx.x; i < tiles * 128 * 16; i += SM::kSoftWarps * 32) {
-                const int r = i >> 4, c = i & 15, t = r >> 7, rr = r & 127;
-                const int row = row0 + r;
-                uint8_t* to = smem + SM::kQ + t * PARTS * SM::kQTile + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-                uint4 v[PARTS];
+    if (warp < SM::kSoftWarps) {
+        // -------------------------------- softmax --------------------------------
+        regs_up<SM::kSoftRegs>();
+        const int t = warp >> 2;
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
+            const SharedItem it = find_item(p, item, 128 * T);
+            const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
+            // Q' rows into their tiles (zeros behind the last row): thread = chunk c of rows r0, r0 + 8 T, ..
+            {
+                const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+                constexpr int kStep = SM::kSoftWarps * 2, kBatch = PARTS == 1 ? 8 : 4;
+                for (int i0 = 0; i0 < tiles * 128; i0 += kStep * kBatch) {
+                    uint4 v[kBatch][PARTS];
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) v[part] = make_uint4(0u, 0u, 0u, 0u);
-                if (row < gi.members * p.G) {
-                    const size_t at = ((size_t)__ldg(members + row / p.G) * p.hk + kv) * p.G + row % p.G;
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = i0 + kStep * i + r0, row = it.row0 + r;
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-                        v[part] = __ldg(reinterpret_cast<const uint4*>(p.qrow + ((size_t)part * p.B * p.hq + at) * kD) + c);
+                        for (int part = 0; part < PARTS; ++part) v[i][part] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < it.rows) {
+                            const size_t at = ((size_t)__ldg(it.members + row / p.G) * p.hk + it.kv) * p.G + row % p.G;
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part)
+                                v[i][part] = __ldg(reinterpret_cast<const uint4*>(p.qrow + ((size_t)part * p.B * p.hq + at) * kD) + c);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const int r = i0 + kStep * i + r0, rr = r & 127;
+                        uint8_t* to = smem + SM::kQ + (r >> 7) * PARTS * SM::kQTile + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) *reinterpret_cast<uint4*>(to + part * SM::kQTile) = v[i][part];
+                    }
                 }
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) *reinterpret_cast<uint4*>(to + part * SM::kQTile) = v[part];
+                fence_async();
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncthreads();
-
-        if (warp < SM::kSoftWarps) {
-            // ------------------------------ softmax ------------------------------
-            const int t = warp >> 2;
+            block_sync();
             if (t < tiles) {
-                const int r = row0 + t * 128 + (warp & 3) * 32 + lane;
-                const bool row_on = r < gi.members * p.G;
-                const int b = row_on ? __ldg(members + r / p.G) : 0, head = row_on ? r % p.G : 0;
-                const float kq = row_on ? __ldg(p.qkinv + ((size_t)b * p.hk + kv) * 4) : 1.f;  // 2^-e of the Q' rows
+                const int r = t * 128 + (warp & 3) * 32 + lane, row = it.row0 + r;
+                const bool row_on = r < it.rows;
+                const int b = row_on ? __ldg(it.members + row / p.G) : 0, head = row_on ? row % p.G : 0;
+                const float kq = row_on ? __ldg(p.qkinv + ((size_t)b * p.hk + it.kv) * 4) : 1.f;  // 2^-e of the Q' rows
                 const uint32_t lanes = tmem + t * SM::kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
                 float m_run = -INFINITY, l0 = 0.f, l1 = 0.f;
                 float o[PARTS == 2 ? kD : 1];
                 if constexpr (PARTS == 2)
 #pragma unroll
                     for (int d = 0; d < kD; ++d) o[d] = 0.f;
-                const uint32_t g0 = T == 2 ? tile_done[t] : done;
+                const uint32_t g0 = t == 1 ? done1 : done;
                 for (int j = 0; j < n && ok; ++j) {
                     const uint32_t g = g0 + j, buf = g & 1u;
                     if (!(ok = wait(&s_full[2 * t + buf], (g >> 1) & 1u))) break;
@@ -444,13 +500,13 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     tmem_ld32(s[1], sa + 32);
                     tmem_wait_ld(s[0]);
                     tmem_wait_ld(s[1]);
-                    float mx = -INFINITY;
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, fmaxf(__uint_as_float(s[0][i]), __uint_as_float(s[1][i])));
-                    mx *= kq;
+                    for (int i = 0; i < 32; ++i)
+                        mx4[i & 3] = fmaxf(mx4[i & 3], fmaxf(__uint_as_float(s[0][i]), __uint_as_float(s[1][i])));
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * kq;
                     float alpha = 1.f;
-                    const bool over = PARTS == 2 ? mx > m_run : mx > m_run + kSlack;
-                    const bool any = __any_sync(kFull, over);
+                    const bool any = __any_sync(kFull, PARTS == 2 ? mx > m_run : mx > m_run + kSlack);
                     if (any) {
                         const float m_new = fmaxf(m_run, mx);
                         alpha = m_new > m_run ? ex2(m_run - m_new) : 1.f;
@@ -458,33 +514,37 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                         l0 *= alpha;
                         l1 *= alpha;
                     }
-                    const float off = finite_max(m_run) - kShift;
+                    const float off = finite_max(m_run);
                     const float2 kk = make_float2(kq, kq), oo = make_float2(-off, -off);
-                    float2 sum = make_float2(0.f, 0.f);
-                    uint32_t ph[2][16], pl[PARTS == 2 ? 2 : 1][16];
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    const uint32_t pa = PARTS == 1 ? sa : lanes + SM::kColP + buf * 64;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t ph[16], pl[PARTS == 2 ? 16 : 1];
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
                             // tokens i .. i + 3; stored (0, 2), (1, 3)
                             const float2 x = fma2(make_float2(__uint_as_float(s[h][i]), __uint_as_float(s[h][i + 2])), kk, oo);
                             const float2 y = fma2(make_float2(__uint_as_float(s[h][i + 1]), __uint_as_float(s[h][i + 3])), kk, oo);
-                            const float2 pa = make_float2(ex2(x.x), ex2(x.y)), pb = make_float2(ex2(y.x), ex2(y.y));
-                            sum = add2(sum, add2(pa, pb));
-                            ph[h][i / 2] = pack_f16x2_rn(pa.x, pa.y);
-                            ph[h][i / 2 + 1] = pack_f16x2_rn(pb.x, pb.y);
+                            const float2 e0 = make_float2(ex2(x.x), ex2(x.y)), e1 = make_float2(ex2(y.x), ex2(y.y));
+                            sum[(i >> 2) & 1] = add2(sum[(i >> 2) & 1], add2(e0, e1));
+                            ph[i / 2] = pack_f16x2_rn(e0.x, e0.y);
+                            ph[i / 2 + 1] = pack_f16x2_rn(e1.x, e1.y);
                             if constexpr (PARTS == 2) {
-                                pl[h][i / 2] = pack_f16x2_rn(pa.x - half_lo(ph[h][i / 2]), pa.y - half_hi(ph[h][i / 2]));
-                                pl[h][i / 2 + 1] = pack_f16x2_rn(pb.x - half_lo(ph[h][i / 2 + 1]), pb.y - half_hi(ph[h][i / 2 + 1]));
+                                pl[i / 2] = pack_f16x2_rn(e0.x - half_lo(ph[i / 2]), e0.y - half_hi(ph[i / 2]));
+                                pl[i / 2 + 1] = pack_f16x2_rn(e1.x - half_lo(ph[i / 2 + 1]), e1.y - half_hi(ph[i / 2 + 1]));
                             }
                         }
-                    l0 += sum.x;
-                    l1 += sum.y;
+                        tmem_st16(pa + 16 * h, ph);
+                        if constexpr (PARTS == 2) tmem_st16(pa + 32 + 16 * h, pl);
+                    }
+                    l0 += sum[0].x + sum[1].x;
+                    l1 += sum[0].y + sum[1].y;
                     if constexpr (PARTS == 1) {
                         if (any && j > 0) {  // rescale O, once the products of the page before are in it
                             if (!(ok = wait(&o_done[t], (g - 1) & 1u))) break;
                             tc_after();
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < kD; c += 32) {
                                 uint32_t v[32];
                                 tmem_ld32(v, lanes + SM::kColO + c);
@@ -494,14 +554,6 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                                 tmem_st32(lanes + SM::kColO + c, v);
                             }
                         }
-                        tmem_st16(sa, ph[0]);
-                        tmem_st16(sa + 16, ph[1]);
-                    } else {
-                        const uint32_t pa = lanes + SM::kColP + buf * 64;
-                        tmem_st16(pa, ph[0]);
-                        tmem_st16(pa + 16, ph[1]);
-                        tmem_st16(pa + 32, pl[0]);
-                        tmem_st16(pa + 48, pl[1]);
                     }
                     tmem_wait_st();
                     tc_before();
@@ -517,8 +569,13 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                                 uint32_t v[32];
                                 tmem_ld32(v, lanes + SM::kColO + (buf ^ 1u) * kD + c);
                                 tmem_wait_ld(v);
+                                const float2 aa = make_float2(alpha, alpha);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[c + i] = (o[c + i] + __uint_as_float(v[i])) * alpha;
+                                for (int i = 0; i < 32; i += 2) {
+                                    const float2 x = mul2(add2(make_float2(o[c + i], o[c + i + 1]), make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))), aa);
+                                    o[c + i] = x.x;
+                                    o[c + i + 1] = x.y;
+                                }
                             }
                         }
                     }
@@ -533,7 +590,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                 }
                 if (ok) {
                     const float l = l0 + l1;
-                    float* part = p.sh_part + ((size_t)gi.first_part + ((size_t)kv * gi.splits + split) * gi.members + (row_on ? r / p.G : 0)) * p.part_stride;
+                    float* part = p.sh_part + ((size_t)it.g.first_part + ((size_t)it.kv * it.g.splits + it.split) * it.g.members + (row_on ? row / p.G : 0)) * p.part_stride;
 #pragma unroll
                     for (int c = 0; c < kD; c += 32) {
                         uint32_t v[32];
@@ -552,40 +609,52 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                                 *reinterpret_cast<uint4*>(part + head * kD + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                     if (row_on) {
-                        part[p.G * kD + head] = l == 0.f ? -INFINITY : finite_max(m_run) - kShift;
+                        part[p.G * kD + head] = l == 0.f ? -INFINITY : finite_max(m_run);
                         part[p.G * kD + p.G + head] = l;
                     }
                 }
                 tc_before();
             }
-        } else if (warp < SM::kSoftWarps + 4) {
-            // --------------------------- dequantisation ---------------------------
-            const int wq = warp - SM::kSoftWarps;
-            const int ng = 4 >> p.gshift;
-            uint16_t* sS = reinterpret_cast<uint16_t*>(smem + SM::kPairs) + wq * (2 * 4 * kPage);  // [4 groups][64] s, then z
-            uint16_t* zS = sS + 4 * kPage;
+            block_sync();
+            if (*dead) break;
+            done += n;
+            if (tiles == 2) done1 += n;
+        }
+    } else if (warp < SM::kMmaWarp) {
+        // ----------------------------- dequantisation -----------------------------
+        regs_down<SM::kDequantRegs>();
+        const int dw = warp - SM::kSoftWarps;
+        const int ng = 4 >> p.gshift;
+        // K: a lane's token and 16-byte code chunk (lanes of a wavefront on distinct banks)
+        const int ka = lane & 3, kt = 8 * dw + ((((lane >> 2) & 1) << 2) | (lane >> 3));
+        // V: tokens 16 tc .. + 15; 4 bits: plane 8 dw + lane / 4, positions 2 plane, + 1, of group dw / 2;
+        // 2 bits: plane 4 dw + lane / 4 % 4, positions 32 i + plane of slots i = i0, i0 + 1
+        const int tc = lane & 3;
+        const int plane = BITS == 4 ? 8 * dw + (lane >> 2) : 4 * dw + ((lane >> 2) & 3);
+        const int i0 = BITS == 4 ? 0 : 2 * (lane >> 4);
+        uint16_t* pairS = reinterpret_cast<uint16_t*>(smem + SM::kPairs + dw * SM::kPairBytes);  // [group][s, z][64]
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
+            const SharedItem it = find_item(p, item, 128 * T);
+            const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
+            block_sync();
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t g = done + j, st = g % NS, rs = g % NR;
                 if (!(ok = wait(&raw_full[rs], (g / NR) & 1u))) break;
                 const uint8_t* blk = smem + SM::kRawAt + rs * SM::kRaw;
                 if (g >= NS && !(ok = wait(&k_empty[st], ((g / NS) - 1) & 1u))) break;
-                uint8_t* kS = smem + SM::kK + st * PARTS * SM::kOperand;
-                const int a = lane & 3, t8 = (((lane >> 2) & 1) << 2) | (lane >> 3);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t = 16 * wq + 8 * u + t8;
+                {
+                    uint8_t* row = smem + SM::kK + st * PARTS * SM::kOperand + kt * 128;
                     uint32_t w[4], sz[4];
                     if constexpr (BITS == 4) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(blk + t * 64 + 16 * a);
+                        const uint4 x = *reinterpret_cast<const uint4*>(blk + kt * 64 + 16 * ka);
                         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
                     } else {
-                        const uint2 x = *reinterpret_cast<const uint2*>(blk + t * 32 + 8 * a);
+                        const uint2 x = *reinterpret_cast<const uint2*>(blk + kt * 32 + 8 * ka);
                         w[0] = x.x; w[1] = x.y; w[2] = x.x >> 8; w[3] = x.y >> 8;
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        sz[k] = *reinterpret_cast<const uint32_t*>(blk + (BITS == 4 ? kCodes4 : kKScale) + (t * ng + (k >> p.gshift)) * 4);
-                    uint8_t* row = kS + t * 128;
+                        sz[k] = *reinterpret_cast<const uint32_t*>(blk + (BITS == 4 ? kCodes4 : kKScale) + (kt * ng + (k >> p.gshift)) * 4);
                     auto chunk = [&](auto kk) {
                         constexpr int k = decltype(kk)::value;
                         const uint32_t s2 = __byte_perm(sz[k], 0u, 0x1010), z2 = __byte_perm(sz[k], 0u, 0x3232);
@@ -604,7 +673,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) value_pair<PARTS>(s2, c[i], z2, hi[i], lo[i]);
-                        uint8_t* to = row + (k >> 1) * (kPage * 128) + (((4 * (k & 1) + a) ^ (t & 7)) << 4);
+                        uint8_t* to = row + (k >> 1) * (kPage * 128) + (((4 * (k & 1) + ka) ^ (kt & 7)) << 4);
                         *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         if constexpr (PARTS == 2) *reinterpret_cast<uint4*>(to + SM::kOperand) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     };
@@ -613,182 +682,183 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     chunk(std::integral_constant<int, 2>{});
                     chunk(std::integral_constant<int, 3>{});
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&k_full[st]);
-                // V: the pairs first, by group and in the tokens' order of the products
-                if (g >= NS && !(ok = wait(&v_empty[st], ((g / NS) - 1) & 1u))) break;
-                uint8_t* vS = smem + SM::kV + st * PARTS * SM::kOperand;
+                // V: its pairs go by group and in the tokens' order of the products
                 const uint8_t* vh = blk + (BITS == 4 ? half_bytes4(p.gshift) : kVCodes);
                 const uint8_t* vp = blk + (BITS == 4 ? half_bytes4(p.gshift) + kCodes4 : v_scale_off(p.gshift));
+                uint4 x = *reinterpret_cast<const uint4*>(vh + plane * kPage + 16 * tc);
+                if constexpr (BITS == 2) {
+                    x.x >>= 2 * i0; x.y >>= 2 * i0; x.z >>= 2 * i0; x.w >>= 2 * i0;
+                }
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int t = lane + 32 * u, at = (t & ~3) | pv_slot(t & 3);
-                    if constexpr (BITS == 4) {  // warp wq: positions 32 wq .. + 31, one group
-                        const uint32_t x = *reinterpret_cast<const uint32_t*>(vp + (t * ng + (wq >> p.gshift)) * 4);
-                        sS[at] = (uint16_t)x;
-                        zS[at] = (uint16_t)(x >> 16);
-                    } else {
-                        for (int k = 0; k < ng; ++k) {
-                            const uint32_t x = *reinterpret_cast<const uint32_t*>(vp + (t * ng + k) * 4);
-                            sS[k * kPage + at] = (uint16_t)x;
-                            zS[k * kPage + at] = (uint16_t)(x >> 16);
-                        }
+                    for (int gr = 0; gr < (BITS == 4 ? 1 : ng); ++gr) {
+                        const uint32_t y = *reinterpret_cast<const uint32_t*>(vp + (t * ng + (BITS == 4 ? (dw >> 1) >> p.gshift : gr)) * 4);
+                        pairS[gr * 2 * kPage + at] = (uint16_t)y;
+                        pairS[gr * 2 * kPage + kPage + at] = (uint16_t)(y >> 16);
                     }
                 }
+                fence_async();
                 __syncwarp();
-                const int tc = lane & 3, jj = lane >> 2;
+                if (lane == 0) mbar_arrive(&k_full[st]);
+                if (g >= NS && !(ok = wait(&v_empty[st], ((g / NS) - 1) & 1u))) break;
+                uint8_t* vS = smem + SM::kV + st * PARTS * SM::kOperand;
                 // one row (stored position pos) of 16 tokens from the codes at bits P of the plane words x
-                auto v_row = [&](auto pp, int pos, const uint4& x, const uint32_t (&s)[8], const uint32_t (&z)[8]) {
+                auto v_row = [&](auto pp, int pos, const uint32_t (&s)[8], const uint32_t (&z)[8]) {
                     constexpr int P = decltype(pp)::value;
                     constexpr uint32_t field = BITS == 4 ? 0x000f000fu : 0x00030003u;
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        value_pair<PARTS>(s[2 * i], code_at<P>(w[i], field), z[2 * i], hi[2 * i], lo[2 * i]);
-                        value_pair<PARTS>(s[2 * i + 1], code_at<P>(w[i] >> 8, field), z[2 * i + 1], hi[2 * i + 1], lo[2 * i + 1]);
-                    }
                     uint8_t* row = vS + pos * 128;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            value_pair<PARTS>(s[4 * h + 2 * i], code_at<P>(w[2 * h + i], field), z[4 * h + 2 * i], hi[2 * i], lo[2 * i]);
+                            value_pair<PARTS>(s[4 * h + 2 * i + 1], code_at<P>(w[2 * h + i] >> 8, field), z[4 * h + 2 * i + 1], hi[2 * i + 1], lo[2 * i + 1]);
+                        }
                         uint8_t* to = row + (((2 * tc + h) ^ (pos & 7)) << 4);
-                        *reinterpret_cast<uint4*>(to) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-                        if constexpr (PARTS == 2) *reinterpret_cast<uint4*>(to + SM::kOperand) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+                        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if constexpr (PARTS == 2) *reinterpret_cast<uint4*>(to + SM::kOperand) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 };
-                auto pairs_of = [&](int k, uint32_t (&s)[8], uint32_t (&z)[8]) {
-                    const uint4* sp = reinterpret_cast<const uint4*>(sS + k * kPage + 16 * tc);
-                    const uint4* zp = reinterpret_cast<const uint4*>(zS + k * kPage + 16 * tc);
+                auto pairs_of = [&](const uint16_t* at, uint32_t (&s)[8], uint32_t (&z)[8]) {
+                    const uint4* sp = reinterpret_cast<const uint4*>(at + 16 * tc);
+                    const uint4* zp = reinterpret_cast<const uint4*>(at + kPage + 16 * tc);
                     const uint4 s0 = sp[0], s1 = sp[1], z0 = zp[0], z1 = zp[1];
                     s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
                     z[0] = z0.x; z[1] = z0.y; z[2] = z0.z; z[3] = z0.w; z[4] = z1.x; z[5] = z1.y; z[6] = z1.z; z[7] = z1.w;
                 };
                 uint32_t s[8], z[8];
                 if constexpr (BITS == 4) {
-                    pairs_of(0, s, z);
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int plane = 16 * wq + 8 * u + jj;
-                        const uint4 x = *reinterpret_cast<const uint4*>(vh + plane * kPage + 16 * tc);
-                        v_row(std::integral_constant<int, 0>{}, 2 * plane, x, s, z);
-                        v_row(std::integral_constant<int, 4>{}, 2 * plane + 1, x, s, z);
-                    }
+                    pairs_of(pairS, s, z);
+                    v_row(std::integral_constant<int, 0>{}, 2 * plane, s, z);
+                    v_row(std::integral_constant<int, 4>{}, 2 * plane + 1, s, z);
                 } else {
-                    const int plane = 8 * wq + jj;
-                    const uint4 x = *reinterpret_cast<const uint4*>(vh + plane * kPage + 16 * tc);
-                    auto slot = [&](auto ii) {
+                    auto slot = [&](auto ii) {  // (x is shifted down by the half warp's first slot)
                         constexpr int i = decltype(ii)::value;
-                        pairs_of(i >> p.gshift, s, z);
-                        v_row(std::integral_constant<int, 2 * i>{}, 32 * i + plane, x, s, z);
+                        pairs_of(pairS + ((i + i0) >> p.gshift) * 2 * kPage, s, z);
+                        v_row(std::integral_constant<int, 2 * i>{}, 32 * (i + i0) + plane, s, z);
                     };
                     slot(std::integral_constant<int, 0>{});
                     slot(std::integral_constant<int, 1>{});
-                    slot(std::integral_constant<int, 2>{});
-                    slot(std::integral_constant<int, 3>{});
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                fence_async();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&v_full[st]);
                     mbar_arrive(&raw_empty[rs]);
                 }
             }
-        } else if (warp == SM::kSoftWarps + 4) {
-            // ------------------------------ products ------------------------------
-            const uint32_t qa = smem_u32(smem + SM::kQ), ka = smem_u32(smem + SM::kK), va = smem_u32(smem + SM::kV);
-            bool issued = false;
-            auto values_of = [&](int j) {  // O (+)= P V of page j
-                const uint32_t g = done + j, st = g % NS;
-                for (int t = 0; t < tiles; ++t) {
-                    const uint32_t gt = (T == 2 ? tile_done[t] : done) + j, buf = gt & 1u;
-                    if (!wait(&p_full[2 * t + buf], (gt >> 1) & 1u)) return false;
-                    if (t == 0 && !wait(&v_full[st], (g / NS) & 1u)) return false;
-                    tc_after();
-                    if (lane == 0) {
+            block_sync();
+            if (*dead) break;
+            done += n;
+            if (tiles == 2) done1 += n;
+        }
+    } else {
+        regs_down<SM::kOtherRegs>();  // (the warps of a warpgroup take the same instruction)
+        if (warp == SM::kMmaWarp) {
+            // -------------------------------- products --------------------------------
+            const uint64_t qd = tc_desc(smem_u32(smem + SM::kQ)), kd = tc_desc(smem_u32(smem + SM::kK)), vd = tc_desc(smem_u32(smem + SM::kV));
+            const uint32_t on = elect_lane();
+            for (int item = blockIdx.x; item < total; item += gridDim.x) {
+                const SharedItem it = find_item(p, item, 128 * T);
+                const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
+                block_sync();
+                bool issued = false;
+                auto values_of = [&](int j) {  // O (+)= P V of page j
+                    const uint32_t g = done + j, st = g % NS;
+    #pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        if (t >= tiles) break;
+                        const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
+                        if (!wait(&p_full[2 * t + buf], (gt >> 1) & 1u)) return false;
+                        if (t == 0 && !wait(&v_full[st], (g / NS) & 1u)) return false;
+                        tc_after();
                         const uint32_t tt = tmem + t * SM::kTileCols;
                         const uint32_t pa = tt + SM::kColP + buf * 64, o = tt + SM::kColO + (PARTS == 2 ? buf * kD : 0);
-#pragma unroll
+    #pragma unroll
                         for (int pr = 0; pr < (PARTS == 1 ? 1 : 3); ++pr)  // hi hi, lo hi, hi lo
-#pragma unroll
+    #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                tc_mma_ts(o, pa + (pr == 1 ? 32 : 0) + 8 * k, tc_desc(va + (st * PARTS + (pr == 2)) * SM::kOperand + 32 * k),
-                                          tc_idesc(kD), (PARTS == 1 && j > 0) || pr > 0 || k > 0);
-                        tc_commit(&o_done[t]);
+                                tc_mma_ts(on, o, pa + (pr == 1 ? 32 : 0) + 8 * k, vd + (((st * PARTS + (pr == 2)) * SM::kOperand + 32 * k) >> 4), tc_idesc(kD),
+                                          (PARTS == 1 && j > 0) || pr > 0 || k > 0);
+                        tc_commit(on, &o_done[t]);
                     }
-                    __syncwarp();
-                }
-                if (lane == 0) tc_commit(&v_empty[st]);
-                __syncwarp();
-                return true;
-            };
-            for (int j = 0; j < n && ok; ++j) {
-                const uint32_t g = done + j, st = g % NS;
-                if (!(ok = wait(&k_full[st], (g / NS) & 1u))) break;
-                for (int t = 0; t < tiles && ok; ++t) {
-                    const uint32_t gt = (T == 2 ? tile_done[t] : done) + j, buf = gt & 1u;
-                    // S takes the place of the P of two pages before: its products are to be done
-                    if (PARTS == 1 && j >= 2 && !(ok = wait(&o_done[t], gt & 1u))) break;
-                    tc_after();
-                    if (lane == 0) {
+                    tc_commit(on, &v_empty[st]);
+                    return true;
+                };
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t g = done + j, st = g % NS;
+                    if (!(ok = wait(&k_full[st], (g / NS) & 1u))) break;
+    #pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        if (t >= tiles || !ok) break;
+                        const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
+                        // S takes the place of the P of two pages before: its products are to be done
+                        if (PARTS == 1 && j >= 2 && !(ok = wait(&o_done[t], gt & 1u))) break;
+                        tc_after();
                         const uint32_t s = tmem + t * SM::kTileCols + buf * 64;
-#pragma unroll
+    #pragma unroll
                         for (int pr = 0; pr < (PARTS == 1 ? 1 : 3); ++pr)
-#pragma unroll
+    #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                tc_mma_ss(s, tc_desc(qa + (t * PARTS + (pr == 1)) * SM::kQTile + (k >> 2) * (128 * 128) + 32 * (k & 3)),
-                                          tc_desc(ka + (st * PARTS + (pr == 2)) * SM::kOperand + (k >> 2) * (kPage * 128) + 32 * (k & 3)),
-                                          tc_idesc(kPage), pr > 0 || k > 0);
-                        tc_commit(&s_full[2 * t + buf]);
+                                tc_mma_ss(on, s, qd + (((t * PARTS + (pr == 1)) * SM::kQTile + (k >> 2) * (128 * 128) + 32 * (k & 3)) >> 4),
+                                          kd + (((st * PARTS + (pr == 2)) * SM::kOperand + (k >> 2) * (kPage * 128) + 32 * (k & 3)) >> 4), tc_idesc(kPage),
+                                          pr > 0 || k > 0);
+                        tc_commit(on, &s_full[2 * t + buf]);
+                        issued = true;
                     }
-                    issued = true;
-                    __syncwarp();
+                    if (!ok) break;
+                    tc_commit(on, &k_empty[st]);
+                    if (j > 0) ok = values_of(j - 1);
                 }
-                if (!ok) break;
-                if (lane == 0) tc_commit(&k_empty[st]);
-                __syncwarp();
-                if (j > 0) ok = values_of(j - 1);
-            }
-            if (ok && n > 0) ok = values_of(n - 1);
-            if (!ok && issued) {  // whatever was issued ends before the block does
-                if (lane == 0) tc_commit(drain);
-                __syncwarp();
-                (void)mbar_wait_bounded(drain, 0, kWaitPolls);
+                if (ok && n > 0) ok = values_of(n - 1);
+                if (!ok && issued) {  // whatever was issued ends before the block does
+                    tc_commit(on, drain);
+                    (void)mbar_wait_bounded(drain, 0, kWaitPolls);
+                }
+                block_sync();
+                if (*dead) break;
+                done += n;
+                if (tiles == 2) done1 += n;
             }
         } else {
-            // ------------------------------ producer ------------------------------
-            int j = 0;  // pages issued
-            for (int q0 = pg0; q0 < pg1 && ok; q0 += 32) {
-                const int q = q0 + lane;
-                const int id = q < pg1 ? __ldg(table + q) : -1;
-                const bool good = id >= 0 && id < p.num_pages;
-                if (q < pg1 && !good) report(p.status, OSCAR_STATUS_BAD_PAGE);
-                const unsigned have = __ballot_sync(kFull, good);
-                for (unsigned left = have; left && ok; left &= left - 1) {
-                    const int page = __shfl_sync(kFull, id, __ffs(left) - 1);
-                    const uint32_t g = done + j, rs = g % NR;
-                    if (g >= NR && !(ok = wait(&raw_empty[rs], ((g / NR) - 1) & 1u))) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&raw_full[rs], p.block_bytes);
-                        bulk_g2s(smem + SM::kRawAt + rs * SM::kRaw, p.pool + ((size_t)page * p.hk + kv) * p.block_bytes, p.block_bytes, &raw_full[rs]);
+            // -------------------------------- producer --------------------------------
+            for (int item = blockIdx.x; item < total; item += gridDim.x) {
+                const SharedItem it = find_item(p, item, 128 * T);
+                block_sync();
+                if (warp == SM::kMmaWarp + 1) {
+                    int j = 0;  // pages issued
+                    for (int q0 = it.pg0; q0 < it.pg1 && ok; q0 += 32) {
+                        const int q = q0 + lane;
+                        const int id = q < it.pg1 ? __ldg(it.table + q) : -1;
+                        const bool good = id >= 0 && id < p.num_pages;
+                        if (q < it.pg1 && !good) report(p.status, OSCAR_STATUS_BAD_PAGE);
+                        for (unsigned left = __ballot_sync(kFull, good); left && ok; left &= left - 1) {
+                            const int page = __shfl_sync(kFull, id, __ffs(left) - 1);
+                            const uint32_t g = done + j, rs = g % NR;
+                            if (g >= NR && !(ok = wait(&raw_empty[rs], ((g / NR) - 1) & 1u))) break;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&raw_full[rs], p.block_bytes);
+                                bulk_g2s(smem + SM::kRawAt + rs * SM::kRaw, p.pool + ((size_t)page * p.hk + it.kv) * p.block_bytes, p.block_bytes, &raw_full[rs]);
+                            }
+                            __syncwarp();
+                            ++j;
+                        }
                     }
-                    __syncwarp();
-                    ++j;
+                    if (!ok)  // copies in flight land before the block ends
+                        for (uint32_t g = done + j > NR ? done + j - NR : 0; g < done + j; ++g)
+                            (void)mbar_wait_bounded(&raw_full[g % NR], (g / NR) & 1u, kWaitPolls);
                 }
+                block_sync();
+                if (*dead) break;
+                done += it.n;
             }
-            if (!ok)  // copies in flight land before the block ends
-                for (uint32_t g = done + j > NR ? done + j - NR : 0; g < done + j; ++g)
-                    (void)mbar_wait_bounded(&raw_full[g % NR], (g / NR) & 1u, kWaitPolls);
         }
-        __syncthreads();
-        if (*dead) break;
-        done += n;
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-            if (t < tiles) tile_done[t] += n;
     }
     tc_before();
-    __syncthreads();
+    block_sync();
     if (warp == 0) tmem_free(tmem, SM::kCols);
 }
 
