@@ -306,12 +306,12 @@ struct SharedSmem {
     static constexpr int kPairGroups = BITS == 4 ? 1 : 4;      // groups that a warp's rows of V belong to, at most
     static constexpr int kPairBytes = kPairGroups * 2 * kPage * 2;
     static constexpr int kBars = kPairs + kDequantWarps * kPairBytes;
-    static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 4 + T + 1;
+    static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 6 + T + 3;
     static constexpr int kBytes = kBars + kNumBars * 8 + 32;
     static constexpr int kAlloc = kBytes + 1024;        // the swizzled operands start on 1024 bytes
     static_assert(kAlloc <= 227 * 1024, "shared memory of a block");
-    // warps by role, in whole warpgroups: softmax, dequantisation, then the warp of the
-    // products, the producer and two that are idle
+    // warps by role, in whole warpgroups: softmax, dequantisation, then one that issues the
+    // products of logits, one those of values, the producer and an idle one
     static constexpr int kSoftWarps = 4 * T;
     static constexpr int kMmaWarp = kSoftWarps + kDequantWarps, kThreads = (kMmaWarp + 4) * 32;
     // registers per thread: of the launch, then of each role (their sum is within the launch's)
@@ -392,9 +392,11 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     uint64_t* v_empty = v_full + NS;
     uint64_t* s_full = v_empty + NS;   // [T][2]
     uint64_t* p_full = s_full + 2 * T; // [T][2]
-    uint64_t* o_done = p_full + 2 * T; // [T]
-    uint64_t* drain = o_done + T;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* s_free = p_full + 2 * T; // [T][2]
+    uint64_t* o_done = s_free + 2 * T; // [T]
+    uint64_t* q_full = o_done + T;
+    uint64_t* drain = q_full + 1;      // [2] the two warps of the products
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);  // (uniform for the compiler)
 
@@ -412,9 +414,12 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         for (int i = 0; i < 2 * T; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+            mbar_init(&s_free[i], 1);
         }
         for (int i = 0; i < T; ++i) mbar_init(&o_done[i], 1);
-        mbar_init(drain, 1);
+        mbar_init(q_full, SM::kSoftWarps);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         fence_mbar_init();
         *dead = 0;
     }
@@ -436,9 +441,10 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         }
         return false;
     };
-    // Every role walks the block's items by itself; two barriers of the block per
-    // item: Q' is in place, and the item is done (with a timeout: the last one).
+    // Every role walks the block's items by itself; a barrier of the block ends an
+    // item (with a timeout: the last one).
     bool ok = true;
+    uint32_t items = 0;  // of this block so far
     uint32_t done = 0;   // pages of earlier items: the rings of the pages, and tile 0
     uint32_t done1 = 0;  // the same of tile 1, which an item may lack
 
@@ -476,8 +482,9 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     }
                 }
                 fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
             }
-            block_sync();
             if (t < tiles) {
                 const int r = t * 128 + (warp & 3) * 32 + lane, row = it.row0 + r;
                 const bool row_on = r < it.rows;
@@ -589,26 +596,43 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     tc_after();
                 }
                 if (ok) {
+                    // o' goes through the warp's quarter of its Q' tile (no product reads that any more), so
+                    // that a store of the warp covers whole lines: 16 rows' 16 bytes a piece cost eight times
+                    // the cycles.  Row r's chunk c of 16 lies at chunk c ^ (r & 15).
                     const float l = l0 + l1;
-                    float* part = p.sh_part + ((size_t)it.g.first_part + ((size_t)it.kv * it.g.splits + it.split) * it.g.members + (row_on ? row / p.G : 0)) * p.part_stride;
+                    uint8_t* stage = smem + SM::kQ + t * PARTS * SM::kQTile + (warp & 3) * (SM::kQTile / 4);
+                    float* parts = p.sh_part + ((size_t)it.g.first_part + ((size_t)it.kv * it.g.splits + it.split) * it.g.members) * p.part_stride;
 #pragma unroll
-                    for (int c = 0; c < kD; c += 32) {
-                        uint32_t v[32];
+                    for (int h = 0; h < 2; ++h) {  // 64 positions at a time
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                        if (n > 0) {
-                            tmem_ld32(v, lanes + SM::kColO + (PARTS == 2 ? ((g0 + n - 1) & 1u) * kD : 0) + c);
-                            tmem_wait_ld(v);
-                        }
-                        if constexpr (PARTS == 2)
+                        for (int c = 0; c < 64; c += 32) {
+                            uint32_t v[32];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(o[c + i] + __uint_as_float(v[i]));
-                        if (row_on)
+                            for (int i = 0; i < 32; ++i) v[i] = 0u;
+                            if (n > 0) {
+                                tmem_ld32(v, lanes + SM::kColO + (PARTS == 2 ? ((g0 + n - 1) & 1u) * kD : 0) + 64 * h + c);
+                                tmem_wait_ld(v);
+                            }
+                            if constexpr (PARTS == 2)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(o[64 * h + c + i] + __uint_as_float(v[i]));
 #pragma unroll
                             for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4*>(part + head * kD + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                                *reinterpret_cast<uint4*>(stage + lane * 256 + ((((c + i) >> 2) ^ (lane & 15)) << 4)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
+                        __syncwarp();
+                        const int first = t * 128 + (warp & 3) * 32, c = lane & 15;
+#pragma unroll 4
+                        for (int i = lane >> 4; i < 32; i += 2) {
+                            if (first + i >= it.rows) break;
+                            const int rw = it.row0 + first + i;
+                            const uint4 x = *reinterpret_cast<const uint4*>(stage + i * 256 + ((c ^ (i & 15)) << 4));
+                            *reinterpret_cast<uint4*>(parts + (size_t)(rw / p.G) * p.part_stride + rw % p.G * kD + 64 * h + 4 * c) = x;
+                        }
+                        __syncwarp();
                     }
                     if (row_on) {
+                        float* part = parts + (size_t)(row / p.G) * p.part_stride;
                         part[p.G * kD + head] = l == 0.f ? -INFINITY : finite_max(m_run);
                         part[p.G * kD + p.G + head] = l;
                     }
@@ -635,8 +659,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         uint16_t* pairS = reinterpret_cast<uint16_t*>(smem + SM::kPairs + dw * SM::kPairBytes);  // [group][s, z][64]
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
             const SharedItem it = find_item(p, item, 128 * T);
-            const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
-            block_sync();
+            const int n = it.n;
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t g = done + j, st = g % NS, rs = g % NR;
                 if (!(ok = wait(&raw_full[rs], (g / NR) & 1u))) break;
@@ -753,55 +776,35 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
             block_sync();
             if (*dead) break;
             done += n;
-            if (tiles == 2) done1 += n;
         }
     } else {
         regs_down<SM::kOtherRegs>();  // (the warps of a warpgroup take the same instruction)
+        const uint32_t on = elect_lane();
         if (warp == SM::kMmaWarp) {
-            // -------------------------------- products --------------------------------
-            const uint64_t qd = tc_desc(smem_u32(smem + SM::kQ)), kd = tc_desc(smem_u32(smem + SM::kK)), vd = tc_desc(smem_u32(smem + SM::kV));
-            const uint32_t on = elect_lane();
-            for (int item = blockIdx.x; item < total; item += gridDim.x) {
+            // --------------------------- products of logits ---------------------------
+            // (The two kinds of products have a warp each: with one for both, its six waits
+            // and 24 issues per page, one after the other, were the kernel's critical path.)
+            const uint64_t qd = tc_desc(smem_u32(smem + SM::kQ)), kd = tc_desc(smem_u32(smem + SM::kK));
+            for (int item = blockIdx.x; item < total; item += gridDim.x, ++items) {
                 const SharedItem it = find_item(p, item, 128 * T);
                 const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
-                block_sync();
                 bool issued = false;
-                auto values_of = [&](int j) {  // O (+)= P V of page j
-                    const uint32_t g = done + j, st = g % NS;
-    #pragma unroll
-                    for (int t = 0; t < T; ++t) {
-                        if (t >= tiles) break;
-                        const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
-                        if (!wait(&p_full[2 * t + buf], (gt >> 1) & 1u)) return false;
-                        if (t == 0 && !wait(&v_full[st], (g / NS) & 1u)) return false;
-                        tc_after();
-                        const uint32_t tt = tmem + t * SM::kTileCols;
-                        const uint32_t pa = tt + SM::kColP + buf * 64, o = tt + SM::kColO + (PARTS == 2 ? buf * kD : 0);
-    #pragma unroll
-                        for (int pr = 0; pr < (PARTS == 1 ? 1 : 3); ++pr)  // hi hi, lo hi, hi lo
-    #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc_mma_ts(on, o, pa + (pr == 1 ? 32 : 0) + 8 * k, vd + (((st * PARTS + (pr == 2)) * SM::kOperand + 32 * k) >> 4), tc_idesc(kD),
-                                          (PARTS == 1 && j > 0) || pr > 0 || k > 0);
-                        tc_commit(on, &o_done[t]);
-                    }
-                    tc_commit(on, &v_empty[st]);
-                    return true;
-                };
+                ok = wait(q_full, items & 1u);
                 for (int j = 0; j < n && ok; ++j) {
                     const uint32_t g = done + j, st = g % NS;
                     if (!(ok = wait(&k_full[st], (g / NS) & 1u))) break;
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < T; ++t) {
                         if (t >= tiles || !ok) break;
                         const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
-                        // S takes the place of the P of two pages before: its products are to be done
-                        if (PARTS == 1 && j >= 2 && !(ok = wait(&o_done[t], gt & 1u))) break;
+                        // S takes the place of the S, and P, of two pages before, whose products of values are to be
+                        // done (a barrier for each buffer: those of the page before may be done too)
+                        if (gt >= 2 && !(ok = wait(&s_free[2 * t + buf], ((gt >> 1) - 1) & 1u))) break;
                         tc_after();
                         const uint32_t s = tmem + t * SM::kTileCols + buf * 64;
-    #pragma unroll
-                        for (int pr = 0; pr < (PARTS == 1 ? 1 : 3); ++pr)
-    #pragma unroll
+#pragma unroll
+                        for (int pr = 0; pr < (PARTS == 1 ? 1 : 3); ++pr)  // hi hi, lo hi, hi lo
+#pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 tc_mma_ss(on, s, qd + (((t * PARTS + (pr == 1)) * SM::kQTile + (k >> 2) * (128 * 128) + 32 * (k & 3)) >> 4),
                                           kd + (((st * PARTS + (pr == 2)) * SM::kOperand + (k >> 2) * (kPage * 128) + 32 * (k & 3)) >> 4), tc_idesc(kPage),
@@ -809,14 +812,50 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                         tc_commit(on, &s_full[2 * t + buf]);
                         issued = true;
                     }
-                    if (!ok) break;
-                    tc_commit(on, &k_empty[st]);
-                    if (j > 0) ok = values_of(j - 1);
+                    if (ok) tc_commit(on, &k_empty[st]);
                 }
-                if (ok && n > 0) ok = values_of(n - 1);
                 if (!ok && issued) {  // whatever was issued ends before the block does
-                    tc_commit(on, drain);
-                    (void)mbar_wait_bounded(drain, 0, kWaitPolls);
+                    tc_commit(on, &drain[0]);
+                    (void)mbar_wait_bounded(&drain[0], 0, kWaitPolls);
+                }
+                block_sync();
+                if (*dead) break;
+                done += n;
+                if (tiles == 2) done1 += n;
+            }
+        } else if (warp == SM::kMmaWarp + 1) {
+            // --------------------------- products of values ---------------------------
+            const uint64_t vd = tc_desc(smem_u32(smem + SM::kV));
+            for (int item = blockIdx.x; item < total; item += gridDim.x) {
+                const SharedItem it = find_item(p, item, 128 * T);
+                const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
+                bool issued = false;
+                for (int j = 0; j < n && ok; ++j) {  // O (+)= P V
+                    const uint32_t g = done + j, st = g % NS;
+                    if (!(ok = wait(&v_full[st], (g / NS) & 1u))) break;
+#pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        if (t >= tiles || !ok) break;
+                        const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
+                        if (!(ok = wait(&p_full[2 * t + buf], (gt >> 1) & 1u))) break;
+                        tc_after();
+                        const uint32_t tt = tmem + t * SM::kTileCols;
+                        const uint32_t pa = tt + SM::kColP + buf * 64, o = tt + SM::kColO + (PARTS == 2 ? buf * kD : 0);
+#pragma unroll
+                        for (int pr = 0; pr < (PARTS == 1 ? 1 : 3); ++pr)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc_mma_ts(on, o, pa + (pr == 1 ? 32 : 0) + 8 * k, vd + (((st * PARTS + (pr == 2)) * SM::kOperand + 32 * k) >> 4), tc_idesc(kD),
+                                          (PARTS == 1 && j > 0) || pr > 0 || k > 0);
+                        tc_commit(on, &o_done[t]);
+                        tc_commit(on, &s_free[2 * t + buf]);
+                        issued = true;
+                    }
+                    if (ok) tc_commit(on, &v_empty[st]);
+                }
+                if (!ok && issued) {
+                    tc_commit(on, &drain[1]);
+                    (void)mbar_wait_bounded(&drain[1], 0, kWaitPolls);
                 }
                 block_sync();
                 if (*dead) break;
@@ -827,8 +866,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
             // -------------------------------- producer --------------------------------
             for (int item = blockIdx.x; item < total; item += gridDim.x) {
                 const SharedItem it = find_item(p, item, 128 * T);
-                block_sync();
-                if (warp == SM::kMmaWarp + 1) {
+                if (warp == SM::kMmaWarp + 2) {
                     int j = 0;  // pages issued
                     for (int q0 = it.pg0; q0 < it.pg1 && ok; q0 += 32) {
                         const int q = q0 + lane;
