@@ -6,11 +6,15 @@
 // The r-th greatest score is found digit by digit from the top (a radix select
 // over 11 + 11 + 10 bits of the scores' order-preserving patterns, with
 // histograms in shared memory); then every warp knows from prefix sums where its
-// kept tokens go in the ascending list.  One pass over memory: the scores stay
-// in shared memory.
+// kept tokens go in the ascending list.
 //
-// A cluster of thread blocks serves a sequence, each a contiguous part of it;
-// they add their histograms through distributed shared memory.
+// The bytes are few (4 per token read, 8 per kept token written: 2 MB, 0.3 us for
+// eight histories of 32K), so the time is latency and instructions: the patterns
+// are made once and stay in shared memory, four per access, and positions behind
+// the last are the pattern 0, below every score's, so that no loop asks for the
+// end.  A cluster of thread blocks serves a long sequence, each a contiguous part
+// of it; a histogram is added up over the cluster in two steps of 64 sums and 32
+// bins (read whole by every block, 16 KB a pass, it took 4500 of a pass's cycles).
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -26,9 +30,10 @@ constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxCached = 32768;  // scores that a block keeps in shared memory; longer parts are read again
+constexpr int kMaxCached = 32768;  // patterns that a block keeps in shared memory; longer parts are read again
+constexpr int kRunStep = 128;      // a warp's run of tokens: whole steps of four per lane
 
-// Scores in order as unsigned integers: -0 as 0, NaN above all.
+// Scores in order as unsigned integers: -0 as 0, NaN above all.  No score has the pattern 0.
 __device__ __forceinline__ uint32_t score_key(float w) {
     const uint32_t b = __float_as_uint(w + 0.f);
     if (w != w) return 0xffffffffu;
@@ -40,19 +45,45 @@ __device__ __forceinline__ uint32_t pass_mask(int pass) { return pass == 2 ? 0x3
 
 struct SelShared {
     int hist[kPasses][kBins];
-    int warp_sum[kSelWarps];
-    int2 warp_count[kSelWarps];  // (greater than the threshold, equal to it)
-    int2 count;                  // of the block, read by the others of the cluster
+    int coarse[kPasses][kBins / 32];  // sums of 32 neighbouring bins
+    int2 warp_count[kSelWarps];       // (greater than the threshold, equal to it)
+    int2 count;                       // of the block, read by the others of the cluster
     int bin, above;
 };
 
+// Of 32 lanes' numbers c, the highest bins first: the lane in whose bin the need-th
+// greatest lies, and how many lie above it.  (Called by a whole warp.)
+__device__ __forceinline__ int find_bin(int c, int need, int& above) {
+    const int lane = threadIdx.x & 31;
+    int sum = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(kFull, sum, d);
+        if (lane >= d) sum += v;
+    }
+    const int at = __ffs(__ballot_sync(kFull, sum >= need)) - 1;  // (there are that many)
+    above = __shfl_sync(kFull, sum - c, at);
+    return at;
+}
+
+// CLUSTER: several blocks per sequence; else one, with barriers and reads of its own only.
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams p, int cached) {
-    extern __shared__ __align__(16) float cacheS[];
-    __shared__ SelShared sh;
+    extern __shared__ __align__(16) uint32_t keyS[];
+    __shared__ __align__(16) SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
-    const int nblk = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int nblk = CLUSTER ? (int)cluster.num_blocks() : 1, rank = CLUSTER ? (int)cluster.block_rank() : 0;
+    auto sync_all = [&]() {
+        if constexpr (CLUSTER) cluster.sync();
+        else __syncthreads();
+    };
+    auto of_block = [&](auto* at, int r) {
+        if constexpr (CLUSTER) return cluster.map_shared_rank(at, r);
+        else return at;
+    };
     const int b = blockIdx.x / nblk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < kPasses * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(&sh.hist[0][0])[i] = make_int4(0, 0, 0, 0);
     pdl_wait();
     int n = __ldg(p.hist_len + b), m = __ldg(p.budget + b);
     if (rank == 0 && threadIdx.x == 0 && (n < 0 || n > p.stride || m < 0)) report(p.status, OSCAR_STATUS_BAD_POS);
@@ -69,57 +100,74 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
     int32_t* keep = p.keep + (size_t)b * p.keep_stride;
     float* kept = p.kept_weight ? p.kept_weight + (size_t)b * p.kept_stride : nullptr;
 
-    // this block's part: warps' contiguous runs of `run` tokens (a multiple of 32)
-    const int run = ((cand + nblk * kSelWarps - 1) / (nblk * kSelWarps) + 31) & ~31;
-    const int part0 = rank * kSelWarps * run;
+    // this block's part: warps' contiguous runs of `run` tokens
+    const int run = ((cand + nblk * kSelWarps - 1) / (nblk * kSelWarps) + kRunStep - 1) / kRunStep * kRunStep;
+    const int part0 = rank * kSelWarps * run, size = kSelWarps * run;
     const int mine0 = warp * run;                             // offset of the warp's run in the part
     const bool choose = need > 0 && need < cand;              // (the same in every block of the cluster)
-    const bool in_cache = choose && run * kSelWarps <= cached;
-    auto score = [&](int off) {                               // score of token part0 + off < cand
-        return in_cache ? cacheS[off] : __ldg(w + part0 + off);
+    const bool all = need > 0 && !choose;
+    const bool in_cache = choose && size <= cached;
+    // patterns of tokens part0 + off .. + 3 (off a multiple of four)
+    auto keys = [&](int off) {
+        if (in_cache) return *reinterpret_cast<const uint4*>(keyS + off);
+        uint32_t k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = part0 + off + i < cand ? score_key(__ldg(w + part0 + off + i)) : 0u;
+        return make_uint4(k[0], k[1], k[2], k[3]);
     };
     uint32_t prefix = 0, known = 0;                           // the threshold's digits so far, and which bits they are
     if (choose) {
-        for (int i = threadIdx.x; i < kPasses * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
         if (in_cache) {
 #pragma unroll 8
-            for (int off = threadIdx.x; off < run * kSelWarps; off += kSelThreads)
-                cacheS[off] = part0 + off < cand ? __ldg(w + part0 + off) : 0.f;
+            for (int off = threadIdx.x; off < size; off += kSelThreads)
+                keyS[off] = part0 + off < cand ? score_key(__ldg(w + part0 + off)) : 0u;
         }
         for (int pass = 0; pass < kPasses; ++pass) {
             __syncthreads();
             const int shift = pass_shift(pass);
             const uint32_t mask = pass_mask(pass);
-            for (int off = threadIdx.x; off < run * kSelWarps && part0 + off < cand; off += kSelThreads) {
-                const uint32_t k = score_key(score(off));
-                if ((k & known) == prefix) atomicAdd(&sh.hist[pass][(k >> shift) & mask], 1);
+            int* hist = sh.hist[pass];
+#pragma unroll 2
+            for (int off = 4 * threadIdx.x; off < size; off += 4 * kSelThreads) {
+                const uint4 k = keys(off);
+                if ((k.x & known) == prefix) atomicAdd(hist + ((k.x >> shift) & mask), 1);
+                if ((k.y & known) == prefix) atomicAdd(hist + ((k.y >> shift) & mask), 1);
+                if ((k.z & known) == prefix) atomicAdd(hist + ((k.z >> shift) & mask), 1);
+                if ((k.w & known) == prefix) atomicAdd(hist + ((k.w >> shift) & mask), 1);
             }
-            cluster.sync();
-            // thread t: bins 2 (1023 - t) + 1 and 2 (1023 - t), from the top, over all blocks
-            const int top = kBins - 2 - 2 * threadIdx.x;
-            int c0 = 0, c1 = 0;
-            for (int r = 0; r < nblk; ++r) {
-                const int2 v = *reinterpret_cast<const int2*>(cluster.map_shared_rank(&sh.hist[pass][top], r));
-                c0 += v.x;
-                c1 += v.y;
-            }
-            int sum = c0 + c1;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int v = __shfl_up_sync(kFull, sum, d);
-                if (lane >= d) sum += v;
-            }
-            if (lane == 31) sh.warp_sum[warp] = sum;
             __syncthreads();
-            int before = lane < warp ? sh.warp_sum[lane] : 0;
-            before = __reduce_add_sync(kFull, before);
-            const int above = before + sum - c0 - c1;         // scores above this thread's bins
-            if (above < need && above + c1 >= need) {
-                sh.bin = top + 1;
-                sh.above = above;
-            } else if (above + c1 < need && above + c1 + c0 >= need) {
-                sh.bin = top;
-                sh.above = above + c1;
+            {   // sums of 32 bins: a half warp each
+                const int2 v = *reinterpret_cast<const int2*>(hist + 64 * warp + 2 * lane);
+                int sum = v.x + v.y;
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+                if ((lane & 15) == 0) sh.coarse[pass][2 * warp + (lane >> 4)] = sum;
+            }
+            sync_all();
+            if (warp == 0) {
+                // over all blocks: first the 64 sums (two a lane), then the 32 bins of one
+                int2 c = make_int2(0, 0);
+#pragma unroll
+                for (int r = 0; r < (CLUSTER ? kMaxCluster : 1); ++r) {
+                    const int2 v = r < nblk ? *reinterpret_cast<const int2*>(of_block(&sh.coarse[pass][62 - 2 * lane], r)) : make_int2(0, 0);
+                    c.x += v.x;
+                    c.y += v.y;
+                }
+                int above;
+                const int at = find_bin(c.x + c.y, need, above);
+                const int upper = __shfl_sync(kFull, c.y, at);  // (the higher of the lane's two)
+                const bool low = above + upper < need;
+                if (low) above += upper;
+                const int bins = 32 * (62 - 2 * at + (low ? 0 : 1));
+                int f = 0;
+#pragma unroll
+                for (int r = 0; r < (CLUSTER ? kMaxCluster : 1); ++r) f += r < nblk ? *of_block(&sh.hist[pass][bins + 31 - lane], r) : 0;
+                int fine;
+                const int bin = bins + 31 - find_bin(f, need - above, fine);
+                if (lane == 0) {
+                    sh.bin = bin;
+                    sh.above = above + fine;
+                }
             }
             __syncthreads();
             prefix |= (uint32_t)sh.bin << shift;
@@ -129,16 +177,15 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
     }
     // threshold `prefix`: every greater score stays, and the first `need` equal ones;
     // without a choice all or none do
-    const bool all = need > 0 && !choose;
     int gt = 0, eq = 0;
-    for (int off = mine0 + lane; off < mine0 + run; off += 32) {
-        if (part0 + off >= cand) break;
-        if (all) {
-            ++gt;
-        } else if (choose) {
-            const uint32_t k = score_key(score(off));
-            gt += k > prefix;
-            eq += k == prefix;
+    if (all) {
+        gt = lane == 0 ? max(0, min(run, cand - part0 - mine0)) : 0;
+    } else if (choose) {
+#pragma unroll 2
+        for (int off = mine0 + 4 * lane; off < mine0 + run; off += kRunStep) {
+            const uint4 k = keys(off);
+            gt += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+            eq += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
         }
     }
     gt = __reduce_add_sync(kFull, gt);
@@ -150,34 +197,58 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
         const int2 c = sh.warp_count[lane];
         gt0 = __reduce_add_sync(kFull, lane < warp ? c.x : 0);
         eq0 = __reduce_add_sync(kFull, lane < warp ? c.y : 0);
-        if (warp == 0) {
+        if (CLUSTER && warp == 0) {
             const int g = __reduce_add_sync(kFull, c.x), e = __reduce_add_sync(kFull, c.y);
             if (lane == 0) sh.count = make_int2(g, e);
         }
     }
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        const int2 c = *cluster.map_shared_rank(&sh.count, r);
-        gt0 += c.x;
-        eq0 += c.y;
+    if constexpr (CLUSTER) {
+        cluster.sync();
+        const int2 c = lane < rank ? *cluster.map_shared_rank(&sh.count, lane) : make_int2(0, 0);
+        gt0 += __reduce_add_sync(kFull, c.x);
+        eq0 += __reduce_add_sync(kFull, c.y);
+        cluster.barrier_arrive();  // (no block leaves while another reads its shared memory: see the end)
     }
-    cluster.sync();  // no block leaves while another reads its shared memory
-    const uint32_t below = (1u << lane) - 1u;
-    if (all || choose) {
-        for (int off = mine0 + lane; off - lane < mine0 + run && part0 + off - lane < cand; off += 32) {
-            const bool in = part0 + off < cand;
-            const float x = in ? score(off) : 0.f;
-            const uint32_t k = score_key(x);
-            const bool g = in && (all || k > prefix), e = in && !all && k == prefix;
-            const uint32_t gm = __ballot_sync(kFull, g), em = __ballot_sync(kFull, e);
-            const int eq_before = eq0 + __popc(em & below);
-            if (g || (e && eq_before < need)) {
-                const int to = gt0 + __popc(gm & below) + min(eq_before, need);
-                keep[to] = part0 + off;
-                if (kept) kept[to] = x;
+    if (all) {
+        for (int i = mine0 + lane; i < mine0 + gt; i += 32) {
+            keep[part0 + i] = part0 + i;
+            if (kept) kept[part0 + i] = __ldg(w + part0 + i);
+        }
+    } else if (choose) {
+#pragma unroll 2
+        for (int off0 = mine0; off0 < mine0 + run; off0 += kRunStep) {
+            const int off = off0 + 4 * lane;
+            const uint4 kv = keys(off);
+            const uint32_t k[4] = {kv.x, kv.y, kv.z, kv.w};
+            int g = 0, e = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g += k[i] > prefix;
+                e += k[i] == prefix;
             }
-            gt0 += __popc(gm);
-            eq0 += __popc(em);
+            // both counts of the lanes below in one scan (at most 128 each)
+            const int mine = g | (e << 16);
+            int sum = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(kFull, sum, d);
+                if (lane >= d) sum += v;
+            }
+            const int total = __shfl_sync(kFull, sum, 31), before = sum - mine;
+            int gb = gt0 + (before & 0xffff), eb = eq0 + (before >> 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool is_g = k[i] > prefix, is_e = k[i] == prefix;
+                if (is_g || (is_e && eb < need)) {
+                    const int to = gb + min(eb, need);
+                    keep[to] = part0 + off + i;
+                    if (kept) kept[to] = __ldg(w + part0 + off + i);
+                }
+                gb += is_g;
+                eb += is_e;
+            }
+            gt0 += total & 0xffff;
+            eq0 += total >> 16;
         }
     }
     for (int i = rank * kSelThreads + threadIdx.x; i < newest; i += nblk * kSelThreads) {
@@ -185,6 +256,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
         if (kept) kept[m - newest + i] = w[cand + i];
     }
     if (rank == 0 && threadIdx.x == 0) p.n_keep[b] = m;
+    if constexpr (CLUSTER) cluster.barrier_wait();
 }
 
 }  // namespace
@@ -195,7 +267,8 @@ cudaError_t launch_history_select(const HistorySelectParams& p, cudaStream_t st)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (!attr_set[dev & 63]) {
-        e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
+        e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
         if (e != cudaSuccess) return e;
         attr_set[dev & 63] = true;
     }
@@ -204,8 +277,8 @@ cudaError_t launch_history_select(const HistorySelectParams& p, cudaStream_t st)
     int blocks = 1;
     while (blocks < kMaxCluster && p.stride > 4096 * blocks && (int64_t)p.batch * blocks * 2 <= 304) blocks *= 2;
     while (blocks < kMaxCluster && p.stride > kMaxCached * blocks) blocks *= 2;
-    const int per_block = ((p.stride + blocks * kSelWarps - 1) / (blocks * kSelWarps) + 31) / 32 * 32 * kSelWarps;
-    const int cached = std::min(per_block, kMaxCached);
+    const int64_t per_block = (((int64_t)p.stride + blocks * kSelWarps - 1) / (blocks * kSelWarps) + kRunStep - 1) / kRunStep * kRunStep * kSelWarps;
+    const int cached = (int)std::min<int64_t>(per_block, kMaxCached);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.batch * blocks));
     cfg.blockDim = dim3(kSelThreads);
@@ -218,8 +291,8 @@ cudaError_t launch_history_select(const HistorySelectParams& p, cudaStream_t st)
     attr[1].val.clusterDim.x = blocks;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, select_kernel, p, cached);
+    cfg.numAttrs = blocks > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, blocks > 1 ? select_kernel<true> : select_kernel<false>, p, cached);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
