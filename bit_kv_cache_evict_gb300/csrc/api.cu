@@ -582,7 +582,7 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
                                   void* stream) {
     constexpr int32_t kMost = INT32_MAX - (1 << 16);  // positions rounded up to a thread block's parts are int32
     if (batch < 0 || weight_stride < 0 || weight_stride > kMost || protect < 0 || keep_stride < 0 || kept_stride < 0 ||
-        batch > INT32_MAX / 8)
+        batch > INT32_MAX / 16)
         return OSCAR_ERR_INVALID_ARG;
     if (batch == 0) return OSCAR_OK;
     if (!hist_len || !budget || !n_keep || (weight_stride > 0 && !weight) || (keep_stride > 0 && !keep))

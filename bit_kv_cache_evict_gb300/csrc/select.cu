@@ -13,8 +13,9 @@
 // are made once and stay in shared memory, four per access, and positions behind
 // the last are the pattern 0, below every score's, so that no loop asks for the
 // end.  A cluster of thread blocks serves a long sequence, each a contiguous part
-// of it; a histogram is added up over the cluster in two steps of 64 sums and 32
-// bins (read whole by every block, 16 KB a pass, it took 4500 of a pass's cycles).
+// of it; a histogram is added up over the cluster in two steps, 64 sums that every
+// block stores to every other, then 32 bins that a warp each reads (the whole of it
+// read by every block took 4500 cycles a pass, these two about 1000).
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -29,7 +30,7 @@ namespace {
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPasses = 3;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;   // 8 where the GPU has no room for clusters of 16
 constexpr int kMaxCached = 32768;  // patterns that a block keeps in shared memory; longer parts are read again
 constexpr int kRunStep = 128;      // a warp's run of tokens: whole steps of four per lane
 
@@ -40,12 +41,16 @@ __device__ __forceinline__ uint32_t score_key(float w) {
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+__device__ __forceinline__ float key_score(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu)); }
+
 __device__ __forceinline__ int pass_shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
 __device__ __forceinline__ uint32_t pass_mask(int pass) { return pass == 2 ? 0x3ffu : 0x7ffu; }
 
+static_assert(kMaxCluster <= 16, "a half warp's lanes store to the blocks");
 struct SelShared {
     int hist[kPasses][kBins];
-    int coarse[kPasses][kBins / 32];  // sums of 32 neighbouring bins
+    int coarse[kPasses][kMaxCluster][kBins / 32];  // sums of 32 neighbouring bins, of every block
+    int fine[kMaxCluster][32];                     // the 32 bins of one, of every block
     int2 warp_count[kSelWarps];       // (greater than the threshold, equal to it)
     int2 count;                       // of the block, read by the others of the cluster
     int bin, above;
@@ -68,7 +73,7 @@ __device__ __forceinline__ int find_bin(int c, int need, int& above) {
 
 // CLUSTER: several blocks per sequence; else one, with barriers and reads of its own only.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams p, int cached) {
+__global__ void __launch_bounds__(kSelThreads, 2) select_kernel(HistorySelectParams p, int cached) {
     extern __shared__ __align__(16) uint32_t keyS[];
     __shared__ __align__(16) SelShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -84,6 +89,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
     const int b = blockIdx.x / nblk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int i = threadIdx.x; i < kPasses * kBins / 4; i += kSelThreads) reinterpret_cast<int4*>(&sh.hist[0][0])[i] = make_int4(0, 0, 0, 0);
+    if constexpr (CLUSTER) cluster.barrier_arrive();  // (every block runs before another stores to it)
     pdl_wait();
     int n = __ldg(p.hist_len + b), m = __ldg(p.budget + b);
     if (rank == 0 && threadIdx.x == 0 && (n < 0 || n > p.stride || m < 0)) report(p.status, OSCAR_STATUS_BAD_POS);
@@ -115,6 +121,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
         for (int i = 0; i < 4; ++i) k[i] = part0 + off + i < cand ? score_key(__ldg(w + part0 + off + i)) : 0u;
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
+    if constexpr (CLUSTER) cluster.barrier_wait();
     uint32_t prefix = 0, known = 0;                           // the threshold's digits so far, and which bits they are
     if (choose) {
         if (in_cache) {
@@ -141,27 +148,30 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
                 int sum = v.x + v.y;
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-                if ((lane & 15) == 0) sh.coarse[pass][2 * warp + (lane >> 4)] = sum;
+                if ((lane & 15) < nblk) of_block(&sh.coarse[pass][rank][2 * warp + (lane >> 4)], lane & 15)[0] = sum;
             }
             sync_all();
-            if (warp == 0) {
-                // over all blocks: first the 64 sums (two a lane), then the 32 bins of one
+            // the 64 sums over all blocks, two a lane from the top; then the 32 bins of one: a
+            // warp for each block's
+            int above = 0, bins = 0;
+            if (warp < nblk) {
                 int2 c = make_int2(0, 0);
-#pragma unroll
-                for (int r = 0; r < (CLUSTER ? kMaxCluster : 1); ++r) {
-                    const int2 v = r < nblk ? *reinterpret_cast<const int2*>(of_block(&sh.coarse[pass][62 - 2 * lane], r)) : make_int2(0, 0);
+                for (int r = 0; r < nblk; ++r) {
+                    const int2 v = *reinterpret_cast<const int2*>(&sh.coarse[pass][r][62 - 2 * lane]);
                     c.x += v.x;
                     c.y += v.y;
                 }
-                int above;
                 const int at = find_bin(c.x + c.y, need, above);
                 const int upper = __shfl_sync(kFull, c.y, at);  // (the higher of the lane's two)
                 const bool low = above + upper < need;
                 if (low) above += upper;
-                const int bins = 32 * (62 - 2 * at + (low ? 0 : 1));
+                bins = 32 * (62 - 2 * at + (low ? 0 : 1));
+                sh.fine[warp][lane] = *of_block(&sh.hist[pass][bins + 31 - lane], warp);
+            }
+            if (CLUSTER) __syncthreads();
+            if (warp == 0) {
                 int f = 0;
-#pragma unroll
-                for (int r = 0; r < (CLUSTER ? kMaxCluster : 1); ++r) f += r < nblk ? *of_block(&sh.hist[pass][bins + 31 - lane], r) : 0;
+                for (int r = 0; r < nblk; ++r) f += sh.fine[r][lane];
                 int fine;
                 const int bin = bins + 31 - find_bin(f, need - above, fine);
                 if (lane == 0) {
@@ -242,7 +252,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
                 if (is_g || (is_e && eb < need)) {
                     const int to = gb + min(eb, need);
                     keep[to] = part0 + off + i;
-                    if (kept) kept[to] = __ldg(w + part0 + off + i);
+                    // (the pattern gives the score back, but for the sign of a zero and a NaN's bits)
+                    if (kept) kept[to] = k[i] == 0x80000000u || k[i] == 0xffffffffu ? __ldg(w + part0 + off + i) : key_score(k[i]);
                 }
                 gb += is_g;
                 eb += is_e;
@@ -262,35 +273,45 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(HistorySelectParams
 }  // namespace
 
 cudaError_t launch_history_select(const HistorySelectParams& p, cudaStream_t st) {
-    static bool attr_set[64];
+    static int most_blocks[64];  // of a cluster on each device; 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (!attr_set[dev & 63]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    if (!most_blocks[dev & 63]) {
         e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        attr_set[dev & 63] = true;
+        int clusters = 0;
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.dynamicSmemBytes = kMaxCached * 4;
+        attr[0].val.clusterDim.x = kMaxCluster;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&clusters, select_kernel<true>, &cfg);
+        if (e != cudaSuccess) (void)cudaGetLastError();  // (an answer too: none)
+        most_blocks[dev & 63] = e == cudaSuccess && clusters > 0 ? kMaxCluster : kMaxCluster / 2;
     }
+    const int most = most_blocks[dev & 63];
     // Blocks per sequence: one for every 4096 tokens, as far as the blocks of the
     // batch still run side by side (two per SM).
     int blocks = 1;
-    while (blocks < kMaxCluster && p.stride > 4096 * blocks && (int64_t)p.batch * blocks * 2 <= 304) blocks *= 2;
-    while (blocks < kMaxCluster && p.stride > kMaxCached * blocks) blocks *= 2;
+    while (blocks < most && p.stride > 4096 * blocks && (int64_t)p.batch * blocks * 2 <= 304) blocks *= 2;
+    while (blocks < most && p.stride > kMaxCached * blocks) blocks *= 2;
     const int64_t per_block = (((int64_t)p.stride + blocks * kSelWarps - 1) / (blocks * kSelWarps) + kRunStep - 1) / kRunStep * kRunStep * kSelWarps;
     const int cached = (int)std::min<int64_t>(per_block, kMaxCached);
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.batch * blocks));
-    cfg.blockDim = dim3(kSelThreads);
     cfg.dynamicSmemBytes = (size_t)cached * 4;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = blocks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
+    attr[0].val.clusterDim.x = blocks;
+    cfg.attrs = blocks > 1 ? attr : attr + 1;
     cfg.numAttrs = blocks > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, blocks > 1 ? select_kernel<true> : select_kernel<false>, p, cached);
     return e != cudaSuccess ? e : cudaGetLastError();
