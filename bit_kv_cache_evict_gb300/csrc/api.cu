@@ -70,7 +70,7 @@ static int tail_pages_of(int pps) { return pps > kShortItemPages ? 2 * kShortIte
 struct WsLayout {
     size_t counter, item_start, item_start2, qfrag, qsum, qkinv, qrot, part, bf_part, total;
     size_t logits, slot_logits, norm;  // kModeWeights
-    size_t skip, sref, member, groups, qrow, sh_part;  // kModeShared
+    size_t skip, sref, qref, items, qtile, qtile_kinv, sh_part;  // kModeShared
     int NT, pps, tail_pg, part_stride, parts;  // parts: partials per item
     int64_t max_items;   // split-K items at most (int64: batch x KV heads x splits can exceed int32)
 };
@@ -94,11 +94,18 @@ static int64_t items4_bound(int64_t pairs, int max_pages) {
 //   one item for each block at most; or, where whole groups are more, four times
 //   that and one per KV head and row tile for the rounding; runs have
 //   kMinSharedPages pages at least but for one per group and KV head.
+// Row tiles: each group's last one may be partly filled; groups have two members at least.
+static int64_t shared_tiles_bound(const oscar_shape* s, int batch, int n_groups) {
+    const int64_t hk = s->num_kv_heads, G = s->num_q_heads / hk, groups = std::min(n_groups, batch / 2);
+    return groups ? hk * ((batch * G + 127) / 128 + groups) : 0;
+}
+static int64_t shared_items_bound(const oscar_shape* s, int batch, int n_groups) {
+    const int64_t tiles = shared_tiles_bound(s, batch, n_groups);
+    return tiles ? 17 * kMaxSharedBlocks / 4 + tiles : 0;  // (runs of 16 pages at least, rounded down)
+}
 static int64_t shared_parts_bound(const oscar_shape* s, int batch, int max_pages, int n_groups) {
     const int64_t hk = s->num_kv_heads, G = s->num_q_heads / hk, rows = 256;
-    const int64_t tiles = (batch * G + 127) / 128 + std::min(n_groups, batch / 2 + 1);
-    const int64_t items = 17 * kMaxSharedBlocks / 4 + hk * tiles;  // (runs of 16 pages at least, rounded down)
-    return std::min(items * (rows / G), batch * hk * ((max_pages + kMinSharedPages - 1) / kMinSharedPages));
+    return std::min(shared_items_bound(s, batch, n_groups) * (rows / G), batch * hk * ((max_pages + kMinSharedPages - 1) / kMinSharedPages));
 }
 
 static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bits, Mode mode = kModePlain, int n_groups = 0) {
@@ -147,12 +154,14 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bi
         off = round_up(off + (size_t)batch * 4, 256);
         w.sref = off;
         off = round_up(off + (size_t)batch * 16, 256);
-        w.member = off;
-        off = round_up(off + (size_t)batch * 4, 256);
-        w.groups = off;
-        off = round_up(off + (size_t)n_groups * sizeof(SharedGroup), 256);
-        w.qrow = off;
-        off = round_up(off + (size_t)2 * batch * s->num_q_heads * kD * 2, 256);
+        w.qref = off;
+        off = round_up(off + (size_t)batch * 16, 256);
+        w.items = off;
+        off = round_up(off + (size_t)shared_items_bound(s, batch, n_groups) * sizeof(SharedItem), 256);
+        w.qtile = off;
+        off = round_up(off + (size_t)shared_tiles_bound(s, batch, n_groups) * 2 * kQTileBytes, 256);
+        w.qtile_kinv = off;
+        off = round_up(off + (size_t)shared_tiles_bound(s, batch, n_groups) * 128 * 4, 256);
         w.sh_part = off;
         off = round_up(off + (size_t)shared_parts_bound(s, batch, max_pages, n_groups) * w.part_stride * 4, 256);
     }
@@ -473,9 +482,10 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
         x.n_groups = extra->n_groups;
         x.skip = reinterpret_cast<int32_t*>(ws + w.skip);
         x.sref = reinterpret_cast<int4*>(ws + w.sref);
-        x.member = reinterpret_cast<int32_t*>(ws + w.member);
-        x.groups = reinterpret_cast<SharedGroup*>(ws + w.groups);
-        x.qrow = reinterpret_cast<uint16_t*>(ws + w.qrow);
+        x.qref = reinterpret_cast<int4*>(ws + w.qref);
+        x.items = reinterpret_cast<SharedItem*>(ws + w.items);
+        x.qtile = ws + w.qtile;
+        x.qtile_kinv = reinterpret_cast<float*>(ws + w.qtile_kinv);
         x.sh_part = reinterpret_cast<float*>(ws + w.sh_part);
         const cudaStream_t st = static_cast<cudaStream_t>(stream);
         const cudaError_t e = mode == kModeWeights ? launch_decode_weights(x, bits, st) : launch_decode_shared(x, bits, st);

@@ -336,10 +336,18 @@ __device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
         const float v[4] = {qs[base] * up, qs[base + second] * up, qs[base + 1] * up, qs[base + second + 1] * up};
         uint32_t h01, h23, l01, l23;
         split_f16(v, h01, h23, l01, l23);
-        if constexpr (MODE == kModeShared) {  // the row of the shared pages' products, positions in the same order
-            uint16_t* row = const_cast<uint16_t*>(p.qrow) + ((size_t)b * p.hq + kv * p.G + hl) * kD + 8 * (4 * (ks >> 1) + tq) + 4 * (ks & 1);
-            *reinterpret_cast<uint2*>(row) = make_uint2(h01, h23);
-            *reinterpret_cast<uint2*>(row + (size_t)p.B * p.hq * kD) = make_uint2(l01, l23);
+        if constexpr (MODE == kModeShared) {
+            // the row of the shared pages' products, its positions in the same order, in the swizzled
+            // layout that they read: 16-byte chunk c of row r at chunk c ^ (r & 7) of a 128-byte row
+            const int4 ref = __ldg(p.qref + b);
+            if (ref.x >= 0) {
+                const int r = ref.z * p.G + hl, rr = r & 127, c = 4 * (ks >> 1) + tq;
+                const size_t tile = (size_t)ref.x + kv * ref.y + (r >> 7);
+                uint8_t* at = p.qtile + tile * 2 * kQTileBytes + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4) + 8 * (ks & 1);
+                *reinterpret_cast<uint2*>(at) = make_uint2(h01, h23);
+                *reinterpret_cast<uint2*>(at + kQTileBytes) = make_uint2(l01, l23);
+                if (lane == 0) p.qtile_kinv[tile * 128 + rr] = __uint_as_float((uint32_t)(127 - e) << 23);
+            }
         }
         if (p.NT == 2) {
             // eight heads: column = head, hi and lo parts in two fragment sets

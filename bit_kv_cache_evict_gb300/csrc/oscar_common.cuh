@@ -423,8 +423,12 @@ constexpr int kSharedItems = 10;        // index of the shared pages' item count
 constexpr int kMinSharedPages = 4;      // pages of an item of a group at least (but for its last)
 constexpr int kMaxSharedGroups = 8192;
 constexpr int kMaxSharedBlocks = 160;   // thread blocks of shared_kernel, one per SM, at most
-struct SharedGroup {
-    int pages, members, first_member, splits, first_part, first_item, tiles, pad;
+constexpr int kQTileBytes = 128 * kD * 2;  // a tile of 128 rows of fp16 q', as the products read it
+// An item of shared_kernel: up to 256 (bf16 output) or 128 rows of a group and KV
+// head against a run of its pages.
+struct __align__(16) SharedItem {
+    int seq, kv, pg0, pages;        // the group's first sequence (its page-table row), the run
+    int rows, row0, qtile, part0;   // rows, the first one's number in the group, its tile of q', first partial of the run
 };
 
 // The parameters of the chains of the last two modes, for 2 and 4 bits.
@@ -442,9 +446,10 @@ struct DecodeParamsX : DecodeParams4 {
     const int32_t* group_pages;   // [n_groups] first pages that a group shares
     int32_t* skip;                // [B] pages that the sequence's group attends
     int4* sref;                   // [B] its partials of them: (first, splits, members, index)
-    int32_t* member;              // [B] sequences by group
-    SharedGroup* groups;          // [n_groups]
-    const uint16_t* qrow;         // [2][B*Hq][kD] fp16 q' (times 2^e), high and low parts, in the products' order
+    int4* qref;                   // [B] its rows of q': (first tile of KV head 0 or -1, tiles per KV head, index, 0)
+    SharedItem* items;
+    uint8_t* qtile;               // [tiles][2] kQTileBytes: fp16 q' (times 2^e), high and low parts
+    float* qtile_kinv;            // [tiles][128] 2^-e of each row
     float* sh_part;               // partials [part_stride]: (KV head, split, member) of each group
     int n_groups, shared_blocks;
 };

@@ -39,31 +39,40 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMinMembers = 2;  // smaller groups attend by themselves
 
 // One block.  skip[b]: pages of sequence b that its group attends; sref[b]: its
-// partials (first, splits, members, index); the groups' items.
+// partials (first, splits, members, index); qref[b]: its rows of q'; and the items.
 __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, int rows) {
     extern __shared__ int32_t gsm[];
-    int32_t* count = gsm;                 // [n_groups] members
-    int32_t* first = gsm + p.n_groups;    // [n_groups] first member's place
+    int32_t* count = gsm;                          // [n_groups] members; 0 for a group that is not attended together
+    int32_t* pages = count + p.n_groups;           // [n_groups]
+    int32_t* first_item = pages + p.n_groups;      // [n_groups]
+    int32_t* first_part = first_item + p.n_groups;
+    int32_t* first_tile = first_part + p.n_groups;
+    int32_t* first_seq = first_tile + p.n_groups;  // whose page-table row tells the group's pages
     __shared__ int32_t chunk_group[kPlanThreads], chunk_index[kPlanThreads];
+    __shared__ int sh_pps, sh_total;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) count[g] = 0;
     pdl_wait();
     pdl_trigger();
-    auto pages_of = [&](int g) { return min(max(__ldg(p.group_pages + g), 0), p.max_pages); };
+    int g_first = threadIdx.x < p.B ? __ldg(p.prefix_group + threadIdx.x) : -1;  // (one round trip for all three)
+    int h_first = threadIdx.x < p.B ? __ldg(p.hist_len + threadIdx.x) : 0;
+    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+        const int raw = __ldg(p.group_pages + g), n = min(max(raw, 0), p.max_pages);
+        if (raw != n) report(p.status, OSCAR_STATUS_BAD_POS);
+        count[g] = 0;
+        pages[g] = n;
+    }
+    __syncthreads();
     // members in order of their sequences, by warp 0 (one order, whatever the launch)
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
-        int g = b < p.B ? __ldg(p.prefix_group + b) : -1;
+        int g = b0 == 0 ? g_first : b < p.B ? __ldg(p.prefix_group + b) : -1;
+        const int h = b0 == 0 ? h_first : b < p.B ? __ldg(p.hist_len + b) : 0;
         if (g >= p.n_groups) {
             report(p.status, OSCAR_STATUS_BAD_POS);
             g = -1;
         }
-        if (g >= 0) {
-            const int raw = __ldg(p.group_pages + g), pages = pages_of(g);
-            if (raw != pages) report(p.status, OSCAR_STATUS_BAD_POS);
-            const int hist = min(max(__ldg(p.hist_len + b), 0), p.max_pages * kPage);
-            if (pages == 0 || hist / kPage < pages) g = -1;  // (a history that ends inside the prefix goes by itself)
-        }
+        // (a history that ends inside the prefix goes by itself)
+        if (g >= 0 && (pages[g] == 0 || min(max(h, 0), p.max_pages * kPage) / kPage < pages[g])) g = -1;
         chunk_group[threadIdx.x] = g;
         __syncthreads();
         if (warp == 0) {
@@ -71,8 +80,7 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
                 const int gg = chunk_group[i + lane];
                 const unsigned peers = __match_any_sync(kFull, gg);
                 const int rank = __popc(peers & ((1u << lane) - 1u));
-                int base = 0;
-                if (gg >= 0) base = count[gg];
+                const int base = gg >= 0 ? count[gg] : 0;
                 chunk_index[i + lane] = base + rank;
                 __syncwarp();
                 if (gg >= 0 && rank == 0) count[gg] = base + __popc(peers);
@@ -82,88 +90,104 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
         __syncthreads();
         if (b < p.B) p.sref[b] = make_int4(0, 0, chunk_group[threadIdx.x], chunk_index[threadIdx.x]);
     }
+    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads)
+        if (count[g] < kMinMembers) count[g] = 0;
     __syncthreads();
-    auto tiles_of = [&](int g) {  // row tiles of a group; 0: it is not attended together
-        const int n = count[g];
-        return n >= kMinMembers ? (n * p.G + rows - 1) / rows : 0;
-    };
+    auto row_tiles = [&](int g, int of) { return (count[g] * p.G + of - 1) / of; };
     if (warp == 0) {
         // Pages per item: the smallest number that leaves at most one item for each
         // block; where even whole groups are more, a quarter of a block's share.
-        auto sum_over = [&](auto f) {
-            long n = 0;
-            for (int g = lane; g < p.n_groups; g += 32) n += f(g);
-#pragma unroll
-            for (int m = 16; m > 0; m >>= 1) n += __shfl_xor_sync(kFull, n, m);
-            return n;
-        };
-        auto items_at = [&](int pps) {
-            return sum_over([&](int g) { return (long)tiles_of(g) * ((pages_of(g) + pps - 1) / pps); }) * p.hk;
+        auto items_at = [&](int pps) {  // (each group's share is cut off far above what it is compared with)
+            unsigned n = 0;
+            for (int g = lane; g < p.n_groups; g += 32)
+                n += (unsigned)min((long)row_tiles(g, rows) * ((pages[g] + pps - 1) / pps) * p.hk, 1l << 16);
+            return __reduce_add_sync(kFull, n);
         };
         int lo = kMinSharedPages, hi = max(lo, p.max_pages);
         int pps;
-        if (items_at(hi) <= p.shared_blocks) {
+        if (items_at(hi) <= (unsigned)p.shared_blocks) {
             while (lo < hi) {
                 const int mid = lo + (hi - lo) / 2;
-                if (items_at(mid) <= p.shared_blocks) hi = mid;
+                if (items_at(mid) <= (unsigned)p.shared_blocks) hi = mid;
                 else lo = mid + 1;
             }
             pps = lo;
         } else {
-            const long total = sum_over([&](int g) { return (long)tiles_of(g) * pages_of(g); }) * p.hk;
-            pps = (int)max((long)kMinItemPages4, min((long)p.max_pages, total / (4 * p.shared_blocks)));
+            long total = 0;
+            for (int g = lane; g < p.n_groups; g += 32) total += (long)row_tiles(g, rows) * pages[g];
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+            pps = (int)max((long)kMinItemPages4, min((long)p.max_pages, total * p.hk / (4 * p.shared_blocks)));
         }
-        int run_member = 0, run_part = 0, run_item = 0;
+        int run_part = 0, run_item = 0, run_tile = 0;
         for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
             const int g = g0 + lane;
-            const int tiles = g < p.n_groups ? tiles_of(g) : 0;
-            const int members = tiles ? count[g] : 0, pages = tiles ? pages_of(g) : 0;
-            const int splits = (pages + pps - 1) / pps;
-            int m = members, pt = splits * members * p.hk, it = splits * tiles * p.hk;
+            const bool on = g < p.n_groups && count[g] > 0;
+            const int splits = on ? (pages[g] + pps - 1) / pps : 0;
+            const int np = on ? splits * count[g] * p.hk : 0, ni = on ? splits * row_tiles(g, rows) * p.hk : 0;
+            const int nt = on ? row_tiles(g, 128) * p.hk : 0;
+            int pt = np, it = ni, qt = nt;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int a = __shfl_up_sync(kFull, m, d), b = __shfl_up_sync(kFull, pt, d), c = __shfl_up_sync(kFull, it, d);
+                const int x = __shfl_up_sync(kFull, pt, d), y = __shfl_up_sync(kFull, it, d), z = __shfl_up_sync(kFull, qt, d);
                 if (lane >= d) {
-                    m += a;
-                    pt += b;
-                    it += c;
+                    pt += x;
+                    it += y;
+                    qt += z;
                 }
             }
             if (g < p.n_groups) {
-                first[g] = run_member + m - members;
-                SharedGroup gi;
-                gi.pages = pages;
-                gi.members = members;
-                gi.first_member = first[g];
-                gi.splits = splits;
-                gi.first_part = run_part + pt - splits * members * p.hk;
-                gi.first_item = run_item + it - splits * tiles * p.hk;
-                gi.tiles = tiles;
-                gi.pad = 0;
-                p.groups[g] = gi;
+                first_part[g] = run_part + pt - np;
+                first_item[g] = run_item + it - ni;
+                first_tile[g] = run_tile + qt - nt;
             }
-            run_member += __shfl_sync(kFull, m, 31);
             run_part += __shfl_sync(kFull, pt, 31);
             run_item += __shfl_sync(kFull, it, 31);
+            run_tile += __shfl_sync(kFull, qt, 31);
         }
         if (lane == 0) {
             p.counter[kSharedItems] = run_item;
+            sh_pps = pps;
+            sh_total = run_item;
         }
     }
     __syncthreads();
+    const int pps = sh_pps, total = sh_total;
     for (int b = threadIdx.x; b < p.B; b += kPlanThreads) {
         const int4 r = p.sref[b];
         const int g = r.z;
-        int4 out = make_int4(0, 0, 0, 0);
+        int4 part = make_int4(0, 0, 0, 0), q = make_int4(-1, 0, 0, 0);
         int skip = 0;
-        if (g >= 0 && tiles_of(g) > 0) {
-            const SharedGroup gi = p.groups[g];
-            p.member[gi.first_member + r.w] = b;
-            out = make_int4(gi.first_part, gi.splits, gi.members, r.w);
-            skip = gi.pages;
+        if (g >= 0 && count[g] > 0) {
+            part = make_int4(first_part[g], (pages[g] + pps - 1) / pps, count[g], r.w);
+            q = make_int4(first_tile[g], row_tiles(g, 128), r.w, 0);
+            skip = pages[g];
+            if (r.w == 0) first_seq[g] = b;
         }
-        p.sref[b] = out;
+        p.sref[b] = part;
+        p.qref[b] = q;
         p.skip[b] = skip;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kPlanThreads) {
+        int lo = 0, hi = p.n_groups;  // the last group that starts at or before item i and has items
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first_item[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int splits = (pages[lo] + pps - 1) / pps, rel = i - first_item[lo];
+        const int split = rel % splits, kv = rel / splits % p.hk, rt = rel / splits / p.hk;
+        SharedItem it;
+        it.seq = first_seq[lo];
+        it.kv = kv;
+        it.pg0 = (int)((long)pages[lo] * split / splits);
+        it.pages = (int)((long)pages[lo] * (split + 1) / splits) - it.pg0;
+        it.row0 = rt * rows;
+        it.rows = min(rows, count[lo] * p.G - it.row0);
+        it.qtile = first_tile[lo] + kv * row_tiles(lo, 128) + rt * (rows / 128);
+        it.part0 = first_part[lo] + (kv * splits + split) * count[lo];
+        p.items[i] = it;
     }
 }
 
@@ -297,7 +321,7 @@ struct SharedSmem {
     static constexpr int kRawStages = PARTS == 1 ? 4 : 2;
     static constexpr int kStages = 2;                   // dequantised pages
     static constexpr int kOperand = kPage * kD * 2;     // fp16 K (or V) of a page
-    static constexpr int kQTile = 128 * kD * 2;
+    static constexpr int kQTile = kQTileBytes;
     static constexpr int kQ = 0;                        // [T][PARTS] tiles, each two atoms [128 rows][128 bytes]
     static constexpr int kK = kQ + T * PARTS * kQTile;  // [kStages][PARTS], each two atoms [64 rows][128 bytes]
     static constexpr int kV = kK + kStages * PARTS * kOperand;  // [kStages][PARTS] [128 rows][128 bytes]
@@ -306,7 +330,7 @@ struct SharedSmem {
     static constexpr int kPairGroups = BITS == 4 ? 1 : 4;      // groups that a warp's rows of V belong to, at most
     static constexpr int kPairBytes = kPairGroups * 2 * kPage * 2;
     static constexpr int kBars = kPairs + kDequantWarps * kPairBytes;
-    static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 6 + T + 3;
+    static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 6 + 3;
     static constexpr int kBytes = kBars + kNumBars * 8 + 32;
     static constexpr int kAlloc = kBytes + 1024;        // the swizzled operands start on 1024 bytes
     static_assert(kAlloc <= 227 * 1024, "shared memory of a block");
@@ -340,38 +364,24 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // with 8 every second page of logits of deviation 5 did, at 2000 cycles each.
 constexpr float kSlack = 15.f;
 
-// An item: a group's KV head, row tile(s) and run of pages.
-struct SharedItem {
-    SharedGroup g;
-    const int32_t* members;
-    const int32_t* table;  // of the group's first sequence
-    int kv, split, row0, rows, pg0, pg1, n;  // rows: of the item's tiles; n: pages that can be read
+// An item's record, its page-table row and the number of its pages that can be read.
+struct Work {
+    SharedItem it;
+    const int32_t* table;
+    int n;
 };
-
-__device__ __forceinline__ SharedItem find_item(const DecodeParamsX& p, int item, int tile_rows) {
-    SharedItem r;
-    int lo = 0, hi = p.n_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(&p.groups[mid].first_item) <= item) lo = mid;
-        else hi = mid;
-    }
-    r.g = p.groups[lo];
-    const int rel = item - r.g.first_item;
-    r.split = rel % r.g.splits;
-    r.kv = rel / r.g.splits % p.hk;
-    r.row0 = rel / r.g.splits / p.hk * tile_rows;
-    r.rows = min(tile_rows, r.g.members * p.G - r.row0);
-    r.pg0 = (int)((long)r.g.pages * r.split / r.g.splits);
-    r.pg1 = (int)((long)r.g.pages * (r.split + 1) / r.g.splits);
-    r.members = p.member + r.g.first_member;
-    r.table = p.page_table + (size_t)__ldg(r.members) * p.max_pages;
+__device__ __forceinline__ Work find_item(const DecodeParamsX& p, int item) {
+    Work r;
+    const int4 x = __ldg(reinterpret_cast<const int4*>(p.items + item)), y = __ldg(reinterpret_cast<const int4*>(p.items + item) + 1);
+    r.it.seq = x.x; r.it.kv = x.y; r.it.pg0 = x.z; r.it.pages = x.w;
+    r.it.rows = y.x; r.it.row0 = y.y; r.it.qtile = y.z; r.it.part0 = y.w;
+    r.table = p.page_table + (size_t)r.it.seq * p.max_pages + r.it.pg0;
     r.n = 0;
     const int lane = threadIdx.x & 31;
-    for (int q0 = r.pg0; q0 < r.pg1; q0 += 128) {
+    for (int q0 = 0; q0 < r.it.pages; q0 += 128) {
         int id[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) id[i] = q0 + 32 * i + lane < r.pg1 ? __ldg(r.table + q0 + 32 * i + lane) : -1;
+        for (int i = 0; i < 4; ++i) id[i] = q0 + 32 * i + lane < r.it.pages ? __ldg(r.table + q0 + 32 * i + lane) : -1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.n += __popc(__ballot_sync(kFull, id[i] >= 0 && id[i] < p.num_pages));
     }
@@ -392,9 +402,8 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     uint64_t* v_empty = v_full + NS;
     uint64_t* s_full = v_empty + NS;   // [T][2]
     uint64_t* p_full = s_full + 2 * T; // [T][2]
-    uint64_t* s_free = p_full + 2 * T; // [T][2]
-    uint64_t* o_done = s_free + 2 * T; // [T]
-    uint64_t* q_full = o_done + T;
+    uint64_t* pv_done = p_full + 2 * T; // [T][2]
+    uint64_t* q_full = pv_done + 2 * T;
     uint64_t* drain = q_full + 1;      // [2] the two warps of the products
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
@@ -414,10 +423,9 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         for (int i = 0; i < 2 * T; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
-            mbar_init(&s_free[i], 1);
+            mbar_init(&pv_done[i], 1);
         }
-        for (int i = 0; i < T; ++i) mbar_init(&o_done[i], 1);
-        mbar_init(q_full, SM::kSoftWarps);
+        mbar_init(q_full, 1);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         fence_mbar_init();
@@ -428,9 +436,8 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     block_sync();
     tc_after();
     const uint32_t tmem = *tmem_at;
-    pdl_wait();     // plan and Q' rows
-    pdl_trigger();
-
+    // The plan was complete before prep_kernel let this grid start; what prep_kernel makes,
+    // q' and its scales, is waited for by the warps that read it.
     const int total = __ldg(p.counter + kSharedItems);
     auto wait = [&](uint64_t* bar, uint32_t parity) {  // by a whole warp
         if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
@@ -441,6 +448,10 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         }
         return false;
     };
+    // The products of values of page g of tile t are done.  (A parity tells two
+    // neighbouring phases of a barrier apart and no more: with a barrier for each of the
+    // two buffers, the next phase of one needs the waiting warp itself.)
+    auto wait_values = [&](int t, uint32_t g) { return wait(&pv_done[2 * t + (g & 1u)], (g >> 1) & 1u); };
     // Every role walks the block's items by itself; a barrier of the block ends an
     // item (with a timeout: the last one).
     bool ok = true;
@@ -451,45 +462,18 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     if (warp < SM::kSoftWarps) {
         // -------------------------------- softmax --------------------------------
         regs_up<SM::kSoftRegs>();
+        pdl_wait();
+        pdl_trigger();
         const int t = warp >> 2;
-        for (int item = blockIdx.x; item < total; item += gridDim.x) {
-            const SharedItem it = find_item(p, item, 128 * T);
-            const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
-            // Q' rows into their tiles (zeros behind the last row): thread = chunk c of rows r0, r0 + 8 T, ..
-            {
-                const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
-                constexpr int kStep = SM::kSoftWarps * 2, kBatch = PARTS == 1 ? 8 : 4;
-                for (int i0 = 0; i0 < tiles * 128; i0 += kStep * kBatch) {
-                    uint4 v[kBatch][PARTS];
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = i0 + kStep * i + r0, row = it.row0 + r;
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part) v[i][part] = make_uint4(0u, 0u, 0u, 0u);
-                        if (r < it.rows) {
-                            const size_t at = ((size_t)__ldg(it.members + row / p.G) * p.hk + it.kv) * p.G + row % p.G;
-#pragma unroll
-                            for (int part = 0; part < PARTS; ++part)
-                                v[i][part] = __ldg(reinterpret_cast<const uint4*>(p.qrow + ((size_t)part * p.B * p.hq + at) * kD) + c);
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const int r = i0 + kStep * i + r0, rr = r & 127;
-                        uint8_t* to = smem + SM::kQ + (r >> 7) * PARTS * SM::kQTile + (c >> 3) * (128 * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part) *reinterpret_cast<uint4*>(to + part * SM::kQTile) = v[i][part];
-                    }
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
-            }
+        const int gsh = 31 - __clz(p.G);  // G is a power of two
+        for (int item = blockIdx.x; item < total; item += gridDim.x, ++items) {
+            const Work wk = find_item(p, item);
+            const SharedItem& it = wk.it;
+            const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = wk.n;
             if (t < tiles) {
                 const int r = t * 128 + (warp & 3) * 32 + lane, row = it.row0 + r;
                 const bool row_on = r < it.rows;
-                const int b = row_on ? __ldg(it.members + row / p.G) : 0, head = row_on ? row % p.G : 0;
-                const float kq = row_on ? __ldg(p.qkinv + ((size_t)b * p.hk + it.kv) * 4) : 1.f;  // 2^-e of the Q' rows
+                const float kq = row_on ? __ldg(p.qtile_kinv + (size_t)it.qtile * 128 + r) : 0.f;  // 2^-e of the row of q'
                 const uint32_t lanes = tmem + t * SM::kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
                 float m_run = -INFINITY, l0 = 0.f, l1 = 0.f;
                 float o[PARTS == 2 ? kD : 1];
@@ -549,7 +533,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     l1 += sum[0].y + sum[1].y;
                     if constexpr (PARTS == 1) {
                         if (any && j > 0) {  // rescale O, once the products of the page before are in it
-                            if (!(ok = wait(&o_done[t], (g - 1) & 1u))) break;
+                            if (!(ok = wait_values(t, g - 1))) break;
                             tc_after();
 #pragma unroll 1
                             for (int c = 0; c < kD; c += 32) {
@@ -569,7 +553,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     if constexpr (PARTS == 2) {
                         // the page before: its products, in its own maximum's units, then this page's
                         if (j > 0) {
-                            if (!(ok = wait(&o_done[t], (g - 1) & 1u))) break;
+                            if (!(ok = wait_values(t, g - 1))) break;
                             tc_after();
 #pragma unroll
                             for (int c = 0; c < kD; c += 32) {
@@ -589,11 +573,10 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                 }
                 // ---- the row's partial
                 if (ok && n > 0) {
-                    // (a parity tells two neighbouring phases apart: the one before the last comes first;
-                    // inside the loop S of page j is there only once the products of page j - 2 are done)
-                    if (PARTS == 1 && n > 1) ok = wait(&o_done[t], (g0 + n - 2) & 1u);
-                    ok = ok && wait(&o_done[t], (g0 + n - 1) & 1u);
+                    ok = wait_values(t, g0 + n - 1);
                     tc_after();
+                } else if (ok) {
+                    ok = wait(q_full, items & 1u);  // (nothing else says that q' has landed, whose place is written below)
                 }
                 if (ok) {
                     // o' goes through the warp's quarter of its Q' tile (no product reads that any more), so
@@ -601,7 +584,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     // the cycles.  Row r's chunk c of 16 lies at chunk c ^ (r & 15).
                     const float l = l0 + l1;
                     uint8_t* stage = smem + SM::kQ + t * PARTS * SM::kQTile + (warp & 3) * (SM::kQTile / 4);
-                    float* parts = p.sh_part + ((size_t)it.g.first_part + ((size_t)it.kv * it.g.splits + it.split) * it.g.members) * p.part_stride;
+                    float* parts = p.sh_part + (size_t)it.part0 * p.part_stride;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 64 positions at a time
 #pragma unroll
@@ -627,17 +610,19 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                             if (first + i >= it.rows) break;
                             const int rw = it.row0 + first + i;
                             const uint4 x = *reinterpret_cast<const uint4*>(stage + i * 256 + ((c ^ (i & 15)) << 4));
-                            *reinterpret_cast<uint4*>(parts + (size_t)(rw / p.G) * p.part_stride + rw % p.G * kD + 64 * h + 4 * c) = x;
+                            *reinterpret_cast<uint4*>(parts + (size_t)(rw >> gsh) * p.part_stride + (rw & (p.G - 1)) * kD + 64 * h + 4 * c) = x;
                         }
                         __syncwarp();
                     }
                     if (row_on) {
-                        float* part = parts + (size_t)(row / p.G) * p.part_stride;
+                        float* part = parts + (size_t)(row >> gsh) * p.part_stride;
+                        const int head = row & (p.G - 1);
                         part[p.G * kD + head] = l == 0.f ? -INFINITY : finite_max(m_run);
                         part[p.G * kD + p.G + head] = l;
                     }
                 }
                 tc_before();
+                fence_async();  // (the next item's q' is copied over the staged rows)
             }
             block_sync();
             if (*dead) break;
@@ -658,8 +643,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         const int i0 = BITS == 4 ? 0 : 2 * (lane >> 4);
         uint16_t* pairS = reinterpret_cast<uint16_t*>(smem + SM::kPairs + dw * SM::kPairBytes);  // [group][s, z][64]
         for (int item = blockIdx.x; item < total; item += gridDim.x) {
-            const SharedItem it = find_item(p, item, 128 * T);
-            const int n = it.n;
+            const int n = find_item(p, item).n;
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t g = done + j, st = g % NS, rs = g % NR;
                 if (!(ok = wait(&raw_full[rs], (g / NR) & 1u))) break;
@@ -786,8 +770,8 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
             // and 24 issues per page, one after the other, were the kernel's critical path.)
             const uint64_t qd = tc_desc(smem_u32(smem + SM::kQ)), kd = tc_desc(smem_u32(smem + SM::kK));
             for (int item = blockIdx.x; item < total; item += gridDim.x, ++items) {
-                const SharedItem it = find_item(p, item, 128 * T);
-                const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
+                const Work wk = find_item(p, item);
+                const int tiles = T == 2 && wk.it.rows > 128 ? 2 : 1, n = wk.n;
                 bool issued = false;
                 ok = wait(q_full, items & 1u);
                 for (int j = 0; j < n && ok; ++j) {
@@ -797,9 +781,8 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     for (int t = 0; t < T; ++t) {
                         if (t >= tiles || !ok) break;
                         const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
-                        // S takes the place of the S, and P, of two pages before, whose products of values are to be
-                        // done (a barrier for each buffer: those of the page before may be done too)
-                        if (gt >= 2 && !(ok = wait(&s_free[2 * t + buf], ((gt >> 1) - 1) & 1u))) break;
+                        // S takes the place of the S, and P, of two pages before, whose products of values are to be done
+                        if (gt >= 2 && !(ok = wait_values(t, gt - 2))) break;
                         tc_after();
                         const uint32_t s = tmem + t * SM::kTileCols + buf * 64;
 #pragma unroll
@@ -827,8 +810,8 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
             // --------------------------- products of values ---------------------------
             const uint64_t vd = tc_desc(smem_u32(smem + SM::kV));
             for (int item = blockIdx.x; item < total; item += gridDim.x) {
-                const SharedItem it = find_item(p, item, 128 * T);
-                const int tiles = T == 2 && it.rows > 128 ? 2 : 1, n = it.n;
+                const Work wk = find_item(p, item);
+                const int tiles = T == 2 && wk.it.rows > 128 ? 2 : 1, n = wk.n;
                 bool issued = false;
                 for (int j = 0; j < n && ok; ++j) {  // O (+)= P V
                     const uint32_t g = done + j, st = g % NS;
@@ -847,8 +830,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                             for (int k = 0; k < 4; ++k)
                                 tc_mma_ts(on, o, pa + (pr == 1 ? 32 : 0) + 8 * k, vd + (((st * PARTS + (pr == 2)) * SM::kOperand + 32 * k) >> 4), tc_idesc(kD),
                                           (PARTS == 1 && j > 0) || pr > 0 || k > 0);
-                        tc_commit(on, &o_done[t]);
-                        tc_commit(on, &s_free[2 * t + buf]);
+                        tc_commit(on, &pv_done[2 * t + buf]);
                         issued = true;
                     }
                     if (ok) tc_commit(on, &v_empty[st]);
@@ -863,16 +845,17 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                 if (tiles == 2) done1 += n;
             }
         } else {
-            // -------------------------------- producer --------------------------------
-            for (int item = blockIdx.x; item < total; item += gridDim.x) {
-                const SharedItem it = find_item(p, item, 128 * T);
+            // --------------------------- copies: pages, and q' ------------------------
+            if (warp == SM::kMmaWarp + 3) pdl_wait();
+            for (int item = blockIdx.x; item < total; item += gridDim.x, ++items) {
+                const Work wk = find_item(p, item);
+                const SharedItem& it = wk.it;
                 if (warp == SM::kMmaWarp + 2) {
                     int j = 0;  // pages issued
-                    for (int q0 = it.pg0; q0 < it.pg1 && ok; q0 += 32) {
-                        const int q = q0 + lane;
-                        const int id = q < it.pg1 ? __ldg(it.table + q) : -1;
+                    for (int q0 = 0; q0 < it.pages && ok; q0 += 32) {
+                        const int id = q0 + lane < it.pages ? __ldg(wk.table + q0 + lane) : -1;
                         const bool good = id >= 0 && id < p.num_pages;
-                        if (q < it.pg1 && !good) report(p.status, OSCAR_STATUS_BAD_PAGE);
+                        if (q0 + lane < it.pages && !good) report(p.status, OSCAR_STATUS_BAD_PAGE);
                         for (unsigned left = __ballot_sync(kFull, good); left && ok; left &= left - 1) {
                             const int page = __shfl_sync(kFull, id, __ffs(left) - 1);
                             const uint32_t g = done + j, rs = g % NR;
@@ -888,10 +871,20 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     if (!ok)  // copies in flight land before the block ends
                         for (uint32_t g = done + j > NR ? done + j - NR : 0; g < done + j; ++g)
                             (void)mbar_wait_bounded(&raw_full[g % NR], (g / NR) & 1u, kWaitPolls);
+                } else {
+                    // (rows behind the last one hold whatever the workspace does: no other row sees them)
+                    const int tiles = T == 2 && it.rows > 128 ? 2 : 1;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, tiles * PARTS * kQTileBytes);
+                        for (int t = 0; t < tiles; ++t)
+                            bulk_g2s(smem + SM::kQ + t * PARTS * SM::kQTile, p.qtile + (size_t)(it.qtile + t) * 2 * kQTileBytes, PARTS * kQTileBytes, q_full);
+                    }
+                    __syncwarp();
+                    ok = wait(q_full, items & 1u) && ok;  // (lands before the block ends, whoever else reads it)
                 }
                 block_sync();
                 if (*dead) break;
-                done += it.n;
+                done += wk.n;
             }
         }
     }
@@ -917,11 +910,11 @@ cudaError_t launch_parts(const DecodeParamsX& p, cudaStream_t st, int dev) {
 cudaError_t launch_shared_plan(const DecodeParamsX& p, cudaStream_t st, int dev) {
     static bool set[64];
     if (!set[dev & 63]) {
-        const cudaError_t e = set_smem(group_kernel, 2 * kMaxSharedGroups * 4, false);
+        const cudaError_t e = set_smem(group_kernel, 6 * kMaxSharedGroups * 4, false);
         if (e != cudaSuccess) return e;
         set[dev & 63] = true;
     }
-    return launch_pdl(group_kernel, dim3(1), dim3(kPlanThreads), (size_t)2 * p.n_groups * 4, st, p, p.out_bf16 ? 256 : 128);
+    return launch_pdl(group_kernel, dim3(1), dim3(kPlanThreads), (size_t)6 * p.n_groups * 4, st, p, p.out_bf16 ? 256 : 128);
 }
 
 cudaError_t launch_shared(const DecodeParamsX& p, int bits, cudaStream_t st, int dev) {

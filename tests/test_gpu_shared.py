@@ -29,8 +29,12 @@ def run(c, dtype=F32, status=None, stream=None, ws=None, group=None, group_pages
     gp = d["group_pages"] if group_pages is None else group_pages
     if ws is None:
         ws = torch.full((O.oscar_decode_workspace_bytes_shared(c.sh, c.bits, c.B, c.max_pages, gp.numel()),), 0xFF, dtype=torch.uint8, device="cuda")
+    own = torch.zeros(1, dtype=torch.int32, device="cuda") if status is None else status
     O.oscar_decode_attn_shared(c.sh, c.bits, d["q"], d["kv"], d["len"], d["pool"], d["table"], c.max_pages, c.num_pages, d["hist"],
-                               d["group"] if group is None else group, gp, d["U"], SCALE, out, ws, dev_status=status, stream=stream)
+                               d["group"] if group is None else group, gp, d["U"], SCALE, out, ws, dev_status=own, stream=stream)
+    if status is None:
+        (stream or torch.cuda.current_stream()).synchronize()
+        assert int(own) == 0                               # no wait of the kernels ran out either
     return out
 
 
