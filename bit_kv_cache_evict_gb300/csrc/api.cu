@@ -374,7 +374,7 @@ struct DecodeExtra {
     float decay;
     const int32_t* prefix_group;
     const int32_t* group_pages;
-    int32_t n_groups;
+    int32_t n_groups, min_members;
 };
 
 static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const void* q, const void* bf16_kv,
@@ -480,6 +480,7 @@ static oscar_status decode_impl(const oscar_shape* shape, int32_t batch, const v
         x.prefix_group = extra->prefix_group;
         x.group_pages = extra->group_pages;
         x.n_groups = extra->n_groups;
+        x.min_members = extra->min_members;
         x.skip = reinterpret_cast<int32_t*>(ws + w.skip);
         x.sref = reinterpret_cast<int4*>(ws + w.sref);
         x.qref = reinterpret_cast<int4*>(ws + w.qref);
@@ -561,7 +562,7 @@ oscar_status oscar_decode_attn_weights(const oscar_shape* shape, int32_t bits, i
     if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
     if (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) return OSCAR_ERR_INVALID_ARG;
     if (max_pages > INT32_MAX / kPage) return OSCAR_ERR_INVALID_ARG;  // positions are int32
-    const DecodeExtra extra{kModeWeights, weight, weight_stride, slot_weight, decay, nullptr, nullptr, 0};
+    const DecodeExtra extra{kModeWeights, weight, weight_stride, slot_weight, decay, nullptr, nullptr, 0, 0};
     return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
                        nullptr, nullptr, sm_scale, static_cast<float*>(out), workspace, ws_bytes, dev_status, stream,
                        bits, out_type, &extra);
@@ -571,16 +572,16 @@ oscar_status oscar_decode_attn_shared(const oscar_shape* shape, int32_t bits, in
                                       const void* bf16_kv, const int32_t* bf16_len, const uint8_t* pool,
                                       const int32_t* page_table, int32_t max_pages, int32_t num_pages,
                                       const int32_t* hist_len, const int32_t* prefix_group, int32_t n_groups,
-                                      const int32_t* group_pages, const float* U, float sm_scale, void* out,
-                                      int32_t out_type, void* workspace, size_t* ws_bytes, int32_t* dev_status,
+                                      const int32_t* group_pages, int32_t min_members, const float* U, float sm_scale,
+                                      void* out, int32_t out_type, void* workspace, size_t* ws_bytes, int32_t* dev_status,
                                       void* stream) {
     const oscar_status sst = check_shape(shape);
     if (sst != OSCAR_OK) return sst;
     if (bits != 2 && bits != 4) return OSCAR_ERR_UNSUPPORTED;
     if (out_type != OSCAR_OUT_F32 && out_type != OSCAR_OUT_BF16) return OSCAR_ERR_INVALID_ARG;
     if (max_pages > INT32_MAX / kPage) return OSCAR_ERR_INVALID_ARG;  // positions are int32
-    if (n_groups < 0 || n_groups > kMaxSharedGroups) return OSCAR_ERR_INVALID_ARG;
-    const DecodeExtra extra{kModeShared, nullptr, 0, nullptr, 1.f, prefix_group, group_pages, n_groups};
+    if (n_groups < 0 || n_groups > kMaxSharedGroups || min_members < 0) return OSCAR_ERR_INVALID_ARG;
+    const DecodeExtra extra{kModeShared, nullptr, 0, nullptr, 1.f, prefix_group, group_pages, n_groups, min_members};
     return decode_impl(shape, batch, q, bf16_kv, bf16_len, pool, page_table, max_pages, num_pages, hist_len, U,
                        nullptr, nullptr, sm_scale, static_cast<float*>(out), workspace, ws_bytes, dev_status, stream,
                        bits, out_type, &extra);

@@ -452,6 +452,7 @@ struct DecodeParamsX : DecodeParams4 {
     float* qtile_kinv;            // [tiles][128] 2^-e of each row
     float* sh_part;               // partials [part_stride]: (KV head, split, member) of each group
     int n_groups, shared_blocks;
+    int min_members;  // of a group that attends together; 0: where it pays
 };
 
 // Split-K geometry of one sequence with npg history pages: the last

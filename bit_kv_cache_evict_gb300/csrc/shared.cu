@@ -36,7 +36,20 @@ namespace {
 // plan
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
-constexpr int kMinMembers = 2;  // smaller groups attend by themselves
+// Which groups attend together, where the caller leaves it to the library.  A page of a
+// KV head costs the members' own kernels 0.28 us of an SM per sequence (64 x 28K, 32:8
+// heads: 504 us without sharing, 88 us of it not the prefix), shared_kernel about 0.8 us
+// for up to 128 rows and 1.06 for 256 with a bf16 output, 1.8 for 128 rows with fp32: as
+// many sequences as this.
+__device__ __forceinline__ int shared_cost(int members, int G, int rows) {
+    const int n = members * G;
+    if (rows == 256) return n <= 128 ? 3 : (n + 255) / 256 * 4;
+    return (n + 127) / 128 * (G == 8 ? 5 : 6);
+}
+// and 8 us for its start and end and its partials' merge, of all groups together: the
+// pages of a KV head and sequence that take as long.  Eight members, 16K tokens: 44 us,
+// 53 each by itself; 4K: 36 and 29; pairs behind 16K in eight groups: 132 and 97.
+constexpr long kMinSaved = 4300;
 
 // One block.  skip[b]: pages of sequence b that its group attends; sref[b]: its
 // partials (first, splits, members, index); qref[b]: its rows of q'; and the items.
@@ -50,6 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
     int32_t* first_seq = first_tile + p.n_groups;  // whose page-table row tells the group's pages
     __shared__ int32_t chunk_group[kPlanThreads], chunk_index[kPlanThreads];
     __shared__ int sh_pps, sh_total;
+    __shared__ unsigned long long sh_saved;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
@@ -61,6 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
         count[g] = 0;
         pages[g] = n;
     }
+    if (threadIdx.x == 0) sh_saved = 0;
     __syncthreads();
     // members in order of their sequences, by warp 0 (one order, whatever the launch)
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
@@ -90,8 +105,14 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
         __syncthreads();
         if (b < p.B) p.sref[b] = make_int4(0, 0, chunk_group[threadIdx.x], chunk_index[threadIdx.x]);
     }
-    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads)
-        if (count[g] < kMinMembers) count[g] = 0;
+    for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) {
+        const int gain = p.min_members > 0 ? count[g] - max(p.min_members, 2) + 1 : count[g] - shared_cost(count[g], p.G, rows);
+        if (gain <= 0) count[g] = 0;
+        else atomicAdd(&sh_saved, (unsigned long long)gain * pages[g] * p.hk);
+    }
+    __syncthreads();
+    if (p.min_members == 0 && sh_saved < kMinSaved)
+        for (int g = threadIdx.x; g < p.n_groups; g += kPlanThreads) count[g] = 0;
     __syncthreads();
     auto row_tiles = [&](int g, int of) { return (count[g] * p.G + of - 1) / of; };
     if (warp == 0) {
@@ -408,6 +429,13 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
     const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);  // (uniform for the compiler)
+    // The plan was complete before prep_kernel let this grid start; what prep_kernel makes,
+    // q' and its scales, is waited for by the warps that read it.
+    const int total = __ldg(p.counter + kSharedItems);
+    if ((int)blockIdx.x >= total) {  // (this grid is not complete before prep_kernel is)
+        if (threadIdx.x == 0) pdl_wait();
+        return;
+    }
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NR; ++i) {
@@ -436,9 +464,6 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     block_sync();
     tc_after();
     const uint32_t tmem = *tmem_at;
-    // The plan was complete before prep_kernel let this grid start; what prep_kernel makes,
-    // q' and its scales, is waited for by the warps that read it.
-    const int total = __ldg(p.counter + kSharedItems);
     auto wait = [&](uint64_t* bar, uint32_t parity) {  // by a whole warp
         if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
         if (__all_sync(kFull, mbar_wait_bounded(bar, parity, kWaitPolls))) return true;

@@ -132,7 +132,7 @@ def lib() -> ctypes.CDLL:
         L.oscar_decode_attn_weights.argtypes = [S, I32, I32, _P, _P, _P, _P, _P, I32, I32, _P, _P, F32, _P, I32, _P, I32, _P,
                                                 F32, _P, ctypes.POINTER(ctypes.c_size_t), _P, _P]
         L.oscar_decode_attn_shared.restype = ctypes.c_int
-        L.oscar_decode_attn_shared.argtypes = [S, I32, I32, _P, _P, _P, _P, _P, I32, I32, _P, _P, I32, _P, _P, F32, _P, I32, _P,
+        L.oscar_decode_attn_shared.argtypes = [S, I32, I32, _P, _P, _P, _P, _P, I32, I32, _P, _P, I32, _P, I32, _P, F32, _P, I32, _P,
                                                ctypes.POINTER(ctypes.c_size_t), _P, _P]
         L.oscar_history_select.restype = ctypes.c_int
         L.oscar_history_select.argtypes = [I32, _P, I32, _P, _P, I32, _P, I32, _P, _P, I32, _P, _P]
@@ -797,19 +797,19 @@ def oscar_history_select(weight, hist_len, budget, keep, n_keep, protect: int = 
 def oscar_decode_workspace_bytes_shared(shape: oscar_shape, bits: int, batch: int, max_pages: int, n_groups: int) -> int:
     ws = ctypes.c_size_t(0)
     st = lib().oscar_decode_attn_shared(ctypes.byref(shape), bits, batch, None, None, None, None, None, max_pages, 0, None,
-                                        None, n_groups, None, None, 1.0, None, OSCAR_OUT_F32, None, ctypes.byref(ws), None,
-                                        None)
+                                        None, n_groups, None, 0, None, 1.0, None, OSCAR_OUT_F32, None, ctypes.byref(ws),
+                                        None, None)
     _check("oscar_decode_attn_shared", st)
     return int(ws.value)
 
 
 def oscar_decode_attn_shared(shape: oscar_shape, bits: int, q, bf16_kv, bf16_len, pool, page_table, max_pages: int,
                              num_pages: int, hist_len, prefix_group, group_pages, U, sm_scale: float, out, workspace,
-                             dev_status=None, stream=None) -> None:
+                             min_members: int = 0, dev_status=None, stream=None) -> None:
     """oscar_decode_attn (bits 2) or oscar_decode_attn_int4 (bits 4) with the
     first group_pages[g] (int32 [n_groups]) pages of the sequences whose
-    prefix_group (int32 [B]; negative: none) is g read once for all of them;
-    out may be float32 or bfloat16; see include/oscar.h.  ``workspace``: CUDA
+    prefix_group (int32 [B]; negative: none) is g read once for all of them, if
+    they are at least min_members (0: where it is faster); out may be float32 or bfloat16; see include/oscar.h.  ``workspace``: CUDA
     uint8 tensor of at least oscar_decode_workspace_bytes_shared(shape, bits,
     batch, max_pages, n_groups) bytes."""
     kind = _out_type(out)
@@ -821,8 +821,8 @@ def oscar_decode_attn_shared(shape: oscar_shape, bits: int, q, bf16_kv, bf16_len
         _arg(pool, "pool", _U8, num_pages * hk * _pool_block(shape, bits), dev),
         _arg(page_table, "page_table", _I32, B * max_pages, dev), max_pages, num_pages,
         _arg(hist_len, "hist_len", _I32, B, dev), _arg(prefix_group, "prefix_group", _I32, B, dev), n_groups,
-        _arg(group_pages, "group_pages", _I32, n_groups, dev), _arg(U, "U", _F32, hk * 2 * d * d, dev), sm_scale,
-        _arg(out, "out", out.dtype, rows, dev), kind, _arg(workspace, "workspace", _U8, 1 if B else 0, dev),
+        _arg(group_pages, "group_pages", _I32, n_groups, dev), min_members, _arg(U, "U", _F32, hk * 2 * d * d, dev),
+        sm_scale, _arg(out, "out", out.dtype, rows, dev), kind, _arg(workspace, "workspace", _U8, 1 if B else 0, dev),
         ctypes.byref(ctypes.c_size_t(workspace.numel())), _arg(dev_status, "dev_status", _I32, 1, dev),
         _stream_arg(stream, dev))
     if st:

@@ -666,14 +666,18 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
  *                 page-table rows, read from the row of its first sequence.
  *                 Pages that a row shares with some members only do not count.
  *   n_groups      at most 8192
+ *   min_members   groups of at least this many members (and two) attend their
+ *                 pages together; 0: those for which it is faster, by the
+ *                 library's rule on members, rows and pages.  The results do
+ *                 not depend on it but for the roundings below.
  *   out           as oscar_decode_attn_int4, for 2 bits too
  *   workspace     as oscar_decode_attn; the size depends on n_groups too
  * Both arrays are read on the device, so that a captured graph follows them.  A
  * sequence whose history ends inside its group's pages attends by itself, as
- * do groups of one.  A prefix_group of n_groups or more (no group) and
+ * do the members of groups that are too small.  A prefix_group of n_groups or more (no group) and
  * group_pages outside [0, max_pages] (clamped) are reported as BAD_POS.
  * Precision: fp32 output as oscar_decode_attn_int4.  For a bf16 output the
- * shared pages' queries, values s * code + z and weights enter their products
+ * pages attended together: queries, values s * code + z and weights enter products
  * as fp16, one rounding of 2^-11 (relative) each; the rest as for fp32, but that 2-bit
  * pages of a sequence's own are summed as in oscar_decode_attn.  Shared
  * values s * code + z have to be finite in fp16 (|value| < 65520); NaN, and
@@ -684,8 +688,8 @@ oscar_status oscar_decode_attn_shared(const oscar_shape* shape, int32_t bits, in
                                       const void* bf16_kv, const int32_t* bf16_len, const uint8_t* pool,
                                       const int32_t* page_table, int32_t max_pages, int32_t num_pages,
                                       const int32_t* hist_len, const int32_t* prefix_group, int32_t n_groups,
-                                      const int32_t* group_pages, const float* U, float sm_scale, void* out,
-                                      int32_t out_type, void* workspace, size_t* ws_bytes, int32_t* dev_status,
+                                      const int32_t* group_pages, int32_t min_members, const float* U, float sm_scale,
+                                      void* out, int32_t out_type, void* workspace, size_t* ws_bytes, int32_t* dev_status,
                                       void* stream);
 
 /*

@@ -23,7 +23,7 @@ def _lib():
     O.lib()
 
 
-def run(c, dtype=F32, status=None, stream=None, ws=None, group=None, group_pages=None):
+def run(c, dtype=F32, status=None, stream=None, ws=None, group=None, group_pages=None, min_members=2):
     d = getattr(c, "d", None) or c.device()
     out = torch.full((c.B, c.hq, D), float("nan"), dtype=dtype, device="cuda")
     gp = d["group_pages"] if group_pages is None else group_pages
@@ -31,7 +31,7 @@ def run(c, dtype=F32, status=None, stream=None, ws=None, group=None, group_pages
         ws = torch.full((O.oscar_decode_workspace_bytes_shared(c.sh, c.bits, c.B, c.max_pages, gp.numel()),), 0xFF, dtype=torch.uint8, device="cuda")
     own = torch.zeros(1, dtype=torch.int32, device="cuda") if status is None else status
     O.oscar_decode_attn_shared(c.sh, c.bits, d["q"], d["kv"], d["len"], d["pool"], d["table"], c.max_pages, c.num_pages, d["hist"],
-                               d["group"] if group is None else group, gp, d["U"], SCALE, out, ws, dev_status=own, stream=stream)
+                               d["group"] if group is None else group, gp, d["U"], SCALE, out, ws, min_members=min_members, dev_status=own, stream=stream)
     if status is None:
         (stream or torch.cuda.current_stream()).synchronize()
         assert int(own) == 0                               # no wait of the kernels ran out either
@@ -192,7 +192,7 @@ def test_same_bits_streams_and_a_graph_that_follows_the_groups(bits, dtype):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         O.oscar_decode_attn_shared(c.sh, bits, d["q"], d["kv"], d["len"], d["pool"], d["table"], c.max_pages, c.num_pages, d["hist"], d["group"],
-                                   d["group_pages"], d["U"], SCALE, out, ws)
+                                   d["group_pages"], d["U"], SCALE, out, ws, min_members=2)
     for group, pages in (([i % 2 for i in range(12)], [9, 9]), ([-1] * 6 + [i % 2 for i in range(6)], [4, 9]), ([-1] * 12, [0, 0])):
         d["group"].copy_(torch.tensor(group, dtype=torch.int32))
         d["group_pages"].copy_(torch.tensor(pages, dtype=torch.int32))
@@ -210,3 +210,16 @@ def test_wide_tables_and_no_windows(bits):
     want = c.want()
     for dtype in (F32, BF16):
         check(c, run(c, dtype), want, dtype)
+
+
+@BOTH
+@TYPES
+def test_the_librarys_rule_on_both_sides_of_its_border(bits, dtype):
+    """min_members 0 shares where it is faster, by members and pages; a minimum above the members shares nothing.  The
+    result is the same to its tolerance on both sides: 70 sequences of 8 KV heads, 3 and 9 of 64, fewer and more pages."""
+    for members, hk, pages in ((70, 8, 7), (70, 8, 12), (9, 64, 20), (9, 64, 30), (3, 64, 20)):
+        c = Scene(21, bits, [64 * pages + i for i in range(members)], hk, hk, 128, groups=[0] * members, shared=pages)
+        c.len[:] = 4
+        want = c.want()
+        for least in (0, 2, members, members + 1):
+            check(c, run(c, dtype, min_members=least), want, dtype)

@@ -52,11 +52,11 @@ def test_weights_refusals(lib):
     assert weights(lib, s=sh(hq=24)) == UNSUP
 
 
-def shared(lib, s=None, bits=4, B=4, q=F, kv=F, bl=F, pool=F, table=F, max_pages=10, num_pages=1, hl=F, group=F, n_groups=2, pages=F, U=F, scale=1.0,
-           out=F, kind=O.OSCAR_OUT_F32, ws=F, room=1 << 40, status=None):
+def shared(lib, s=None, bits=4, B=4, q=F, kv=F, bl=F, pool=F, table=F, max_pages=10, num_pages=1, hl=F, group=F, n_groups=2, pages=F, least=0, U=F,
+           scale=1.0, out=F, kind=O.OSCAR_OUT_F32, ws=F, room=1 << 40, status=None):
     n = ctypes.c_size_t(room)
-    return lib.oscar_decode_attn_shared(ctypes.byref(s or sh()), bits, B, q, kv, bl, pool, table, max_pages, num_pages, hl, group, n_groups, pages, U,
-                                        scale, out, kind, ws, ctypes.byref(n), status, None)
+    return lib.oscar_decode_attn_shared(ctypes.byref(s or sh()), bits, B, q, kv, bl, pool, table, max_pages, num_pages, hl, group, n_groups, pages, least,
+                                        U, scale, out, kind, ws, ctypes.byref(n), status, None)
 
 
 def test_shared_refusals(lib):
@@ -68,6 +68,7 @@ def test_shared_refusals(lib):
         assert shared(lib, **{name: None}) == BAD, name
     for name in ("q", "kv", "pool", "U", "out", "ws", "status", "group", "pages", "bl", "hl", "table"):
         assert shared(lib, **{name: M}) == BAD, name
+    assert shared(lib, least=-1) == BAD
     assert shared(lib, n_groups=-1) == BAD and shared(lib, n_groups=8193) == BAD
     assert shared(lib, kind=2) == BAD and shared(lib, scale=float("nan")) == BAD and shared(lib, max_pages=0) == BAD
     for bits in (0, 1, 3, 8):
