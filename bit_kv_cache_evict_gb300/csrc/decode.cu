@@ -392,12 +392,13 @@ struct StageInfo {
 // Blocks per SM and ring stages of an int2_kernel instantiation: three
 // blocks (128 registers) with eight stages for up to four heads; for eight
 // heads three blocks with seven stages (the shared memory of three blocks),
-// except the Lloyd-Max and boost kernels, which keep two blocks (168
-// registers) and eight stages.
-template <int NT, bool LM, bool BOOST>
-__host__ __device__ constexpr int int2_blocks_per_sm() { return (NT == 1 || !(LM || BOOST)) ? 3 : 2; }
-template <int NT, bool LM, bool BOOST>
-__host__ __device__ constexpr int int2_stages() { return (NT == 2 && int2_blocks_per_sm<NT, LM, BOOST>() == 3) ? kStages - 1 : kStages; }
+// except the Lloyd-Max and boost kernels, and that of the centred value products,
+// which keep two blocks (168 registers) and eight stages (the last, 32 x 8K, groups
+// of 128, logits kept: 113 us with three blocks and 528 bytes of spills, 104 with two).
+template <int NT, bool LM, bool BOOST, bool CENTRE = false>
+__host__ __device__ constexpr int int2_blocks_per_sm() { return (NT == 1 || !(LM || BOOST || CENTRE)) ? 3 : 2; }
+template <int NT, bool LM, bool BOOST, bool CENTRE = false>
+__host__ __device__ constexpr int int2_stages() { return (NT == 2 && int2_blocks_per_sm<NT, LM, BOOST, CENTRE>() == 3) ? kStages - 1 : kStages; }
 // Whether an instantiation prefetches each item's q' data into shared
 // memory (the uniform four-head kernel; the others load it at the item's
 // first page).
@@ -1186,11 +1187,11 @@ __device__ __forceinline__ void attend_page_g8(const uint8_t* blk, int valid, ui
 
 // CENTRE: the P.V products of page_values_centred.
 template <int NT, bool LM = false, bool BOOST = false, Mode MODE = kModePlain, bool CENTRE = false>
-__global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOST>()))
+__global__ void __launch_bounds__(kInt2Threads, (int2_blocks_per_sm<NT, LM, BOOST, CENTRE>()))
 int2_kernel(Params<false, MODE> p) {
     static_assert(MODE == kModePlain || !(LM || BOOST), "the modes are for the uniform levels");
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int NS = int2_stages<NT, LM, BOOST>();  // ring stages
+    constexpr int NS = int2_stages<NT, LM, BOOST, CENTRE>();  // ring stages
     using SM = Int2Smem<NT, NS>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t* stages = smem + SM::kStage;
@@ -2249,16 +2250,16 @@ static Int2Attr& attr_for_device(int dev) {
 
 template <int NT, bool LM = false, bool BOOST = false, Mode MODE = kModePlain, bool CENTRE = false>
 static cudaError_t launch_int2(const Params<false, MODE>& p, cudaStream_t st, int sms, bool& attr_set) {
-    using SM = Int2Smem<NT, int2_stages<NT, LM, BOOST>()>;
+    using SM = Int2Smem<NT, int2_stages<NT, LM, BOOST, CENTRE>()>;
     constexpr int smem = int2_q_prefetch<NT, LM, BOOST>() ? SM::kBytesQP : ((LM || BOOST) ? SM::kBytesLM : SM::kBytes);
     // the blocks of one SM share its 228 KB (1 KB of it reserved per block)
-    static_assert(int2_blocks_per_sm<NT, LM, BOOST>() * (smem + 1024) <= 228 * 1024, "blocks per SM must fit");
+    static_assert(int2_blocks_per_sm<NT, LM, BOOST, CENTRE>() * (smem + 1024) <= 228 * 1024, "blocks per SM must fit");
     if (!attr_set) {
         cudaError_t e = set_smem(int2_kernel<NT, LM, BOOST, MODE, CENTRE>, smem, !(NT == 2 && LM));
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    const int per_sm = int2_blocks_per_sm<NT, LM, BOOST>();
+    const int per_sm = int2_blocks_per_sm<NT, LM, BOOST, CENTRE>();
     const int64_t max_items =
         (int64_t)p.B * p.hk * ((p.max_pages + p.pps - 1) / p.pps + p.tail_pg / kShortItemPages);
     int blocks = (int)std::min<int64_t>((int64_t)per_sm * sms, max_items);
