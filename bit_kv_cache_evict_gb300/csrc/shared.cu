@@ -351,18 +351,22 @@ struct SharedSmem {
     static constexpr int kPairGroups = BITS == 4 ? 1 : 4;      // groups that a warp's rows of V belong to, at most
     static constexpr int kPairBytes = kPairGroups * 2 * kPage * 2;
     static constexpr int kBars = kPairs + kDequantWarps * kPairBytes;
-    static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 6 + 3;
-    static constexpr int kBytes = kBars + kNumBars * 8 + 32;
+    static constexpr int kNumBars = 2 * kRawStages + 4 * kStages + T * 6 + 4 + 3;
+    static constexpr int kAlpha = kBars + kNumBars * 8 + 32;    // PARTS = 2: [2][128] factors that a page's maxima give the sums so far
+    static constexpr int kBytes = kAlpha + (PARTS == 2 ? 2 * 128 * 4 : 0);
     static constexpr int kAlloc = kBytes + 1024;        // the swizzled operands start on 1024 bytes
     static_assert(kAlloc <= 227 * 1024, "shared memory of a block");
-    // warps by role, in whole warpgroups: softmax, dequantisation, then one that issues the
-    // products of logits, one those of values, the producer and an idle one
+    // warps by role, in whole warpgroups: softmax (four per tile), PARTS = 2: four that add up the
+    // products of values, dequantisation, then one that issues the products of logits, one
+    // those of values, one that copies pages and one that copies q'
     static constexpr int kSoftWarps = 4 * T;
-    static constexpr int kMmaWarp = kSoftWarps + kDequantWarps, kThreads = (kMmaWarp + 4) * 32;
+    static constexpr int kRowWarps = 8;  // softmax and sums: the warps that a row's thread is in
+    static constexpr int kMmaWarp = kRowWarps + kDequantWarps, kThreads = (kMmaWarp + 4) * 32;
     // registers per thread: of the launch, then of each role (their sum is within the launch's)
-    static constexpr int kLaunchRegs = PARTS == 1 ? 96 : 128;
-    static constexpr int kSoftRegs = PARTS == 1 ? 136 : 216, kDequantRegs = PARTS == 1 ? 80 : 112, kOtherRegs = PARTS == 1 ? 40 : 56;
-    static_assert(kSoftWarps * kSoftRegs + kDequantWarps * kDequantRegs + 4 * kOtherRegs <= (kMmaWarp + 4) * kLaunchRegs, "registers");
+    static constexpr int kLaunchRegs = 96;
+    static constexpr int kSoftRegs = PARTS == 1 ? 136 : 128, kSumRegs = PARTS == 1 ? 136 : 168;
+    static constexpr int kDequantRegs = PARTS == 1 ? 80 : 72, kOtherRegs = 40;
+    static_assert(4 * (kSoftRegs + kSumRegs) + kDequantWarps * kDequantRegs + 4 * kOtherRegs <= (kMmaWarp + 4) * kLaunchRegs, "registers");
     static_assert(kThreads * kLaunchRegs <= 65536, "registers of the SM");
     // tensor memory, columns: PARTS = 1: per tile S [2][64] (P in the first 32 columns
     // of its S) and O [128]; PARTS = 2: S [2][64], P [2][64] (hi, lo), O [2][128]
@@ -424,7 +428,9 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     uint64_t* s_full = v_empty + NS;   // [T][2]
     uint64_t* p_full = s_full + 2 * T; // [T][2]
     uint64_t* pv_done = p_full + 2 * T; // [T][2]
-    uint64_t* q_full = pv_done + 2 * T;
+    uint64_t* a_full = pv_done + 2 * T; // [2] PARTS = 2: a page's factors
+    uint64_t* o_free = a_full + 2;      // [2] PARTS = 2: its products and factors have been taken
+    uint64_t* q_full = o_free + 2;
     uint64_t* drain = q_full + 1;      // [2] the two warps of the products
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drain + 2);
     volatile int* dead = reinterpret_cast<volatile int*>(tmem_at + 1);
@@ -453,6 +459,10 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&a_full[i], 4);
+            mbar_init(&o_free[i], 4);
+        }
         mbar_init(q_full, 1);
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
@@ -477,6 +487,37 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
     // neighbouring phases of a barrier apart and no more: with a barrier for each of the
     // two buffers, the next phase of one needs the waiting warp itself.)
     auto wait_values = [&](int t, uint32_t g) { return wait(&pv_done[2 * t + (g & 1u)], (g >> 1) & 1u); };
+    float* alphaS = reinterpret_cast<float*>(smem + SM::kAlpha);
+    // The o' of a warp's 32 rows of tile t into their partials, by value(c, v): positions c .. c + 31
+    // of the lane's row.  They go through the warp's quarter of the q' tile (no product reads that
+    // any more), so that a store of the warp covers whole lines: 16 bytes of each of 32 rows
+    // a store cost eight times the cycles.  Chunk c of row r lies at chunk c ^ (r & 15).
+    const int gsh = 31 - __clz(p.G);  // G is a power of two
+    auto store_rows = [&](const SharedItem& it, int t, auto value) {
+        uint8_t* stage = smem + SM::kQ + t * PARTS * SM::kQTile + (warp & 3) * (SM::kQTile / 4);
+        float* parts = p.sh_part + (size_t)it.part0 * p.part_stride;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 64 positions at a time
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t v[32];
+                value(64 * h + c, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<uint4*>(stage + lane * 256 + ((((c + i) >> 2) ^ (lane & 15)) << 4)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+            __syncwarp();
+            const int first = t * 128 + (warp & 3) * 32, c = lane & 15;
+#pragma unroll 4
+            for (int i = lane >> 4; i < 32; i += 2) {
+                if (first + i >= it.rows) break;
+                const int rw = it.row0 + first + i;
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + i * 256 + ((c ^ (i & 15)) << 4));
+                *reinterpret_cast<uint4*>(parts + (size_t)(rw >> gsh) * p.part_stride + (rw & (p.G - 1)) * kD + 64 * h + 4 * c) = x;
+            }
+            __syncwarp();
+        }
+    };
     // Every role walks the block's items by itself; a barrier of the block ends an
     // item (with a timeout: the last one).
     bool ok = true;
@@ -490,7 +531,6 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
         pdl_wait();
         pdl_trigger();
         const int t = warp >> 2;
-        const int gsh = 31 - __clz(p.G);  // G is a power of two
         for (int item = blockIdx.x; item < total; item += gridDim.x, ++items) {
             const Work wk = find_item(p, item);
             const SharedItem& it = wk.it;
@@ -501,10 +541,6 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                 const float kq = row_on ? __ldg(p.qtile_kinv + (size_t)it.qtile * 128 + r) : 0.f;  // 2^-e of the row of q'
                 const uint32_t lanes = tmem + t * SM::kTileCols + ((uint32_t)((warp & 3) * 32) << 16);
                 float m_run = -INFINITY, l0 = 0.f, l1 = 0.f;
-                float o[PARTS == 2 ? kD : 1];
-                if constexpr (PARTS == 2)
-#pragma unroll
-                    for (int d = 0; d < kD; ++d) o[d] = 0.f;
                 const uint32_t g0 = t == 1 ? done1 : done;
                 for (int j = 0; j < n && ok; ++j) {
                     const uint32_t g = g0 + j, buf = g & 1u;
@@ -529,6 +565,12 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                         m_run = m_new;
                         l0 *= alpha;
                         l1 *= alpha;
+                    }
+                    if constexpr (PARTS == 2) {
+                        if (g >= 2 && !(ok = wait(&o_free[buf], ((g >> 1) - 1) & 1u))) break;
+                        alphaS[buf * 128 + (warp & 3) * 32 + lane] = alpha;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&a_full[buf]);
                     }
                     const float off = finite_max(m_run);
                     const float2 kk = make_float2(kq, kq), oo = make_float2(-off, -off);
@@ -575,76 +617,31 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                     tc_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&p_full[2 * t + buf]);
-                    if constexpr (PARTS == 2) {
-                        // the page before: its products, in its own maximum's units, then this page's
-                        if (j > 0) {
-                            if (!(ok = wait_values(t, g - 1))) break;
-                            tc_after();
-#pragma unroll
-                            for (int c = 0; c < kD; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(v, lanes + SM::kColO + (buf ^ 1u) * kD + c);
-                                tmem_wait_ld(v);
-                                const float2 aa = make_float2(alpha, alpha);
-#pragma unroll
-                                for (int i = 0; i < 32; i += 2) {
-                                    const float2 x = mul2(add2(make_float2(o[c + i], o[c + i + 1]), make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))), aa);
-                                    o[c + i] = x.x;
-                                    o[c + i + 1] = x.y;
-                                }
-                            }
-                        }
-                    }
                 }
                 // ---- the row's partial
-                if (ok && n > 0) {
-                    ok = wait_values(t, g0 + n - 1);
-                    tc_after();
-                } else if (ok) {
-                    ok = wait(q_full, items & 1u);  // (nothing else says that q' has landed, whose place is written below)
-                }
-                if (ok) {
-                    // o' goes through the warp's quarter of its Q' tile (no product reads that any more), so
-                    // that a store of the warp covers whole lines: 16 rows' 16 bytes a piece cost eight times
-                    // the cycles.  Row r's chunk c of 16 lies at chunk c ^ (r & 15).
-                    const float l = l0 + l1;
-                    uint8_t* stage = smem + SM::kQ + t * PARTS * SM::kQTile + (warp & 3) * (SM::kQTile / 4);
-                    float* parts = p.sh_part + (size_t)it.part0 * p.part_stride;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // 64 positions at a time
-#pragma unroll
-                        for (int c = 0; c < 64; c += 32) {
-                            uint32_t v[32];
+                if constexpr (PARTS == 1) {
+                    if (ok && n > 0) {
+                        ok = wait_values(t, g0 + n - 1);
+                        tc_after();
+                    } else if (ok) {
+                        ok = wait(q_full, items & 1u);  // (nothing else says that q' has landed, whose place is written below)
+                    }
+                    if (ok)
+                        store_rows(it, t, [&](int c, uint32_t (&v)[32]) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = 0u;
                             if (n > 0) {
-                                tmem_ld32(v, lanes + SM::kColO + (PARTS == 2 ? ((g0 + n - 1) & 1u) * kD : 0) + 64 * h + c);
+                                tmem_ld32(v, lanes + SM::kColO + c);
                                 tmem_wait_ld(v);
                             }
-                            if constexpr (PARTS == 2)
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(o[64 * h + c + i] + __uint_as_float(v[i]));
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<uint4*>(stage + lane * 256 + ((((c + i) >> 2) ^ (lane & 15)) << 4)) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        }
-                        __syncwarp();
-                        const int first = t * 128 + (warp & 3) * 32, c = lane & 15;
-#pragma unroll 4
-                        for (int i = lane >> 4; i < 32; i += 2) {
-                            if (first + i >= it.rows) break;
-                            const int rw = it.row0 + first + i;
-                            const uint4 x = *reinterpret_cast<const uint4*>(stage + i * 256 + ((c ^ (i & 15)) << 4));
-                            *reinterpret_cast<uint4*>(parts + (size_t)(rw >> gsh) * p.part_stride + (rw & (p.G - 1)) * kD + 64 * h + 4 * c) = x;
-                        }
-                        __syncwarp();
-                    }
-                    if (row_on) {
-                        float* part = parts + (size_t)(row >> gsh) * p.part_stride;
-                        const int head = row & (p.G - 1);
-                        part[p.G * kD + head] = l == 0.f ? -INFINITY : finite_max(m_run);
-                        part[p.G * kD + p.G + head] = l;
-                    }
+                        });
+                }
+                if (ok && row_on) {
+                    const float l = l0 + l1;
+                    float* part = p.sh_part + ((size_t)it.part0 + (row >> gsh)) * p.part_stride;
+                    const int head = row & (p.G - 1);
+                    part[p.G * kD + head] = l == 0.f ? -INFINITY : finite_max(m_run);
+                    part[p.G * kD + p.G + head] = l;
                 }
                 tc_before();
                 fence_async();  // (the next item's q' is copied over the staged rows)
@@ -654,10 +651,61 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
             done += n;
             if (tiles == 2) done1 += n;
         }
+    } else if (warp < SM::kRowWarps) {
+        // ------------------- sums of the products of values (PARTS = 2) ------------------
+        // (Registers for the softmax's 64 logits and these 128 sums were 3300 cycles of one
+        // warp per page.)
+        if constexpr (PARTS == 2) {
+            regs_up<SM::kSumRegs>();
+            pdl_wait();
+            for (int item = blockIdx.x; item < total; item += gridDim.x, ++items) {
+                const Work wk = find_item(p, item);
+                const int n = wk.n;
+                const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+                float o[kD];
+#pragma unroll
+                for (int d = 0; d < kD; ++d) o[d] = 0.f;
+                for (int j = 0; j < n && ok; ++j) {
+                    const uint32_t g = done + j, buf = g & 1u;
+                    if (!(ok = wait(&a_full[buf], (g >> 1) & 1u) && wait_values(0, g))) break;
+                    tc_after();
+                    const float alpha = alphaS[buf * 128 + (warp & 3) * 32 + lane];
+                    const float2 aa = make_float2(alpha, alpha);
+#pragma unroll
+                    for (int c = 0; c < kD; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(v, lanes + SM::kColO + buf * kD + c);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 x = fma2(make_float2(o[c + i], o[c + i + 1]), aa, make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                            o[c + i] = x.x;
+                            o[c + i + 1] = x.y;
+                        }
+                    }
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[buf]);
+                }
+                if (ok && n == 0) ok = wait(q_full, items & 1u);
+                if (ok)
+                    store_rows(wk.it, 0, [&](int c, uint32_t (&v)[32]) {
+#pragma unroll
+                        for (int d = 0; d < kD; d += 32)
+                            if (d == c)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(o[d + i]);
+                    });
+                fence_async();  // (as above)
+                block_sync();
+                if (*dead) break;
+                done += n;
+            }
+        }
     } else if (warp < SM::kMmaWarp) {
         // ----------------------------- dequantisation -----------------------------
         regs_down<SM::kDequantRegs>();
-        const int dw = warp - SM::kSoftWarps;
+        const int dw = warp - SM::kRowWarps;
         const int ng = 4 >> p.gshift;
         // K: a lane's token and 16-byte code chunk (lanes of a wavefront on distinct banks)
         const int ka = lane & 3, kt = 8 * dw + ((((lane >> 2) & 1) << 2) | (lane >> 3));
@@ -846,6 +894,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
                         if (t >= tiles || !ok) break;
                         const uint32_t gt = (t == 1 ? done1 : done) + j, buf = gt & 1u;
                         if (!(ok = wait(&p_full[2 * t + buf], (gt >> 1) & 1u))) break;
+                        if (PARTS == 2 && gt >= 2 && !(ok = wait(&o_free[buf], ((gt >> 1) - 1) & 1u))) break;
                         tc_after();
                         const uint32_t tt = tmem + t * SM::kTileCols;
                         const uint32_t pa = tt + SM::kColP + buf * 64, o = tt + SM::kColO + (PARTS == 2 ? buf * kD : 0);
