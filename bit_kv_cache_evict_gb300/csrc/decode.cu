@@ -274,9 +274,9 @@ __device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
         }
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, m));
-        // (4-bit: a head whose q' overflows fp32 does not set the power of two that its
-        // neighbours share, which would leave nothing of theirs)
-        if (lane == 0) mxU[u] = INT4 && !(mx < INFINITY) ? 0.f : mx;
+        // (4-bit and the modes: a head whose q' overflows fp32 does not set the power of two
+        // that its neighbours share, which would leave nothing of theirs)
+        if (lane == 0) mxU[u] = (INT4 || MODE != kModePlain) && !(mx < INFINITY) ? 0.f : mx;
         __syncwarp();
         if (p.boost)  // q' itself for the boost corrections
             *reinterpret_cast<float4*>(p.qrot + ((size_t)bk * p.NT * 4 + hl) * kD + 4 * lane) =

@@ -614,9 +614,12 @@ oscar_status oscar_pages_copy_device(size_t page_bytes, int32_t n_copies, const 
  *   workspace     as oscar_decode_attn, with room for the logits: 4 * Hq
  *                 bytes for each of the batch's 64 * max_pages positions
  * Sums are fp32, over the heads in order: the same call gives the same bits.
- * Tokens of a page that is skipped (a bad id) have weight 0.  A row that is
- * NaN in the output gives its weights NaN (4 bits; for 2 bits, whose decode
- * drops parts with a NaN sum, the weights of such a row are not specified).
+ * Tokens of a page that is skipped (a bad id) have weight 0.  A NaN or
+ * +infinite logit makes its output row NaN, as in the definition, and with it
+ * the scores of its tokens (for 2 bits too, unlike oscar_decode_attn).
+ * Precision: as oscar_decode_attn_int4; for 2 bits with an fp32 output the
+ * value products are centred and summed page by page, and a bf16 output's are
+ * those of oscar_decode_attn.
  * Errors: as the decode calls; UNSUPPORTED for other bits.
  */
 oscar_status oscar_decode_attn_weights(const oscar_shape* shape, int32_t bits, int32_t batch, const void* q,

@@ -174,6 +174,22 @@ def test_nan_in_a_shared_page_reaches_the_group_alone(bits, dtype):
 
 @BOTH
 @TYPES
+@pytest.mark.parametrize("bad", [0x7F80, 0x7FC0])          # bf16 infinity, NaN
+def test_a_bad_query_is_its_rows_matter_alone(bits, dtype, bad):
+    c = Scene(22, bits, [64 * 4 + 10] * 3 + [200], 8, 2, 64, groups=[0, 0, 0, -1], shared=4)
+    want = c.want()
+    rows = np.zeros((4, 8), bool)
+    for b, h in ((0, 1), (2, 7), (3, 0)):
+        c.q[b, h, 11] = bad
+        rows[b, h] = True
+    out = run(c, dtype)
+    assert out.isnan().cpu().numpy()[rows].all()
+    err = np.abs(out.float().cpu().numpy() - want[0])
+    assert (err <= out_tolerance(want[0], want[3], bits, dtype == BF16, dtype == BF16))[~rows].all()
+
+
+@BOTH
+@TYPES
 def test_same_bits_streams_and_a_graph_that_follows_the_groups(bits, dtype):
     c = Scene(19, bits, [64 * 9 + 17 * i for i in range(12)], 16, 4, 32, groups=[i % 2 for i in range(12)], shared=9)
     want = c.want()

@@ -110,8 +110,9 @@ def test_a_bad_page_is_reported_and_has_weight_0(bits, hq, hk):
     assert (got[1][0, 192:256] == 0.5).all() and (got[1][1, 256:300] == 0.5).all() and bad
 
 
-def test_a_nan_logit_makes_its_rows_and_weights_nan():
-    c = Scene(6, 4, [200, 90, 300], 8, 2, 32)
+@pytest.mark.parametrize("bits", [2, 4])
+def test_a_nan_logit_makes_its_rows_and_weights_nan(bits):
+    c = Scene(6, bits, [200, 90, 300], 8, 2, 32)
     want = c.want()
     v = c.pairs(c.table[0, 1], 1, 0, 5)
     v[0, 0] = np.nan
@@ -120,8 +121,24 @@ def test_a_nan_logit_makes_its_rows_and_weights_nan():
     assert out[0, 4:].isnan().all() and out[0, :4].isfinite().all()
     assert w[0, :200].isnan().all() and (w[0, 200:] == 0.5).all() and sw[0].isnan().all()
     ref, rw = want[0], want[1]
-    assert out[1:].isfinite().all() and np.abs(out[1:].cpu().numpy() - ref[1:]).max() < 1e-3
-    assert np.abs(w[1:].cpu().numpy() - 0.5 - rw[1:])[:, :90].max() < 1e-4
+    tol = out_tolerance(ref, want[3], bits, False)
+    assert (np.abs(out[1:].cpu().numpy() - ref[1:]) <= tol[1:]).all()
+    assert (np.abs(w[1:].cpu().numpy() - 0.5 - rw[1:])[:, :90] <= weight_tolerance(rw, want[4], 0.5, 8, bits)[1:, :90]).all()
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("bad", [0x7F80, 0x7FC0])          # bf16 infinity, NaN
+def test_a_bad_query_leaves_the_other_heads_of_its_group(bits, bad):
+    c = Scene(10, bits, [700, 64], 8, 2, 64)
+    want = c.want()
+    c.q[0, 1, 7] = bad
+    c.q[1, 6, 0] = bad
+    out, w, _ = run(c)
+    rows = np.zeros((2, 8), bool)
+    rows[0, 1] = rows[1, 6] = True
+    assert out.isnan().cpu().numpy()[rows].all()
+    tol = out_tolerance(want[0], want[3], bits, False)
+    assert (np.abs(out.cpu().numpy() - want[0]) <= tol)[~rows].all()
 
 
 @pytest.mark.parametrize("bits", [2, 4])

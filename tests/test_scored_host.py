@@ -110,6 +110,78 @@ def test_the_scenes_values_are_the_oracles(bits, g):
     assert np.allclose(want[1].sum(1) + want[2].sum(1), 4)
 
 
+class Fake:
+    """What the binding looks at of a contiguous CUDA tensor."""
+
+    is_cuda = True
+
+    def __init__(self, *shape, dtype=None):
+        import torch
+        self.shape, self.dtype = shape, dtype or torch.int32
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 4096
+
+
+def test_the_binding_refuses_wrong_tensors(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)   # (no GPU here)
+    O._torch_names()
+    monkeypatch.setattr(O, "_raw_stream", lambda d: 0)
+    monkeypatch.setattr(O, "_current_device", lambda: 0)
+    f32, bf16, u8 = torch.float32, torch.bfloat16, torch.uint8
+    B_, hq, hk, pages = 2, 8, 2, 3
+    good = dict(q=Fake(B_, hq, 128, dtype=bf16), kv=Fake(B_, 320, hk, 2, 128, dtype=bf16), len=Fake(B_), pool=Fake(9 * hk * 10240, dtype=u8),
+                table=Fake(B_, pages), hist=Fake(B_), U=Fake(hk, 2, 128, 128, dtype=f32), out=Fake(B_, hq, 128, dtype=f32),
+                ws=Fake(1 << 40, dtype=u8), w=Fake(B_, 64 * pages, dtype=f32), sw=Fake(B_, 320, dtype=f32), group=Fake(B_), gp=Fake(1))
+
+    def weights(**k):
+        a = good | k
+        O.oscar_decode_attn_weights(sh(hq, hk), 4, a["q"], a["kv"], a["len"], a["pool"], a["table"], pages, 9, a["hist"], a["U"], 0.1, a["out"], a["w"],
+                                    a["ws"], slot_weight=a["sw"])
+
+    def shared(**k):
+        a = good | k
+        O.oscar_decode_attn_shared(sh(hq, hk), 4, a["q"], a["kv"], a["len"], a["pool"], a["table"], pages, 9, a["hist"], a["group"], a["gp"], a["U"],
+                                   0.1, a["out"], a["ws"])
+
+    bad = (dict(q=Fake(B_, hq, 128, dtype=f32)), dict(kv=Fake(5, dtype=bf16)), dict(len=Fake(1)), dict(pool=Fake(9 * hk * 10240 - 1, dtype=u8)),
+           dict(table=Fake(B_, pages - 1)), dict(hist=Fake(1)), dict(U=Fake(1, dtype=f32)), dict(out=Fake(B_, hq, 127, dtype=f32)),
+           dict(out=Fake(B_, hq, 128, dtype=torch.float16)))
+    for k in bad:
+        with pytest.raises((TypeError, ValueError)):
+            weights(**k)
+        with pytest.raises((TypeError, ValueError)):
+            shared(**k)
+    for k in (dict(w=Fake(1, 64 * pages, dtype=f32)), dict(w=Fake(B_ * 64 * pages, dtype=f32)), dict(w=Fake(B_, 64 * pages)), dict(sw=Fake(B_, 319, dtype=f32))):
+        with pytest.raises((TypeError, ValueError)):
+            weights(**k)
+    with pytest.raises(O.OscarError):                       # the library's own refusal: rows too short for the table
+        weights(w=Fake(B_, 64 * pages - 1, dtype=f32))
+    for k in (dict(group=Fake(1)), dict(gp=Fake(1, dtype=f32))):
+        with pytest.raises((TypeError, ValueError)):
+            shared(**k)
+    ok = dict(weight=Fake(2, 50, dtype=f32), hist_len=Fake(2), budget=Fake(2), keep=Fake(2, 10), n_keep=Fake(2), kept_weight=Fake(2, 10, dtype=f32))
+    for k in (dict(keep=Fake(1, 10)), dict(kept_weight=Fake(1, 10, dtype=f32)), dict(kept_weight=Fake(20, dtype=f32)), dict(hist_len=Fake(1)),
+              dict(budget=Fake(2, dtype=f32)), dict(n_keep=Fake(1)), dict(weight=Fake(2, 50))):
+        with pytest.raises((TypeError, ValueError)):
+            O.oscar_history_select(**(ok | k))
+    with pytest.raises(O.OscarError):                       # every Fake lies at one address: kept_weight over weight
+        O.oscar_history_select(**ok)
+
+
 def I_f64(bits):
     from history_scene import f64
     return f64(bits)
