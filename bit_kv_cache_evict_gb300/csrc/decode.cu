@@ -2417,7 +2417,7 @@ static cudaError_t decode_weights(const DecodeParamsX& pin, cudaStream_t st) {
     const int rpb = kMergeWarps / p.merge_wpr;
     dim3 mg((p.B * p.G + rpb - 1) / rpb, p.hk);
     if ((e = launch_pdl(merge_kernel<INT4, MODE>, mg, dim3(kMergeThreads), kMergeSmem, st, p)) != cudaSuccess) return e;
-    const int chunks = (p.max_pages * kPage + kWeightThreads - 1) / kWeightThreads;
+    const int chunks = (p.max_pages + kWeightThreads / kPage - 1) / (kWeightThreads / kPage);
     const int slot_chunks = p.slot_weight ? (p.nslot + kWeightThreads - 1) / kWeightThreads : 0;
     return launch_pdl(weights_kernel, dim3((unsigned)p.B * (chunks + slot_chunks)), dim3(kWeightThreads), 0, st, p, chunks, slot_chunks);
 }

@@ -185,3 +185,16 @@ def test_layers_accumulate_into_one_array():
     inside = np.arange(ref.shape[1]) < a.hist[:, None]
     tol = weight_tolerance(wa[1], wa[4], 1.0, 8, 4) + weight_tolerance(wb[1], wb[4], 2.0, 4, 4)
     assert (np.abs(w.cpu().numpy() - ref)[inside] <= tol[inside]).all()
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+def test_the_widest_table(bits):
+    """64 * max_pages positions just below 2^31 (the scores and the workspace take 9 GB each)."""
+    c = Scene(11, bits, [700], 1, 1, 128)
+    want, d, most = c.want(), c.device(), (2**31 - 1) // 64
+    c.d = dict(d, table=torch.cat([d["table"], torch.full((1, most - c.max_pages), -1, dtype=torch.int32, device="cuda")], 1))
+    c.max_pages = most
+    out, w, sw = run(c)
+    n = want[1].shape[1]
+    assert bool((w[:, n:] == 0.5).all())
+    check(c, (out, w[:, :n], sw), want, F32)
