@@ -1591,9 +1591,11 @@ constexpr int kBfThreads = 32 * kBfWarps;
 constexpr int kBfItemTok = 16 * kBfWarps;          // tokens per block
 constexpr int kBfPitch = 528;                      // bytes per staged token row (512 + 16)
 constexpr int kBfWarpBytes = 16 * kBfPitch;        // also holds the warp's state [G][kD + 2] at the end
-constexpr int kBfQBytes = 8 * kD * 2;                 // query rows of one KV group (up to 8 heads)
+constexpr int kBfState = kD + 8;                      // floats per head of a warp's state: o[128], m, l (rows on distinct banks)
+constexpr int kBfQPitch = kD * 2 + 16;                // bytes per staged query row (rows on distinct banks)
+constexpr int kBfQBytes = 8 * kBfQPitch;              // query rows of one KV group (up to 8 heads)
 constexpr int kBfSmem = 2 * kBfWarps * kBfWarpBytes + 2 * kBfQBytes;  // two buffers
-static_assert(8 * (kD + 2) * 4 <= kBfWarpBytes, "warp state must fit in the warp's row tile");
+static_assert(8 * kBfState * 4 <= kBfWarpBytes && kBfWarpBytes % 16 == 0, "warp state must fit in the warp's row tile");
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -1638,7 +1640,7 @@ __device__ __forceinline__ bool holds(float l) {
 }
 
 // One warp's 16-token tile from staged rows and the staged query rows of
-// its KV group (qsm: [G][kD] bf16); leaves the warp's state (o, m, l) per
+// its KV group (qsm: [G][kBfQPitch] bytes, bf16); leaves the warp's state (o, m, l) per
 // head in rows.  MMA row h holds head h (rows G..15 are zero): S = Q.K^T,
 // then O += P.V twice into the same accumulators, with A = the bf16 high
 // part of P (its low 16 bits cleared, exact) and A = the rounded remainder,
@@ -1647,18 +1649,18 @@ __device__ __forceinline__ bool holds(float l) {
 // that a bf16 output is the fp32 one rounded.
 // keep (kModeWeights): the tile's logits go to keep[token][G].
 template <int G, bool INT4, Mode MODE>
-__device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, float qscale, float* keep) {
+__device__ __forceinline__ void bf16_tile(int nvalid, uint8_t* rows, const uint8_t* qsm, float qscale, float* keep) {
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
-    float* st = reinterpret_cast<float*>(rows);  // [G][kD + 2] at the end
+    float* st = reinterpret_cast<float*>(rows);  // [G][kBfState] at the end
     if (nvalid <= 0) {
-        for (int i = lane; i < G * (kD + 2); i += 32) {
-            const int c = i % (kD + 2);
+        for (int i = lane; i < G * kBfState; i += 32) {
+            const int c = i % kBfState;
             st[i] = (c == kD) ? -INFINITY : 0.f;
         }
         return;
     }
     const bool row_on = gID < G;
-    const __nv_bfloat16* qa = qsm + (row_on ? gID : 0) * kD;
+    const __nv_bfloat16* qa = reinterpret_cast<const __nv_bfloat16*>(qsm + (row_on ? gID : 0) * kBfQPitch);
     uint32_t qf[8][2];  // A fragments (rows gID: a0, a2; rows gID + 8 are zero)
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
@@ -1745,10 +1747,46 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
     if (row_on) {  // head gID: accumulator row gID
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            *reinterpret_cast<float2*>(st + gID * (kD + 2) + 8 * j + 2 * tq) = make_float2(o[j][0], o[j][1]);
-        if (tq == 0) {
-            st[gID * (kD + 2) + kD] = ma;
-            st[gID * (kD + 2) + kD + 1] = la;
+            *reinterpret_cast<float2*>(st + gID * kBfState + 8 * j + 2 * tq) = make_float2(o[j][0], o[j][1]);
+        if (tq == 0) *reinterpret_cast<float2*>(st + gID * kBfState + kD) = make_float2(ma, la);
+    }
+}
+
+// The four warps' states (in rows0 + w * kBfWarpBytes) into the item's partial: a warp
+// per head, a lane per four dimensions.
+template <int G, bool INT4>
+__device__ __forceinline__ void bf16_merge(const uint8_t* rows0, float* part) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = threadIdx.x >> 5; h < G; h += kBfWarps) {
+        float2 ml[kBfWarps];
+        float4 o[kBfWarps];
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kBfWarps; ++w) {
+            const float* src = reinterpret_cast<const float*>(rows0 + w * kBfWarpBytes) + h * kBfState;
+            ml[w] = *reinterpret_cast<const float2*>(src + kD);
+            o[w] = *reinterpret_cast<const float4*>(src + 4 * lane);
+            M = fmaxf(M, ml[w].x);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
+        if (INT4 || M != -INFINITY) {
+            const float sub = INT4 ? finite_max(M) : M;
+#pragma unroll
+            for (int w = 0; w < kBfWarps; ++w) {
+                const float sc = ex2(ml[w].x - sub);
+                acc.x = fmaf(sc, o[w].x, acc.x);
+                acc.y = fmaf(sc, o[w].y, acc.y);
+                acc.z = fmaf(sc, o[w].z, acc.z);
+                acc.w = fmaf(sc, o[w].w, acc.w);
+                L = fmaf(sc, ml[w].y, L);
+            }
+        }
+        *reinterpret_cast<float4*>(part + h * kD + 4 * lane) = acc;
+        if (lane == 0) {
+            part[G * kD + h] = M;
+            part[G * kD + G + h] = L;
         }
     }
 }
@@ -1756,7 +1794,10 @@ __device__ void bf16_tile(int nvalid, uint8_t* rows, const __nv_bfloat16* qsm, f
 // Persistent: 3 blocks per SM loop over the (sequence, KV head, 64-slot
 // block) items with two buffers per warp, so that the next item's rows (and
 // its query rows, staged by warp 0) are in flight while the current item is
-// attended.  Launched as a programmatic dependent of int2_kernel, whose
+// attended.  What bounds it is the length of an item's way through a block, at 12
+// warps per SM: two barriers per item, state and query rows on distinct banks, a
+// merge of one warp per head and the first item's copies before the counter's atomics
+// took 82 -> 71 us (256 windows of 320, 32:8 heads: 335 MB).  Launched as a programmatic dependent of int2_kernel, whose
 // results it does not read; its block 0 waits for int2_kernel's completion
 // before it exits (the others leave when their items are done), so this grid
 // completes after int2_kernel and the merge after it sees both.
@@ -1780,7 +1821,7 @@ bf16_kernel(std::conditional_t<MODE == kModeWeights, DecodeParamsX, DecodeParams
                 const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + ((size_t)b * p.hq + kv * p.G) * kD);
                 uint8_t* qdst = q_of(buf);
                 for (int c = lane; c < p.G * (kD * 2 / 8); c += 32)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(qdst + 8 * c)),
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(qdst + (c >> 5) * kBfQPitch + 8 * (c & 31))),
                                  "l"(qsrc + 8 * c)
                                  : "memory");
             }
@@ -1795,68 +1836,47 @@ bf16_kernel(std::conditional_t<MODE == kModeWeights, DecodeParamsX, DecodeParams
     __shared__ int s_it[2];
     int32_t* ctr = p.counter + kBfCounter;
     int pend = 0;  // thread 0: the item after the next one
+    int it = blockIdx.x;
+    stage(it, 0);
     if (threadIdx.x == 0) {
-        s_it[0] = blockIdx.x;
         s_it[1] = gridDim.x + atomicAdd(ctr, 1);
         pend = gridDim.x + atomicAdd(ctr, 1);
     }
-    __syncthreads();
     int buf = 0;
-    int it = s_it[0];
-    stage(it, 0);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
     for (; it < total; buf ^= 1) {
         const int nxt = s_it[buf ^ 1];
         stage(nxt, buf ^ 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();  // this item's rows and query rows have landed
         const int bk = it / p.bf_items, item = it % p.bf_items;
         const int b = bk / p.hk;
         const int n = min(max(__ldg(p.bf16_len + b), 0), p.nslot);
         const int t0 = item * kBfItemTok + 16 * warp;
-        uint8_t* rows = rows_of(buf, warp);
-        const __nv_bfloat16* qsm = reinterpret_cast<const __nv_bfloat16*>(q_of(buf));
         float* keep = nullptr;
         if constexpr (MODE == kModeWeights) keep = p.slot_logits + ((size_t)bk * p.nslot + t0) * p.G;
-        switch (p.G) {
-            case 1: bf16_tile<1, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
-            case 2: bf16_tile<2, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
-            case 4: bf16_tile<4, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
-            default: bf16_tile<8, INT4, MODE>(n - t0, rows, qsm, p.qscale, keep); break;
-        }
-        __syncthreads();
-        // merge the four warps: thread -> dimension
         float* part = p.bf_part + ((size_t)bk * p.bf_items + item) * p.part_stride;
-        const int d = threadIdx.x;
-        for (int h = 0; h < p.G; ++h) {
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kBfWarps; ++w)
-                M = fmaxf(M, reinterpret_cast<const float*>(rows_of(buf, w))[h * (kD + 2) + kD]);
-            float acc = 0.f, L = 0.f;
-            if (INT4 || M != -INFINITY) {
-                const float sub = INT4 ? finite_max(M) : M;
-#pragma unroll
-                for (int w = 0; w < kBfWarps; ++w) {
-                    const float* src = reinterpret_cast<const float*>(rows_of(buf, w)) + h * (kD + 2);
-                    const float sc = ex2(src[kD] - sub);
-                    acc = fmaf(sc, src[d], acc);
-                    L = fmaf(sc, src[kD + 1], L);
-                }
-            }
-            part[(size_t)h * kD + d] = acc;
-            if (d == 0) {
-                part[(size_t)p.G * kD + h] = M;
-                part[(size_t)p.G * kD + p.G + h] = L;
-            }
+        auto attend = [&](auto heads) {
+            constexpr int G = decltype(heads)::value;
+            bf16_tile<G, INT4, MODE>(n - t0, rows_of(buf, warp), q_of(buf), p.qscale, keep);
+            __syncthreads();
+            bf16_merge<G, INT4>(rows_of(buf, 0), part);
+        };
+        switch (p.G) {
+            case 1: attend(std::integral_constant<int, 1>{}); break;
+            case 2: attend(std::integral_constant<int, 2>{}); break;
+            case 4: attend(std::integral_constant<int, 4>{}); break;
+            default: attend(std::integral_constant<int, 8>{}); break;
         }
         if (threadIdx.x == 0) {  // the item staged into this buffer after nxt
             s_it[buf] = pend;
             pend = gridDim.x + atomicAdd(ctr, 1);
         }
-        __syncthreads();  // states read before this buffer is refilled; s_it[buf] visible
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // states read before this buffer is refilled; s_it[buf] visible; the next item's rows
+        // and query rows have landed
+        __syncthreads();
         it = nxt;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) pdl_wait();  // this grid completes after int2_kernel
 }
 
