@@ -206,9 +206,7 @@ __device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + 16 * i)), "l"(src + 16 * i)
                          : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    __syncthreads();
 
     // Two passes over the block's (b, nt, hh) units.  Pass 1: q' of every
     // unit into shared memory and its largest |q'|.  Pass 2: one power of
@@ -219,6 +217,46 @@ __device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
     const int units = nseq * p.NT * 4;
     float* qU = psm + kD * kD;               // [unit][kD] q' in stored order
     float* mxU = qU + kPrepUnits * kD;       // [unit] largest |q'| (0 for padding)
+    // q U_K first: a warp per 32 columns and half of the units, a lane per column.  An element of U_K
+    // is read once for the warp's units, the units' x[a] come as one or two 16-byte broadcasts
+    // (a warp per unit read all of U_K for each, 80 % of the shared-memory rate).
+    float* xS = qU;                          // [a][kPrepUnits] first, then the products [unit][kD]
+    for (int u = warp; u < kPrepUnits; u += kPrepThreads / 32) {
+        const int hl = 4 * ((u >> 2) % p.NT) + (u & 3), b = b0 + (u >> 2) / p.NT;
+        uint2 qr = make_uint2(0u, 0u);
+        if (u < units && hl < p.G) qr = *reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.hq + kv * p.G + hl) * kD + 4 * lane);
+        xS[(4 * lane + 0) * kPrepUnits + u] = bf16_lo(qr.x);
+        xS[(4 * lane + 1) * kPrepUnits + u] = bf16_hi(qr.x);
+        xS[(4 * lane + 2) * kPrepUnits + u] = bf16_lo(qr.y);
+        xS[(4 * lane + 3) * kPrepUnits + u] = bf16_hi(qr.y);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    const int col = 32 * (warp & 3) + lane, half = warp >> 2;
+    auto products = [&](auto quads) {        // units 4 Q half .. + 4 Q - 1
+        constexpr int Q = decltype(quads)::value;
+        float y[4 * Q];
+#pragma unroll
+        for (int i = 0; i < 4 * Q; ++i) y[i] = 0.f;
+#pragma unroll 4
+        for (int a = 0; a < kD; ++a) {
+            const float uu = Us[a * kD + col];
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const float4 x = *reinterpret_cast<const float4*>(xS + a * kPrepUnits + 4 * (Q * half + i));
+                y[4 * i] = fmaf(x.x, uu, y[4 * i]);
+                y[4 * i + 1] = fmaf(x.y, uu, y[4 * i + 1]);
+                y[4 * i + 2] = fmaf(x.z, uu, y[4 * i + 2]);
+                y[4 * i + 3] = fmaf(x.w, uu, y[4 * i + 3]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4 * Q; ++i) qU[(4 * Q * half + i) * kD + col] = y[i];
+    };
+    if (p.NT == 1) products(std::integral_constant<int, 1>{});
+    else products(std::integral_constant<int, 2>{});
+    __syncthreads();
     for (int u = warp; u < units; u += kPrepThreads / 32) {
         const int hl = 4 * ((u >> 2) % p.NT) + (u & 3);  // head within the KV group
         const int b = b0 + (u >> 2) / p.NT;
@@ -231,22 +269,9 @@ __device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
                     make_float4(0.f, 0.f, 0.f, 0.f);
             continue;
         }
-        const int h = kv * p.G + hl;
-        const uint2 qr = *reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.hq + h) * kD + 4 * lane);
-        const float x[4] = {bf16_lo(qr.x), bf16_hi(qr.x), bf16_lo(qr.y), bf16_hi(qr.y)};
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int a4 = 0; a4 < kD; a4 += 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float xa = __shfl_sync(kFull, x[i], a4 >> 2);
-                const float4 uu = *reinterpret_cast<const float4*>(Us + (size_t)(a4 + i) * kD + 4 * lane);
-                y[0] = fmaf(xa, uu.x, y[0]);
-                y[1] = fmaf(xa, uu.y, y[1]);
-                y[2] = fmaf(xa, uu.z, y[2]);
-                y[3] = fmaf(xa, uu.w, y[3]);
-            }
-        }
+        const float4 prod = *reinterpret_cast<const float4*>(qs + 4 * lane);
+        float y[4] = {prod.x, prod.y, prod.z, prod.w};
+        __syncwarp();  // (q' takes the products' place)
         {  // Hadamard, in-lane stages
             const float t0 = y[0] + y[1], t1 = y[0] - y[1], t2 = y[2] + y[3], t3 = y[2] - y[3];
             y[0] = t0 + t2;
