@@ -643,7 +643,7 @@ oscar_status oscar_decode_attn_weights(const oscar_shape* shape, int32_t bits, i
  *   hist_len, budget (device int32 [batch])
  *   keep         (device int32 [batch][keep_stride], out) the first m entries
  *                of a row are written, the others left as they were
- *   n_keep       (device int32 [batch], out) m
+ *   n_keep       (device int32 [batch], out) m; may be hist_len or budget itself
  *   kept_weight  (device fp32 [batch][kept_stride], out, or NULL) the kept
  *                tokens' scores at their new positions 0 .. m - 1; may not
  *                overlap weight

@@ -147,3 +147,18 @@ def test_a_captured_call_follows_its_inputs():
         for b in range(3):
             want = ref_select(w[b].cpu().numpy(), int(hist[b]), int(budget[b]), 8)
             assert int(n[b]) == len(want) and np.array_equal(keep[b, :len(want)].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n", [700, 20000])
+def test_the_new_lengths_over_the_old(n):
+    """n_keep may be hist_len or budget itself: one thread block per sequence, and several."""
+    rng = np.random.default_rng(n)
+    w = rng.random((3, n)).astype(np.float32)
+    old = {"hist": [n, n // 2, 9], "budget": [n // 3, n, 0]}
+    for place in old:
+        t = {k: torch.tensor(v, dtype=torch.int32, device="cuda") for k, v in old.items()}
+        keep = torch.zeros(3, n, dtype=torch.int32, device="cuda")
+        O.oscar_history_select(torch.from_numpy(w).cuda(), t["hist"], t["budget"], keep, t[place], protect=5)
+        for b in range(3):
+            want = ref_select(w[b], old["hist"][b], old["budget"][b], 5)
+            assert int(t[place][b]) == len(want) and np.array_equal(keep[b, :len(want)].cpu().numpy(), want)
