@@ -20,7 +20,8 @@
 // pages in merge_kernel.
 //
 // PARTS = 1 (bf16 output): Q', K, V and P as fp16, off by 2^-11 at most per rounding.  PARTS = 2
-// (fp32 output): each as two fp16 parts, three products, 22 bits, and the value
+// (fp32 output): each as two fp16 parts, three products, 22 bits (a weight down to 2^-40 of
+// the largest of its run of pages so far), and the value
 // products of each page are summed from zero and added in fp32 registers, as
 // the tensor core truncates its accumulator (int4.cu, page_values).
 #include <algorithm>
@@ -388,6 +389,11 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // 2^-25 off at most below.  A warp rescales when one of its 32 rows asks for it, so
 // with 8 every second page of logits of deviation 5 did, at 2000 cycles each.
 constexpr float kSlack = 15.f;
+// PARTS = 2 has no slack: what is subtracted lies this much below the maximum, so that P takes
+// up to the same 2^15 and the two parts of a weight end 2^-40 below the largest.  (With
+// a P of 1 at most, weights below 2^-25 of it were 0 in the products and counted in their sum: one
+// token in front of 32K others lost the output up to 7e-4 of the largest value, now less than 3e-5.)
+constexpr float kLift2 = 15.f;
 
 // An item's record, its page-table row and the number of its pages that can be read.
 struct Work {
@@ -556,7 +562,7 @@ __global__ void __launch_bounds__(SharedSmem<BITS, PARTS>::kThreads, 1) shared_k
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         mx4[i & 3] = fmaxf(mx4[i & 3], fmaxf(__uint_as_float(s[0][i]), __uint_as_float(s[1][i])));
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * kq;
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * kq - (PARTS == 2 ? kLift2 : 0.f);
                     float alpha = 1.f;
                     const bool any = __any_sync(kFull, PARTS == 2 ? mx > m_run : mx > m_run + kSlack);
                     if (any) {

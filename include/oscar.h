@@ -679,7 +679,8 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
  * sequence whose history ends inside its group's pages attends by itself, as
  * do the members of groups that are too small.  A prefix_group of n_groups or more (no group) and
  * group_pages outside [0, max_pages] (clamped) are reported as BAD_POS.
- * Precision: fp32 output as oscar_decode_attn_int4.  For a bf16 output the
+ * Precision: fp32 output as oscar_decode_attn_int4; a weight below 2^-40 of the
+ * largest of its run of shared pages is 0 in the products.  For a bf16 output the
  * pages attended together: queries, values s * code + z and weights enter products
  * as fp16, one rounding of 2^-11 (relative) each; the rest as for fp32, but that 2-bit
  * pages of a sequence's own are summed as in oscar_decode_attn.  Shared
