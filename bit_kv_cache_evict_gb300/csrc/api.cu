@@ -90,22 +90,26 @@ static int64_t items4_bound(int64_t pairs, int max_pages) {
 }
 
 // Most partials (member, KV head, split) of the shared pages that group_kernel's
-// plan makes: an item is a KV head, up to `rows` rows and a run of pages.
-//   one item for each block at most; or, where whole groups are more, four times
-//   that and one per KV head and row tile for the rounding; runs have
-//   kMinSharedPages pages at least but for one per group and KV head.
+// plan makes: an item is a KV head, up to `rows` rows and a run of pages, of which a group has
+// one for every kMinSharedPages pages at most.
+//   one item for each block at most; or, where the longest runs are more, four times
+//   that and one per KV head and row tile for the rounding; or, where a share is more than
+//   kMaxSharedRun pages, runs of that many.
 // Row tiles: each group's last one may be partly filled; groups have two members at least.
 static int64_t shared_tiles_bound(const oscar_shape* s, int batch, int n_groups) {
     const int64_t hk = s->num_kv_heads, G = s->num_q_heads / hk, groups = std::min(n_groups, batch / 2);
     return groups ? hk * ((batch * G + 127) / 128 + groups) : 0;
 }
-static int64_t shared_items_bound(const oscar_shape* s, int batch, int n_groups) {
+static int64_t shared_share_bound(int64_t tiles) { return tiles ? 17 * kMaxSharedBlocks / 4 + tiles : 0; }  // (runs of 16 pages at least, rounded down)
+static int64_t longest_runs(int max_pages) { return (max_pages + kMaxSharedRun - 1) / kMaxSharedRun; }
+static int64_t shared_items_bound(const oscar_shape* s, int batch, int max_pages, int n_groups) {
     const int64_t tiles = shared_tiles_bound(s, batch, n_groups);
-    return tiles ? 17 * kMaxSharedBlocks / 4 + tiles : 0;  // (runs of 16 pages at least, rounded down)
+    return std::max(shared_share_bound(tiles), tiles * longest_runs(max_pages));
 }
 static int64_t shared_parts_bound(const oscar_shape* s, int batch, int max_pages, int n_groups) {
-    const int64_t hk = s->num_kv_heads, G = s->num_q_heads / hk, rows = 256;
-    return std::min(shared_items_bound(s, batch, n_groups) * (rows / G), batch * hk * ((max_pages + kMinSharedPages - 1) / kMinSharedPages));
+    const int64_t hk = s->num_kv_heads, G = s->num_q_heads / hk, rows = 256, pairs = batch * hk;
+    const int64_t share = shared_share_bound(shared_tiles_bound(s, batch, n_groups)) * (rows / G);
+    return std::min(std::max(share, pairs * longest_runs(max_pages)), pairs * ((max_pages + kMinSharedPages - 1) / kMinSharedPages));
 }
 
 static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bits, Mode mode = kModePlain, int n_groups = 0) {
@@ -157,7 +161,7 @@ static WsLayout ws_layout(const oscar_shape* s, int batch, int max_pages, int bi
         w.qref = off;
         off = round_up(off + (size_t)batch * 16, 256);
         w.items = off;
-        off = round_up(off + (size_t)shared_items_bound(s, batch, n_groups) * sizeof(SharedItem), 256);
+        off = round_up(off + (size_t)shared_items_bound(s, batch, max_pages, n_groups) * sizeof(SharedItem), 256);
         w.qtile = off;
         off = round_up(off + (size_t)shared_tiles_bound(s, batch, n_groups) * 2 * kQTileBytes, 256);
         w.qtile_kinv = off;

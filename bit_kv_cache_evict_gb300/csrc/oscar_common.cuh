@@ -421,6 +421,10 @@ enum Mode { kModePlain = 0, kModeWeights = 1, kModeShared = 2 };
 
 constexpr int kSharedItems = 10;        // index of the shared pages' item count in the counters
 constexpr int kMinSharedPages = 4;      // pages of an item of a group at least (but for its last)
+// and at most: with a bf16 output the products of values of an item are summed where the tensor
+// core truncates them, 2^-24 of the running sum at each; over 2^14 tokens that stays
+// below 2^-10 of the largest value (16384 pages as one item: up to 2 % of it, a flat softmax 0.7 %).
+constexpr int kMaxSharedRun = 256;
 constexpr int kMaxSharedGroups = 8192;
 constexpr int kMaxSharedBlocks = 160;   // thread blocks of shared_kernel, one per SM, at most
 constexpr int kQTileBytes = 128 * kD * 2;  // a tile of 128 rows of fp16 q', as the products read it

@@ -118,14 +118,14 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
     auto row_tiles = [&](int g, int of) { return (count[g] * p.G + of - 1) / of; };
     if (warp == 0) {
         // Pages per item: the smallest number that leaves at most one item for each
-        // block; where even whole groups are more, a quarter of a block's share.
+        // block; where even whole groups (or the longest runs) are more, a quarter of a block's share.
         auto items_at = [&](int pps) {  // (each group's share is cut off far above what it is compared with)
             unsigned n = 0;
             for (int g = lane; g < p.n_groups; g += 32)
                 n += (unsigned)min((long)row_tiles(g, rows) * ((pages[g] + pps - 1) / pps) * p.hk, 1l << 16);
             return __reduce_add_sync(kFull, n);
         };
-        int lo = kMinSharedPages, hi = max(lo, p.max_pages);
+        int lo = kMinSharedPages, hi = min(max(lo, p.max_pages), kMaxSharedRun);
         int pps;
         if (items_at(hi) <= (unsigned)p.shared_blocks) {
             while (lo < hi) {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) group_kernel(DecodeParamsX p, in
             for (int g = lane; g < p.n_groups; g += 32) total += (long)row_tiles(g, rows) * pages[g];
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
-            pps = (int)max((long)kMinItemPages4, min((long)p.max_pages, total * p.hk / (4 * p.shared_blocks)));
+            pps = (int)max((long)kMinItemPages4, min((long)min(p.max_pages, kMaxSharedRun), total * p.hk / (4 * p.shared_blocks)));
         }
         int run_part = 0, run_item = 0, run_tile = 0;
         for (int g0 = 0; g0 < p.n_groups; g0 += 32) {

@@ -682,7 +682,9 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
  * Precision: fp32 output as oscar_decode_attn_int4; a weight below 2^-40 of the
  * largest of its run of shared pages is 0 in the products.  For a bf16 output the
  * pages attended together: queries, values s * code + z and weights enter products
- * as fp16, one rounding of 2^-11 (relative) each; the rest as for fp32, but that 2-bit
+ * as fp16, one rounding of 2^-11 (relative; a weight: or of 2^-25 of the largest) each, and the
+ * products of values are summed over up to 2^14 tokens in the tensor core, within
+ * 2^-10 of the largest value; the rest as for fp32, but that 2-bit
  * pages of a sequence's own are summed as in oscar_decode_attn.  Shared
  * values s * code + z have to be finite in fp16 (|value| < 65520); NaN, and
  * what overflows, reaches the rows that attend it as NaN.

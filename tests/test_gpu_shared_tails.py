@@ -79,3 +79,17 @@ def test_fp32(bits, at, peak):
     tol = share * mean * 2 * gap[:, None] * 2.0 ** -19 + big * (2.0 ** -20 + 512 * 2.0 ** -24)
     err = np.abs(got - ref)
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("bits", [2, 4])
+@pytest.mark.parametrize("at,peak", [(0, (25.3, 27.7)), (63, (25.3, 27.7)), (0, (0.0, 0.5))])
+def test_bf16(bits, at, peak):
+    """16384 shared pages: a long tail (up to 2.5 % of the weight), and a flat softmax.  Bound: q' and k rounded to fp16 move a logit
+    by A 2^-10 and a tail weight by 2 ln 2 times that; weights and values rounded to fp16, 2^-10 of the largest value; the
+    products, truncated to 2^-24 of a sum over 256 pages at most: half of 2^14 2^-24 on the average of a flat softmax, and of a tail no more than its
+    share in 256 pages is lost, 2^-11: 2^-11 of the largest; 2^-8 for the output."""
+    c, ref, gap, share, big, mean = tail_scene(bits, 16384, at, peak)
+    got = run(c, BF16)
+    tol = share * mean * 2 * gap[:, None] * 2.0 ** -10 + big * (2.0 ** -10 + 2.0 ** -11) + np.abs(ref) * 2.0 ** -8
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (err / tol).max()
