@@ -501,18 +501,49 @@ __device__ __forceinline__ int pv_pos(int t) {
     return 4 * (4 * tq + (m ^ tq)) + pv_slot(t & 3);
 }
 constexpr int kPvRow = 72;  // floats per probability / V-scale row (64 + 8: conflict-free stores)
+constexpr int kPvUp = 64;   // (of those 8)
+
+// A power of two for the V scales of a page: 2^w that puts the largest in [2^13, 2^14) (subnormal
+// ones below it).  Called by a whole warp, the same for all lanes.
+template <bool FULL, int GS>
+__device__ __forceinline__ float page_value_up(const uint8_t* blk, int valid) {
+    constexpr int NG = 4 >> GS;  // (s, z) pairs per token vector
+    const int lane = threadIdx.x & 31;
+    __half2 mx = __float2half2_rn(0.f);  // (of s, and of z, which nothing asks for)
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        const int t = lane + 32 * it;
+        if (FULL || t < valid) {
+            const __half2* at = reinterpret_cast<const __half2*>(blk + v_scale_off(GS) + t * 4 * NG);
+            __half2 w[NG];
+            if constexpr (NG == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at);
+            else if constexpr (NG == 2) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
+            else w[0] = *at;
+#pragma unroll
+            for (int k = 0; k < NG; ++k) mx = __hmax2(mx, __habs2(w[k]));
+        }
+    }
+    const uint32_t s = __reduce_max_sync(kFull, (uint32_t)__half_as_ushort(__low2half(mx)));
+    return __uint_as_float((uint32_t)(127 + 13 + 15 - max((int)(s >> 10), 1)) << 23);
+}
 
 // The page's scales into the warp's scratch: for each token row and each
 // 32-position block b (quantisation group b >> GS), fp32 s scaled by the
 // block's power of two (K: k_scale_up) and z; rows past the
 // valid tokens are zero.  K rows: s~ and z as float4 per token; V rows: z per
 // token, and s~ in the P.V token order (pv_pos).
-// CENTRE: V z + 1.5 s in place of z (the codes then count from 1.5).
+// CENTRE: V z + 1.5 s in place of z (the codes then count from 1.5), V s~ times
+// page_value_up's power of two and its inverse at vsS[kPvUp] (an fp16 product of a weight and a
+// scale would lose its bits below 2^-14: values of 2^-13 came out 5e-4 off; 2 % of the kernel).
 template <bool FULL, int GS, bool CENTRE>
 __device__ __forceinline__ void page_scales_g(const uint8_t* blk, int valid, float4* ksS, float4* kzS, float4* vzS,
                                               float* vsS, float kmul, float vmul) {
     constexpr int NG = 4 >> GS;  // (s, z) pairs per token vector
     const int lane = threadIdx.x & 31;
+    if constexpr (CENTRE) {
+        vmul = page_value_up<FULL, GS>(blk, valid);
+        if (lane == 0) vsS[kPvUp] = __uint_as_float((254u << 23) - __float_as_uint(vmul));
+    }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int which = it >> 1, t = lane + 32 * (it & 1);
@@ -635,6 +666,7 @@ template <int NT>
 __device__ __forceinline__ void page_values_centred(const uint8_t* blk, const float* pS, const float* vsS,
                                                     const SplitSel& take_lo, float (&acc_o)[8][4]) {
     const int lane = threadIdx.x & 31, gID = lane >> 2, tq = lane & 3;
+    const float down = vsS[kPvUp];
     uint32_t pv[4][4];  // [plane 8 k + gID][m]
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -673,7 +705,7 @@ __device__ __forceinline__ void page_values_centred(const uint8_t* blk, const fl
                 if constexpr (NT == 2) mma_f16_16816(t, a0, a1, a2, a3, w[m][2], w[m][3]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc_o[2 * g + half][e] += t[e];
+            for (int e = 0; e < 4; ++e) acc_o[2 * g + half][e] = fmaf(t[e], down, acc_o[2 * g + half][e]);
         }
     };
     slot_tiles(std::integral_constant<int, 0>{});
