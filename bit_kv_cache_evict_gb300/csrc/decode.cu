@@ -2356,9 +2356,8 @@ static int bf16_blocks(const DecodeParams& p, int sms) {
 // Fewer history pages (at most) than two waves of minimum items on the INT2
 // grid (a batch of one or two long sequences): items of one wave instead, so that
 // no block takes a second item while others idle.  Longer items only lower
-// the item count the workspace was sized for.
-static void one_wave_items(DecodeParams& p, int sms) {
-    const int per_sm = (p.NT == 1 || !(p.codebook || p.boost)) ? 3 : 2;  // as int2_blocks_per_sm
+// the item count the workspace was sized for.  per_sm: int2_blocks_per_sm of the kernel launched.
+static void one_wave_items(DecodeParams& p, int sms, int per_sm) {
     const int64_t blocks = (int64_t)per_sm * sms;
     const int64_t line = (int64_t)p.B * p.hk * p.max_pages;
     if (p.pps == kShortItemPages && line < 2 * kShortItemPages * blocks) {
@@ -2381,7 +2380,8 @@ cudaError_t launch_decode(const DecodeParams& pin, cudaStream_t st, cudaEvent_t 
         if (e != cudaSuccess) return e;
     }
     DecodeParams p = pin;
-    one_wave_items(p, at.sms);
+    one_wave_items(p, at.sms, p.NT == 1 ? int2_blocks_per_sm<1, false, false>()
+                              : p.codebook || p.boost ? int2_blocks_per_sm<2, true, false>() : int2_blocks_per_sm<2, false, false>());
     if (!at.setp) {
         e = set_smem(prep_kernel<false>, kPrepSmem);
         if (e != cudaSuccess) return e;
@@ -2485,7 +2485,7 @@ static cudaError_t decode_weights(const DecodeParamsX& pin, cudaStream_t st) {
     if ((e = mode_attributes<INT4, MODE>(dev)) != cudaSuccess) return e;
     DecodeParamsX p = pin;
     if constexpr (INT4) p.blocks = std::min(int4_blocks_per_sm(p.NT, p.gshift) * at.sms, kMaxBlocks4);
-    else one_wave_items(p, at.sms);
+    else one_wave_items(p, at.sms, p.NT == 2 && !p.out_bf16 ? int2_blocks_per_sm<2, false, false, true>() : int2_blocks_per_sm<1, false, false>());
     dim3 pg((p.B + kPrepSeqs - 1) / kPrepSeqs + 1, p.hk);
     if ((e = launch_pdl(prep_kernel<INT4, MODE>, pg, dim3(kPrepThreads), kPrepSmem, st, p)) != cudaSuccess) return e;
     if constexpr (INT4) e = launch_int4(p, MODE, st, dev);
