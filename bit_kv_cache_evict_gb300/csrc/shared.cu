@@ -978,7 +978,12 @@ cudaError_t launch_parts(const DecodeParamsX& p, cudaStream_t st, int dev) {
     using SM = SharedSmem<BITS, PARTS>;
     static bool set[64];
     if (!set[dev & 63]) {
-        const cudaError_t e = set_smem(shared_kernel<BITS, PARTS>, SM::kAlloc);
+        // setmaxnreg moves registers between the roles and waits for ever where they are not there: the
+        // shares were added up for a launch with kLaunchRegs
+        cudaFuncAttributes a;
+        cudaError_t e = cudaFuncGetAttributes(&a, shared_kernel<BITS, PARTS>);
+        if (e == cudaSuccess && a.numRegs != SM::kLaunchRegs) e = cudaErrorInvalidConfiguration;
+        if (e == cudaSuccess) e = set_smem(shared_kernel<BITS, PARTS>, SM::kAlloc);
         if (e != cudaSuccess) return e;
         set[dev & 63] = true;
     }
