@@ -217,47 +217,65 @@ __device__ __forceinline__ void prep_body(const Params<INT4, MODE>& p) {
     const int units = nseq * p.NT * 4;
     float* qU = psm + kD * kD;               // [unit][kD] q' in stored order
     float* mxU = qU + kPrepUnits * kD;       // [unit] largest |q'| (0 for padding)
-    // q U_K first: a warp per 32 columns and half of the units, a lane per column.  An element of U_K
-    // is read once for the warp's units, the units' x[a] come as one or two 16-byte broadcasts
-    // (a warp per unit read all of U_K for each, 80 % of the shared-memory rate: the scored
-    // decode of 32 x 8K with eight heads took 101 us, 95 with this; 256 x 8K shared 283, 280).
-    // x[a] of unit u lies at quad (u / 4) ^ (a / 4 % 4) of row a (else a warp's stores go to one bank).
+    // q U_K first, of the block's (sequence, head) rows without padding: a warp per 32 columns and half
+    // of the rows, a lane per column.  An element of U_K is read once for the warp's rows, the rows'
+    // x[a] come as one or two broadcasts of up to 16 bytes (a warp per row read all of U_K for each,
+    // 80 % of the shared-memory rate: the scored decode of 32 x 8K with eight heads took 101 us, 95
+    // with this; 256 x 8K shared 283, 280).  Both halves have work whatever the number of rows (with
+    // a lone sequence's eight heads in one of them 1 x 705 took 19.2 us in 4 bits, 17.4 with this).
+    // x[a] of row r lies at quad (r / 4) ^ (a / 4 % 4) of [a] (else a warp's stores go to one bank).
     float* xS = qU;                          // [a][kPrepUnits] first, then the products [unit][kD]
-    for (int u = warp; u < kPrepUnits; u += kPrepThreads / 32) {
-        const int hl = 4 * ((u >> 2) % p.NT) + (u & 3), b = b0 + (u >> 2) / p.NT;
+    const int rows = nseq * p.G, each = max(1, rows >> 1), gsh = 31 - __clz(p.G);  // (powers of two)
+    for (int r = warp; r < 2 * each; r += kPrepThreads / 32) {
         uint2 qr = make_uint2(0u, 0u);
-        if (u < units && hl < p.G) qr = *reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.hq + kv * p.G + hl) * kD + 4 * lane);
-        xS[(4 * lane + 0) * kPrepUnits + (u ^ ((lane & 3) << 2))] = bf16_lo(qr.x);
-        xS[(4 * lane + 1) * kPrepUnits + (u ^ ((lane & 3) << 2))] = bf16_hi(qr.x);
-        xS[(4 * lane + 2) * kPrepUnits + (u ^ ((lane & 3) << 2))] = bf16_lo(qr.y);
-        xS[(4 * lane + 3) * kPrepUnits + (u ^ ((lane & 3) << 2))] = bf16_hi(qr.y);
+        if (r < rows) qr = *reinterpret_cast<const uint2*>(p.q + ((size_t)(b0 + (r >> gsh)) * p.hq + kv * p.G + (r & (p.G - 1))) * kD + 4 * lane);
+        xS[(4 * lane + 0) * kPrepUnits + (r ^ ((lane & 3) << 2))] = bf16_lo(qr.x);
+        xS[(4 * lane + 1) * kPrepUnits + (r ^ ((lane & 3) << 2))] = bf16_hi(qr.x);
+        xS[(4 * lane + 2) * kPrepUnits + (r ^ ((lane & 3) << 2))] = bf16_lo(qr.y);
+        xS[(4 * lane + 3) * kPrepUnits + (r ^ ((lane & 3) << 2))] = bf16_hi(qr.y);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
     const int col = 32 * (warp & 3) + lane, half = warp >> 2;
-    auto products = [&](auto quads) {        // units 4 Q half .. + 4 Q - 1
-        constexpr int Q = decltype(quads)::value;
-        float y[4 * Q];
+    auto products = [&](auto count) {        // rows N half .. + N - 1
+        constexpr int N = decltype(count)::value;
+        float y[N];
 #pragma unroll
-        for (int i = 0; i < 4 * Q; ++i) y[i] = 0.f;
-#pragma unroll 4
+        for (int i = 0; i < N; ++i) y[i] = 0.f;
+#pragma unroll(N == 1 ? 16 : N == 2 ? 8 : 4)
         for (int a = 0; a < kD; ++a) {
             const float uu = Us[a * kD + col];
+            const float* xa = xS + a * kPrepUnits;
+            if constexpr (N == 1) {
+                y[0] = fmaf(xa[half ^ (a & 12)], uu, y[0]);
+            } else if constexpr (N == 2) {
+                const float2 x = *reinterpret_cast<const float2*>(xa + ((2 * half) ^ (a & 12)));
+                y[0] = fmaf(x.x, uu, y[0]);
+                y[1] = fmaf(x.y, uu, y[1]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                const float4 x = *reinterpret_cast<const float4*>(xS + a * kPrepUnits + 4 * ((Q * half + i) ^ ((a >> 2) & 3)));
-                y[4 * i] = fmaf(x.x, uu, y[4 * i]);
-                y[4 * i + 1] = fmaf(x.y, uu, y[4 * i + 1]);
-                y[4 * i + 2] = fmaf(x.z, uu, y[4 * i + 2]);
-                y[4 * i + 3] = fmaf(x.w, uu, y[4 * i + 3]);
+                for (int i = 0; i < N; i += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(xa + ((N * half + i) ^ (a & 12)));
+                    y[i] = fmaf(x.x, uu, y[i]);
+                    y[i + 1] = fmaf(x.y, uu, y[i + 1]);
+                    y[i + 2] = fmaf(x.z, uu, y[i + 2]);
+                    y[i + 3] = fmaf(x.w, uu, y[i + 3]);
+                }
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4 * Q; ++i) qU[(4 * Q * half + i) * kD + col] = y[i];
+        for (int i = 0; i < N; ++i) {
+            const int r = N * half + i;
+            qU[((r >> gsh) * p.NT * 4 + (r & (p.G - 1))) * kD + col] = y[i];
+        }
     };
-    if (p.NT == 1) products(std::integral_constant<int, 1>{});
-    else products(std::integral_constant<int, 2>{});
+    switch (each) {                          // (the same in the whole block)
+        case 1: products(std::integral_constant<int, 1>{}); break;
+        case 2: products(std::integral_constant<int, 2>{}); break;
+        case 4: products(std::integral_constant<int, 4>{}); break;
+        default: products(std::integral_constant<int, 8>{}); break;
+    }
     __syncthreads();
     for (int u = warp; u < units; u += kPrepThreads / 32) {
         const int hl = 4 * ((u >> 2) % p.NT) + (u & 3);  // head within the KV group
