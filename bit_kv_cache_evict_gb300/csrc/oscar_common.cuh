@@ -420,9 +420,11 @@ struct DecodeParams4 : DecodeParams {
 enum Mode { kModePlain = 0, kModeWeights = 1, kModeShared = 2 };
 
 constexpr int kSharedItems = 10;        // index of the shared pages' item count in the counters
-constexpr int kMinSharedPages = 4;      // pages of an item of a group at least (but for its last)
-// and at most: with a bf16 output the products of values of an item are summed where the tensor
-// core truncates them, 2^-24 of the running sum at each; over 2^14 tokens that stays
+// Pages of an item of a group: the plan cuts a group's pages into ceil(pages / n) even runs, n this
+// many at least
+constexpr int kMinSharedPages = 4;
+// and at most this many: with a bf16 output the products of values of an item are summed where the
+// tensor core truncates them, 2^-24 of the running sum at each; over 2^14 tokens that stays
 // below 2^-10 of the largest value (16384 pages as one item: up to 2 % of it, a flat softmax 0.7 %).
 constexpr int kMaxSharedRun = 256;
 constexpr int kMaxSharedGroups = 8192;

@@ -13,9 +13,10 @@
 //
 // group_kernel  makes the plan: members of each group, its split of the pages.
 // shared_kernel a block per item (group, KV head, up to 256 rows, run of pages):
-//               a producer warp (bulk copies of the packed pages), four warps
-//               that dequantise, a warp that issues the products, and four
-//               warps of softmax per 128 rows (a thread per row).
+//               four warps of softmax per 128 rows (a thread per row), with an fp32
+//               output four that add up the products of values, eight warps that
+//               dequantise, two that issue the products (of logits, of values) and two that
+//               copy (the packed pages, q').
 // Partials (o', m, l) per row and run join the split-K partials of the members' own
 // pages in merge_kernel.
 //

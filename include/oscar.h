@@ -660,7 +660,8 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
  * oscar_decode_attn_int4 (bits 4) for a batch in which groups of sequences
  * share the first pages of their histories (oscar_pool_layout's prefix groups,
  * pages adopted from the radix cache): the shared pages are read and
- * dequantised once for all members.  The result is that of the plain decode.
+ * dequantised once for all members.  The result is that of the plain decode, to
+ * the precision below, where the shared values are finite in fp16.
  *
  *   prefix_group  (device int32 [batch]) the group of each sequence, in [0,
  *                 n_groups); negative: none
@@ -672,7 +673,10 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
  *   min_members   groups of at least this many members (and two) attend their
  *                 pages together; 0: those for which it is faster, by the
  *                 library's rule on members, rows and pages.  The results do
- *                 not depend on it but for the roundings below.
+ *                 not depend on it but for the roundings below: which groups attend
+ *                 together depends on the batch, and with it how a bf16 output of a
+ *                 sequence is rounded; more than the batch has: none do.  A call
+ *                 in which none do takes about 10 us more than the plain decode.
  *   out           as oscar_decode_attn_int4, for 2 bits too
  *   workspace     as oscar_decode_attn; the size depends on n_groups too
  * Both arrays are read on the device, so that a captured graph follows them.  A
@@ -682,12 +686,13 @@ oscar_status oscar_history_select(int32_t batch, const float* weight, int32_t we
  * Precision: fp32 output as oscar_decode_attn_int4; a weight below 2^-40 of the
  * largest of its run of shared pages is 0 in the products.  For a bf16 output the
  * pages attended together: queries, values s * code + z and weights enter products
- * as fp16, one rounding of 2^-11 (relative; a weight: or of 2^-25 of the largest) each, and the
- * products of values are summed over up to 2^14 tokens in the tensor core, within
- * 2^-10 of the largest value; the rest as for fp32, but that 2-bit
- * pages of a sequence's own are summed as in oscar_decode_attn.  Shared
- * values s * code + z have to be finite in fp16 (|value| < 65520); NaN, and
- * what overflows, reaches the rows that attend it as NaN.
+ * as fp16, one rounding of 2^-11 (relative; a weight: or of 2^-25 of the largest)
+ * each, where the plain decode has 22 bits, and the products of values are summed
+ * over up to 2^14 tokens in the tensor core, within 2^-10 of the largest value; the
+ * rest as for fp32, but that 2-bit pages of a sequence's own are summed as in
+ * oscar_decode_attn.  Shared values s * code + z have to be finite in fp16
+ * (|value| < 65520), for an fp32 output too; NaN, and what overflows, reaches the
+ * rows that attend it as NaN.
  * Errors: as the decode calls; UNSUPPORTED for other bits.
  */
 oscar_status oscar_decode_attn_shared(const oscar_shape* shape, int32_t bits, int32_t batch, const void* q,
