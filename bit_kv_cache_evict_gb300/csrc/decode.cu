@@ -533,7 +533,7 @@ __device__ __forceinline__ float page_value_up(const uint8_t* blk, int valid) {
         const int t = lane + 32 * it;
         if (FULL || t < valid) {
             const __half2* at = reinterpret_cast<const __half2*>(blk + v_scale_off(GS) + t * 4 * NG);
-            __half2 w[NG];
+            alignas(16) __half2 w[NG];
             if constexpr (NG == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(at);
             else if constexpr (NG == 2) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(at);
             else w[0] = *at;
