@@ -55,8 +55,8 @@ DEFAULT_WORKLOAD = "qwen3_8b_36l"
 # units processed, only while the kernel source is the one captured.
 INT2_TRAFFIC_CAPTURE = {
     "workload": "qwen3_8b_36l",
-    "source_sha256_16": "6a76d98138f4c6b5",     # int2_sources(), comments removed
-    "traffic_bytes": 917.48e6 + 11.46e6,
+    "source_sha256_16": "c70ca4cbd80bc6c9",     # int2_sources(), comments removed
+    "traffic_bytes": 917.42e6 + 12.05e6,
     "algorithmic_bytes": 911.11e6,
 }
 
